@@ -2,7 +2,9 @@
 
 The compute path is liblkv.so (hand-written CUDA for sm_103a behind the C ABI
 in include/lkv.h). This package only marshals torch tensors into that ABI:
-``Context`` owns one liblkv context; every method is one C call.
+``Context`` owns one liblkv context; every method is one C call. ``Cache8``
+and ``Rope`` are the calls that have no context: a key/value cache held in 8
+bits with its attention, and rotary positions.
 """
 from __future__ import annotations
 
@@ -14,7 +16,7 @@ import torch
 from . import _lib
 from ._lib import LKVError, lkv_config  # noqa: F401
 
-__all__ = ["Context", "LKVError", "build"]
+__all__ = ["Cache8", "Context", "LKVError", "Rope", "build"]
 
 
 def build(force: bool = False) -> str:
@@ -208,3 +210,6 @@ class Context:
         """Failure-path check: a device wait that nothing completes runs out
         after limit_ns; the next sync() raises LKV_ETIMEOUT."""
         _lib.lkv_diag_wait_timeout(self._ctx, limit_ns)
+
+
+from .cache8 import Cache8, Rope  # noqa: E402  (uses the helpers above)

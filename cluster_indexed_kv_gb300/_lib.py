@@ -22,10 +22,16 @@ EXPORTED = ("lkv_create", "lkv_destroy", "lkv_build_index", "lkv_load_index",
             "lkv_sync", "lkv_last_error", "lkv_set_profiling", "lkv_get_profile",
             "lkv_kmeans_static", "lkv_kmeans_static_status", "lkv_set_kmeans_filter",
             "lkv_diag_wait_timeout", "lkv_uva_read", "lkv_read_ceiling", "lkv_set_policy", "lkv_build_pages",
-            "lkv_build_index_async", "lkv_build_paris", "lkv_paris_levels")
+            "lkv_build_index_async", "lkv_build_paris", "lkv_paris_levels",
+            "lkv_rope_init", "lkv_rope_apply", "lkv_cache8_write", "lkv_cache8_read",
+            "lkv_cache8_attend", "lkv_cache8_attend_workspace", "lkv_cache8_status")
 LKV_FILTER_TENSOR, LKV_FILTER_SIMT = 0, 1
 LKV_TRIGGER_ADAPTIVE, LKV_TRIGGER_EVERY, LKV_TRIGGER_INTERVAL = 0, 1, 2
 LKV_FILL_PREFIX, LKV_FILL_SKIP = 0, 1
+LKV_ROPE_HALF, LKV_ROPE_INTERLEAVED = 0, 1
+LKV_ROPE_NONE, LKV_ROPE_LINEAR, LKV_ROPE_NTK, LKV_ROPE_YARN = range(4)
+LKV_CACHE8_BLOCK = 16
+LKV_CODE_INT8, LKV_CODE_E4M3 = 0, 1
 
 
 class lkv_config(C.Structure):
@@ -45,6 +51,25 @@ class lkv_policy(C.Structure):
 
 class lkv_paris_params(C.Structure):
     _fields_ = [("rho", C.c_int32), ("n_cand", C.c_int32), ("seed", C.c_uint64)]
+
+
+class lkv_rope_params(C.Structure):
+    _fields_ = [("rotary_dim", C.c_int32), ("layout", C.c_int32), ("scaling", C.c_int32),
+                ("orig_len", C.c_int32), ("base", C.c_double), ("factor", C.c_double),
+                ("beta_fast", C.c_double), ("beta_slow", C.c_double)]
+
+
+class lkv_rope(C.Structure):
+    _fields_ = [("rotary_dim", C.c_int32), ("layout", C.c_int32), ("gain", C.c_float),
+                ("reserved", C.c_int32), ("turn", C.c_uint64 * 64)]
+
+
+class lkv_cache8(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("n_kv_heads", C.c_int32), ("capacity", C.c_int32),
+                ("dtype", C.c_int32), ("code", C.c_int32), ("reserved", C.c_int32),
+                ("k_codes", C.c_void_p), ("v_codes", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("k_tail", C.c_void_p), ("v_tail", C.c_void_p),
+                ("lengths", C.c_void_p), ("ticket", C.c_void_p)]
 
 
 class lkv_decode_state(C.Structure):
@@ -126,6 +151,20 @@ def load(path: str = LIB_PATH):
         L.lkv_build_paris.restype = st
         L.lkv_paris_levels.argtypes = [vp, vp]
         L.lkv_paris_levels.restype = st
+        L.lkv_rope_init.argtypes = [C.POINTER(lkv_rope_params), C.POINTER(lkv_rope)]
+        L.lkv_rope_init.restype = st
+        L.lkv_rope_apply.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+        L.lkv_rope_apply.restype = st
+        L.lkv_cache8_write.argtypes = [vp, vp, vp, i32, vp, vp, vp]
+        L.lkv_cache8_write.restype = st
+        L.lkv_cache8_read.argtypes = [vp, vp, i32, vp, vp, vp]
+        L.lkv_cache8_read.restype = st
+        L.lkv_cache8_attend.argtypes = [vp, vp, i32, i32, vp, f32, i32, i32, i32, vp, vp, i64, vp]
+        L.lkv_cache8_attend.restype = st
+        L.lkv_cache8_attend_workspace.argtypes = [vp, i32, i32, i32, i32, i32, C.POINTER(i64)]
+        L.lkv_cache8_attend_workspace.restype = st
+        L.lkv_cache8_status.argtypes = [vp, vp]
+        L.lkv_cache8_status.restype = st
         L.lkv_sync.argtypes = [vp]
         L.lkv_sync.restype = st
         L.lkv_last_error.argtypes = [vp]
@@ -249,6 +288,53 @@ def lkv_uva_read(host_ptr, dev_ptr, nbytes: int, stream_ptr) -> None:
 
 def lkv_read_ceiling(dev_ptr, nbytes: int, stream_ptr) -> None:
     _check(load().lkv_read_ceiling(dev_ptr, nbytes, stream_ptr), None)
+
+
+def lkv_rope_init(rotary_dim, layout, scaling, orig_len, base, factor, beta_fast, beta_slow):
+    """The filled lkv_rope table (host only)."""
+    prm = lkv_rope_params(rotary_dim, layout, scaling, orig_len, base, factor, beta_fast, beta_slow)
+    table = lkv_rope()
+    _check(load().lkv_rope_init(C.byref(prm), C.byref(table)), None)
+    return table
+
+
+def lkv_rope_apply(table, dtype, batch, n_heads, n_kv_heads, n, q_ptr, k_ptr, pos_ptr, q_out_ptr,
+                   k_out_ptr, stream_ptr) -> None:
+    status = (_lib or load()).lkv_rope_apply(table, dtype, batch, n_heads, n_kv_heads, n, q_ptr, k_ptr,
+                                             pos_ptr, q_out_ptr, k_out_ptr, stream_ptr)
+    if status:
+        _check(status, None)
+
+
+def lkv_cache8_write(cache, k_ptr, v_ptr, n, start_ptr, counts_ptr, stream_ptr) -> None:
+    status = (_lib or load()).lkv_cache8_write(cache, k_ptr, v_ptr, n, start_ptr, counts_ptr, stream_ptr)
+    if status:
+        _check(status, None)
+
+
+def lkv_cache8_read(cache, first_ptr, n, k_ptr, v_ptr, stream_ptr) -> None:
+    status = (_lib or load()).lkv_cache8_read(cache, first_ptr, n, k_ptr, v_ptr, stream_ptr)
+    if status:
+        _check(status, None)
+
+
+def lkv_cache8_attend(cache, q_ptr, group, n, counts_ptr, scale, window, sinks, max_len, out_ptr,
+                      ws_ptr, ws_bytes, stream_ptr) -> None:
+    status = (_lib or load()).lkv_cache8_attend(cache, q_ptr, group, n, counts_ptr, scale, window, sinks,
+                                                max_len, out_ptr, ws_ptr, ws_bytes, stream_ptr)
+    if status:
+        _check(status, None)
+
+
+def lkv_cache8_attend_workspace(cache, group, n, window, sinks, max_len) -> int:
+    n_bytes = C.c_int64(0)
+    _check(load().lkv_cache8_attend_workspace(cache, group, n, window, sinks, max_len,
+                                              C.byref(n_bytes)), None)
+    return n_bytes.value
+
+
+def lkv_cache8_status(cache, stream_ptr) -> None:
+    _check(load().lkv_cache8_status(cache, stream_ptr), None)
 
 
 def lkv_diag_wait_timeout(ctx, limit_ns: int) -> None:

@@ -1,0 +1,218 @@
+"""Rotary positions, and the key/value cache held in 8 bits (include/lkv.h:
+lkv_rope_*, lkv_cache8_*). ``Rope`` holds one table, ``Cache8`` one cache's
+tensors; the methods run on the current stream of the tensors' device, allocate
+only the outputs they return (and an attention's workspace, where it needs
+one), and can be captured into CUDA graphs.
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import _lib
+
+_DTYPES = {torch.float32: _lib.LKV_DTYPE_FP32, torch.bfloat16: _lib.LKV_DTYPE_BF16}
+_CODES = {torch.int8: _lib.LKV_CODE_INT8, torch.float8_e4m3fn: _lib.LKV_CODE_E4M3}
+_FORMATS = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+_D = 128
+_BLOCK = _lib.LKV_CACHE8_BLOCK
+
+
+def _tensor(t, name, shape, dtype, device) -> int:
+    """Data pointer of a contiguous CUDA tensor of this shape, type and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _optional(t, name, shape, dtype, device):
+    return None if t is None else _tensor(t, name, shape, dtype, device)
+
+
+def _call(device, fn, *args) -> None:
+    """fn(*args, stream) on the device's current stream, with the device current."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            fn(*args, stream)
+
+
+class Rope:
+    """A table of rotary positions (lkv_rope_init): layout "half" pairs values
+    (i, i + rotary_dim / 2), "interleaved" (2 i, 2 i + 1); scaling "none",
+    "linear", "ntk" or "yarn" stretches the positions by ``factor``."""
+
+    def __init__(self, *, rotary_dim: int = _D, layout: str = "half", base: float = 10000.0,
+                 scaling: str = "none", factor: float = 1.0, orig_len: int = 0,
+                 beta_fast: float = 32.0, beta_slow: float = 1.0):
+        lay = {"half": _lib.LKV_ROPE_HALF, "interleaved": _lib.LKV_ROPE_INTERLEAVED}[layout]
+        how = {"none": _lib.LKV_ROPE_NONE, "linear": _lib.LKV_ROPE_LINEAR, "ntk": _lib.LKV_ROPE_NTK,
+               "yarn": _lib.LKV_ROPE_YARN}[scaling]
+        self.table = _lib.lkv_rope_init(rotary_dim, lay, how, orig_len, base, factor, beta_fast,
+                                        beta_slow)
+        self._at = C.addressof(self.table)
+
+    def apply(self, q: torch.Tensor, positions: torch.Tensor, k: torch.Tensor | None = None, *,
+              q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
+        """Rotate q [B, H, n, 128] and, if given, k [B, H_kv, n, 128] by
+        positions int32 [B, n]. Returns q_out, or (q_out, k_out) with k; the
+        outputs may be q and k themselves (in place), and are new tensors by
+        default."""
+        if not isinstance(q, torch.Tensor) or not q.is_cuda:
+            raise ValueError("q must be a CUDA tensor")
+        if q.dtype not in _DTYPES:
+            raise TypeError("q must be float32 or bfloat16")
+        if q.dim() != 4 or q.shape[3] != _D:
+            raise ValueError(f"q must have shape [B, H, n, {_D}], got {tuple(q.shape)}")
+        dev, dt = q.device, q.dtype
+        batch, heads, n, _ = q.shape
+        qp = _tensor(q, "q", q.shape, dt, dev)
+        pp = _tensor(positions, "positions", (batch, n), torch.int32, dev)
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        qo = _tensor(q_out, "q_out", q.shape, dt, dev)
+        kp = ko = None
+        kv_heads = 0
+        if k is not None:
+            if not isinstance(k, torch.Tensor) or k.dim() != 4:
+                raise ValueError(f"k must be a tensor of shape [B, H_kv, n, {_D}]")
+            kv_heads = k.shape[1]
+            shape = (batch, kv_heads, n, _D)
+            kp = _tensor(k, "k", shape, dt, dev)
+            k_out = torch.empty_like(k) if k_out is None else k_out
+            ko = _tensor(k_out, "k_out", shape, dt, dev)
+        elif k_out is not None:
+            raise ValueError("k_out without k")
+        _call(dev, _lib.lkv_rope_apply, self._at, _DTYPES[dt], batch, heads, kv_heads, n, qp, kp, pp,
+              qo, ko)
+        return q_out if k is None else (q_out, k_out)
+
+
+class Cache8:
+    """A key/value cache held in 8 bits (lkv_cache8): ``k_codes``, ``v_codes``
+    [B, H_kv, capacity, 128] (int8 or float8_e4m3fn), ``k_scale``, ``v_scale``
+    fp32 [B, H_kv, capacity / 16], ``k_tail``, ``v_tail`` [B, H_kv, 16, 128]
+    (the last block in full precision) and ``lengths`` int32 [B], all on the
+    device and the caller's to read. Methods that write must not overlap, on
+    the GPU, with others on the same cache."""
+
+    def __init__(self, *, batch: int, n_kv_heads: int, capacity: int, dtype: torch.dtype,
+                 fmt: str = "int8", device: torch.device | str = "cuda"):
+        if fmt not in _FORMATS:
+            raise ValueError('fmt must be "int8" or "e4m3"')
+        if capacity < 1 or capacity % _BLOCK:
+            raise ValueError(f"capacity must be a multiple of {_BLOCK}")
+        slices = (batch, n_kv_heads)
+        z = dict(device=device)
+        codes = [torch.zeros(*slices, capacity, _D, dtype=torch.int8, **z).view(_FORMATS[fmt])
+                 for _ in range(2)]
+        scale = [torch.zeros(*slices, capacity // _BLOCK, dtype=torch.float32, **z) for _ in range(2)]
+        tail = [torch.zeros(*slices, _BLOCK, _D, dtype=dtype, **z) for _ in range(2)]
+        self._bind(*codes, *scale, *tail, torch.zeros(batch, dtype=torch.int32, **z))
+
+    @classmethod
+    def from_tensors(cls, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
+                     v_scale: torch.Tensor, k_tail: torch.Tensor, v_tail: torch.Tensor,
+                     lengths: torch.Tensor) -> "Cache8":
+        """A cache on tensors that already hold one (they are not copied)."""
+        self = cls.__new__(cls)
+        self._bind(k_codes, v_codes, k_scale, v_scale, k_tail, v_tail, lengths)
+        return self
+
+    def _bind(self, k_codes, v_codes, k_scale, v_scale, k_tail, v_tail, lengths):
+        if not isinstance(k_codes, torch.Tensor) or not k_codes.is_cuda:
+            raise ValueError("k_codes must be a CUDA tensor")
+        if k_codes.dtype not in _CODES:
+            raise TypeError("k_codes must be int8 or float8_e4m3fn")
+        if k_codes.dim() != 4 or k_codes.shape[3] != _D or k_codes.shape[2] % _BLOCK:
+            raise ValueError(f"k_codes must have shape [B, H_kv, capacity (a multiple of {_BLOCK}), {_D}]")
+        if not isinstance(k_tail, torch.Tensor) or k_tail.dtype not in _DTYPES:
+            raise TypeError("k_tail must be a float32 or bfloat16 tensor")
+        self.batch, self.n_kv_heads, self.capacity, _ = k_codes.shape
+        self.device, self.dtype = k_codes.device, k_tail.dtype
+        slices, dev = (self.batch, self.n_kv_heads), self.device
+        blocks, tails = (*slices, self.capacity // _BLOCK), (*slices, _BLOCK, _D)
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.k_tail, self.v_tail, self.lengths = k_tail, v_tail, lengths
+        self._ticket = torch.zeros(self.batch + 1, dtype=torch.int32, device=dev)
+        self._view = _lib.lkv_cache8(
+            self.batch, self.n_kv_heads, self.capacity, _DTYPES[self.dtype], _CODES[k_codes.dtype], 0,
+            _tensor(k_codes, "k_codes", k_codes.shape, k_codes.dtype, dev),
+            _tensor(v_codes, "v_codes", k_codes.shape, k_codes.dtype, dev),
+            _tensor(k_scale, "k_scale", blocks, torch.float32, dev),
+            _tensor(v_scale, "v_scale", blocks, torch.float32, dev),
+            _tensor(k_tail, "k_tail", tails, self.dtype, dev),
+            _tensor(v_tail, "v_tail", tails, self.dtype, dev),
+            _tensor(lengths, "lengths", (self.batch,), torch.int32, dev),
+            self._ticket.data_ptr())
+        self._at = C.addressof(self._view)
+
+    def write(self, k: torch.Tensor, v: torch.Tensor, *, start: torch.Tensor | None = None,
+              counts: torch.Tensor | None = None) -> None:
+        """Append k, v [B, H_kv, n, 128]: sequence b takes its first counts[b]
+        rows (default: all n) at positions start[b].. (default: its length),
+        and its length becomes start[b] + counts[b]. start may take back
+        tokens of the last block, or down to a multiple of 16."""
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError(f"k must be a tensor of shape [B, H_kv, n, {_D}]")
+        dev, dt = self.device, self.dtype
+        shape = (self.batch, self.n_kv_heads, k.shape[2], _D)
+        kp, vp = _tensor(k, "k", shape, dt, dev), _tensor(v, "v", shape, dt, dev)
+        sp = _optional(start, "start", (self.batch,), torch.int32, dev)
+        cp = _optional(counts, "counts", (self.batch,), torch.int32, dev)
+        _call(dev, _lib.lkv_cache8_write, self._at, kp, vp, shape[2], sp, cp)
+
+    def read(self, n: int, *, first: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+             v_out: torch.Tensor | None = None):
+        """Rows first[b] .. first[b] + n - 1 (default: from 0) of every
+        sequence as (k, v) [B, H_kv, n, 128] of the cache's dtype; zeros
+        outside a sequence. The layout is the one Context.build_index takes."""
+        dev, dt = self.device, self.dtype
+        shape = (self.batch, self.n_kv_heads, n, _D)
+        k_out = torch.empty(shape, dtype=dt, device=dev) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=dt, device=dev) if v_out is None else v_out
+        kp, vp = _tensor(k_out, "k_out", shape, dt, dev), _tensor(v_out, "v_out", shape, dt, dev)
+        fp = _optional(first, "first", (self.batch,), torch.int32, dev)
+        _call(dev, _lib.lkv_cache8_read, self._at, fp, n, kp, vp)
+        return k_out, v_out
+
+    def attend(self, q: torch.Tensor, *, counts: torch.Tensor | None = None, scale: float | None = None,
+               window: int = 0, sinks: int = 0, max_len: int = 0,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+        """Causal attention of each sequence's last n tokens, whose keys and
+        values the cache holds: q [B, H, n, 128], H a multiple of H_kv. With
+        counts, the first counts[b] rows of sequence b are its last tokens and
+        its other rows are padding (zero in the output). scale defaults to
+        1 / sqrt(128). window > 0: a token sees the `window` last ones up to
+        itself and the `sinks` first ones. max_len: a bound of the lengths
+        known to the caller (0: none); it only steers the split of the work."""
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError(f"q must be a tensor of shape [B, H, n, {_D}]")
+        dev, dt = self.device, self.dtype
+        heads, n = q.shape[1], q.shape[2]
+        group = heads // self.n_kv_heads
+        if group * self.n_kv_heads != heads or heads == 0:
+            raise ValueError(f"q's {heads} heads are not a multiple of the cache's {self.n_kv_heads}")
+        shape = (self.batch, heads, n, _D)
+        qp = _tensor(q, "q", shape, dt, dev)
+        cp = _optional(counts, "counts", (self.batch,), torch.int32, dev)
+        out = torch.empty(shape, dtype=dt, device=dev) if out is None else out
+        op = _tensor(out, "out", shape, dt, dev)
+        _call(dev, _lib.lkv_cache8_attend, self._at, qp, group, n, cp,
+              _D ** -0.5 if scale is None else float(scale), window, sinks, max_len, op, None, 0)
+        return out
+
+    def check(self) -> None:
+        """Wait for the current stream; raise LKVError if a write since the
+        last check did not fit or held a value that is not finite."""
+        _call(self.device, _lib.lkv_cache8_status, self._at)

@@ -1,0 +1,488 @@
+// cache8.cu -- the 8-bit key/value cache: writing, reading back, status.
+#include "cache8.cuh"
+
+#include <cuda_fp16.h>
+
+namespace lkv {
+
+constexpr int kCacheThreads = 128;
+constexpr int kCacheWarps = kCacheThreads / 32;
+
+const char *check_cache8(const lkv_cache8 *c) {
+  if (!c) return "null cache";
+  if (c->batch < 1 || c->batch > (1 << 20)) return "batch must be 1..2^20";
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 4096) return "n_kv_heads must be 1..4096";
+  if (c->capacity < kBlock || c->capacity % kBlock != 0 || c->capacity > (1 << 30))
+    return "capacity must be a multiple of 16, 16..2^30";
+  if (c->dtype != LKV_DTYPE_FP32 && c->dtype != LKV_DTYPE_BF16) return "bad dtype";
+  if (c->code != LKV_CODE_INT8 && c->code != LKV_CODE_E4M3) return "unknown code";
+  if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || !c->k_tail || !c->v_tail || !c->lengths || !c->ticket)
+    return "null array of the cache";
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_tail, 16) || !aligned(c->v_tail, 16) ||
+      !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) || !aligned(c->lengths, 4) || !aligned(c->ticket, 4))
+    return "the cache's codes and tails must be 16-byte aligned, its other arrays 4-byte aligned";
+  return nullptr;
+}
+
+bool overlaps_cache8(const lkv_cache8 *c, const void *p, int64_t bytes) {
+  const int64_t slices = (int64_t)c->batch * c->n_kv_heads, es = c->dtype == LKV_DTYPE_BF16 ? 2 : 4;
+  const int64_t codes = slices * c->capacity * kHeadDim, scales = slices * (c->capacity / kBlock) * 4;
+  const int64_t tail = slices * kBlock * kHeadDim * es;
+  return overlap(p, bytes, c->k_codes, codes) || overlap(p, bytes, c->v_codes, codes) ||
+         overlap(p, bytes, c->k_scale, scales) || overlap(p, bytes, c->v_scale, scales) ||
+         overlap(p, bytes, c->k_tail, tail) || overlap(p, bytes, c->v_tail, tail) ||
+         overlap(p, bytes, c->lengths, (int64_t)c->batch * 4) || overlap(p, bytes, c->ticket, ((int64_t)c->batch + 1) * 4);
+}
+
+// ---------------------------------------------------------------- write
+
+// The code of x in a block of largest magnitude amax, decided exactly: the
+// quotient's distance from the halfway point between two codes has the sign
+// of a difference of two products that fp64 holds exactly (24-bit by 9-bit
+// significands). Only values within the fp32 quotient's error of such a
+// point come here.
+__device__ __noinline__ int int8_exact(float x, float amax) {
+  const float a = fabsf(x);
+  const int m = (int)rintf(a * __fdiv_rn(127.f, amax) - 0.5f);  // the halfway point is m + 1/2
+  const double d = 254.0 * (double)a - (double)(2 * m + 1) * (double)amax;
+  const int k = d > 0.0 ? m + 1 : d < 0.0 ? m : (m + (m & 1));
+  return x < 0.f ? -k : k;
+}
+
+__device__ __noinline__ float e4m3_exact(float x, float amax) {
+  const float a = fabsf(x), q = a * __fdiv_rn(448.f, amax);
+  // step of the code's binade: 2^(e - 3), 2^-9 below 2^-6
+  const float step = q < 0x1p-6f ? 0x1p-9f : __uint_as_float((__float_as_uint(q) & 0x7f800000u) - (3u << 23));
+  const float m = rintf(q / step - 0.5f);
+  const double d = 448.0 * (double)a - (double)(m + 0.5f) * (double)step * (double)amax;
+  const float k = d > 0.0 ? m + 1.f : d < 0.0 ? m : (m + (float)((int)m & 1));
+  return copysignf(k * step, x);
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four codes of x[0..3] in one word; inv is about 127 / amax or 448 / amax.
+// The fp32 quotient is off by at most 2 units in its last place; where that
+// could change the code, the lane settles it exactly.
+template <int CODE>
+__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv, float amax) {
+  float q[4];
+  if constexpr (CODE == LKV_CODE_INT8) {
+    float far = 0.f;
+    uint32_t r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      q[e] = x[e] * inv;
+      const float s = __fadd_rn(q[e], 12582912.f);  // 1.5 * 2^23: the sum's low bits are the rounded integer
+      r[e] = __float_as_uint(s);
+      far = fmaxf(far, fabsf(q[e] - (s - 12582912.f)));
+    }
+    if (far > 0.5f - 0x1p-14f) {  // |q| < 128 is off by less than 2^-15
+#pragma unroll 1
+      for (int e = 0; e < 4; ++e) r[e] = (uint32_t)int8_exact(x[e], amax);
+    }
+    return __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
+  } else {
+    uint32_t near = 0xffffffffu;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      q[e] = x[e] * inv;
+      // adding 2^-6 to a magnitude below it gives the codes there the spacing
+      // of the first binade; the 20 bits behind a code are then 0x80000 halfway
+      float a = fabsf(q[e]);
+      a = a < 0x1p-6f ? a + 0x1p-6f : a;
+      near = min(near, (uint32_t)abs((int)(__float_as_uint(a) & 0xfffffu) - 0x80000));
+    }
+    if (near <= 8u) {
+#pragma unroll 1
+      for (int e = 0; e < 4; ++e) q[e] = e4m3_exact(x[e], amax);
+    }
+    return e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
+  }
+}
+
+// One block of one (sequence, KV head) of K or V: the rows of a block from
+// the tail and the new rows, codes and scale where the block is full, and the
+// new rows of the last block into the tail.
+template <int DT, int CODE>
+struct BlockWriter {
+  static constexpr int E = DT == 1 ? 8 : 4;         // values of a 16-byte load
+  static constexpr int LPR = kHeadDim / E;          // lanes of a row
+  static constexpr int RPL = 32 / LPR;              // rows of a load
+  static constexpr int NL = kBlock / RPL;           // loads of a block
+  const uint4 *src;      // new rows of the slice
+  uint4 *tail;           // the slice's tail
+  uint8_t *codes;        // the slice's codes
+  float *scale;          // the slice's scales
+  int32_t *anomalies;
+  int start, end, lane;
+
+  // largest |x| of two bf16 or one fp32, as bits that order like the values
+  static __device__ __forceinline__ uint32_t mag(uint32_t w) {
+    return DT == 1 ? w & 0x7fff7fffu : w & 0x7fffffffu;
+  }
+  static __device__ __forceinline__ uint32_t top(uint32_t a, uint32_t b) {
+    return DT == 1 ? __vmaxu2(a, b) : max(a, b);
+  }
+
+  static __device__ __forceinline__ float amax_of(const uint4 (&w)[NL]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      m = top(m, top(top(mag(w[i].x), mag(w[i].y)), top(mag(w[i].z), mag(w[i].w))));
+    if (DT == 1) m = max(m << 16, m & 0xffff0000u);
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, m));
+  }
+
+  // NaN to 0, infinities to the largest finite value
+  static __device__ __forceinline__ uint32_t finite(uint32_t w) {
+    if (DT == 1) {
+      uint32_t lo = w & 0xffffu, hi = w >> 16;
+      if ((lo & 0x7fffu) >= 0x7f80u) lo = (lo & 0x7fffu) > 0x7f80u ? 0u : (lo & 0x8000u) | 0x7f7fu;
+      if ((hi & 0x7fffu) >= 0x7f80u) hi = (hi & 0x7fffu) > 0x7f80u ? 0u : (hi & 0x8000u) | 0x7f7fu;
+      return lo | (hi << 16);
+    }
+    if ((w & 0x7fffffffu) < 0x7f800000u) return w;
+    return (w & 0x7fffffffu) > 0x7f800000u ? 0u : (w & 0x80000000u) | 0x7f7fffffu;
+  }
+
+  static __device__ __forceinline__ void values4(const uint4 &w, int h, float f, float (&x)[4]) {
+    if (DT == 1) {
+      const uint32_t a = h ? w.z : w.x, b = h ? w.w : w.y;
+      x[0] = __uint_as_float(a << 16) * f; x[1] = __uint_as_float(a & 0xffff0000u) * f;
+      x[2] = __uint_as_float(b << 16) * f; x[3] = __uint_as_float(b & 0xffff0000u) * f;
+    } else {
+      x[0] = __uint_as_float(w.x) * f; x[1] = __uint_as_float(w.y) * f;
+      x[2] = __uint_as_float(w.z) * f; x[3] = __uint_as_float(w.w) * f;
+    }
+  }
+
+  __device__ __forceinline__ void put(const uint4 (&w)[NL], int64_t block, float inv, float amax, float f) const {
+    const int64_t at = (block * kBlock + lane / LPR) * kHeadDim + (lane % LPR) * E;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      float x[4];
+      values4(w[i], 0, f, x);
+      const uint32_t c0 = codes4<CODE>(x, inv, amax);
+      if constexpr (DT == 1) {
+        values4(w[i], 1, f, x);
+        *(uint2 *)(codes + at + (int64_t)i * RPL * kHeadDim) = make_uint2(c0, codes4<CODE>(x, inv, amax));
+      } else {
+        *(uint32_t *)(codes + at + (int64_t)i * RPL * kHeadDim) = c0;
+      }
+    }
+  }
+
+  __device__ __forceinline__ void block(int j) const {
+    uint4 w[NL];
+    const int p0 = j * kBlock, sub = lane / LPR, chunk = lane % LPR;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int r = i * RPL + sub, pos = p0 + r;
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (pos < start) w[i] = tail[r * LPR + chunk];
+      else if (pos < end) w[i] = __ldcs(src + (int64_t)(pos - start) * LPR + chunk);
+    }
+    float amax = amax_of(w);
+    if (!(amax <= 0x1.fffffep127f)) {  // an infinity or a NaN
+#pragma unroll
+      for (int i = 0; i < NL; ++i)
+        w[i] = make_uint4(finite(w[i].x), finite(w[i].y), finite(w[i].z), finite(w[i].w));
+      amax = amax_of(w);
+      if (lane == 0) atomicOr(anomalies, kAnomNotFinite);
+    }
+    constexpr float kTop = CODE == LKV_CODE_INT8 ? 127.f : 448.f;
+    if (p0 + kBlock <= end) {
+      if (amax >= 0x1p-100f) {
+        put(w, j, __fdiv_rn(kTop, amax), amax, 1.f);
+      } else if (amax > 0.f) {
+        // tiny blocks: scaled by 2^126 (exactly), or kTop / amax would overflow
+        const float up = amax * 0x1p126f;
+        put(w, j, __fdiv_rn(kTop, up), up, 0x1p126f);
+      } else {
+        uint4 *to = (uint4 *)(codes + (int64_t)j * kBlock * kHeadDim);
+#pragma unroll
+        for (int i = 0; i < kBlock * kHeadDim / 512; ++i) to[i * 32 + lane] = make_uint4(0, 0, 0, 0);
+      }
+      if (lane == 0) scale[j] = __fdiv_rn(amax, kTop);
+    }
+    __syncwarp();  // every lane has read the tail
+    if (p0 + kBlock >= end) {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int r = i * RPL + sub, pos = p0 + r;
+        if (pos >= start && pos < end) tail[r * LPR + chunk] = w[i];
+      }
+    }
+  }
+};
+
+struct WriteArgs {
+  lkv_cache8 c;
+  const void *k, *v;
+  const int32_t *start, *counts;
+  int32_t n;
+  int32_t per;        // blocks that a warp takes
+  int32_t chunks;     // warps of a (sequence, KV head) and tensor
+  int64_t tasks;
+};
+
+// A warp takes a run of blocks of one (sequence, KV head) of K or V: a block
+// is 16 rows in registers (4 KB of bf16), its largest magnitude one warp
+// reduction, its codes one store. Reading, writing and the arithmetic of
+// different warps overlap; nothing passes through shared memory.
+//
+// The tail is read by the first block and written by the last one, so where
+// the first block starts in the tail, its warp takes the last block too.
+// The last warp of a sequence to finish sets the length (every warp has
+// read it by then).
+//
+// Bound: bytes (2 or 4 in, 1 out a value).
+template <int DT, int CODE>
+__global__ void __launch_bounds__(kCacheThreads) k_cache8_write(const __grid_constant__ WriteArgs a) {
+  const int64_t task = (int64_t)blockIdx.x * kCacheWarps + threadIdx.x / 32;
+  if (task >= a.tasks) return;
+  const lkv_cache8 &c = a.c;
+  const int ch = (int)(task % a.chunks);
+  const int64_t rest = task / a.chunks;
+  const int kv = (int)(rest & 1);
+  const int64_t slice = rest >> 1;
+  const int b = (int)(slice / c.n_kv_heads);
+  const int len = __ldcg(c.lengths + b);
+  const int start = a.start ? a.start[b] : len;
+  const int cnt = a.counts ? a.counts[b] : a.n;
+  int anomaly = 0;
+  if (len < 0 || len > c.capacity || cnt < 0 || cnt > a.n) anomaly = kAnomRange;
+  else if (cnt > 0) {
+    const bool fits = start >= 0 && start <= len && (start % kBlock == 0 || start / kBlock == (len - 1) / kBlock);
+    if (!fits) anomaly = kAnomRange;
+    else if (cnt > c.capacity - start) anomaly = kAnomCapacity;
+  }
+  const int end = anomaly ? 0 : start + cnt;
+  if (!anomaly && cnt > 0) {
+    BlockWriter<DT, CODE> w;
+    const int64_t es = DT == 1 ? 2 : 4;
+    w.src = (const uint4 *)((const char *)(kv ? a.v : a.k) + slice * a.n * kHeadDim * es);
+    w.tail = (uint4 *)((char *)(kv ? c.v_tail : c.k_tail) + slice * kBlock * kHeadDim * es);
+    w.codes = (uint8_t *)(kv ? c.v_codes : c.k_codes) + slice * c.capacity * kHeadDim;
+    w.scale = (kv ? c.v_scale : c.k_scale) + slice * (c.capacity / kBlock);
+    w.anomalies = c.ticket + c.batch;
+    w.start = start;
+    w.end = end;
+    w.lane = threadIdx.x & 31;
+    const int first = start / kBlock, last = (end - 1) / kBlock;
+    const bool both = start % kBlock != 0 && last != first;
+    const int j0 = first + ch * a.per, j1 = min(j0 + a.per, last + 1);
+    for (int j = j0; j < j1; ++j)
+      if (!(both && j == last)) w.block(j);
+    if (both && ch == 0) w.block(last);
+  }
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    __threadfence();
+    const int all = 2 * c.n_kv_heads * a.chunks;
+    if (atomicAdd(c.ticket + b, 1) == all - 1) {
+      c.ticket[b] = 0;
+      if (anomaly) atomicOr(c.ticket + c.batch, anomaly);
+      else if (cnt > 0) c.lengths[b] = end;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- read
+
+struct ReadArgs {
+  lkv_cache8 c;
+  const int32_t *first;
+  void *k_out, *v_out;
+  int32_t n;
+  int32_t groups;     // warps of a (sequence, KV head) and tensor: 16 rows each
+  int64_t tasks;
+};
+
+template <int CODE>
+__device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
+  if constexpr (CODE == LKV_CODE_INT8) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = (float)(int8_t)(w >> (8 * e));
+  } else {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+    const float2 a = __half22float2(*(__half2 *)&lo), b = __half22float2(*(__half2 *)&hi);
+    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+  }
+}
+
+// A warp takes 16 rows, all its loads first: codes (8 or 4 bytes a lane) and
+// the rows' scales, then one rounded product a value. Bound: bytes (1 in, 2
+// or 4 out a value).
+template <int DT, int CODE>
+__global__ void __launch_bounds__(kCacheThreads) k_cache8_read(const __grid_constant__ ReadArgs a) {
+  constexpr int E = DT == 1 ? 8 : 4, LPR = kHeadDim / E, RPL = 32 / LPR, NL = kBlock / RPL;
+  const int64_t task = (int64_t)blockIdx.x * kCacheWarps + threadIdx.x / 32;
+  if (task >= a.tasks) return;
+  const lkv_cache8 &c = a.c;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, chunk = lane % LPR;
+  const int r0 = (int)(task % a.groups) * kBlock;
+  const int64_t rest = task / a.groups;
+  const int kv = (int)(rest & 1);
+  const int64_t slice = rest >> 1;
+  const int b = (int)(slice / c.n_kv_heads);
+  const int len = min(max(c.lengths[b], 0), c.capacity), full = len / kBlock * kBlock;
+  const int64_t p0 = (int64_t)(a.first ? a.first[b] : 0) + r0;
+  const uint8_t *codes = (const uint8_t *)(kv ? c.v_codes : c.k_codes) + slice * c.capacity * kHeadDim;
+  const float *scale = (kv ? c.v_scale : c.k_scale) + slice * (c.capacity / kBlock);
+  const uint4 *tail = (const uint4 *)((const char *)(kv ? c.v_tail : c.k_tail) + slice * kBlock * kHeadDim * (DT == 1 ? 2 : 4));
+  uint4 *out = (uint4 *)((char *)(kv ? a.v_out : a.k_out) + slice * a.n * kHeadDim * (DT == 1 ? 2 : 4));
+  uint2 w[NL];
+  float s[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int64_t pos = p0 + i * RPL + sub;
+    w[i] = make_uint2(0, 0);
+    s[i] = 0.f;
+    if (pos >= 0 && pos < full && r0 + i * RPL + sub < a.n) {
+      const uint8_t *p = codes + pos * kHeadDim + chunk * E;
+      if constexpr (DT == 1) w[i] = __ldcs((const uint2 *)p);
+      else w[i].x = __ldcs((const uint32_t *)p);
+      s[i] = scale[pos / kBlock];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int r = r0 + i * RPL + sub;
+    const int64_t pos = p0 + i * RPL + sub;
+    if (r >= a.n) continue;
+    uint4 o;
+    if (pos >= full && pos < len) {
+      o = tail[(int)(pos % kBlock) * LPR + chunk];
+    } else {
+      float x[4], y[4];
+      decode4<CODE>(w[i].x, x);
+      if constexpr (DT == 1) {
+        decode4<CODE>(w[i].y, y);
+        o = make_uint4(pack_bf16(x[0] * s[i], x[1] * s[i]), pack_bf16(x[2] * s[i], x[3] * s[i]),
+                       pack_bf16(y[0] * s[i], y[1] * s[i]), pack_bf16(y[2] * s[i], y[3] * s[i]));
+      } else {
+        o = make_uint4(__float_as_uint(x[0] * s[i]), __float_as_uint(x[1] * s[i]), __float_as_uint(x[2] * s[i]),
+                       __float_as_uint(x[3] * s[i]));
+      }
+    }
+    __stcs(out + (int64_t)r * LPR + chunk, o);
+  }
+}
+
+}  // namespace lkv
+
+extern "C" lkv_status lkv_cache8_write(const lkv_cache8 *c, const void *k, const void *v, int32_t n,
+                                       const int32_t *start, const int32_t *counts, void *stream) {
+  using namespace lkv;
+  if (const char *m = check_cache8(c)) {
+    char buf[160];
+    std::snprintf(buf, sizeof buf, "lkv_cache8_write: %s", m);
+    return refuse(buf);
+  }
+  if (n < 0) return refuse("lkv_cache8_write: n must be >= 0");
+  if (n == 0) return LKV_OK;
+  if (!k || !v) return refuse("lkv_cache8_write: null keys or values");
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4) || !aligned(counts, 4))
+    return refuse("lkv_cache8_write: keys and values must be 16-byte aligned, start and counts 4-byte aligned");
+  const int64_t slices = (int64_t)c->batch * c->n_kv_heads;
+  const int64_t bytes = slices * n * kHeadDim * (c->dtype == LKV_DTYPE_BF16 ? 2 : 4), ib = (int64_t)c->batch * 4;
+  if (overlaps_cache8(c, k, bytes) || overlaps_cache8(c, v, bytes) || overlaps_cache8(c, start, ib) ||
+      overlaps_cache8(c, counts, ib))
+    return refuse("lkv_cache8_write: an input overlaps the cache's arrays");
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_refuse("lkv_cache8_write", e);
+  WriteArgs a{};
+  a.c = *c;
+  a.k = k; a.v = v; a.start = start; a.counts = counts;
+  a.n = n;
+  // n rows from any start touch at most this many blocks
+  const int64_t touch = ((int64_t)n + 2 * kBlock - 2) / kBlock;
+  // runs of blocks, so that fewer warps meet at a sequence's ticket, but
+  // only as long as the GPU stays full (32 warps an SM)
+  const int64_t per = 2 * slices * touch / ((int64_t)sms * 32 * 4);
+  a.per = (int32_t)(per < 1 ? 1 : per > 8 ? 8 : per);
+  a.chunks = (int32_t)((touch + a.per - 1) / a.per);
+  if (2 * (int64_t)c->n_kv_heads * a.chunks > 0x7fffffff) return refuse("lkv_cache8_write: too many rows");
+  a.tasks = 2 * slices * a.chunks;
+  const int64_t blocks = (a.tasks + kCacheWarps - 1) / kCacheWarps;
+  if (blocks > 0x7fffffff) return refuse("lkv_cache8_write: too many rows");
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool bf = c->dtype == LKV_DTYPE_BF16, i8 = c->code == LKV_CODE_INT8;
+  if (bf && i8) k_cache8_write<1, LKV_CODE_INT8><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
+  else if (bf) k_cache8_write<1, LKV_CODE_E4M3><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
+  else if (i8) k_cache8_write<0, LKV_CODE_INT8><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
+  else k_cache8_write<0, LKV_CODE_E4M3><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_write", e);
+}
+
+extern "C" lkv_status lkv_cache8_read(const lkv_cache8 *c, const int32_t *first, int32_t n, void *k_out, void *v_out,
+                                      void *stream) {
+  using namespace lkv;
+  if (const char *m = check_cache8(c)) {
+    char buf[160];
+    std::snprintf(buf, sizeof buf, "lkv_cache8_read: %s", m);
+    return refuse(buf);
+  }
+  if (n < 0) return refuse("lkv_cache8_read: n must be >= 0");
+  if (n == 0) return LKV_OK;
+  if (!k_out || !v_out) return refuse("lkv_cache8_read: null output");
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(first, 4))
+    return refuse("lkv_cache8_read: outputs must be 16-byte aligned, first 4-byte aligned");
+  const int64_t slices = (int64_t)c->batch * c->n_kv_heads;
+  const int64_t bytes = slices * n * kHeadDim * (c->dtype == LKV_DTYPE_BF16 ? 2 : 4), ib = (int64_t)c->batch * 4;
+  if (overlaps_cache8(c, k_out, bytes) || overlaps_cache8(c, v_out, bytes) || overlap(k_out, bytes, v_out, bytes) ||
+      overlap(first, ib, k_out, bytes) || overlap(first, ib, v_out, bytes))
+    return refuse("lkv_cache8_read: an output overlaps the cache's arrays or another tensor");
+  ReadArgs a{};
+  a.c = *c;
+  a.first = first;
+  a.k_out = k_out; a.v_out = v_out;
+  a.n = n;
+  a.groups = (int32_t)(((int64_t)n + kBlock - 1) / kBlock);
+  a.tasks = 2 * slices * a.groups;
+  const int64_t blocks = (a.tasks + kCacheWarps - 1) / kCacheWarps;
+  if (blocks > 0x7fffffff) return refuse("lkv_cache8_read: too many rows");
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool bf = c->dtype == LKV_DTYPE_BF16, i8 = c->code == LKV_CODE_INT8;
+  if (bf && i8) k_cache8_read<1, LKV_CODE_INT8><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
+  else if (bf) k_cache8_read<1, LKV_CODE_E4M3><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
+  else if (i8) k_cache8_read<0, LKV_CODE_INT8><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
+  else k_cache8_read<0, LKV_CODE_E4M3><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_read", e);
+}
+
+extern "C" lkv_status lkv_cache8_status(const lkv_cache8 *c, void *stream) {
+  using namespace lkv;
+  if (const char *m = check_cache8(c)) {
+    char buf[160];
+    std::snprintf(buf, sizeof buf, "lkv_cache8_status: %s", m);
+    return refuse(buf);
+  }
+  cudaStream_t st = (cudaStream_t)stream;
+  int32_t bits = 0, *at = c->ticket + c->batch;
+  cudaError_t e = cudaMemcpyAsync(&bits, at, sizeof bits, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && bits) e = cudaMemsetAsync(at, 0, sizeof bits, st);
+  if (e == cudaSuccess && bits) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return cuda_refuse("lkv_cache8_status", e);
+  if (bits & kAnomCapacity) {
+    set_unbound_error("lkv_cache8: a write went past the capacity; that sequence was left as it was");
+    return LKV_ECAPACITY;
+  }
+  if (bits & kAnomRange)
+    return refuse("lkv_cache8: a write's start or count was out of range; that sequence was left as it was");
+  if (bits & kAnomNotFinite) return refuse("lkv_cache8: a NaN or an infinity was written");
+  return LKV_OK;
+}

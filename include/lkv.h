@@ -442,6 +442,172 @@ lkv_status lkv_read_ceiling(const void *dev_src, int64_t bytes, void *stream);
  * clears it; the context stays usable. Asynchronous. */
 lkv_status lkv_diag_wait_timeout(lkv_ctx *ctx, int64_t limit_ns);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions, and a key/value cache held in 8 bits with the attention
+ * that reads it. These calls have no context: they work on the caller's
+ * device memory, on the stream that each call names, allocate nothing, and
+ * can be captured into CUDA graphs. Together they are one serving step
+ * without retrieval: rotate q and k, write k and v, attend. That step is what
+ * the retrieval is measured against (attention over the full cache) and the
+ * sink and local regions of ParisKV [ParisKV, memory regions] with an 8-bit
+ * cache [CTkvr, quantisation table].
+ *   - Tensors are head-major and contiguous, as in lkv_build_index:
+ *     q [B][H][n][d], k and v [B][H_kv][n][d], H = H_kv * group, d = 128.
+ *   - Every tensor pointer is device memory on the current device, 16-byte
+ *     aligned (index arrays 4-byte aligned).
+ *   - Errors of the call itself are returned at once (text via
+ *     lkv_last_error(NULL)); what only the device can see (a sequence that
+ *     does not fit) is recorded in the cache and reported by
+ *     lkv_cache8_status.
+ */
+
+/* Rotary positions. Pair i < rotary_dim / 2 of a row turns by the angle
+ * position * f_i, f_i = base^(-2 i / rotary_dim):
+ *   (x1, x2) -> gain * (x1 cos - x2 sin, x2 cos + x1 sin).
+ * layout LKV_ROPE_HALF pairs (i, i + rotary_dim / 2),
+ * LKV_ROPE_INTERLEAVED (2 i, 2 i + 1); values from rotary_dim on are copied.
+ * scaling, for positions beyond those a model was made for:
+ *   LKV_ROPE_NONE    f_i (gain 1)
+ *   LKV_ROPE_LINEAR  f_i / factor (gain 1)
+ *   LKV_ROPE_NTK     base * factor^(rotary_dim / (rotary_dim - 2)) in place
+ *                    of base (gain 1; rotary_dim > 2)
+ *   LKV_ROPE_YARN    f_i (g + (1 - g) / factor), g = (r - beta_slow) /
+ *                    (beta_fast - beta_slow) clamped to 0..1, r = orig_len *
+ *                    f_i / (2 pi) the turns of pair i in orig_len positions;
+ *                    gain 0.1 ln(factor) + 1
+ * rotary_dim even, 2..128; base, factor >= 1 and finite; orig_len >= 1 and
+ * beta_fast > beta_slow >= 0 (LKV_ROPE_YARN). */
+enum { LKV_ROPE_HALF = 0, LKV_ROPE_INTERLEAVED = 1 };
+enum { LKV_ROPE_NONE = 0, LKV_ROPE_LINEAR = 1, LKV_ROPE_NTK = 2, LKV_ROPE_YARN = 3 };
+typedef struct lkv_rope_params {
+  int32_t rotary_dim;
+  int32_t layout;
+  int32_t scaling;
+  int32_t orig_len;
+  double base;
+  double factor;
+  double beta_fast;
+  double beta_slow;
+} lkv_rope_params;
+
+/* The table that lkv_rope_apply takes: turn[i] is f_i / (2 pi) in units of
+ * 2^-64 turns, so that a position times turn[i], modulo 2^64, is the angle's
+ * fraction of a turn however far the position is. */
+typedef struct lkv_rope {
+  int32_t rotary_dim;
+  int32_t layout;
+  float gain;
+  int32_t reserved;
+  uint64_t turn[64];
+} lkv_rope;
+
+/* Fill *rope (host only, no GPU). Errors: LKV_EINVAL. */
+lkv_status lkv_rope_init(const lkv_rope_params *params, lkv_rope *rope);
+
+/* Rotate q [B][H][n][d] into q_out and, unless n_kv_heads is 0, k
+ * [B][H_kv][n][d] into k_out, in one launch. positions: device int32 [B][n]
+ * (any sign), shared by the heads. dtype: of all four tensors; the arithmetic
+ * is fp32, rounded once. q_out may be q and k_out may be k (in place); any
+ * other overlap of an output with an input or output is LKV_EINVAL. batch, n
+ * and the head counts may be 0. *rope is read before the call returns.
+ * Asynchronous on stream. Errors: LKV_EINVAL, LKV_ECUDA. */
+lkv_status lkv_rope_apply(const lkv_rope *rope, int32_t dtype, int32_t batch, int32_t n_heads,
+                          int32_t n_kv_heads, int32_t n, const void *q, const void *k,
+                          const int32_t *positions, void *q_out, void *k_out, void *stream);
+
+/* A key/value cache held in 8 bits: the caller's device arrays. Blocks of
+ * LKV_CACHE8_BLOCK tokens of one (sequence, KV head) share a scale; token i
+ * is row i. A block is quantised when its last token is written:
+ *   LKV_CODE_INT8  scale = amax / 127, code = 127 x / amax rounded to the
+ *                  nearest integer (ties to even)
+ *   LKV_CODE_E4M3  scale = amax / 448, code = 448 x / amax rounded to the
+ *                  nearest e4m3 value (ties to even)
+ * amax the largest magnitude of the block's 16 x 128 values (amax 0: scale 0,
+ * codes 0). The rounding is that of the exact quotient. Tokens of a block
+ * that is not full yet are read from the tail, which holds the last block in
+ * full precision, so what the cache holds does not depend on how its tokens
+ * were split over calls. Values have to be finite: a NaN is held as 0 and an
+ * infinity as the largest finite value of dtype, and lkv_cache8_status then
+ * reports LKV_EINVAL. Calls that write a cache (lkv_cache8_write) may not
+ * overlap on the GPU with any other call on it; calls that only read it
+ * (lkv_cache8_read, lkv_cache8_attend) may overlap with one another. */
+#define LKV_CACHE8_BLOCK 16
+enum { LKV_CODE_INT8 = 0, LKV_CODE_E4M3 = 1 };
+typedef struct lkv_cache8 {
+  int32_t batch;
+  int32_t n_kv_heads;
+  int32_t capacity;   /* rows per (sequence, KV head): a multiple of 16 */
+  int32_t dtype;      /* lkv_dtype of the tails and of k, v, q and out */
+  int32_t code;       /* LKV_CODE_INT8 or LKV_CODE_E4M3 */
+  int32_t reserved;
+  void *k_codes;      /* 8-bit [B][H_kv][capacity][d] */
+  void *v_codes;
+  float *k_scale;     /* [B][H_kv][capacity / 16] */
+  float *v_scale;
+  void *k_tail;       /* dtype [B][H_kv][16][d]: rows of the last block (the one that
+                         holds token length - 1), token i in row i % 16 */
+  void *v_tail;
+  int32_t *lengths;   /* [B]: tokens held */
+  int32_t *ticket;    /* [B + 1]: all zero before the first call, then the library's:
+                         arrivals of a running write, and the anomalies */
+} lkv_cache8;
+
+/* Append k, v [B][H_kv][n][d] (dtype of the cache): sequence b takes its
+ * first counts[b] rows (counts NULL: all n) at positions start[b],
+ * start[b] + 1, ... and lengths[b] becomes start[b] + counts[b]. start and
+ * counts are device int32 [B], not part of the cache's own arrays; start
+ * NULL: at lengths[b]. A start below the length takes tokens back (drafts
+ * that were not accepted): it may be any position of the last block, or a
+ * multiple of 16. A sequence with counts[b] = 0 is left as it is. A sequence
+ * that asks for what does not fit (start above the length or inside an older
+ * block, a count outside 0..n, a row past the capacity) is left as it is
+ * too, and lkv_cache8_status reports LKV_ECAPACITY (past the capacity) or
+ * LKV_EINVAL. k and v may not overlap the cache's arrays. n may be 0.
+ * Asynchronous on stream. Errors: LKV_EINVAL, LKV_ECUDA. */
+lkv_status lkv_cache8_write(const lkv_cache8 *cache, const void *k, const void *v, int32_t n,
+                            const int32_t *start, const int32_t *counts, void *stream);
+
+/* Read rows first[b] .. first[b] + n - 1 of every (sequence, KV head) back
+ * into k_out, v_out [B][H_kv][n][d] (dtype of the cache): code * scale
+ * rounded once, the tail's rows as they are, and zeros for rows below 0 or at
+ * or past the length. first: device int32 [B] or NULL (from row 0). The
+ * layout is the one lkv_build_index takes. Asynchronous on stream. Errors:
+ * LKV_EINVAL, LKV_ECUDA. */
+lkv_status lkv_cache8_read(const lkv_cache8 *cache, const int32_t *first, int32_t n, void *k_out,
+                           void *v_out, void *stream);
+
+/* Causal attention of the last tokens of every sequence over the cache, which
+ * holds them already: q [B][H][n][d], H = H_kv * group (group 1..128), and
+ * out [B][H][n][d], both in the cache's dtype. Row i < counts[b] (counts:
+ * device int32 [B] or NULL for n everywhere; clamped to 0..n) is the token at
+ * position lengths[b] - counts[b] + i and sees the tokens j at or before its
+ * own position; with window > 0 only those with j > position - window or
+ * j < sinks (the first tokens stay visible). out = sum over them of
+ * softmax(scale * q . k_j) v_j; a row that sees nothing (a position below 0),
+ * and every row at or past counts[b], is zero. Scores, softmax and sums are
+ * fp32. n = 1 is a decode step; any n is taken. max_len: an upper bound of the
+ * lengths that the caller knows (0: the capacity); it steers how the work is
+ * split, and results stay right when a length is above it. workspace: device
+ * memory of at least lkv_cache8_attend_workspace bytes for the same sizes
+ * (NULL when that is 0), not shared by calls that may overlap.
+ * out may not overlap q or the cache. Asynchronous on stream. Errors:
+ * LKV_EINVAL (scale not finite too), LKV_ECUDA. */
+lkv_status lkv_cache8_attend(const lkv_cache8 *cache, const void *q, int32_t group, int32_t n,
+                             const int32_t *counts, float scale, int32_t window, int32_t sinks,
+                             int32_t max_len, void *out, void *workspace, int64_t workspace_bytes,
+                             void *stream);
+
+/* Bytes of workspace that lkv_cache8_attend needs for these sizes (often 0),
+ * into *bytes. Errors: LKV_EINVAL. */
+lkv_status lkv_cache8_attend_workspace(const lkv_cache8 *cache, int32_t group, int32_t n,
+                                       int32_t window, int32_t sinks, int32_t max_len,
+                                       int64_t *bytes);
+
+/* Blocking: waits for stream, then reports and clears what writes to this
+ * cache recorded: LKV_OK, LKV_ECAPACITY or LKV_EINVAL. May not be captured.
+ * Errors: also LKV_ECUDA. */
+lkv_status lkv_cache8_status(const lkv_cache8 *cache, void *stream);
+
 /* Wait for the context's stream; report device-side anomalies. */
 lkv_status lkv_sync(lkv_ctx *ctx);
 
