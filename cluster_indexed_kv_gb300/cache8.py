@@ -17,35 +17,34 @@ _CODES = {torch.int8: _lib.LKV_CODE_INT8, torch.float8_e4m3fn: _lib.LKV_CODE_E4M
 _FORMATS = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
 _D = 128
 _BLOCK = _lib.LKV_CACHE8_BLOCK
+_SCALE = _D ** -0.5
 
 
-def _tensor(t, name, shape, dtype, device) -> int:
-    """Data pointer of a contiguous CUDA tensor of this shape, type and device."""
+def _tensor(t, name, shape, dtype, index) -> int:
+    """Data pointer of a contiguous tensor of this shape and type on CUDA device `index`."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _optional(t, name, shape, dtype, device):
-    return None if t is None else _tensor(t, name, shape, dtype, device)
-
-
-def _call(device, fn, *args) -> None:
+def _call(index, fn, *args) -> None:
     """fn(*args, stream) on the device's current stream, with the device current."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        fn(*args, stream)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            fn(*args, stream)
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        _lib._check(status, None)
 
 
 class Rope:
@@ -62,6 +61,7 @@ class Rope:
         self.table = _lib.lkv_rope_init(rotary_dim, lay, how, orig_len, base, factor, beta_fast,
                                         beta_slow)
         self._at = C.addressof(self.table)
+        self._apply = _lib.load().lkv_rope_apply
 
     def apply(self, q: torch.Tensor, positions: torch.Tensor, k: torch.Tensor | None = None, *,
               q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
@@ -71,16 +71,20 @@ class Rope:
         default."""
         if not isinstance(q, torch.Tensor) or not q.is_cuda:
             raise ValueError("q must be a CUDA tensor")
-        if q.dtype not in _DTYPES:
+        dt, dev, q_shape = q.dtype, q.get_device(), q.shape
+        if dt not in _DTYPES:
             raise TypeError("q must be float32 or bfloat16")
-        if q.dim() != 4 or q.shape[3] != _D:
-            raise ValueError(f"q must have shape [B, H, n, {_D}], got {tuple(q.shape)}")
-        dev, dt = q.device, q.dtype
-        batch, heads, n, _ = q.shape
-        qp = _tensor(q, "q", q.shape, dt, dev)
+        if len(q_shape) != 4 or q_shape[3] != _D:
+            raise ValueError(f"q must have shape [B, H, n, {_D}], got {tuple(q_shape)}")
+        batch, heads, n, _ = q_shape
+        if not q.is_contiguous():
+            raise ValueError("q must be contiguous")
         pp = _tensor(positions, "positions", (batch, n), torch.int32, dev)
-        q_out = torch.empty_like(q) if q_out is None else q_out
-        qo = _tensor(q_out, "q_out", q.shape, dt, dev)
+        if q_out is None:
+            q_out = torch.empty_like(q)
+            qo = q_out.data_ptr()
+        else:
+            qo = _tensor(q_out, "q_out", q_shape, dt, dev)
         kp = ko = None
         kv_heads = 0
         if k is not None:
@@ -89,11 +93,14 @@ class Rope:
             kv_heads = k.shape[1]
             shape = (batch, kv_heads, n, _D)
             kp = _tensor(k, "k", shape, dt, dev)
-            k_out = torch.empty_like(k) if k_out is None else k_out
-            ko = _tensor(k_out, "k_out", shape, dt, dev)
+            if k_out is None:
+                k_out = torch.empty_like(k)
+                ko = k_out.data_ptr()
+            else:
+                ko = _tensor(k_out, "k_out", shape, dt, dev)
         elif k_out is not None:
             raise ValueError("k_out without k")
-        _call(dev, _lib.lkv_rope_apply, self._at, _DTYPES[dt], batch, heads, kv_heads, n, qp, kp, pp,
+        _call(dev, self._apply, self._at, _DTYPES[dt], batch, heads, kv_heads, n, q.data_ptr(), kp, pp,
               qo, ko)
         return q_out if k is None else (q_out, k_out)
 
@@ -140,11 +147,12 @@ class Cache8:
             raise TypeError("k_tail must be a float32 or bfloat16 tensor")
         self.batch, self.n_kv_heads, self.capacity, _ = k_codes.shape
         self.device, self.dtype = k_codes.device, k_tail.dtype
-        slices, dev = (self.batch, self.n_kv_heads), self.device
+        slices, dev = (self.batch, self.n_kv_heads), k_codes.get_device()
+        self._index = dev
         blocks, tails = (*slices, self.capacity // _BLOCK), (*slices, _BLOCK, _D)
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
         self.k_tail, self.v_tail, self.lengths = k_tail, v_tail, lengths
-        self._ticket = torch.zeros(self.batch + 1, dtype=torch.int32, device=dev)
+        self._ticket = torch.zeros(self.batch + 1, dtype=torch.int32, device=self.device)
         self._view = _lib.lkv_cache8(
             self.batch, self.n_kv_heads, self.capacity, _DTYPES[self.dtype], _CODES[k_codes.dtype], 0,
             _tensor(k_codes, "k_codes", k_codes.shape, k_codes.dtype, dev),
@@ -156,6 +164,10 @@ class Cache8:
             _tensor(lengths, "lengths", (self.batch,), torch.int32, dev),
             self._ticket.data_ptr())
         self._at = C.addressof(self._view)
+        self._ws_bytes = {}  # workspace of an attention, by its sizes
+        lib = _lib.load()
+        self._write, self._read = lib.lkv_cache8_write, lib.lkv_cache8_read
+        self._attend, self._status = lib.lkv_cache8_attend, lib.lkv_cache8_status
 
     def write(self, k: torch.Tensor, v: torch.Tensor, *, start: torch.Tensor | None = None,
               counts: torch.Tensor | None = None) -> None:
@@ -165,25 +177,27 @@ class Cache8:
         tokens of the last block, or down to a multiple of 16."""
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise ValueError(f"k must be a tensor of shape [B, H_kv, n, {_D}]")
-        dev, dt = self.device, self.dtype
-        shape = (self.batch, self.n_kv_heads, k.shape[2], _D)
+        dev, dt, batch = self._index, self.dtype, self.batch
+        shape = (batch, self.n_kv_heads, k.shape[2], _D)
         kp, vp = _tensor(k, "k", shape, dt, dev), _tensor(v, "v", shape, dt, dev)
-        sp = _optional(start, "start", (self.batch,), torch.int32, dev)
-        cp = _optional(counts, "counts", (self.batch,), torch.int32, dev)
-        _call(dev, _lib.lkv_cache8_write, self._at, kp, vp, shape[2], sp, cp)
+        sp = None if start is None else _tensor(start, "start", (batch,), torch.int32, dev)
+        cp = None if counts is None else _tensor(counts, "counts", (batch,), torch.int32, dev)
+        _call(dev, self._write, self._at, kp, vp, shape[2], sp, cp)
 
     def read(self, n: int, *, first: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
              v_out: torch.Tensor | None = None):
         """Rows first[b] .. first[b] + n - 1 (default: from 0) of every
         sequence as (k, v) [B, H_kv, n, 128] of the cache's dtype; zeros
         outside a sequence. The layout is the one Context.build_index takes."""
-        dev, dt = self.device, self.dtype
+        dev, dt = self._index, self.dtype
         shape = (self.batch, self.n_kv_heads, n, _D)
-        k_out = torch.empty(shape, dtype=dt, device=dev) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=dt, device=dev) if v_out is None else v_out
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dt, device=self.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=dt, device=self.device)
         kp, vp = _tensor(k_out, "k_out", shape, dt, dev), _tensor(v_out, "v_out", shape, dt, dev)
-        fp = _optional(first, "first", (self.batch,), torch.int32, dev)
-        _call(dev, _lib.lkv_cache8_read, self._at, fp, n, kp, vp)
+        fp = None if first is None else _tensor(first, "first", (self.batch,), torch.int32, dev)
+        _call(dev, self._read, self._at, fp, n, kp, vp)
         return k_out, v_out
 
     def attend(self, q: torch.Tensor, *, counts: torch.Tensor | None = None, scale: float | None = None,
@@ -198,21 +212,34 @@ class Cache8:
         known to the caller (0: none); it only steers the split of the work."""
         if not isinstance(q, torch.Tensor) or q.dim() != 4:
             raise ValueError(f"q must be a tensor of shape [B, H, n, {_D}]")
-        dev, dt = self.device, self.dtype
-        heads, n = q.shape[1], q.shape[2]
+        dev, dt = self._index, self.dtype
+        _, heads, n, _ = q.shape
         group = heads // self.n_kv_heads
         if group * self.n_kv_heads != heads or heads == 0:
             raise ValueError(f"q's {heads} heads are not a multiple of the cache's {self.n_kv_heads}")
         shape = (self.batch, heads, n, _D)
         qp = _tensor(q, "q", shape, dt, dev)
-        cp = _optional(counts, "counts", (self.batch,), torch.int32, dev)
-        out = torch.empty(shape, dtype=dt, device=dev) if out is None else out
-        op = _tensor(out, "out", shape, dt, dev)
-        _call(dev, _lib.lkv_cache8_attend, self._at, qp, group, n, cp,
-              _D ** -0.5 if scale is None else float(scale), window, sinks, max_len, op, None, 0)
+        cp = None if counts is None else _tensor(counts, "counts", (self.batch,), torch.int32, dev)
+        if out is None:
+            out = torch.empty_like(q)
+            op = out.data_ptr()
+        else:
+            op = _tensor(out, "out", shape, dt, dev)
+        sizes = (group, n, window, sinks, max_len)
+        ws_bytes = self._ws_bytes.get(sizes)
+        if ws_bytes is None:
+            with torch.cuda.device(dev):
+                ws_bytes = _lib.lkv_cache8_attend_workspace(self._at, *sizes)
+            if len(self._ws_bytes) > 1000:
+                self._ws_bytes.clear()
+            self._ws_bytes[sizes] = ws_bytes
+        # a new workspace for each call: calls on several streams do not share one
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device) if ws_bytes else None
+        _call(dev, self._attend, self._at, qp, group, n, cp, _SCALE if scale is None else scale, window,
+              sinks, max_len, op, ws.data_ptr() if ws_bytes else None, ws_bytes)
         return out
 
     def check(self) -> None:
         """Wait for the current stream; raise LKVError if a write since the
         last check did not fit or held a value that is not finite."""
-        _call(self.device, _lib.lkv_cache8_status, self._at)
+        _call(self._index, self._status, self._at)

@@ -2,12 +2,17 @@
 #include "cache8.cuh"
 
 #include <cuda_fp16.h>
+#include "tma.cuh"
 
 namespace lkv {
 
-constexpr int kAtThreads = 128;
-constexpr int kAtWarps = kAtThreads / 32;
-constexpr int kAtMaxCluster = 16;
+constexpr int kAtWarps = 6;
+constexpr int kAtThreads = 32 * kAtWarps;
+constexpr int kAtMaxCluster = 8;
+constexpr int kAtGroups = 512;      // (sequence, row tile) pairs that a streamed launch takes
+constexpr int kCodeBytes = kBlock * kHeadDim;      // one block of K or V
+constexpr int kTurnBytes = 2 * 2 * kCodeBytes;     // two blocks of both
+constexpr int kRingBytes = kAtWarps * 2 * kTurnBytes;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttendArgs {
@@ -17,17 +22,32 @@ struct AttendArgs {
   const int32_t *counts;
   int32_t n, group, window, sinks;
   int32_t row_tiles;
+  int32_t streamed;   // the CTAs share all tiles' blocks evenly (see k_attend8)
+  float *ws;          // streamed: 2 partials a CTA
   float scale_log2;   // scale * log2(e)
 };
 
 // c += a * b, fp16 operands, fp32 accumulators
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// c = a * b
+__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *(const uint32_t *)&h; }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // 2^e as a float, e clamped to the normal range
 __device__ __forceinline__ float pow2f(int e) {
@@ -75,45 +95,12 @@ __device__ __forceinline__ void codes_across(uint32_t wa, uint32_t wb, int h, ui
   }
 }
 
-// The attention of RT = 8 NT rows (a row is one query head of one token; the
-// rows of a KV head are ordered token-major) over a share of the visible
-// blocks of one (sequence, KV head).
-//
-// A warp takes one block of 16 tokens at a time. Scores are mma.sync
-// m16n8k16 products with the rows as M (fp16; rows 8..15 hold the remainders
-// of fp32 queries, or a second 8 rows) and 8 tokens as N; the contraction's
-// order over d is free, so a lane's K operands are 16-byte runs of a token's
-// row, straight from global memory. P V takes 16 values of d as M, the 16
-// tokens as K and 8 rows as N: the score accumulators are its B operand as
-// they stand, and a lane's V operands are again 16-byte runs of four tokens.
-// 8-bit codes are exact in fp16. The queries are scaled by a power of two
-// into fp16's range, scores get the block's K scale in fp32, and each block's
-// P V partial gets its V scale in fp32 when it is added.
-//
-// Softmax in base 2 with a reference per row that only moves when a score
-// passes it by 2^8: the weights lie below 2^(8 + kPShift) <= 2^15, fp16's
-// range, and small ones keep 2^-30 of the reference. For fp32 outputs the
-// weights carry an fp16 remainder too (one more product a block).
-//
-// The shares of a tile of rows are the CTAs of one cluster. Each CTA merges
-// its warps in shared memory, then every CTA of the cluster merges a part of
-// the outputs over distributed shared memory: one launch, no workspace, no
-// atomics, the same result each time.
 constexpr float kPShift = 6.f;
 constexpr float kSlack = 8.f;
+constexpr int kNoUnit = -1000;
+constexpr int kUnitSpan = 90;  // V scales below 2^-90 of the largest are taken for that
 
-template <int NT>
-struct AtSmem {
-  static constexpr int RT = 8 * NT;
-  static constexpr int RS = 20;               // floats between rows (bank spread)
-  static constexpr int IS = RT * RS + 8;      // floats between the 8 d-pair planes
-  float o[kAtWarps][8 * IS];
-  float part[RT][kHeadDim];                   // the CTA's merged partial
-  float m[kAtWarps][RT], l[kAtWarps][RT];
-  float f[kAtWarps][RT];
-  float pm[RT], pl[RT];
-};
-
+// A warp's part of a tile's attention (see k_attend8).
 template <int DT, int CODE, int NT>
 struct Warp {
   static constexpr int RT = 8 * NT;
@@ -122,46 +109,86 @@ struct Warp {
   uint32_t qa[QL][8][4];      // A fragments of the queries for the 8 steps over d
   float rc[NT];               // row g (+8): query scale * scale * log2(e)
   int pos[NT];                // its position, -1 for none
-  float mref[NT], l[NT];
+  float ref[NT], l[NT];
+  bool seen[NT];              // the row has a reference (rows that are not there have one from the start)
+  float limit;                // a y above it moves a reference
+  int unit;                   // V scales count in units of 2^unit
   float o[NT][8][4];
   int lane, g, t;
+  int tk, cg;                 // the lane's token of 8 and its V chunk of 8 (see step)
+  int koff, voff;
   int pmin, pmax, window, sinks;
+  int open0, open1;           // blocks [open0, open1) are visible to every row as a whole
 
-  // Scores of the block, masked, turned into weights; the reference moves if needed.
-  __device__ __forceinline__ void weights(float (&s)[2][4], float ks, int block, uint32_t (&ph)[NT][2], uint32_t (&pl)[NT][2]) {
-    const int p0 = block * kBlock;
-    float x[NT][4];
-    bool jump = false;
-    const bool all = p0 + kBlock - 1 <= pmin &&
-                     (window == 0 || p0 > pmax - window || p0 + kBlock <= sinks);
+  // V scales up to 2^(e + 1) are to come: o counts in units of 2^(ref + unit), l in units of 2^ref.
+  __device__ __forceinline__ void raise_unit(int e) {
+    if (e <= unit) return;
+    const float k = unit == kNoUnit ? 1.f : exp2f((float)(unit - e));
+    unit = e;
 #pragma unroll
-    for (int r = 0; r < NT; ++r) {
-      const float f = rc[r] * ks;
-      const bool rem = SPLIT && NT == 1;
+    for (int r = 0; r < NT; ++r)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = e >> 1, col = e & 1;
-        float v = s[j][2 * r + col];
-        if (rem) v += s[j][2 + col];
-        v *= f;
-        if (!all) {
-          const int tok = p0 + 8 * j + 2 * t + col;
-          if (!(tok <= pos[r] && (window == 0 || tok > pos[r] - window || tok < sinks))) v = -INFINITY;
-        }
-        x[r][e] = v;
-        jump |= v > mref[r] + kSlack;
-      }
-    }
-    if (__any_sync(0xffffffffu, jump)) {
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[r][i][c] *= k;
+  }
+
+  // Scores of NB blocks, masked, turned into weights; the reference moves if
+  // needed. ks: the blocks' K scales, lu: log2 of their V scales, iu: 1 / those.
+  template <int NB>
+  __device__ __forceinline__ void weights(float (&s)[NB][2][4], const float (&ks)[NB], const float (&lu)[NB], const float (&iu)[NB],
+                                          const int (&block)[NB], uint32_t (&ph)[NB][NT][2], uint32_t (&pl)[NB][NT][2]) {
+    float y[NB][NT][4];
+    float far = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
 #pragma unroll
       for (int r = 0; r < NT; ++r) {
-        float m = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+        const float f = rc[r] * ks[n], at = lu[n] - ref[r];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = e >> 1, col = e & 1;
+          float v = s[n][j][2 * r + col];
+          if (SPLIT && NT == 1) v += s[n][j][2 + col];
+          y[n][r][e] = __fmaf_rn(v, f, at);
+        }
+      }
+      if (block[n] < open0 || block[n] >= open1) {  // not every token is visible to every row
+#pragma unroll
+        for (int r = 0; r < NT; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tok = block[n] * kBlock + 8 * (e >> 1) + t + 4 * (e & 1);
+            if (!(tok <= pos[r] && (window == 0 || tok > pos[r] - window || tok < sinks))) y[n][r][e] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int r = 0; r < NT; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) far = fmaxf(far, y[n][r][e]);
+    }
+    if (__any_sync(0xffffffffu, far > limit)) {
+      limit = kPShift + kSlack;
+#pragma unroll
+      for (int r = 0; r < NT; ++r) {
+        // the reference is the exponent of weight 1: it goes kPShift below the
+        // row's largest y, anywhere the first time and only up from there
+        float m = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) m = fmaxf(fmaxf(m, fmaxf(y[n][r][0], y[n][r][1])), fmaxf(y[n][r][2], y[n][r][3]));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const float now = fmaxf(mref[r], m);
-        const float k = now == -INFINITY ? 1.f : exp2f(mref[r] - now);
-        mref[r] = now;
+        float by = m - kPShift;
+        if (seen[r] ? by < 0.f : m == -INFINITY) by = 0.f;
+        const float k = seen[r] ? exp2f(-by) : 1.f;
+        seen[r] |= m > -INFINITY;
+        if (!seen[r]) limit = -INFINITY;
+        ref[r] += by;
         l[r] *= k;
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[n][r][e] -= by;
         // accumulator columns are rows 2 t and 2 t + 1
         const float ka = __shfl_sync(0xffffffffu, k, 8 * t), kb = __shfl_sync(0xffffffffu, k, 8 * t + 4);
 #pragma unroll
@@ -171,69 +198,83 @@ struct Warp {
       }
     }
 #pragma unroll
-    for (int r = 0; r < NT; ++r) {
-      const float ref = mref[r] == -INFINITY ? 0.f : mref[r] - kPShift;
-      float p[4];
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        p[e] = exp2f(x[r][e] - ref);
-        l[r] += p[e];
+      for (int r = 0; r < NT; ++r) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = ex2(y[n][r][e]);
+        l[r] = __fmaf_rn((p[0] + p[1]) + (p[2] + p[3]), iu[n], l[r]);
+        if (SPLIT) {
+          split_h2(p[0], p[1], ph[n][r][0], pl[n][r][0]);
+          split_h2(p[2], p[3], ph[n][r][1], pl[n][r][1]);
+        } else {
+          ph[n][r][0] = h2_bits(__floats2half2_rn(p[0], p[1]));
+          ph[n][r][1] = h2_bits(__floats2half2_rn(p[2], p[3]));
+        }
       }
-      if (SPLIT) {
-        split_h2(p[0], p[1], ph[r][0], pl[r][0]);
-        split_h2(p[2], p[3], ph[r][1], pl[r][1]);
-      } else {
-        ph[r][0] = h2_bits(__floats2half2_rn(p[0], p[1]));
-        ph[r][1] = h2_bits(__floats2half2_rn(p[2], p[3]));
-      }
-    }
   }
 
-  // One quantised block: k[2][2] are the lane's K runs (tokens g and 8 + g,
-  // d 16 t.. and 64 + 16 t..), v[4] its V runs (tokens 2 t, 2 t + 1, 8 + 2 t,
-  // 9 + 2 t, d 16 g..).
-  __device__ __forceinline__ void step(const uint4 (&k)[2][2], const uint4 (&v)[4], float ks, float vs, int block) {
-    float s[2][4] = {};
+  // NB quantised blocks from the ring (K then V of each, as the copies lay
+  // them down: the 16-byte chunk j of row r at j ^ (r & 7)). The lane's K are
+  // tokens (g / 2) + 4 (g & 1) and that + 8, d 16 t.. and 64 + 16 t..; its V
+  // tokens t, t + 4, t + 8, t + 12, d 16 cg..: of every 8 lanes that a
+  // 16-byte load serves together, no two meet in a bank. NB blocks together
+  // give their chains of products and their softmax to one another to hide
+  // behind.
+  template <int NB>
+  __device__ __forceinline__ void step(const unsigned char *ring, const float (&ks)[NB], const float (&lu)[NB], const float (&iu)[NB],
+                                       const int (&block)[NB]) {
+    float s[NB][2][4];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int n = 0; n < NB; ++n) {
+        const uint4 k0 = *(const uint4 *)(ring + n * 2 * kCodeBytes + (koff ^ (64 * c)));
+        const uint4 k1 = *(const uint4 *)(ring + n * 2 * kCodeBytes + 1024 + (koff ^ (64 * c)));
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t w = e == 0 ? k[j][c].x : e == 1 ? k[j][c].y : e == 2 ? k[j][c].z : k[j][c].w;
-          uint32_t b0, b1;
-          codes_row<CODE>(w, b0, b1);
-          mma16816(s[j], qa[0][4 * c + e], b0, b1);
-          if (QL == 2) mma16816(s[j], qa[QL - 1][4 * c + e], b0, b1);
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 &k = j ? k1 : k0;
+            uint32_t b0, b1;
+            codes_row<CODE>(e == 0 ? k.x : e == 1 ? k.y : e == 2 ? k.z : k.w, b0, b1);
+            if (c == 0 && e == 0) mma16816_first(s[n][j], qa[0][0], b0, b1);
+            else mma16816(s[n][j], qa[0][4 * c + e], b0, b1);
+            if (QL == 2) mma16816(s[n][j], qa[QL - 1][4 * c + e], b0, b1);
+          }
         }
       }
     }
-    uint32_t ph[NT][2], pl[NT][2];
-    weights(s, ks, block, ph, pl);
+    uint32_t ph[NB][NT][2], pl[NB][NT][2];
+    weights<NB>(s, ks, lu, iu, block, ph, pl);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t w[4];
+    for (int n = 0; n < NB; ++n) {
+      uint4 v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = e == 0 ? v[j].x : e == 1 ? v[j].y : e == 2 ? v[j].z : v[j].w;
+      for (int j = 0; j < 4; ++j)
+        v[j] = *(const uint4 *)(ring + (2 * n + 1) * kCodeBytes + (j >> 1) * 1024 + (j & 1) * 512 + (voff ^ (64 * (j & 1))));
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t a[4];
-        codes_across<CODE>(w[0], w[1], h, a[0], a[1]);
-        codes_across<CODE>(w[2], w[3], h, a[2], a[3]);
-        accumulate(a, ph, pl, vs, 2 * e + h);
+      for (int e = 0; e < 4; ++e) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = e == 0 ? v[j].x : e == 1 ? v[j].y : e == 2 ? v[j].z : v[j].w;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a[4];
+          codes_across<CODE>(w[0], w[1], h, a[0], a[1]);
+          codes_across<CODE>(w[2], w[3], h, a[2], a[3]);
+          accumulate(a, ph[n], pl[n], 2 * e + h);
+        }
       }
     }
   }
 
-  __device__ __forceinline__ void accumulate(const uint32_t (&a)[4], const uint32_t (&ph)[NT][2], const uint32_t (&pl)[NT][2],
-                                             float vs, int i) {
+  __device__ __forceinline__ void accumulate(const uint32_t (&a)[4], const uint32_t (&ph)[NT][2], const uint32_t (&pl)[NT][2], int i) {
 #pragma unroll
     for (int r = 0; r < NT; ++r) {
-      float c[4] = {};
-      mma16816(c, a, ph[r][0], ph[r][1]);
-      if (SPLIT) mma16816(c, a, pl[r][0], pl[r][1]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[r][i][e] += vs * c[e];
+      mma16816(o[r][i], a, ph[r][0], ph[r][1]);
+      if (SPLIT) mma16816(o[r][i], a, pl[r][0], pl[r][1]);
     }
   }
 
@@ -262,37 +303,39 @@ struct Warp {
   // The last, partial block, from the tails in full precision: the same
   // products on fp16 values and (fp32 tails) their remainders.
   __device__ __noinline__ void tail_step(const void *kt, const void *vt, int rows, int block) {
-    const int ke = tail_exp(kt, rows), ve = tail_exp(vt, rows);
+    const int ke = tail_exp(kt, rows), ve = max(tail_exp(vt, rows), unit - kUnitSpan);
+    raise_unit(ve);
     const float kf = pow2f(-ke), vf = pow2f(-ve);
-    float s[2][4] = {};
+    float s[1][2][4] = {};
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float4 x = tail4(kt, 8 * j + g, 64 * c + 16 * t + 4 * e, rows);
+          const float4 x = tail4(kt, 8 * j + tk, 64 * c + 16 * t + 4 * e, rows);
           uint32_t h0, h1, l0, l1;
           split_h2(x.x * kf, x.y * kf, h0, l0);
           split_h2(x.z * kf, x.w * kf, h1, l1);
 #pragma unroll
           for (int z = 0; z < QL; ++z) {
-            mma16816(s[j], qa[z][4 * c + e], h0, h1);
-            if (SPLIT) mma16816(s[j], qa[z][4 * c + e], l0, l1);
+            mma16816(s[0][j], qa[z][4 * c + e], h0, h1);
+            if (SPLIT) mma16816(s[0][j], qa[z][4 * c + e], l0, l1);
           }
         }
       }
     }
-    uint32_t ph[NT][2], pl[NT][2];
-    weights(s, pow2f(ke), block, ph, pl);
-    const int tok[4] = {2 * t, 2 * t + 1, 8 + 2 * t, 9 + 2 * t};
-    const float back = pow2f(ve);
+    uint32_t ph[1][NT][2], pl[1][NT][2];
+    const float ks[1] = {pow2f(ke)}, lu[1] = {(float)(ve - unit)}, iu[1] = {pow2f(unit - ve)};
+    const int at[1] = {block};
+    weights<1>(s, ks, lu, iu, at, ph, pl);
+    const int tok[4] = {t, t + 4, t + 8, t + 12};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float4 x[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        x[j] = tail4(vt, tok[j], 16 * g + 4 * e, rows);
+        x[j] = tail4(vt, tok[j], 16 * cg + 4 * e, rows);
         x[j].x *= vf; x[j].y *= vf; x[j].z *= vf; x[j].w *= vf;
       }
 #pragma unroll
@@ -302,8 +345,8 @@ struct Warp {
         split_h2(h ? x[0].w : x[0].y, h ? x[1].w : x[1].y, a[1], b[1]);
         split_h2(h ? x[2].z : x[2].x, h ? x[3].z : x[3].x, a[2], b[2]);
         split_h2(h ? x[2].w : x[2].y, h ? x[3].w : x[3].y, a[3], b[3]);
-        accumulate(a, ph, pl, back, 2 * e + h);
-        if (SPLIT) accumulate(b, ph, pl, back, 2 * e + h);
+        accumulate(a, ph[0], pl[0], 2 * e + h);
+        if (SPLIT) accumulate(b, ph[0], pl[0], 2 * e + h);
       }
     }
   }
@@ -342,241 +385,581 @@ __device__ __forceinline__ float2 peer_f2(const void *p, uint32_t rank) {
 // 2^(m - top), 0 for a share that saw nothing
 __device__ __forceinline__ float share(float m, float top) { return m == -INFINITY ? 0.f : exp2f(m - top); }
 
+// The rows of a tile (one row tile of one sequence's KV head) and the blocks they see:
+// the first `sb` (sinks), then lo..hi.
+struct Tile {
+  int len, cnt, pmin, pmax, lo, hi, sb, nb;
+  __device__ __forceinline__ Tile() {}
+  __device__ __forceinline__ Tile(const AttendArgs &a, int b, int rt, int RT) {
+    len = min(max(a.c.lengths[b], 0), a.c.capacity);
+    cnt = a.counts ? min(max(a.counts[b], 0), a.n) : a.n;
+    const int R = a.n * a.group, r0 = rt * RT;
+    const int imin = r0 / a.group, imax = min((min(r0 + RT, R) - 1) / a.group, cnt - 1);
+    pmin = len - cnt + imin;
+    pmax = imin <= imax ? len - cnt + imax : -1;
+    lo = a.window > 0 ? max(0, pmin - a.window + 1) / kBlock : 0;
+    hi = pmax >= 0 ? pmax / kBlock : -1;
+    sb = a.window > 0 && hi >= 0 ? min((min(a.sinks, len) + kBlock - 1) / kBlock, lo) : 0;
+    nb = hi >= 0 ? sb + hi - lo + 1 : 0;
+  }
+  __device__ __forceinline__ int block(int u) const { return u < sb ? u : u - sb + lo; }
+};
+
+// A streamed launch's work: the blocks of all tiles in a row, (sequence, row
+// tile) by (sequence, row tile) and KV head by KV head, CTA i of P taking
+// those from total * i / P on (P the CTAs, but no more than blocks).
+struct Stream {
+  int64_t at[kAtGroups + 1];  // blocks before each (sequence, row tile)
+  int nb[kAtGroups];          // blocks of one of its tiles
+  __device__ void fill(const AttendArgs &a, int RT) {
+    const int G = a.c.batch * a.row_tiles;
+    for (int i = threadIdx.x; i < G; i += blockDim.x) nb[i] = Tile(a, i % a.c.batch, i / a.c.batch, RT).nb;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      int64_t sum = 0;
+      for (int i0 = 0; i0 < G; i0 += 32) {
+        const int i = i0 + threadIdx.x;
+        int64_t x = i < G ? (int64_t)nb[i] * a.c.n_kv_heads : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+          if ((int)threadIdx.x >= d) x += y;
+        }
+        if (i < G) at[i + 1] = sum + x;
+        sum += __shfl_sync(0xffffffffu, x, 31);
+      }
+      if (threadIdx.x == 0) at[0] = 0;
+    }
+    __syncthreads();
+  }
+  // the (sequence, row tile) that block x of the row belongs to
+  __device__ __forceinline__ int group(int64_t x, int G) const {
+    int lo = 0, hi = G;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (at[mid] <= x) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+};
+
+template <int NT>
+struct AtSmem {
+  static constexpr int RT = 8 * NT;
+  static constexpr int RS = 20;               // floats between rows (bank spread)
+  static constexpr int IS = RT * RS + 8;      // floats between the 8 d-pair planes
+  static constexpr int kSlot = RT * kHeadDim + 3 * RT;  // floats of a partial in the workspace
+  float o[kAtWarps][8 * IS];
+  float part[RT][kHeadDim];                   // the CTA's merged partial
+  float m[kAtWarps][RT], t[kAtWarps][RT];     // exponents of the units of o and of l
+  float l[kAtWarps][RT], f[kAtWarps][RT];
+  float pm[RT], pt[RT], pl[RT];
+};
+
+// Values d, d + 1 of a row of the output: o / l * 2^e.
+template <int DT>
+__device__ __forceinline__ void put_out(const AttendArgs &a, int64_t slice, int cnt, int rr, int d, float2 o, float l, float e) {
+  const int i = rr / a.group;
+  if (rr >= a.n * a.group) return;
+  if (i >= cnt || l == 0.f) {
+    o = make_float2(0.f, 0.f);
+  } else {
+    const float unit = exp2f(e);
+    o.x = o.x / l * unit;
+    o.y = o.y / l * unit;
+  }
+  const int64_t at = ((slice * a.group + rr % a.group) * a.n + i) * kHeadDim + d;
+  if (DT == 1) *(uint32_t *)((uint16_t *)a.out + at) = pack_bf16(o.x, o.y);
+  else *(float2 *)((float *)a.out + at) = o;
+}
+
+// The attention of RT = 8 NT rows (a row is one query head of one token; the
+// rows of a KV head are ordered token-major) over the visible blocks of one
+// (sequence, KV head): a tile.
+//
+// A warp takes two blocks of 16 tokens a turn, which one of its lanes has
+// copied into its own ring by TMA a turn ahead. Scores are mma.sync m16n8k16
+// products with the rows as M (fp16; rows 8..15 hold the remainders of fp32
+// queries, or a second 8 rows) and 8 tokens as N; the contraction's order
+// over d is free, so a lane's K operands are 16-byte runs of a token's row.
+// P V takes 16 values of d as M, the 16 tokens as K and 8 rows as N: the
+// score accumulators are its B operand as they stand, and a lane's V operands
+// are again 16-byte runs of four tokens. 8-bit codes are exact in fp16. The
+// queries are scaled by a power of two into fp16's range, and scores get the
+// block's K scale in fp32.
+//
+// Softmax in base 2. The weights carry the block's V scale u as well: with
+// y = score + log2(u), w = 2^(y - reference), out = sum w code / sum w / u, so
+// P V accumulates in the tensor cores' registers as it is. Scales count in
+// units of the largest one that the warp has met (u <= 2), whatever the
+// values' magnitude. The reference of a row only moves when a y passes it by
+// 2^8: the weights lie below 2^(8 + kPShift), fp16's range, and small ones
+// keep 2^-30 of the reference. For fp32 outputs the weights carry an fp16
+// remainder too (one more product a block).
+//
+// Small calls: a tile's blocks are shared by the CTAs of one cluster. Each CTA
+// merges its warps in shared memory, then every CTA of the cluster merges a
+// part of the outputs over distributed shared memory: one launch, no
+// workspace. Streamed: the blocks of all tiles in a row are shared evenly by
+// as many CTAs as the GPU holds, whatever the sequences' lengths; a tile that
+// several CTAs share goes to the workspace in parts, and k_attend8_merge joins
+// them. No atomics in either: the same result each time.
 template <int DT, int CODE, int NT>
-__global__ void __launch_bounds__(kAtThreads) k_attend8(const __grid_constant__ AttendArgs a) {
-  extern __shared__ __align__(16) unsigned char raw[];
-  AtSmem<NT> &sm = *(AtSmem<NT> *)raw;
+__global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
+    k_attend8(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t full_bar[kAtWarps][2];
+  __shared__ Stream stream;
   constexpr int RT = 8 * NT;
   using W = Warp<DT, CODE, NT>;
+  using Sm = AtSmem<NT>;
   const lkv_cache8 &c = a.c;
-  const int parts = (int)cluster_size(), part = (int)cluster_rank();
+  unsigned char *const area = raw + ((1024u - (smem_at(raw) & 1023u)) & 1023u);
+  Sm &sm = *(Sm *)area;
   const int wid = threadIdx.x >> 5;
-  const int64_t tile = blockIdx.x / parts;
-  const int64_t S = (int64_t)c.batch * c.n_kv_heads;
-  const int64_t slice = tile % S;
-  const int rt = a.row_tiles - 1 - (int)(tile / S);  // the rows with most to see come first
-  const int b = (int)(slice / c.n_kv_heads), h = (int)(slice % c.n_kv_heads);
-  const int len = min(max(c.lengths[b], 0), c.capacity);
-  const int cnt = a.counts ? min(max(a.counts[b], 0), a.n) : a.n;
-  const int R = a.n * a.group, r0 = rt * RT;
+  unsigned char *const ring = area + wid * 2 * kTurnBytes;
+  uint64_t *const bar = full_bar[wid];
+  const int parts = a.streamed ? 1 : (int)cluster_size(), part = a.streamed ? 0 : (int)cluster_rank();
+  const int G = c.batch * a.row_tiles;
 
   W w;
   w.lane = threadIdx.x & 31;
   w.g = w.lane >> 2;
   w.t = w.lane & 3;
+  w.tk = (w.g >> 1) | ((w.g & 1) << 2);
+  w.cg = w.tk;
+  w.koff = w.tk * kHeadDim + ((w.t ^ w.tk) << 4);
+  w.voff = w.t * kHeadDim + ((w.t ^ w.cg) << 4);
   w.window = a.window;
   w.sinks = a.sinks;
-  const int imin = r0 / a.group, imax = min((min(r0 + RT, R) - 1) / a.group, cnt - 1);
-  w.pmin = len - cnt + imin;
-  w.pmax = imin <= imax ? len - cnt + imax : -1;
-
-  // the visible blocks: the first `sb` (sinks), then lo..hi
-  const int lo = a.window > 0 ? max(0, w.pmin - a.window + 1) / kBlock : 0;
-  const int hi = w.pmax >= 0 ? w.pmax / kBlock : -1;
-  const int sb = a.window > 0 && hi >= 0 ? min((min(a.sinks, len) + kBlock - 1) / kBlock, lo) : 0;
-  const int nb = hi >= 0 ? sb + hi - lo + 1 : 0;
+  if (w.lane == 0) {
+    bar_init(&bar[0], 1);
+    bar_init(&bar[1], 1);
+    bar_init_fence();
+    if (wid == 0) {
+      tma_prefetch(&kmap);
+      tma_prefetch(&vmap);
+    }
+  }
+  __syncwarp();
+  uint32_t phase = 0;      // parities of the two barriers
+  bool dead = false;       // a copy did not arrive in time: the warp takes no more
   const int64_t es = DT == 1 ? 2 : 4;
 
-#pragma unroll
-  for (int r = 0; r < NT; ++r) {
-    w.mref[r] = -INFINITY;
-    w.l[r] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w.o[r][i][e] = 0.f;
+  int64_t x0 = 0, x1 = 1;  // streamed: the CTA's share of the row of blocks
+  if (a.streamed) {
+    stream.fill(a, RT);
+    const int64_t total = stream.at[G], P = min((int64_t)gridDim.x, total);
+    x0 = blockIdx.x < P ? total * blockIdx.x / P : 0;
+    x1 = blockIdx.x < P ? total * (blockIdx.x + 1) / P : 0;
   }
-  // queries: row g (and g + 8), the 32 values of d that go with the lane's K runs
-#pragma unroll
-  for (int r = 0; r < NT; ++r) {
-    const int row = r0 + 8 * r + w.g;
-    const int i = row / a.group;
-    const bool valid = row < R && i < cnt;
-    w.pos[r] = valid ? len - cnt + i : -1;
-    float x[32];
-    const char *p = (const char *)a.q +
-                    (((int64_t)(b * (int64_t)c.n_kv_heads + h) * a.group + (valid ? row % a.group : 0)) * a.n + (valid ? i : 0)) * kHeadDim * es;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const float4 v = valid ? w.tail4(p, 0, 64 * (u >> 2) + 16 * w.t + 4 * (u & 3), 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-      x[4 * u] = v.x; x[4 * u + 1] = v.y; x[4 * u + 2] = v.z; x[4 * u + 3] = v.w;
+  launch_dependents();
+  for (int64_t x = x0; x < x1;) {
+    Tile tile;
+    int64_t slice;
+    int rt, b0, b1;
+    if (a.streamed) {
+      const int gi = stream.group(x, G), nb = stream.nb[gi];
+      const int64_t off = x - stream.at[gi];
+      const int h = (int)(off / nb), b = gi % c.batch;
+      rt = gi / c.batch;
+      slice = (int64_t)b * c.n_kv_heads + h;
+      tile = Tile(a, b, rt, RT);
+      b0 = (int)(off % nb);
+      b1 = (int)min((int64_t)nb, b0 + (x1 - x));
+      x += b1 - b0;
+    } else {
+      const int64_t id = blockIdx.x / parts, S = (int64_t)c.batch * c.n_kv_heads;
+      slice = id % S;
+      rt = a.row_tiles - 1 - (int)(id / S);  // the rows with most to see come first
+      tile = Tile(a, (int)(slice / c.n_kv_heads), rt, RT);
+      b0 = (int)((int64_t)tile.nb * part / parts);
+      b1 = (int)((int64_t)tile.nb * (part + 1) / parts);
+      x = x1;
     }
-    float m = 0.f;
-#pragma unroll
-    for (int u = 0; u < 32; ++u) m = fmaxf(m, fabsf(x[u]));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const int e = min(max((int)(__float_as_uint(m) >> 23) - 126, -100), 126);
-    const float f = pow2f(-e);
-    w.rc[r] = pow2f(e) * a.scale_log2;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      uint32_t h0, h1, l0, l1;
-      split_h2(x[4 * u] * f, x[4 * u + 1] * f, h0, l0);
-      split_h2(x[4 * u + 2] * f, x[4 * u + 3] * f, h1, l1);
-      w.qa[0][u][r] = h0;
-      w.qa[0][u][2 + r] = h1;
-      if (W::SPLIT && NT == 1) { w.qa[0][u][1] = l0; w.qa[0][u][3] = l1; }
-      if (!W::SPLIT && NT == 1) { w.qa[0][u][1] = 0; w.qa[0][u][3] = 0; }
-      if (W::QL == 2) { w.qa[W::QL - 1][u][r] = l0; w.qa[W::QL - 1][u][2 + r] = l1; }
-    }
-  }
+    const int r0 = rt * RT, full = tile.len / kBlock;  // blocks before `full` are quantised
+    const bool tail = tile.nb > 0 && tile.hi >= full && b1 == tile.nb && b1 > b0;  // the share ends in the partial one
+    const int b2 = dead ? b0 : tail ? b1 - 1 : b1;
 
-  const uint8_t *kc = (const uint8_t *)c.k_codes + slice * c.capacity * kHeadDim;
-  const uint8_t *vc = (const uint8_t *)c.v_codes + slice * c.capacity * kHeadDim;
-  const float *ksc = c.k_scale + slice * (c.capacity / kBlock), *vsc = c.v_scale + slice * (c.capacity / kBlock);
-  const int full = len / kBlock;   // blocks before it are quantised
-  const int b0 = (int)((int64_t)nb * part / parts), b1 = (int)((int64_t)nb * (part + 1) / parts);
-  const bool tail = nb > 0 && hi >= full && b1 == nb && b1 > b0;  // the share's last block is the partial one
-  const int b2 = tail ? b1 - 1 : b1;
-  auto block_of = [&](int u) { return u < sb ? u : u - sb + lo; };
+    // the warp's turn i: units u = b0 + 2 (i kAtWarps + wid) and u + 1
+    auto issue = [&](int i) {
+      const int u = b0 + 2 * (i * kAtWarps + wid);
+      if (u < b2 && w.lane == 0) {
+        unsigned char *to = ring + (i & 1) * kTurnBytes;
+        uint64_t *on = &bar[i & 1];
+        const bool two = u + 1 < b2;
+        bar_expect(on, two ? kTurnBytes : kTurnBytes / 2);
+        const int k0 = tile.block(u) * kBlock;
+        tma_3d(to, &kmap, 0, k0, (int)slice, on);
+        tma_3d(to + kCodeBytes, &vmap, 0, k0, (int)slice, on);
+        if (two) {
+          const int k1 = tile.block(u + 1) * kBlock;
+          tma_3d(to + 2 * kCodeBytes, &kmap, 0, k1, (int)slice, on);
+          tma_3d(to + 3 * kCodeBytes, &vmap, 0, k1, (int)slice, on);
+        }
+      }
+    };
+    issue(0);
+    issue(1);
 
-  struct Frag { uint4 k[2][2], v[4]; };
-  auto load = [&](Frag &f, int u) {
-    const int64_t at = (int64_t)block_of(u) * kBlock * kHeadDim;
+    const float *ksc = c.k_scale + slice * (c.capacity / kBlock), *vsc = c.v_scale + slice * (c.capacity / kBlock);
+    w.pmin = tile.pmin;
+    w.pmax = tile.pmax;
+    w.open0 = a.window > 0 ? max(0, tile.pmax - a.window + kBlock) / kBlock : 0;
+    w.open1 = (tile.pmin + 1) / kBlock;
+    w.limit = -INFINITY;
+    w.unit = kNoUnit;
+    // queries: row g (and g + 8), the 32 values of d that go with the lane's K runs
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int r = 0; r < NT; ++r) {
+      w.ref[r] = 0.f;
+      w.l[r] = 0.f;
 #pragma unroll
-      for (int cc = 0; cc < 2; ++cc)
-        f.k[j][cc] = __ldg((const uint4 *)(kc + at + (8 * j + w.g) * kHeadDim + 64 * cc + 16 * w.t));
-    const int tok[4] = {2 * w.t, 2 * w.t + 1, 8 + 2 * w.t, 9 + 2 * w.t};
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f.v[j] = __ldg((const uint4 *)(vc + at + tok[j] * kHeadDim + 16 * w.g));
-  };
-  Frag x, y;
-  float ks = 0.f, vs = 0.f;
-  int u = b0 + wid, k = 0;
-  if (u < b2) load(x, u);
-  auto one = [&](Frag &cur, Frag &next) {
-    if ((k & 31) == 0) {  // the scales of the warp's next 32 blocks
-      const int mine = u + w.lane * kAtWarps;
-      if (mine < b2) {
-        ks = ksc[block_of(mine)];
-        vs = vsc[block_of(mine)];
+        for (int e = 0; e < 4; ++e) w.o[r][i][e] = 0.f;
+      const int row = r0 + 8 * r + w.g;
+      const int i = row / a.group;
+      const bool valid = row < a.n * a.group && i < tile.cnt;
+      w.pos[r] = valid ? tile.len - tile.cnt + i : -1;
+      w.seen[r] = !valid;
+      float x[32];
+      const char *p = (const char *)a.q + ((slice * a.group + (valid ? row % a.group : 0)) * a.n + (valid ? i : 0)) * kHeadDim * es;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float4 v = valid ? w.tail4(p, 0, 64 * (u >> 2) + 16 * w.t + 4 * (u & 3), 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[4 * u] = v.x; x[4 * u + 1] = v.y; x[4 * u + 2] = v.z; x[4 * u + 3] = v.w;
+      }
+      float m = 0.f;
+#pragma unroll
+      for (int u = 0; u < 32; ++u) m = fmaxf(m, fabsf(x[u]));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int e = min(max((int)(__float_as_uint(m) >> 23) - 126, -100), 126);
+      const float f = pow2f(-e);
+      w.rc[r] = pow2f(e) * a.scale_log2;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        uint32_t h0, h1, l0, l1;
+        split_h2(x[4 * u] * f, x[4 * u + 1] * f, h0, l0);
+        split_h2(x[4 * u + 2] * f, x[4 * u + 3] * f, h1, l1);
+        w.qa[0][u][r] = h0;
+        w.qa[0][u][2 + r] = h1;
+        if (W::SPLIT && NT == 1) { w.qa[0][u][1] = l0; w.qa[0][u][3] = l1; }
+        if (!W::SPLIT && NT == 1) { w.qa[0][u][1] = 0; w.qa[0][u][3] = 0; }
+        if (W::QL == 2) { w.qa[W::QL - 1][u][r] = l0; w.qa[W::QL - 1][u][2 + r] = l1; }
       }
     }
-    if (u + kAtWarps < b2) load(next, u + kAtWarps);
-    w.step(cur.k, cur.v, __shfl_sync(0xffffffffu, ks, k & 31), __shfl_sync(0xffffffffu, vs, k & 31), block_of(u));
-    u += kAtWarps;
-    ++k;
-  };
-  while (u < b2) {
-    one(x, y);
-    if (u >= b2) break;
-    one(y, x);
-  }
-  if (tail && wid == kAtWarps - 1) {
-    W z = w;  // a copy: w itself stays in registers
-    z.tail_step((const char *)c.k_tail + slice * kBlock * kHeadDim * es, (const char *)c.v_tail + slice * kBlock * kHeadDim * es,
-                len - full * kBlock, full);
-    w = z;
-  }
 
-  // the warps' partials
-#pragma unroll
-  for (int r = 0; r < NT; ++r) {
-    float l = w.l[r];
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if (w.t == 0) {
-      sm.m[wid][8 * r + w.g] = w.mref[r];
-      sm.l[wid][8 * r + w.g] = l;
+    float ks = 0.f, vs = 1.f, lu = 0.f;
+    int i = 0;
+    for (int u = b0 + 2 * wid; u < b2; u += 2 * kAtWarps, ++i) {
+      if ((i & 15) == 0) {  // the scales of the warp's next 16 turns
+        const int mine = u + (w.lane >> 1) * 2 * kAtWarps + (w.lane & 1);
+        vs = 0.f;
+        if (mine < b2) {
+          ks = ksc[tile.block(mine)];
+          vs = vsc[tile.block(mine)];
+        }
+        const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vs)));
+        if (top > 0.f) w.raise_unit(min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126));
+        vs = vs > 0.f ? fmaxf(vs * pow2f(-w.unit), pow2f(-kUnitSpan)) : 1.f;  // a block of zeros: any scale does
+        lu = log2f(vs);
+        vs = 1.f / vs;
+      }
+      if (!__all_sync(0xffffffffu, bar_wait(&bar[i & 1], (phase >> (i & 1)) & 1))) {
+        dead = true;
+        break;
+      }
+      phase ^= 1u << (i & 1);
+      const int s0 = (2 * i) & 31, s1 = s0 + 1;
+      const float k0 = __shfl_sync(0xffffffffu, ks, s0), k1 = __shfl_sync(0xffffffffu, ks, s1);
+      const float l0 = __shfl_sync(0xffffffffu, lu, s0), l1 = __shfl_sync(0xffffffffu, lu, s1);
+      const float i0 = __shfl_sync(0xffffffffu, vs, s0), i1 = __shfl_sync(0xffffffffu, vs, s1);
+      const unsigned char *turn = ring + (i & 1) * kTurnBytes;
+      if (u + 1 < b2) {
+        const float kk[2] = {k0, k1}, ll[2] = {l0, l1}, ii[2] = {i0, i1};
+        const int bb[2] = {tile.block(u), tile.block(u + 1)};
+        w.template step<2>(turn, kk, ll, ii, bb);
+      } else {
+        const float kk[1] = {k0}, ll[1] = {l0}, ii[1] = {i0};
+        const int bb[1] = {tile.block(u)};
+        w.template step<1>(turn, kk, ll, ii, bb);
+      }
+      __syncwarp();
+      issue(i + 2);
     }
+    if (dead && b2 > b0) {
+      if (w.lane == 0) atomicOr(c.ticket + c.batch, kAnomTimeout);
+      // copies still in flight land before the ring is used again
+      for (int j = 0; j < 2; ++j)
+        if (b0 + 2 * ((i + j) * kAtWarps + wid) < b2) bar_wait(&bar[(i + j) & 1], (phase >> ((i + j) & 1)) & 1);
+    }
+    if (tail && wid == kAtWarps - 1) {
+      W z = w;  // a copy: w itself stays in registers
+      z.tail_step((const char *)c.k_tail + slice * kBlock * kHeadDim * es, (const char *)c.v_tail + slice * kBlock * kHeadDim * es,
+                  tile.len - full * kBlock, full);
+      w = z;
+    }
+
+    __syncthreads();  // the rings are free: the warps' partials go over them
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int r = 0; r < NT; ++r) {
+      float l = w.l[r];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (w.t == 0) {
+        sm.m[wid][8 * r + w.g] = w.seen[r] && w.unit != kNoUnit ? w.ref[r] + (float)w.unit : -INFINITY;
+        sm.t[wid][8 * r + w.g] = w.seen[r] ? w.ref[r] : -INFINITY;
+        sm.l[wid][8 * r + w.g] = l;
+      }
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        *(float2 *)&sm.o[wid][i * AtSmem<NT>::IS + (8 * r + 2 * w.t + e) * AtSmem<NT>::RS + 2 * w.g] =
-            make_float2(w.o[r][i][e], w.o[r][i][2 + e]);
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *(float2 *)&sm.o[wid][i * Sm::IS + (8 * r + 2 * w.t + e) * Sm::RS + 2 * w.cg] = make_float2(w.o[r][i][e], w.o[r][i][2 + e]);
+    }
+    __syncthreads();
+    if (threadIdx.x < RT) {
+      const int row = threadIdx.x;
+      float top = -INFINITY, topt = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int j = 0; j < kAtWarps; ++j) {
+        top = fmaxf(top, sm.m[j][row]);
+        topt = fmaxf(topt, sm.t[j][row]);
+      }
+#pragma unroll
+      for (int j = 0; j < kAtWarps; ++j) {
+        sm.f[j][row] = share(sm.m[j][row], top);
+        l += share(sm.t[j][row], topt) * sm.l[j][row];
+      }
+      sm.pm[row] = top;
+      sm.pt[row] = topt;
+      sm.pl[row] = l;
+    }
+    __syncthreads();
+    const bool whole = a.streamed ? b0 == 0 && b1 == tile.nb : parts == 1;
+    float *const slot = a.streamed && !whole ? a.ws + (2 * (int64_t)blockIdx.x + (x - (b1 - b0) == x0 ? 0 : 1)) * Sm::kSlot : nullptr;
+    for (int it = threadIdx.x; it < RT * 64; it += kAtThreads) {
+      const int row = it >> 6, p = it & 63;  // values 2 p, 2 p + 1: plane p % 8 of chunk p / 8
+      float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < kAtWarps; ++j) {
+        const float2 x2 = *(const float2 *)&sm.o[j][(p & 7) * Sm::IS + row * Sm::RS + 2 * (p >> 3)];
+        const float f = sm.f[j][row];
+        s.x += f * x2.x;
+        s.y += f * x2.y;
+      }
+      if (whole) put_out<DT>(a, slice, tile.cnt, r0 + row, 2 * p, s, sm.pl[row], sm.pm[row] - sm.pt[row]);
+      else *(float2 *)(slot ? slot + row * kHeadDim + 2 * p : &sm.part[row][2 * p]) = s;
+    }
+    if (slot && threadIdx.x < RT) {
+      slot[RT * kHeadDim + threadIdx.x] = sm.pm[threadIdx.x];
+      slot[RT * kHeadDim + RT + threadIdx.x] = sm.pt[threadIdx.x];
+      slot[RT * kHeadDim + 2 * RT + threadIdx.x] = sm.pl[threadIdx.x];
+    }
+    if (a.streamed) {
+      if (x < x1) {  // the next tile's copies go over what was just read and written here
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+      }
+      continue;
+    }
+    if (whole) return;
+    cluster_barrier();
+    for (int it = threadIdx.x + part * kAtThreads; it < RT * 64; it += parts * kAtThreads) {
+      const int row = it >> 6, p = it & 63;
+      float m[kAtMaxCluster], mt[kAtMaxCluster], top = -INFINITY, topt = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int j = 0; j < kAtMaxCluster; ++j) {
+        if (j >= parts) break;
+        m[j] = peer_f(&sm.pm[row], j);
+        mt[j] = peer_f(&sm.pt[row], j);
+        top = fmaxf(top, m[j]);
+        topt = fmaxf(topt, mt[j]);
+      }
+      float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < kAtMaxCluster; ++j) {
+        if (j >= parts) break;
+        const float f = share(m[j], top);
+        const float2 x2 = peer_f2(&sm.part[row][2 * p], j);
+        l += share(mt[j], topt) * peer_f(&sm.pl[row], j);
+        s.x += f * x2.x;
+        s.y += f * x2.y;
+      }
+      put_out<DT>(a, slice, tile.cnt, r0 + row, 2 * p, s, l, top - topt);
+    }
+    cluster_barrier();  // no CTA leaves while another reads its shared memory
+  }
+}
+
+// Joins the parts of the tiles that several CTAs of a streamed launch share,
+// and zeroes tiles that see nothing. One CTA a row of a tile: every part's
+// factor first, then a thread sums a pair of values over each eighth part and
+// the eight sums are added in order.
+constexpr int kMergeThreads = 512;
+constexpr int kMergeGroups = kMergeThreads / 64;
+constexpr int kMaxCtas = 1024;
+
+template <int DT, int NT>
+__global__ void __launch_bounds__(kMergeThreads) k_attend8_merge(const __grid_constant__ AttendArgs a, int ctas) {
+  __shared__ Stream stream;
+  constexpr int RT = 8 * NT, kSlot = AtSmem<NT>::kSlot;
+  __shared__ float factor[kMaxCtas];
+  __shared__ float2 sums[kMergeGroups][64];
+  __shared__ float total_l, unit;
+  __shared__ int range[3];
+  const int G = a.c.batch * a.row_tiles, row = blockIdx.y;
+  stream.fill(a, RT);  // the lengths and counts are inputs: not the first kernel's
+  const int gi = blockIdx.x / a.c.n_kv_heads, h = blockIdx.x % a.c.n_kv_heads, nb = stream.nb[gi];
+  const int b = gi % a.c.batch, rt = gi / a.c.batch;
+  const int64_t slice = (int64_t)b * a.c.n_kv_heads + h;
+  if (threadIdx.x == 0) {
+    const int64_t total = stream.at[G], P = min((int64_t)ctas, total), p0 = stream.at[gi] + (int64_t)h * nb;
+    auto owner = [&](int64_t x) {
+      int i = (int)(x * P / total);
+      while (total * (i + 1) / P <= x) ++i;
+      while (total * i / P > x) --i;
+      return i;
+    };
+    range[0] = range[1] = range[2] = 0;
+    if (nb > 0) {  // CTAs range[0].. share the tile; the first one's part is its second if it began before
+      range[0] = owner(p0);
+      range[1] = owner(p0 + nb - 1) - range[0] + 1;
+      range[2] = total * range[0] / P < p0;
+    }
   }
   __syncthreads();
-  if (threadIdx.x < RT) {
-    const int row = threadIdx.x;
-    float top = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int j = 0; j < kAtWarps; ++j) top = fmaxf(top, sm.m[j][row]);
-#pragma unroll
-    for (int j = 0; j < kAtWarps; ++j) {
-      const float f = share(sm.m[j][row], top);
-      sm.f[j][row] = f;
-      l += f * sm.l[j][row];
+  const int i0 = range[0], np = range[1], second = range[2];
+  wait_prerequisites();  // by every CTA: this kernel's end stands for the first one's
+  if (np == 1 || rt * RT + row >= a.n * a.group) return;  // one CTA had it all, or the row is none
+  auto slot = [&](int j) { return a.ws + (2 * (int64_t)(i0 + j) + (j == 0 ? second : 0)) * kSlot; };
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    float top = -INFINITY, topt = -INFINITY, l = 0.f;
+    for (int j = lane; j < np; j += 32) {
+      top = fmaxf(top, slot(j)[RT * kHeadDim + row]);
+      topt = fmaxf(topt, slot(j)[RT * kHeadDim + RT + row]);
     }
-    sm.pm[row] = top;
-    sm.pl[row] = l;
+#pragma unroll
+    for (int d = 16; d; d /= 2) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      topt = fmaxf(topt, __shfl_xor_sync(0xffffffffu, topt, d));
+    }
+    for (int j = lane; j < np; j += 32) {
+      factor[j] = share(slot(j)[RT * kHeadDim + row], top);
+      l += share(slot(j)[RT * kHeadDim + RT + row], topt) * slot(j)[RT * kHeadDim + 2 * RT + row];
+    }
+#pragma unroll
+    for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (lane == 0) {
+      total_l = l;
+      unit = top - topt;
+    }
   }
   __syncthreads();
-  auto finish = [&](int row, int d, float2 o, float l) {
-    const int rr = r0 + row, i = rr / a.group;
-    if (rr >= R) return;
-    if (i >= cnt || l == 0.f) o = make_float2(0.f, 0.f);
-    else { o.x = o.x / l; o.y = o.y / l; }
-    const int64_t at = (((int64_t)(b * (int64_t)c.n_kv_heads + h) * a.group + rr % a.group) * a.n + i) * kHeadDim + d;
-    if (DT == 1) *(uint32_t *)((uint16_t *)a.out + at) = pack_bf16(o.x, o.y);
-    else *(float2 *)((float *)a.out + at) = o;
-  };
-  for (int it = threadIdx.x; it < RT * 64; it += kAtThreads) {
-    const int row = it >> 6, p = it & 63;  // values 2 p, 2 p + 1: plane p % 8 of group p / 8
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < kAtWarps; ++j) {
-      const float2 x2 = *(const float2 *)&sm.o[j][(p & 7) * AtSmem<NT>::IS + row * AtSmem<NT>::RS + 2 * (p >> 3)];
-      const float f = sm.f[j][row];
-      s.x += f * x2.x;
-      s.y += f * x2.y;
-    }
-    if (parts == 1) finish(row, 2 * p, s, sm.pl[row]);
-    else *(float2 *)&sm.part[row][2 * p] = s;
+  const int p = threadIdx.x & 63, grp = threadIdx.x >> 6;
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (int j = grp; j < np; j += kMergeGroups) {
+    const float2 x2 = *(const float2 *)(slot(j) + row * kHeadDim + 2 * p);
+    const float f = factor[j];
+    s.x += f * x2.x;
+    s.y += f * x2.y;
   }
-  if (parts == 1) return;
-  cluster_barrier();
-  for (int it = threadIdx.x + part * kAtThreads; it < RT * 64; it += parts * kAtThreads) {
-    const int row = it >> 6, p = it & 63;
-    float m[kAtMaxCluster], top = -INFINITY, l = 0.f;
+  sums[grp][p] = s;
+  __syncthreads();
+  if (grp) return;
 #pragma unroll
-    for (int j = 0; j < kAtMaxCluster; ++j) {
-      if (j >= parts) break;
-      m[j] = peer_f(&sm.pm[row], j);
-      top = fmaxf(top, m[j]);
-    }
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < kAtMaxCluster; ++j) {
-      if (j >= parts) break;
-      const float f = share(m[j], top);
-      const float2 x2 = peer_f2(&sm.part[row][2 * p], j);
-      l += f * peer_f(&sm.pl[row], j);
-      s.x += f * x2.x;
-      s.y += f * x2.y;
-    }
-    finish(row, 2 * p, s, l);
+  for (int j = 1; j < kMergeGroups; ++j) {
+    s.x += sums[j][p].x;
+    s.y += sums[j][p].y;
   }
-  cluster_barrier();  // no CTA leaves while another reads its shared memory
+  const int cnt = a.counts ? min(max(a.counts[b], 0), a.n) : a.n;
+  put_out<DT>(a, slice, cnt, rt * RT + row, 2 * p, s, total_l, unit);
+}
+
+// How a call is split.
+struct AttendPlan {
+  int nt, row_tiles, cluster;
+  int ctas;  // of a streamed launch, 0 if it is none
+  int64_t tiles;
+};
+
+static const char *plan_attend(const lkv_cache8 *c, int32_t group, int32_t n, int32_t window, int32_t sinks, int32_t max_len, int sms,
+                               AttendPlan *p) {
+  const int64_t R = (int64_t)n * group, S = (int64_t)c->batch * c->n_kv_heads;
+  if (R > 0x7fffffff - 16) return "too many rows";
+  p->nt = R <= 8 ? 1 : 2;
+  p->row_tiles = (int)((R + 8 * p->nt - 1) / (8 * p->nt));
+  p->tiles = S * p->row_tiles;
+  // blocks that a tile's rows may see, at most
+  int64_t most = max_len > 0 && max_len < c->capacity ? max_len : c->capacity;
+  if (window > 0 && window < c->capacity) {
+    const int64_t seen = (int64_t)window + (sinks < c->capacity ? sinks : c->capacity) + (8 * p->nt + group - 1) / group;
+    if (seen < most) most = seen;
+  }
+  const int64_t blocks = (most + kBlock - 1) / kBlock + 1;
+  int64_t slots = (int64_t)sms * (c->dtype == LKV_DTYPE_FP32 && p->nt == 2 ? 1 : 2);  // CTAs that the GPU holds
+  if (slots > kMaxCtas) slots = kMaxCtas;
+  int64_t cluster = slots / p->tiles, most_cluster = blocks / (2 * kAtWarps);  // a turn for every warp
+  if (cluster > most_cluster) cluster = most_cluster;
+  p->cluster = (int)(cluster < 1 ? 1 : cluster > kAtMaxCluster ? kAtMaxCluster : cluster);
+  p->ctas = 0;
+  // Streamed where whole tiles would leave over two fifths of the GPU idle (in
+  // their last wave) and are long enough to pay for the second kernel. On a
+  // GB300, int8 and 4 query heads: 8 KV heads of 131,579 tokens 131 us as 64
+  // CTAs in clusters, 56 us streamed; 2 of 8,000 tokens 14.4 and 10.1 us; 160
+  // of 33,000 tokens 306 and 220 us; but 64 of 33,000 tokens (256 CTAs in
+  // clusters) 90 and 105 us.
+  const int64_t ctas = p->tiles * p->cluster, last = ctas <= slots ? ctas : ctas % slots;
+  if (ctas < 3 * slots && last > 0 && last * 5 < slots * 3 && blocks >= 24 * p->cluster &&
+      (int64_t)c->batch * p->row_tiles <= kAtGroups) {
+    // at least 16 blocks for each CTA; few tiles: a whole number of CTAs each,
+    // so that none begins two, and not the last ones (parts cost merging)
+    int64_t most_ctas = p->tiles * blocks / 16;
+    if (most_ctas < p->tiles) most_ctas = p->tiles;
+    const int64_t full = slots * 27 / 32 < most_ctas ? slots * 27 / 32 : most_ctas;
+    p->ctas = (int)(p->tiles * 4 <= full ? full / p->tiles * p->tiles : slots < most_ctas ? slots : most_ctas);
+    p->cluster = 1;
+  }
+  if (p->tiles * p->cluster > 0x7fffffff) return "too many rows";
+  return nullptr;
 }
 
 template <int DT, int CODE, int NT>
-static cudaError_t launch_attend(const AttendArgs &a, int64_t tiles, int cluster, cudaStream_t st) {
+static cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, const CUtensorMap &km, const CUtensorMap &vm, cudaStream_t st) {
   auto *fn = k_attend8<DT, CODE, NT>;
-  const int smem = (int)sizeof(AtSmem<NT>);
+  constexpr int smem = 1024 + ((int)sizeof(AtSmem<NT>) > kRingBytes ? (int)sizeof(AtSmem<NT>) : kRingBytes);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess && cluster > 8) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(tiles * cluster));
+  cfg.gridDim = dim3((unsigned)(p.ctas ? p.ctas : p.tiles * p.cluster));
   cfg.blockDim = dim3(kAtThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.x = p.cluster;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
+  cfg.numAttrs = p.ctas ? 0 : 1;
+  e = cudaLaunchKernelEx(&cfg, fn, a, km, vm);
+  if (e != cudaSuccess || !p.ctas) return e;
+  cfg.gridDim = dim3((unsigned)p.tiles, 8 * NT);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, a);
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, k_attend8_merge<DT, NT>, a, p.ctas);
 }
 
 template <int DT, int CODE>
-static cudaError_t launch_attend(const AttendArgs &a, int nt, int64_t tiles, int cluster, cudaStream_t st) {
-  return nt == 1 ? launch_attend<DT, CODE, 1>(a, tiles, cluster, st) : launch_attend<DT, CODE, 2>(a, tiles, cluster, st);
+static cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, const CUtensorMap &km, const CUtensorMap &vm, cudaStream_t st) {
+  return p.nt == 1 ? launch_attend<DT, CODE, 1>(a, p, km, vm, st) : launch_attend<DT, CODE, 2>(a, p, km, vm, st);
 }
 
 // What the arguments of an attention call have to be, apart from the tensors.
@@ -588,18 +971,31 @@ static const char *check_attend(const lkv_cache8 *c, int32_t group, int32_t n, i
   return nullptr;
 }
 
+static lkv_status refuse_in(const char *where, const char *why) {
+  char buf[192];
+  std::snprintf(buf, sizeof buf, "%s: %s", where, why);
+  return refuse(buf);
+}
+
+static int64_t plan_bytes(const AttendPlan &p) {
+  return p.ctas ? (int64_t)p.ctas * 2 * (p.nt == 1 ? AtSmem<1>::kSlot : AtSmem<2>::kSlot) * 4 : 0;
+}
+
 }  // namespace lkv
 
 extern "C" lkv_status lkv_cache8_attend_workspace(const lkv_cache8 *c, int32_t group, int32_t n, int32_t window,
                                                   int32_t sinks, int32_t max_len, int64_t *bytes) {
   using namespace lkv;
-  if (const char *m = check_attend(c, group, n, window, sinks, max_len)) {
-    char buf[160];
-    std::snprintf(buf, sizeof buf, "lkv_cache8_attend_workspace: %s", m);
-    return refuse(buf);
-  }
+  if (const char *m = check_attend(c, group, n, window, sinks, max_len)) return refuse_in("lkv_cache8_attend_workspace", m);
   if (!bytes) return refuse("lkv_cache8_attend_workspace: null result");
   *bytes = 0;
+  if (n == 0) return LKV_OK;
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_refuse("lkv_cache8_attend_workspace", e);
+  AttendPlan p;
+  if (const char *m = plan_attend(c, group, n, window, sinks, max_len, sms, &p)) return refuse_in("lkv_cache8_attend_workspace", m);
+  *bytes = plan_bytes(p);
   return LKV_OK;
 }
 
@@ -608,26 +1004,28 @@ extern "C" lkv_status lkv_cache8_attend(const lkv_cache8 *c, const void *q, int3
                                         int32_t max_len, void *out, void *workspace, int64_t workspace_bytes,
                                         void *stream) {
   using namespace lkv;
-  if (const char *m = check_attend(c, group, n, window, sinks, max_len)) {
-    char buf[160];
-    std::snprintf(buf, sizeof buf, "lkv_cache8_attend: %s", m);
-    return refuse(buf);
-  }
+  if (const char *m = check_attend(c, group, n, window, sinks, max_len)) return refuse_in("lkv_cache8_attend", m);
   if (!(scale - scale == 0.f)) return refuse("lkv_cache8_attend: scale is not finite");
   if (n == 0) return LKV_OK;
   if (!q || !out) return refuse("lkv_cache8_attend: null queries or output");
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(counts, 4))
-    return refuse("lkv_cache8_attend: queries and output must be 16-byte aligned, counts 4-byte aligned");
-  const int64_t S = (int64_t)c->batch * c->n_kv_heads, R = (int64_t)n * group;
-  const int64_t bytes = S * R * kHeadDim * (c->dtype == LKV_DTYPE_BF16 ? 2 : 4);
-  if (overlaps_cache8(c, out, bytes) || overlap(out, bytes, q, bytes) || overlap(out, bytes, counts, (int64_t)c->batch * 4))
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(counts, 4) || !aligned(workspace, 16))
+    return refuse("lkv_cache8_attend: queries, output and workspace must be 16-byte aligned, counts 4-byte aligned");
+  const int64_t S = (int64_t)c->batch * c->n_kv_heads;
+  const int64_t bytes = S * group * n * kHeadDim * (c->dtype == LKV_DTYPE_BF16 ? 2 : 4), ib = (int64_t)c->batch * 4;
+  if (overlaps_cache8(c, out, bytes) || overlap(out, bytes, q, bytes) || overlap(out, bytes, counts, ib))
     return refuse("lkv_cache8_attend: the output overlaps the cache or an input");
-  (void)workspace;
-  (void)workspace_bytes;
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return cuda_refuse("lkv_cache8_attend", e);
-  if (R > 0x7fffffff - 16) return refuse("lkv_cache8_attend: too many rows");
+  AttendPlan p;
+  if (const char *m = plan_attend(c, group, n, window, sinks, max_len, sms, &p)) return refuse_in("lkv_cache8_attend", m);
+  const int64_t need = plan_bytes(p);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return refuse("lkv_cache8_attend: the workspace is smaller than lkv_cache8_attend_workspace says");
+    if (overlaps_cache8(c, workspace, need) || overlap(workspace, need, q, bytes) || overlap(workspace, need, out, bytes) ||
+        overlap(workspace, need, counts, ib))
+      return refuse("lkv_cache8_attend: the workspace overlaps another tensor");
+  }
   AttendArgs a{};
   a.c = *c;
   a.q = q;
@@ -638,23 +1036,17 @@ extern "C" lkv_status lkv_cache8_attend(const lkv_cache8 *c, const void *q, int3
   a.window = window >= c->capacity ? 0 : window;  // a window that reaches everything is none
   a.sinks = sinks < c->capacity ? sinks : c->capacity;
   a.scale_log2 = scale * kLog2e;
-  const int nt = R <= 8 ? 1 : 2;
-  a.row_tiles = (int32_t)((R + 8 * nt - 1) / (8 * nt));
-  const int64_t tiles = S * a.row_tiles;
-  // blocks that a tile's rows may see, at most
-  int64_t most = max_len > 0 && max_len < c->capacity ? max_len : c->capacity;
-  if (a.window > 0) {
-    const int64_t seen = (int64_t)a.window + a.sinks + (8 * nt + group - 1) / group;
-    if (seen < most) most = seen;
+  a.row_tiles = p.row_tiles;
+  a.streamed = p.ctas > 0;
+  a.ws = (float *)workspace;
+  CUtensorMap km, vm;
+  if (!codes_map(&km, c->k_codes, c->capacity, S, kBlock) || !codes_map(&vm, c->v_codes, c->capacity, S, kBlock)) {
+    set_unbound_error("lkv_cache8_attend: the driver refused a tensor map of the codes");
+    return LKV_ECUDA;
   }
-  const int64_t blocks = (most + kBlock - 1) / kBlock + 1;
-  int cluster = 1;
-  while (cluster < kAtMaxCluster && tiles * cluster < (int64_t)sms * 3 && blocks >= (int64_t)2 * cluster * kAtWarps * 4)
-    cluster *= 2;
-  if (tiles * cluster > 0x7fffffff) return refuse("lkv_cache8_attend: too many rows");
   cudaStream_t st = (cudaStream_t)stream;
   const bool bf = c->dtype == LKV_DTYPE_BF16, i8 = c->code == LKV_CODE_INT8;
-  if (bf) e = i8 ? launch_attend<1, LKV_CODE_INT8>(a, nt, tiles, cluster, st) : launch_attend<1, LKV_CODE_E4M3>(a, nt, tiles, cluster, st);
-  else e = i8 ? launch_attend<0, LKV_CODE_INT8>(a, nt, tiles, cluster, st) : launch_attend<0, LKV_CODE_E4M3>(a, nt, tiles, cluster, st);
+  if (bf) e = i8 ? launch_attend<1, LKV_CODE_INT8>(a, p, km, vm, st) : launch_attend<1, LKV_CODE_E4M3>(a, p, km, vm, st);
+  else e = i8 ? launch_attend<0, LKV_CODE_INT8>(a, p, km, vm, st) : launch_attend<0, LKV_CODE_E4M3>(a, p, km, vm, st);
   return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_attend", e);
 }

@@ -36,27 +36,34 @@ bool overlaps_cache8(const lkv_cache8 *c, const void *p, int64_t bytes) {
 
 // ---------------------------------------------------------------- write
 
-// The code of x in a block of largest magnitude amax, decided exactly: the
-// quotient's distance from the halfway point between two codes has the sign
-// of a difference of two products that fp64 holds exactly (24-bit by 9-bit
-// significands). Only values within the fp32 quotient's error of such a
-// point come here.
-__device__ __noinline__ int int8_exact(float x, float amax) {
-  const float a = fabsf(x);
-  const int m = (int)rintf(a * __fdiv_rn(127.f, amax) - 0.5f);  // the halfway point is m + 1/2
-  const double d = 254.0 * (double)a - (double)(2 * m + 1) * (double)amax;
-  const int k = d > 0.0 ? m + 1 : d < 0.0 ? m : (m + (m & 1));
-  return x < 0.f ? -k : k;
+// The code of x in a block of largest magnitude amax, decided exactly where
+// the fp32 quotient lies within its own error of the halfway point between
+// two codes: the sign of top * |x| - halfway * amax, both products taken with
+// their rounding errors (24-bit by 9-bit significands: an error has at most
+// 9 bits and the difference of two at most 11, so the sum below has the exact
+// sign). fp64 would do too, at a sixty-fourth of the rate; bf16 inputs sit
+// exactly halfway often enough (one value in 600) for that to show.
+__device__ __forceinline__ float halfway_sign(float top, float a, float half, float amax) {
+  const float p = top * a, r = half * amax;
+  return (p - r) + (__fmaf_rn(top, a, -p) - __fmaf_rn(half, amax, -r));
 }
 
-__device__ __noinline__ float e4m3_exact(float x, float amax) {
-  const float a = fabsf(x), q = a * __fdiv_rn(448.f, amax);
+__device__ __forceinline__ uint32_t int8_exact(float x, float inv, float amax) {
+  const float a = fabsf(x);
+  const float m = rintf(__fmaf_rn(a, inv, -0.5f));  // the halfway point is m + 1/2
+  const float d = halfway_sign(254.f, a, 2.f * m + 1.f, amax);
+  const int k = (int)m, up = d > 0.f || (d == 0.f && (k & 1));
+  return (uint32_t)(x < 0.f ? -(k + up) : k + up);
+}
+
+__device__ __forceinline__ float e4m3_exact(float x, float inv, float amax) {
+  const float a = fabsf(x), q = a * inv;
   // step of the code's binade: 2^(e - 3), 2^-9 below 2^-6
   const float step = q < 0x1p-6f ? 0x1p-9f : __uint_as_float((__float_as_uint(q) & 0x7f800000u) - (3u << 23));
   const float m = rintf(q / step - 0.5f);
-  const double d = 448.0 * (double)a - (double)(m + 0.5f) * (double)step * (double)amax;
-  const float k = d > 0.0 ? m + 1.f : d < 0.0 ? m : (m + (float)((int)m & 1));
-  return copysignf(k * step, x);
+  const float d = halfway_sign(448.f, a, (m + 0.5f) * step, amax);
+  const bool up = d > 0.f || (d == 0.f && ((int)m & 1));
+  return copysignf((up ? m + 1.f : m) * step, x);
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -65,41 +72,40 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Four codes of x[0..3] in one word; inv is about 127 / amax or 448 / amax.
-// The fp32 quotient is off by at most 2 units in its last place; where that
-// could change the code, the lane settles it exactly.
+// Four codes of x[0..3] in one word; inv is 127 / amax or 448 / amax, rounded.
+// x * inv is off by at most 2 units in its last place; where that could
+// change a code, the lane settles its four exactly.
 template <int CODE>
 __device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv, float amax) {
-  float q[4];
   if constexpr (CODE == LKV_CODE_INT8) {
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: a sum's low bits are the rounded integer
     float far = 0.f;
     uint32_t r[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      q[e] = x[e] * inv;
-      const float s = __fadd_rn(q[e], 12582912.f);  // 1.5 * 2^23: the sum's low bits are the rounded integer
+      const float s = __fmaf_rn(x[e], inv, kMagic);
       r[e] = __float_as_uint(s);
-      far = fmaxf(far, fabsf(q[e] - (s - 12582912.f)));
+      far = fmaxf(far, fabsf(__fmaf_rn(x[e], inv, kMagic - s)));
     }
-    if (far > 0.5f - 0x1p-14f) {  // |q| < 128 is off by less than 2^-15
-#pragma unroll 1
-      for (int e = 0; e < 4; ++e) r[e] = (uint32_t)int8_exact(x[e], amax);
+    if (far > 0.5f - 0x1p-14f) {  // |x * inv| < 128 is off by less than 2^-15
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = int8_exact(x[e], inv, amax);
     }
     return __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
   } else {
-    uint32_t near = 0xffffffffu;
+    float q[4];
+    uint32_t near = 0xffffffffu, small = 0xffffffffu;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       q[e] = x[e] * inv;
-      // adding 2^-6 to a magnitude below it gives the codes there the spacing
-      // of the first binade; the 20 bits behind a code are then 0x80000 halfway
-      float a = fabsf(q[e]);
-      a = a < 0x1p-6f ? a + 0x1p-6f : a;
-      near = min(near, (uint32_t)abs((int)(__float_as_uint(a) & 0xfffffu) - 0x80000));
+      const uint32_t u = __float_as_uint(q[e]) & 0x7fffffffu;
+      near = min(near, (uint32_t)abs((int)(u & 0xfffffu) - 0x80000));  // the 20 bits behind a code
+      small = min(small, u - 1u);                                      // zero wraps to the top
     }
-    if (near <= 8u) {
-#pragma unroll 1
-      for (int e = 0; e < 4; ++e) q[e] = e4m3_exact(x[e], amax);
+    // below 2^-6 the codes are evenly spaced: settled exactly too
+    if (near <= 8u || small < 0x3c800000u) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[e] = e4m3_exact(x[e], inv, amax);
     }
     return e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
   }
@@ -197,12 +203,13 @@ struct BlockWriter {
     }
     constexpr float kTop = CODE == LKV_CODE_INT8 ? 127.f : 448.f;
     if (p0 + kBlock <= end) {
-      if (amax >= 0x1p-100f) {
+      if (amax >= 0x1p-80f && amax <= 0x1p100f) {
         put(w, j, __fdiv_rn(kTop, amax), amax, 1.f);
       } else if (amax > 0.f) {
-        // tiny blocks: scaled by 2^126 (exactly), or kTop / amax would overflow
-        const float up = amax * 0x1p126f;
-        put(w, j, __fdiv_rn(kTop, up), up, 0x1p126f);
+        // scaled by a power of two (exactly, but for values whose code is 0):
+        // products with kTop and 1 / amax neither overflow nor lose bits
+        const float f = amax < 1.f ? 0x1p126f : 0x1p-32f;
+        put(w, j, __fdiv_rn(kTop, amax * f), amax * f, f);
       } else {
         uint4 *to = (uint4 *)(codes + (int64_t)j * kBlock * kHeadDim);
 #pragma unroll
@@ -282,8 +289,9 @@ __global__ void __launch_bounds__(kCacheThreads) k_cache8_write(const __grid_con
     if (both && ch == 0) w.block(last);
   }
   __syncwarp();
+  // The lengths have been read (they decided the run) when the arrival is
+  // issued; the rows need no fence, since only later launches read them.
   if ((threadIdx.x & 31) == 0) {
-    __threadfence();
     const int all = 2 * c.n_kv_heads * a.chunks;
     if (atomicAdd(c.ticket + b, 1) == all - 1) {
       c.ticket[b] = 0;
@@ -477,6 +485,10 @@ extern "C" lkv_status lkv_cache8_status(const lkv_cache8 *c, void *stream) {
   if (e == cudaSuccess && bits) e = cudaMemsetAsync(at, 0, sizeof bits, st);
   if (e == cudaSuccess && bits) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_refuse("lkv_cache8_status", e);
+  if (bits & kAnomTimeout) {
+    set_unbound_error("lkv_cache8: a device-side wait of an attention gave up; its output is not complete");
+    return LKV_ETIMEOUT;
+  }
   if (bits & kAnomCapacity) {
     set_unbound_error("lkv_cache8: a write went past the capacity; that sequence was left as it was");
     return LKV_ECAPACITY;

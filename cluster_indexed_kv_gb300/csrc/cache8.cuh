@@ -16,6 +16,7 @@ enum : int32_t {
   kAnomRange = 1,      // a write's start or count is not one the cache can take
   kAnomCapacity = 2,   // a write past the capacity
   kAnomNotFinite = 4,  // a NaN or an infinity was written
+  kAnomTimeout = 8,    // a bounded wait in an attention gave up
 };
 
 inline lkv_status refuse(const char *msg) {

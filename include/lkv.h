@@ -603,9 +603,10 @@ lkv_status lkv_cache8_attend_workspace(const lkv_cache8 *cache, int32_t group, i
                                        int32_t window, int32_t sinks, int32_t max_len,
                                        int64_t *bytes);
 
-/* Blocking: waits for stream, then reports and clears what writes to this
- * cache recorded: LKV_OK, LKV_ECAPACITY or LKV_EINVAL. May not be captured.
- * Errors: also LKV_ECUDA. */
+/* Blocking: waits for stream, then reports and clears what calls on this
+ * cache recorded: LKV_OK, LKV_ECAPACITY or LKV_EINVAL (writes), LKV_ETIMEOUT
+ * (an attention whose copies did not arrive). May not be captured. Errors:
+ * also LKV_ECUDA. */
 lkv_status lkv_cache8_status(const lkv_cache8 *cache, void *stream);
 
 /* Wait for the context's stream; report device-side anomalies. */

@@ -126,8 +126,9 @@ def attend_bound(want, dtype, size, vmax, length):
     tensor-core sums may truncate) and scaled by three rounded factors: off by
     at most 2^-18 of sum |q k| |scale| =: size. An error d of the scores moves
     an average of values by at most 2 d vmax (both the weight and the total).
-    exp2 and its rounded argument (magnitudes below 2 size + 16) add
-    2^-22 (2 size + 16) to each weight. Sums over the blocks: one fp32 rounding
+    exp2 and its rounded argument, the logarithm of a V scale in units of the
+    largest one among it (magnitudes below 2 size + 16 for scales within 2^16
+    of each other), add 2^-22 (2 size + 16) to each weight. Sums over the blocks: one fp32 rounding
     a block and merge, length / 16 + 40 of them, 2^-23 each. Weights in fp16
     (bf16 caches) are off by 2^-11 of themselves, and by 2^-31 of the largest
     weight where they are tiny; with remainders (fp32) by 2^-22. Then one

@@ -507,3 +507,36 @@ def test_serving_steps(fmt, dtype, window, sinks):
             err = (out[i].cpu().double() - want).abs()
             assert (err <= ref.attend_bound(want, dtype, size, vmax, lengths[i])).all()
     c.check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("lengths,h,group,n,window,sinks", [
+    ([9000], 1, 4, 1, 0, 0), ([7001, 1, 0, 6000], 2, 1, 1, 0, 0), ([40000, 3], 1, 4, 4, 0, 0), ([12000, 11984], 1, 8, 2, 6000, 20),
+    ([5000, 5001, 4999, 17], 40, 1, 1, 0, 0)])
+def test_attend_streamed(dtype, fmt, lengths, h, group, n, window, sinks):
+    """Few or uneven tiles of long sequences: shared evenly by many CTAs and
+    joined, the empty ones among them; the same bits each time."""
+    g = gen(50)
+    b, top = len(lengths), max(lengths)
+    x, y = (rows(g, b, 1, top, dtype).expand(b, h, top, 128) for _ in range(2))
+    c, k, v = make(x, y, fmt, dtype, (top + 31) // 16 * 16, lengths, garbage=g)
+    view = c._view
+    need = _lib.lkv_cache8_attend_workspace(c._at, group, n, window, sinks, 0)
+    assert need > 0 and view.batch == b, "not a streamed call: the case does not test what it is for"
+    q = torch.randn(b, h * group, n, 128, generator=g).to(dtype)
+    heads = [0, h // 2, h - 1]
+    got = c.attend(q.cuda(), window=window, sinks=sinks)
+    for i, length in enumerate(lengths):
+        for j in heads:
+            kk, vv = (ref.values(a[0][i, j:j + 1], a[1][i, j:j + 1], a[2][i, j:j + 1], length) for a in (k, v))
+            want, size, vmax = ref.attend(q[i, j * group:(j + 1) * group].double(), kk, vv, n, 128 ** -0.5, window, sinks)
+            err = (got[i, j * group:(j + 1) * group].cpu().double() - want).abs()
+            lim = ref.attend_bound(want, dtype, size, vmax, length)
+            assert (err <= lim).all(), f"sequence {i}, head {j}: off by {err.max():.3e}, {(err / lim.clamp_min(1e-300)).max():.2f} of the bound"
+    for _ in range(3):
+        assert torch.equal(c.attend(q.cuda(), window=window, sinks=sinks), got)
+    # a workspace that is too small, or none, is refused
+    L, out, qc = _lib.load(), torch.empty_like(q, device="cuda"), q.cuda()
+    for ws, size in ((None, 0), (out.data_ptr(), need), (torch.empty(need, dtype=torch.uint8, device="cuda").data_ptr(), need - 1)):
+        assert L.lkv_cache8_attend(c._at, qc.data_ptr(), group, n, None, 1.0, window, sinks, 0, out.data_ptr(), ws, size, None) == _lib.LKV_EINVAL
