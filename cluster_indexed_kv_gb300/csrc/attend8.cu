@@ -1,8 +1,5 @@
 // attend8.cu -- causal attention over the 8-bit cache (lkv_cache8_attend).
-#include "cache8.cuh"
-
-#include <cuda_fp16.h>
-#include "tma.cuh"
+#include "attend8.cuh"
 
 namespace lkv {
 
@@ -13,19 +10,6 @@ constexpr int kAtGroups = 512;      // (sequence, row tile) pairs that a streame
 constexpr int kCodeBytes = kBlock * kHeadDim;      // one block of K or V
 constexpr int kTurnBytes = 2 * 2 * kCodeBytes;     // two blocks of both
 constexpr int kRingBytes = kAtWarps * 2 * kTurnBytes;
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct AttendArgs {
-  lkv_cache8 c;
-  const void *q;
-  void *out;
-  const int32_t *counts;
-  int32_t n, group, window, sinks;
-  int32_t row_tiles;
-  int32_t streamed;   // the CTAs share all tiles' blocks evenly (see k_attend8)
-  float *ws;          // streamed: 2 partials a CTA
-  float scale_log2;   // scale * log2(e)
-};
 
 // c += a * b, fp16 operands, fp32 accumulators
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -40,65 +24,6 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-
-__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *(const uint32_t *)&h; }
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 2^e as a float, e clamped to the normal range
-__device__ __forceinline__ float pow2f(int e) {
-  return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23);
-}
-
-// x (fp32) as an fp16 value and an fp16 remainder
-__device__ __forceinline__ void split_h2(float x, float y, uint32_t &hi, uint32_t &lo) {
-  const __half2 h = __floats2half2_rn(x, y);
-  const float2 f = __half22float2(h);
-  hi = h2_bits(h);
-  lo = h2_bits(__floats2half2_rn(x - f.x, y - f.y));
-}
-
-// The two fp16 pairs of the four codes in w (exact in fp16).
-template <int CODE>
-__device__ __forceinline__ void codes_row(uint32_t w, uint32_t &p01, uint32_t &p23) {
-  if constexpr (CODE == LKV_CODE_INT8) {
-    const uint32_t u = w ^ 0x80808080u;  // x + 128; 0x6400 | u is 1024 + u in fp16
-    const __half2 off = __float2half2_rn(1152.f);
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    p01 = h2_bits(__hsub2(*(const __half2 *)&a, off));
-    p23 = h2_bits(__hsub2(*(const __half2 *)&b, off));
-  } else {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(p01), "=r"(p23) : "r"(w));
-  }
-}
-
-// Bytes 2 h and 2 h + 1 of two tokens' words as two fp16 pairs across the tokens.
-template <int CODE>
-__device__ __forceinline__ void codes_across(uint32_t wa, uint32_t wb, int h, uint32_t &even, uint32_t &odd) {
-  if constexpr (CODE == LKV_CODE_INT8) {
-    const uint32_t u = __byte_perm(wa, wb, h ? 0x7632 : 0x5410) ^ 0x80808080u;
-    const __half2 off = __float2half2_rn(1152.f);
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4240), b = __byte_perm(u, 0x64646464u, 0x4341);
-    even = h2_bits(__hsub2(*(const __half2 *)&a, off));
-    odd = h2_bits(__hsub2(*(const __half2 *)&b, off));
-  } else {
-    const uint32_t u = __byte_perm(wa, wb, h ? 0x7362 : 0x5140);
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(even), "=r"(odd) : "r"(u));
-  }
-}
-
-constexpr float kPShift = 6.f;
-constexpr float kSlack = 8.f;
-constexpr int kNoUnit = -1000;
-constexpr int kUnitSpan = 90;  // V scales below 2^-90 of the largest are taken for that
 
 // A warp's part of a tile's attention (see k_attend8).
 template <int DT, int CODE, int NT>
@@ -384,26 +309,6 @@ __device__ __forceinline__ float2 peer_f2(const void *p, uint32_t rank) {
 
 // 2^(m - top), 0 for a share that saw nothing
 __device__ __forceinline__ float share(float m, float top) { return m == -INFINITY ? 0.f : exp2f(m - top); }
-
-// The rows of a tile (one row tile of one sequence's KV head) and the blocks they see:
-// the first `sb` (sinks), then lo..hi.
-struct Tile {
-  int len, cnt, pmin, pmax, lo, hi, sb, nb;
-  __device__ __forceinline__ Tile() {}
-  __device__ __forceinline__ Tile(const AttendArgs &a, int b, int rt, int RT) {
-    len = min(max(a.c.lengths[b], 0), a.c.capacity);
-    cnt = a.counts ? min(max(a.counts[b], 0), a.n) : a.n;
-    const int R = a.n * a.group, r0 = rt * RT;
-    const int imin = r0 / a.group, imax = min((min(r0 + RT, R) - 1) / a.group, cnt - 1);
-    pmin = len - cnt + imin;
-    pmax = imin <= imax ? len - cnt + imax : -1;
-    lo = a.window > 0 ? max(0, pmin - a.window + 1) / kBlock : 0;
-    hi = pmax >= 0 ? pmax / kBlock : -1;
-    sb = a.window > 0 && hi >= 0 ? min((min(a.sinks, len) + kBlock - 1) / kBlock, lo) : 0;
-    nb = hi >= 0 ? sb + hi - lo + 1 : 0;
-  }
-  __device__ __forceinline__ int block(int u) const { return u < sb ? u : u - sb + lo; }
-};
 
 // A streamed launch's work: the blocks of all tiles in a row, (sequence, row
 // tile) by (sequence, row tile) and KV head by KV head, CTA i of P taking
@@ -885,13 +790,17 @@ __global__ void __launch_bounds__(kMergeThreads) k_attend8_merge(const __grid_co
 struct AttendPlan {
   int nt, row_tiles, cluster;
   int ctas;  // of a streamed launch, 0 if it is none
+  bool rows; // the kernel for many rows
   int64_t tiles;
 };
 
 static const char *plan_attend(const lkv_cache8 *c, int32_t group, int32_t n, int32_t window, int32_t sinks, int32_t max_len, int sms,
                                AttendPlan *p) {
   const int64_t R = (int64_t)n * group, S = (int64_t)c->batch * c->n_kv_heads;
-  if (R > 0x7fffffff - 16) return "too many rows";
+  if (R > 0x7fffffff - 256) return "too many rows";
+  p->rows = c->dtype == LKV_DTYPE_BF16 && R >= (getenv("XR") ? atoi(getenv("XR")) : 64);
+  p->ctas = 0;
+  if (p->rows) return nullptr;
   p->nt = R <= 8 ? 1 : 2;
   p->row_tiles = (int)((R + 8 * p->nt - 1) / (8 * p->nt));
   p->tiles = S * p->row_tiles;
@@ -907,7 +816,6 @@ static const char *plan_attend(const lkv_cache8 *c, int32_t group, int32_t n, in
   int64_t cluster = slots / p->tiles, most_cluster = blocks / (2 * kAtWarps);  // a turn for every warp
   if (cluster > most_cluster) cluster = most_cluster;
   p->cluster = (int)(cluster < 1 ? 1 : cluster > kAtMaxCluster ? kAtMaxCluster : cluster);
-  p->ctas = 0;
   // Streamed where whole tiles would leave over two fifths of the GPU idle (in
   // their last wave) and are long enough to pay for the second kernel. On a
   // GB300, int8 and 4 query heads: 8 KV heads of 131,579 tokens 131 us as 64
@@ -978,7 +886,7 @@ static lkv_status refuse_in(const char *where, const char *why) {
 }
 
 static int64_t plan_bytes(const AttendPlan &p) {
-  return p.ctas ? (int64_t)p.ctas * 2 * (p.nt == 1 ? AtSmem<1>::kSlot : AtSmem<2>::kSlot) * 4 : 0;
+  return !p.rows && p.ctas ? (int64_t)p.ctas * 2 * (p.nt == 1 ? AtSmem<1>::kSlot : AtSmem<2>::kSlot) * 4 : 0;
 }
 
 }  // namespace lkv
@@ -1036,9 +944,13 @@ extern "C" lkv_status lkv_cache8_attend(const lkv_cache8 *c, const void *q, int3
   a.window = window >= c->capacity ? 0 : window;  // a window that reaches everything is none
   a.sinks = sinks < c->capacity ? sinks : c->capacity;
   a.scale_log2 = scale * kLog2e;
-  a.row_tiles = p.row_tiles;
+  a.row_tiles = p.rows ? 0 : p.row_tiles;
   a.streamed = p.ctas > 0;
   a.ws = (float *)workspace;
+  if (p.rows) {
+    e = launch_attend_rows(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_attend", e);
+  }
   CUtensorMap km, vm;
   if (!codes_map(&km, c->k_codes, c->capacity, S, kBlock) || !codes_map(&vm, c->v_codes, c->capacity, S, kBlock)) {
     set_unbound_error("lkv_cache8_attend: the driver refused a tensor map of the codes");

@@ -1,0 +1,106 @@
+// attend8.cuh -- what the kernels of the attention over the 8-bit cache share.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "cache8.cuh"
+#include "tma.cuh"
+
+namespace lkv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kPShift = 6.f;
+constexpr float kSlack = 8.f;
+constexpr int kNoUnit = -1000;
+constexpr int kUnitSpan = 90;  // V scales below 2^-90 of the largest are taken for that
+
+struct AttendArgs {
+  lkv_cache8 c;
+  const void *q;
+  void *out;
+  const int32_t *counts;
+  int32_t n, group, window, sinks;
+  int32_t row_tiles;
+  int32_t streamed;   // the CTAs share all tiles' blocks evenly (see k_attend8)
+  float *ws;          // streamed: 2 partials a CTA
+  float scale_log2;   // scale * log2(e)
+};
+
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *(const uint32_t *)&h; }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 2^e as a float, e clamped to the normal range
+__device__ __forceinline__ float pow2f(int e) {
+  return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23);
+}
+
+// x (fp32) as an fp16 value and an fp16 remainder
+__device__ __forceinline__ void split_h2(float x, float y, uint32_t &hi, uint32_t &lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  hi = h2_bits(h);
+  lo = h2_bits(__floats2half2_rn(x - f.x, y - f.y));
+}
+
+// The two fp16 pairs of the four codes in w (exact in fp16).
+template <int CODE>
+__device__ __forceinline__ void codes_row(uint32_t w, uint32_t &p01, uint32_t &p23) {
+  if constexpr (CODE == LKV_CODE_INT8) {
+    const uint32_t u = w ^ 0x80808080u;  // x + 128; 0x6400 | u is 1024 + u in fp16
+    const __half2 off = __float2half2_rn(1152.f);
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    p01 = h2_bits(__hsub2(*(const __half2 *)&a, off));
+    p23 = h2_bits(__hsub2(*(const __half2 *)&b, off));
+  } else {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(p01), "=r"(p23) : "r"(w));
+  }
+}
+
+// Bytes 2 h and 2 h + 1 of two tokens' words as two fp16 pairs across the tokens.
+template <int CODE>
+__device__ __forceinline__ void codes_across(uint32_t wa, uint32_t wb, int h, uint32_t &even, uint32_t &odd) {
+  if constexpr (CODE == LKV_CODE_INT8) {
+    const uint32_t u = __byte_perm(wa, wb, h ? 0x7632 : 0x5410) ^ 0x80808080u;
+    const __half2 off = __float2half2_rn(1152.f);
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4240), b = __byte_perm(u, 0x64646464u, 0x4341);
+    even = h2_bits(__hsub2(*(const __half2 *)&a, off));
+    odd = h2_bits(__hsub2(*(const __half2 *)&b, off));
+  } else {
+    const uint32_t u = __byte_perm(wa, wb, h ? 0x7362 : 0x5140);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(even), "=r"(odd) : "r"(u));
+  }
+}
+
+// The rows of a tile (one row tile of one sequence's KV head) and the blocks they see:
+// the first `sb` (sinks), then lo..hi.
+struct Tile {
+  int len, cnt, pmin, pmax, lo, hi, sb, nb;
+  __device__ __forceinline__ Tile() {}
+  __device__ __forceinline__ Tile(const AttendArgs &a, int b, int rt, int RT) {
+    len = min(max(a.c.lengths[b], 0), a.c.capacity);
+    cnt = a.counts ? min(max(a.counts[b], 0), a.n) : a.n;
+    const int R = a.n * a.group, r0 = rt * RT;
+    const int imin = r0 / a.group, imax = min((min(r0 + RT, R) - 1) / a.group, cnt - 1);
+    pmin = len - cnt + imin;
+    pmax = imin <= imax ? len - cnt + imax : -1;
+    lo = a.window > 0 ? max(0, pmin - a.window + 1) / kBlock : 0;
+    hi = pmax >= 0 ? pmax / kBlock : -1;
+    sb = a.window > 0 && hi >= 0 ? min((min(a.sinks, len) + kBlock - 1) / kBlock, lo) : 0;
+    nb = hi >= 0 ? sb + hi - lo + 1 : 0;
+  }
+  __device__ __forceinline__ int block(int u) const { return u < sb ? u : u - sb + lo; }
+};
+
+// The kernel for many rows (attend8_rows.cu): bf16 caches.
+cudaError_t launch_attend_rows(const AttendArgs &a, cudaStream_t st);
+
+}  // namespace lkv
