@@ -70,12 +70,44 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
                :
                : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t *r) {
+// 8 columns, waited for.
+__device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
       ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+// 32 columns of the thread's lane; valid after tmem_wait32 on the same array.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -90,11 +122,6 @@ __device__ __forceinline__ float2 add_2(float2 a, float2 b) {
   float2 d;
   asm("{\n .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n add.rn.f32x2 rd, ra, rb;\n mov.b64 {%0, %1}, rd;\n}"
       : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float max_3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -288,8 +315,6 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
         const int r = 32 * pw + 8 * it + ks_row;
-        const int u = j * kRwBlocks + (r >> 4);
-        const bool in_tail = tail && u < tile.nb && tile.block(u) == full;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint4 w = kr[2 * it + h];
@@ -298,20 +323,27 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
           codes_row<CODE>(w.y, x[2], x[3]);
           codes_row<CODE>(w.z, x[4], x[5]);
           codes_row<CODE>(w.w, x[6], x[7]);
-          if (in_tail) {
-            const int row = r & 15;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t b2 = row < tail_rows ? *(const uint32_t *)(k_tail + row * kHeadDim + 64 * h + 16 * ks_j + 2 * k) : 0u;
-              x[k] = h2_bits(__floats2half2_rn(__uint_as_float(b2 << 16) * kf, __uint_as_float(b2 & 0xffff0000u) * kf));
-            }
-          }
           unsigned char *to = kt + h * kRwHalf + r * 128;
           *(uint4 *)(to + (((2 * ks_j) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
           *(uint4 *)(to + (((2 * ks_j + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
         }
       }
       if (j + 1 < steps) load_k(j + 1);
+      const bool ends = tail && j + 1 == steps;  // the tile's last block is the partial one
+      const int tail_at = (tile.nb - 1) % kRwBlocks * kBlock;
+      if (ends) {
+        __syncwarp();  // over the zeros of the rows' own warp
+        if (pw == tail_at / 32) {
+#pragma unroll 1
+          for (int r = 0; r < tail_rows; ++r) {
+            const int row = tail_at + r, d = 4 * lane;
+            const uint2 x = *(const uint2 *)(k_tail + r * kHeadDim + d);
+            const uint32_t h0 = h2_bits(__floats2half2_rn(__uint_as_float(x.x << 16) * kf, __uint_as_float(x.x & 0xffff0000u) * kf));
+            const uint32_t h1 = h2_bits(__floats2half2_rn(__uint_as_float(x.y << 16) * kf, __uint_as_float(x.y & 0xffff0000u) * kf));
+            *(uint2 *)(kt + (d >> 6) * kRwHalf + row * 128 + ((((d & 63) >> 3) ^ (row & 7)) << 4) + (d & 7) * 2) = make_uint2(h0, h1);
+          }
+        }
+      }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
@@ -320,8 +352,6 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
       }
       if (!rows_wait_warp(&sy.vempty[st], ((j >> 1) & 1) ^ 1, &abort_s)) break;
       {
-        const int u = j * kRwBlocks + (tc >> 1);
-        const bool in_tail = tail && u < tile.nb && tile.block(u) == full;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint32_t w[8];
@@ -333,16 +363,6 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
 #pragma unroll
             for (int m = 0; m < 4; ++m) codes_across<CODE>(w[2 * m], w[2 * m + 1], h, x[m], y[m]);
             const int d = 16 * dc + 4 * e + 2 * h;
-            if (in_tail) {
-#pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                const int row = 8 * (tc & 1) + 2 * m;
-                const uint32_t p = row < tail_rows ? *(const uint32_t *)(v_tail + row * kHeadDim + d) : 0u;
-                const uint32_t q = row + 1 < tail_rows ? *(const uint32_t *)(v_tail + (row + 1) * kHeadDim + d) : 0u;
-                x[m] = h2_bits(__floats2half2_rn(__uint_as_float(p << 16) * vf, __uint_as_float(q << 16) * vf));
-                y[m] = h2_bits(__floats2half2_rn(__uint_as_float(p & 0xffff0000u) * vf, __uint_as_float(q & 0xffff0000u) * vf));
-              }
-            }
             unsigned char *to = vt + (tc >> 3) * kRwHalf + d * 128;
             *(uint4 *)(to + (((tc & 7) ^ (d & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
             *(uint4 *)(to + 128 + (((tc & 7) ^ ((d + 1) & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
@@ -350,6 +370,21 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
         }
       }
       if (j + 1 < steps) load_v(j + 1);
+      if (ends && (tc >> 1) == tail_at / kBlock) {  // this thread's 8 tokens and 16 values of d
+#pragma unroll 1
+        for (int e = 0; e < 16; ++e) {
+          const int d = 16 * dc + e, first = 8 * (tc & 1);
+          uint32_t x[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const int row = first + 2 * m;
+            const float lo = row < tail_rows ? bf16_bits_to_f32(v_tail[row * kHeadDim + d]) : 0.f;
+            const float hi = row + 1 < tail_rows ? bf16_bits_to_f32(v_tail[(row + 1) * kHeadDim + d]) : 0.f;
+            x[m] = h2_bits(__floats2half2_rn(lo * vf, hi * vf));
+          }
+          *(uint4 *)(vt + (tc >> 3) * kRwHalf + d * 128 + (((tc & 7) ^ (d & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+      }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) bar_arrive(&sy.vfull[st]);
@@ -418,7 +453,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
     const int pmin = tile.len - tile.cnt + q0 / a.group;
     const int pmax = tile.len - tile.cnt + min((min(q0 + kRwRows, R) - 1) / a.group, tile.cnt - 1);
     const int open0 = a.window > 0 ? max(0, pmax - a.window + kBlock) / kBlock : 0, open1 = (pmin + 1) / kBlock;
-    float ref = 0.f, l = 0.f, limit = -INFINITY;
+    float ref = 0.f, l = 0.f, limit = valid ? -1.f : INFINITY;  // limit: of a block's sum of weights
     bool seen = !valid;
     bool ok = true;
     for (int j = 0; ok && j < steps; ++j) {
@@ -428,83 +463,134 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
       // units of the tile that every row sees as a whole
       const int u0 = j * kRwBlocks, b_first = tile.block(u0), b_last = tile.block(u0 + kRwBlocks - 1);
       const bool open = u0 + kRwBlocks <= tile.nb && b_first >= open0 && b_last < open1;
-      uint32_t p[64];
-      float sum;
+      float sum = 0.f;
+      uint32_t r[32];
+      tmem_ld32(s_at, r);
+      // two blocks at a time: scores become weights, over the columns of
+      // blocks that have been read
 #pragma unroll 1
-      for (int round = 0;; ++round) {
-        float far = -INFINITY;
-        sum = 0.f;
-        uint32_t ra[16], rb[16];
-        auto block = [&](const uint32_t(&r)[16], int b) {
-          const float4 sc = scales[j & 3][b];
-          const float f = rc * sc.x, at = sc.y - ref;
-          float2 y[8];
+      for (int b = 0; b < kRwBlocks; b += 2) {
+        const float4 sc0 = scales[j & 3][b], sc1 = scales[j & 3][b + 1];
+        // what a token of block b or b + 1 has to be for this row to see it
+        int hi[2] = {}, lo[2] = {}, si[2] = {};
+        auto see = [&](int e) { return (e & 15) <= hi[e >> 4] && ((e & 15) > lo[e >> 4] || (e & 15) < si[e >> 4]); };
+        if (!open) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            y[e] = fma_2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), make_float2(f, f), make_float2(at, at));
-          if (!open) {
-            const int u = u0 + b, tok = tile.block(u) * kBlock;
-            const int hi = u < tile.nb ? pos - tok : -1;                           // tokens up to it
-            const int lo = a.window > 0 ? pos - a.window - tok : -1;               // and above it, or
-            const int si = a.sinks - tok;                                          // below it
+          for (int k = 0; k < 2; ++k) {
+            const int u = u0 + b + k, tok = tile.block(u) * kBlock;
+            hi[k] = u < tile.nb ? pos - tok : -1;                     // up to it,
+            lo[k] = a.window > 0 ? pos - a.window - tok : -1;         // and above it
+            si[k] = a.sinks - tok;                                    // or below it
+          }
+        }
+        float y[32];
+        tmem_wait32(r);
+        {
+          const float f0 = rc * sc0.x, at0 = sc0.y - ref, f1 = rc * sc1.x, at1 = sc1.y - ref;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const bool see = e <= hi && (e > lo || e < si);
-              if (!see) (e & 1 ? y[e >> 1].y : y[e >> 1].x) = -INFINITY;
+          for (int e = 0; e < 32; e += 2) {
+            const float f = e < 16 ? f0 : f1, at = e < 16 ? at0 : at1;
+            const float2 z = fma_2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), make_float2(f, f), make_float2(at, at));
+            y[e] = z.x;
+            y[e + 1] = z.y;
+          }
+        }
+        if (b + 2 < kRwBlocks) tmem_ld32(s_at + 16 * (b + 2), r);
+        if (!open) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!see(e)) y[e] = -INFINITY;
+        }
+        float t[2];
+        auto weigh = [&]() {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = ex2(y[e]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float2 z = make_float2(y[16 * k], y[16 * k + 1]), z2 = make_float2(y[16 * k + 2], y[16 * k + 3]);
+#pragma unroll
+            for (int e = 4; e < 16; e += 4) {
+              z = add_2(z, make_float2(y[16 * k + e], y[16 * k + e + 1]));
+              z2 = add_2(z2, make_float2(y[16 * k + e + 2], y[16 * k + e + 3]));
             }
+            z = add_2(z, z2);
+            t[k] = z.x + z.y;
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) far = max_3(far, y[e].x, y[e].y);
-          float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            y[e].x = ex2(y[e].x);
-            y[e].y = ex2(y[e].y);
-            s = e ? add_2(s, y[e]) : y[e];
-            p[8 * b + e] = h2_bits(__floats2half2_rn(y[e].x, y[e].y));
-          }
-          sum = __fmaf_rn(s.x + s.y, sc.z, sum);
         };
-        tmem_ld16(s_at, ra);
+        weigh();
+        // a weight is at most its block's sum: below the limit none leaves fp16's range
+        if (__any_sync(0xffffffffu, !(fmaxf(t[0], t[1]) <= limit))) {
+          // references move: kPShift below a row's largest y, up only once there is one
+          float far = -INFINITY;
+          auto again = [&](int c, uint32_t(&x)[8]) {  // y of columns 8 c.. of the two blocks, from the scores
+            tmem_ld8(s_at + 16 * b + 8 * c, x);
+            const float4 sc = scales[j & 3][b + (c >> 1)];
+            const float f = rc * sc.x, at = sc.y - ref;
 #pragma unroll
-        for (int b = 0; b < kRwBlocks; b += 2) {
-          tmem_wait16(ra);
-          tmem_ld16(s_at + 16 * (b + 1), rb);
-          block(ra, b);
-          tmem_wait16(rb);
-          if (b + 2 < kRwBlocks) tmem_ld16(s_at + 16 * (b + 2), ra);
-          block(rb, b + 1);
-        }
-        // (a third round would mean scores beyond what fp32 tells apart)
-        if (!__any_sync(0xffffffffu, far > limit) || round == 2) break;
-        // the references move (kPShift below a row's largest y, up only once
-        // there is one), then the weights are taken again
-        float by = far - kPShift;
-        if (seen ? by < 0.f : far == -INFINITY) by = 0.f;
-        const float k = seen ? exp2f(-by) : 1.f;
-        seen |= far > -INFINITY;
-        limit = seen ? kPShift + kSlack : -INFINITY;
-        ref += by;
-        l *= k;
-        if (j > 0 && __any_sync(0xffffffffu, k != 1.f)) {
-          ok = rows_wait_warp(&sy.odone[w], (j - 1) & 1, &abort_s);
-          if (!ok) break;
-          tmem_after();
-#pragma unroll 1
-          for (int d = 0; d < kHeadDim; d += 16) {
-            tmem_ld16(o_at + d, ra);
-            tmem_wait16(ra);
+            for (int e = 0; e < 8; ++e) {
+              const float v = __fmaf_rn(__uint_as_float(x[e]), f, at);
+              x[e] = __float_as_uint(open || ((8 * (c & 1) + e) <= hi[c >> 1] && ((8 * (c & 1) + e) > lo[c >> 1] || (8 * (c & 1) + e) < si[c >> 1]))
+                                         ? v : -INFINITY);
+            }
+          };
 #pragma unroll
-            for (int e = 0; e < 16; ++e) ra[e] = __float_as_uint(__uint_as_float(ra[e]) * k);
-            tmem_st16(o_at + d, ra);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[8];
+            again(c, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) far = fmaxf(far, __uint_as_float(x[e]));
           }
-          tmem_wait_st();
+          float by = far - kPShift;
+          if (seen ? by < 0.f : far == -INFINITY) by = 0.f;
+          const float k = seen ? exp2f(-by) : 1.f;
+          seen |= far > -INFINITY;
+          limit = seen ? 0x1p15f : -1.f;
+          ref += by;
+          l *= k;
+          sum *= k;
+          if (__any_sync(0xffffffffu, k != 1.f)) {
+            // what is in tensor memory: this tile's weights so far, and O
+            tmem_wait_st();
+            const __half2 kh = __float2half2_rn(k);
+#pragma unroll 1
+            for (int d = 0; d < 8 * b; d += 8) {
+              uint32_t x[8];
+              tmem_ld8(s_at + d, x);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = h2_bits(__hmul2(*(const __half2 *)&x[e], kh));
+              tmem_st8(s_at + d, x);
+            }
+            if (j > 0) {
+              ok &= rows_wait_warp(&sy.odone[w], (j - 1) & 1, &abort_s);
+              tmem_after();
+#pragma unroll 1
+              for (int d = 0; d < kHeadDim; d += 8) {
+                uint32_t x[8];
+                tmem_ld8(o_at + d, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * k);
+                tmem_st8(o_at + d, x);
+              }
+            }
+            tmem_wait_st();
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[8];
+            again(c, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[8 * c + e] = __uint_as_float(x[e]);
+          }
+          weigh();
         }
+        sum = __fmaf_rn(t[0], sc0.z, __fmaf_rn(t[1], sc1.z, sum));
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[e] = h2_bits(__floats2half2_rn(y[2 * e], y[2 * e + 1]));
+        tmem_st16(s_at + 8 * b, p);
       }
       if (!ok) break;
       l += sum;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_st16(s_at + 16 * i, p + 16 * i);
       tmem_wait_st();
       tmem_before();
       __syncwarp();

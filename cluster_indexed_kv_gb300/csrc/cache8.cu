@@ -36,13 +36,11 @@ bool overlaps_cache8(const lkv_cache8 *c, const void *p, int64_t bytes) {
 
 // ---------------------------------------------------------------- write
 
-// The code of x in a block of largest magnitude amax, decided exactly where
-// the fp32 quotient lies within its own error of the halfway point between
-// two codes: the sign of top * |x| - halfway * amax, both products taken with
-// their rounding errors (24-bit by 9-bit significands: an error has at most
-// 9 bits and the difference of two at most 11, so the sum below has the exact
-// sign). fp64 would do too, at a sixty-fourth of the rate; bf16 inputs sit
-// exactly halfway often enough (one value in 600) for that to show.
+// The sign of top * a - half * amax, both products taken with their rounding
+// errors (24-bit by 9-bit significands: an error has at most 9 bits and the
+// difference of two at most 11, so the sum below has the exact sign). fp64
+// would do too, at a sixty-fourth of the rate; bf16 inputs sit exactly halfway
+// often enough (one value in 600) for that to show.
 __device__ __forceinline__ float halfway_sign(float top, float a, float half, float amax) {
   const float p = top * a, r = half * amax;
   return (p - r) + (__fmaf_rn(top, a, -p) - __fmaf_rn(half, amax, -r));
@@ -59,11 +57,11 @@ __device__ __forceinline__ uint32_t int8_exact(float x, float inv, float amax) {
 __device__ __forceinline__ float e4m3_exact(float x, float inv, float amax) {
   const float a = fabsf(x), q = a * inv;
   // step of the code's binade: 2^(e - 3), 2^-9 below 2^-6
-  const float step = q < 0x1p-6f ? 0x1p-9f : __uint_as_float((__float_as_uint(q) & 0x7f800000u) - (3u << 23));
-  const float m = rintf(q / step - 0.5f);
-  const float d = halfway_sign(448.f, a, (m + 0.5f) * step, amax);
+  const uint32_t step = q < 0x1p-6f ? (127u - 9u) << 23 : (__float_as_uint(q) & 0x7f800000u) - (3u << 23);
+  const float m = rintf(__fmaf_rn(q, __uint_as_float((254u << 23) - step), -0.5f));
+  const float d = halfway_sign(448.f, a, (m + 0.5f) * __uint_as_float(step), amax);
   const bool up = d > 0.f || (d == 0.f && ((int)m & 1));
-  return copysignf((up ? m + 1.f : m) * step, x);
+  return copysignf((up ? m + 1.f : m) * __uint_as_float(step), x);
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -72,11 +70,32 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Four codes of x[0..3] in one word; inv is 127 / amax or 448 / amax, rounded.
-// x * inv is off by at most 2 units in its last place; where that could
-// change a code, the lane settles its four exactly.
+// The codes of x[0..3] in a block of largest magnitude amax, decided exactly.
+// Magnitudes far from 1 are scaled by a power of two first (exactly, but for
+// values whose code is 0): no product overflows or loses bits.
 template <int CODE>
-__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv, float amax) {
+__device__ __noinline__ uint32_t settle4(float x0, float x1, float x2, float x3, float amax) {
+  const float f = amax < 0x1p-60f ? 0x1p100f : amax > 0x1p60f ? 0x1p-60f : 1.f;
+  const float x[4] = {x0 * f, x1 * f, x2 * f, x3 * f};
+  amax *= f;
+  if constexpr (CODE == LKV_CODE_INT8) {
+    const float inv = __fdiv_rn(127.f, amax);
+    uint32_t r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = int8_exact(x[e], inv, amax);
+    return __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
+  } else {
+    const float inv = __fdiv_rn(448.f, amax);
+    return e4m3x2(e4m3_exact(x[0], inv, amax), e4m3_exact(x[1], inv, amax)) |
+           (e4m3x2(e4m3_exact(x[2], inv, amax), e4m3_exact(x[3], inv, amax)) << 16);
+  }
+}
+
+// Four codes in one word; inv is 127 / amax or 448 / amax, rounded. x * inv is
+// off by at most 2 units in its last place; where that could change a code, or
+// always (`settle`), the lane settles its four exactly.
+template <int CODE>
+__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv, float amax, bool settle) {
   if constexpr (CODE == LKV_CODE_INT8) {
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: a sum's low bits are the rounded integer
     float far = 0.f;
@@ -87,10 +106,8 @@ __device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv, float
       r[e] = __float_as_uint(s);
       far = fmaxf(far, fabsf(__fmaf_rn(x[e], inv, kMagic - s)));
     }
-    if (far > 0.5f - 0x1p-14f) {  // |x * inv| < 128 is off by less than 2^-15
-#pragma unroll
-      for (int e = 0; e < 4; ++e) r[e] = int8_exact(x[e], inv, amax);
-    }
+    // |x * inv| < 128 is off by less than 2^-15
+    if (far > 0.5f - 0x1p-14f || settle) return settle4<CODE>(x[0], x[1], x[2], x[3], amax);
     return __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
   } else {
     float q[4];
@@ -103,10 +120,7 @@ __device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv, float
       small = min(small, u - 1u);                                      // zero wraps to the top
     }
     // below 2^-6 the codes are evenly spaced: settled exactly too
-    if (near <= 8u || small < 0x3c800000u) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) q[e] = e4m3_exact(x[e], inv, amax);
-    }
+    if (near <= 8u || small < 0x3c800000u || settle) return settle4<CODE>(x[0], x[1], x[2], x[3], amax);
     return e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
   }
 }
@@ -156,29 +170,29 @@ struct BlockWriter {
     return (w & 0x7fffffffu) > 0x7f800000u ? 0u : (w & 0x80000000u) | 0x7f7fffffu;
   }
 
-  static __device__ __forceinline__ void values4(const uint4 &w, int h, float f, float (&x)[4]) {
+  static __device__ __forceinline__ void values4(const uint4 &w, int h, float (&x)[4]) {
     if (DT == 1) {
       const uint32_t a = h ? w.z : w.x, b = h ? w.w : w.y;
-      x[0] = __uint_as_float(a << 16) * f; x[1] = __uint_as_float(a & 0xffff0000u) * f;
-      x[2] = __uint_as_float(b << 16) * f; x[3] = __uint_as_float(b & 0xffff0000u) * f;
+      x[0] = __uint_as_float(a << 16); x[1] = __uint_as_float(a & 0xffff0000u);
+      x[2] = __uint_as_float(b << 16); x[3] = __uint_as_float(b & 0xffff0000u);
     } else {
-      x[0] = __uint_as_float(w.x) * f; x[1] = __uint_as_float(w.y) * f;
-      x[2] = __uint_as_float(w.z) * f; x[3] = __uint_as_float(w.w) * f;
+      x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y);
+      x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
     }
   }
 
-  __device__ __forceinline__ void put(const uint4 (&w)[NL], int64_t block, float inv, float amax, float f) const {
-    const int64_t at = (block * kBlock + lane / LPR) * kHeadDim + (lane % LPR) * E;
+  __device__ __forceinline__ void put(const uint4 (&w)[NL], int64_t block, float inv, float amax, bool settle) const {
+    uint8_t *to = codes + (block * kBlock + lane / LPR) * kHeadDim + (lane % LPR) * E;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       float x[4];
-      values4(w[i], 0, f, x);
-      const uint32_t c0 = codes4<CODE>(x, inv, amax);
+      values4(w[i], 0, x);
+      const uint32_t c0 = codes4<CODE>(x, inv, amax, settle);
       if constexpr (DT == 1) {
-        values4(w[i], 1, f, x);
-        *(uint2 *)(codes + at + (int64_t)i * RPL * kHeadDim) = make_uint2(c0, codes4<CODE>(x, inv, amax));
+        values4(w[i], 1, x);
+        *(uint2 *)(to + i * RPL * kHeadDim) = make_uint2(c0, codes4<CODE>(x, inv, amax, settle));
       } else {
-        *(uint32_t *)(codes + at + (int64_t)i * RPL * kHeadDim) = c0;
+        *(uint32_t *)(to + i * RPL * kHeadDim) = c0;
       }
     }
   }
@@ -203,13 +217,8 @@ struct BlockWriter {
     }
     constexpr float kTop = CODE == LKV_CODE_INT8 ? 127.f : 448.f;
     if (p0 + kBlock <= end) {
-      if (amax >= 0x1p-80f && amax <= 0x1p100f) {
-        put(w, j, __fdiv_rn(kTop, amax), amax, 1.f);
-      } else if (amax > 0.f) {
-        // scaled by a power of two (exactly, but for values whose code is 0):
-        // products with kTop and 1 / amax neither overflow nor lose bits
-        const float f = amax < 1.f ? 0x1p126f : 0x1p-32f;
-        put(w, j, __fdiv_rn(kTop, amax * f), amax * f, f);
+      if (amax > 0.f) {
+        put(w, j, __fdiv_rn(kTop, amax), amax, amax < 0x1p-110f);  // kTop / amax may overflow
       } else {
         uint4 *to = (uint4 *)(codes + (int64_t)j * kBlock * kHeadDim);
 #pragma unroll
@@ -250,7 +259,7 @@ struct WriteArgs {
 //
 // Bound: bytes (2 or 4 in, 1 out a value).
 template <int DT, int CODE>
-__global__ void __launch_bounds__(kCacheThreads) k_cache8_write(const __grid_constant__ WriteArgs a) {
+__global__ void __launch_bounds__(kCacheThreads, DT == 1 ? 6 : 3) k_cache8_write(const __grid_constant__ WriteArgs a) {
   const int64_t task = (int64_t)blockIdx.x * kCacheWarps + threadIdx.x / 32;
   if (task >= a.tasks) return;
   const lkv_cache8 &c = a.c;

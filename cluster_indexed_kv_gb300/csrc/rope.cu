@@ -7,11 +7,12 @@
 
 namespace lkv {
 
-// A thread turns V pairs (2 V values) of one token's row, or copies 2 V of
-// the values that do not rotate, for a run of heads: the sines and cosines of
-// its pairs are the same for every head of the token, so it takes them once.
-// V = 8 (16-byte vectors in both layouts) needs rotary_dim % 16 == 0; V = 1
-// takes every other even size.
+// A thread turns the pairs of one or two 16-byte vectors of one token's row
+// (two where the pairs lie rotary_dim / 2 apart, one where they are
+// neighbours), or copies values that do not rotate, for a run of heads: the
+// sines and cosines of its pairs are the same for every head of the token, so
+// it takes them once. Sizes whose pairs do not fill whole vectors go pair by
+// pair (WIDE = 0).
 //
 // The angle of pair i at position p is p * turn[i] turns. turn[i] is held in
 // units of 2^-64, so the product modulo 2^64 is the exact fraction of a turn,
@@ -23,44 +24,6 @@ namespace lkv {
 // Bound: the tensors' bytes, once in and once out.
 constexpr int kRopeThreads = 128;
 
-template <int DT, int N>
-struct Vals {
-  float x[N];
-  __device__ __forceinline__ void load(const void *base, int64_t i) {
-    if constexpr (N == 1) {
-      x[0] = load_elem<DT>(base, i);
-    } else if constexpr (DT == 1) {
-      const uint4 w = *(const uint4 *)((const uint16_t *)base + i);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[2 * e] = __uint_as_float(u[e] << 16);
-        x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int h = 0; h < N / 4; ++h) {
-        const float4 w = *(const float4 *)((const float *)base + i + 4 * h);
-        x[4 * h] = w.x; x[4 * h + 1] = w.y; x[4 * h + 2] = w.z; x[4 * h + 3] = w.w;
-      }
-    }
-  }
-  __device__ __forceinline__ void store(void *base, int64_t i) const {
-    if constexpr (N == 1) {
-      store_elem<DT>(base, i, x[0]);
-    } else if constexpr (DT == 1) {
-      uint4 w;
-      w.x = pack_bf16(x[0], x[1]); w.y = pack_bf16(x[2], x[3]);
-      w.z = pack_bf16(x[4], x[5]); w.w = pack_bf16(x[6], x[7]);
-      *(uint4 *)((uint16_t *)base + i) = w;
-    } else {
-#pragma unroll
-      for (int h = 0; h < N / 4; ++h)
-        *(float4 *)((float *)base + i + 4 * h) = make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
-    }
-  }
-};
-
 struct RopeArgs {
   lkv_rope r;
   const void *q, *k;
@@ -71,91 +34,137 @@ struct RopeArgs {
   int64_t tokens;    // B * n
 };
 
-template <int DT, int INTER, int V>
+// A thread's piece of a row: V values at o1 and, for NV = 2, at o2.
+template <int DT, int INTER, int WIDE>
+struct RopePiece {
+  static constexpr int V = !WIDE ? 1 : DT == 1 ? 8 : 4;
+  static constexpr int NV = WIDE && INTER ? 1 : 2;
+  static constexpr int PAIRS = V * NV / 2;
+  static constexpr int TPR = kHeadDim / (V * NV);   // threads of a row
+  static constexpr int HB = WIDE ? 8 / NV : 4;      // heads whose loads are in flight together
+  float c[PAIRS], s[PAIRS];
+  int o1, o2;
+  bool rot;
+
+  struct Raw { uint4 w[NV]; float f[2]; };
+  __device__ __forceinline__ void load(Raw &r, const void *row) const {
+    if constexpr (WIDE) {
+      r.w[0] = *(const uint4 *)((const char *)row + o1 * (DT == 1 ? 2 : 4));
+      if constexpr (NV == 2) r.w[NV - 1] = *(const uint4 *)((const char *)row + o2 * (DT == 1 ? 2 : 4));
+    } else {
+      r.f[0] = load_elem<DT>(row, o1);
+      r.f[1] = load_elem<DT>(row, o2);
+    }
+  }
+  static __device__ __forceinline__ void unpack(const uint4 &w, float *x) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (DT == 1) {
+        x[2 * e] = __uint_as_float(u[e] << 16);
+        x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+      } else {
+        x[e] = __uint_as_float(u[e]);
+      }
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float *x) {
+    if constexpr (DT == 1)
+      return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    else
+      return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  }
+  __device__ __forceinline__ void turn(float &x1, float &x2, int e) const {
+    const float y = x1 * c[e] - x2 * s[e];
+    x2 = x2 * c[e] + x1 * s[e];
+    x1 = y;
+  }
+  __device__ __forceinline__ void store(const Raw &r, void *row) const {
+    if constexpr (WIDE) {
+      Raw o = r;
+      if (rot) {
+        float x[V * NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) unpack(r.w[v], x + v * V);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) turn(x[INTER ? 2 * e : e], x[INTER ? 2 * e + 1 : V * (NV - 1) + e], e);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) o.w[v] = pack(x + v * V);
+      }
+      *(uint4 *)((char *)row + o1 * (DT == 1 ? 2 : 4)) = o.w[0];
+      if constexpr (NV == 2) *(uint4 *)((char *)row + o2 * (DT == 1 ? 2 : 4)) = o.w[NV - 1];
+    } else {
+      float x1 = r.f[0], x2 = r.f[1];
+      if (rot) turn(x1, x2, 0);
+      store_elem<DT>(row, o1, x1);
+      store_elem<DT>(row, o2, x2);
+    }
+  }
+};
+
+template <int DT, int INTER, int WIDE>
 __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeArgs a) {
-  constexpr int TPR = 64 / V;  // threads of a row
-  constexpr int HB = DT == 1 ? 4 : 2;  // heads whose loads are in flight together
+  using P = RopePiece<DT, INTER, WIDE>;
   __shared__ uint64_t turn[64];
   if (threadIdx.x < 64) turn[threadIdx.x] = a.r.turn[threadIdx.x];
   __syncthreads();
   const int64_t id = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
-  const int64_t tok = id / TPR;
+  const int64_t tok = id / P::TPR;
   if (tok >= a.tokens) return;
-  const int t = (int)(id % TPR);
+  const int t = (int)(id % P::TPR);
   const int rd = a.r.rotary_dim, half = rd / 2;
   const int64_t b = tok / a.n, i = tok % a.n;
-  const bool rot = t * V < half;
-  float c[V], s[V];
-  int o1, o2;  // the two runs of V values
-  if (rot) {
+  P p;
+  p.rot = t * P::PAIRS < half;
+  if (INTER) {
+    p.o1 = t * P::V * P::NV;
+    p.o2 = p.o1 + P::V;
+  } else if (p.rot) {
+    p.o1 = t * P::V;
+    p.o2 = p.o1 + half;
+  } else {  // the rest of the row, in two halves too
+    p.o1 = rd + (t - half / P::V) * P::V;
+    p.o2 = p.o1 + (kHeadDim - rd) / 2;
+  }
+  if (p.rot) {
     const int64_t pos = a.positions[tok];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int32_t frac = (int32_t)(((uint64_t)pos * turn[t * V + e]) >> 32);
-      sincospif((float)frac * 0x1p-31f, &s[e], &c[e]);
-      s[e] *= a.r.gain;
-      c[e] *= a.r.gain;
-    }
-    o1 = INTER ? 2 * V * t : V * t;
-    o2 = INTER ? o1 + V : half + V * t;
-  } else {
-    o1 = rd + 2 * V * (t - half / V);
-    o2 = o1 + V;
-  }
-  const int h1 = min((int)(blockIdx.y + 1) * a.per, a.heads + a.kv_heads);
-  for (int h0 = (int)blockIdx.y * a.per; h0 < h1; h0 += HB) {
-    Vals<DT, V> x[HB], y[HB];
-    const void *src[HB];
-    void *dst[HB];
-    int64_t row[HB];
-#pragma unroll
-    for (int j = 0; j < HB; ++j) {
-      const int h = h0 + j;
-      if (h >= h1) break;
-      const bool isq = h < a.heads;
-      src[j] = isq ? a.q : a.k;
-      dst[j] = isq ? a.q_out : a.k_out;
-      row[j] = ((isq ? b * a.heads + h : b * a.kv_heads + (h - a.heads)) * a.n + i) * kHeadDim;
-      x[j].load(src[j], row[j] + o1);
-      y[j].load(src[j], row[j] + o2);
-    }
-#pragma unroll
-    for (int j = 0; j < HB; ++j) {
-      if (h0 + j >= h1) break;
-      if (rot) {
-        if constexpr (INTER && V > 1) {
-          // V consecutive pairs lie in x, then y
-#pragma unroll
-          for (int e = 0; e < V / 2; ++e) {
-            const float a0 = x[j].x[2 * e], a1 = x[j].x[2 * e + 1], b0 = y[j].x[2 * e], b1 = y[j].x[2 * e + 1];
-            x[j].x[2 * e] = a0 * c[e] - a1 * s[e];
-            x[j].x[2 * e + 1] = a1 * c[e] + a0 * s[e];
-            y[j].x[2 * e] = b0 * c[V / 2 + e] - b1 * s[V / 2 + e];
-            y[j].x[2 * e + 1] = b1 * c[V / 2 + e] + b0 * s[V / 2 + e];
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float x1 = x[j].x[e], x2 = y[j].x[e];
-            x[j].x[e] = x1 * c[e] - x2 * s[e];
-            y[j].x[e] = x2 * c[e] + x1 * s[e];
-          }
-        }
-      } else if (src[j] == dst[j]) {
-        continue;  // in place: nothing to copy
-      }
-      x[j].store(dst[j], row[j] + o1);
-      y[j].store(dst[j], row[j] + o2);
+    for (int e = 0; e < P::PAIRS; ++e) {
+      const int32_t frac = (int32_t)(((uint64_t)pos * turn[t * P::PAIRS + e]) >> 32);
+      sincospif((float)frac * 0x1p-31f, &p.s[e], &p.c[e]);
+      p.s[e] *= a.r.gain;
+      p.c[e] *= a.r.gain;
     }
   }
+  const int64_t step = (int64_t)a.n * kHeadDim * (DT == 1 ? 2 : 4);  // bytes from head to head
+  auto walk = [&](const void *in, void *out, int heads, int h0, int h1) {
+    if (!p.rot && in == out) return;  // in place: nothing to copy
+    const int64_t at = (b * heads + h0) * step + i * kHeadDim * (DT == 1 ? 2 : 4);
+    const char *src = (const char *)in + at;
+    char *dst = (char *)out + at;
+    for (int h = h0; h < h1; h += P::HB) {
+      typename P::Raw r[P::HB];
+#pragma unroll
+      for (int j = 0; j < P::HB; ++j)
+        if (h + j < h1) p.load(r[j], src + j * step);
+#pragma unroll
+      for (int j = 0; j < P::HB; ++j)
+        if (h + j < h1) p.store(r[j], dst + j * step);
+      src += P::HB * step;
+      dst += P::HB * step;
+    }
+  };
+  const int g0 = (int)blockIdx.y * a.per, g1 = min(g0 + a.per, a.heads + a.kv_heads);
+  if (g0 < a.heads) walk(a.q, a.q_out, a.heads, g0, min(g1, a.heads));
+  if (g1 > a.heads) walk(a.k, a.k_out, a.kv_heads, max(g0, a.heads) - a.heads, g1 - a.heads);
 }
 
-template <int DT, int INTER, int V>
+template <int DT, int INTER, int WIDE>
 static cudaError_t launch_rope(RopeArgs &a, cudaStream_t st) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const int64_t threads = a.tokens * (64 / V);
+  const int64_t threads = a.tokens * RopePiece<DT, INTER, WIDE>::TPR;
   const int64_t blocks = (threads + kRopeThreads - 1) / kRopeThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   // few tokens: the heads are split over CTAs until the GPU is filled once
@@ -164,7 +173,7 @@ static cudaError_t launch_rope(RopeArgs &a, cudaStream_t st) {
   a.per = (int)((all + want - 1) / want);
   const int gy = (all + a.per - 1) / a.per;
   if (gy > 65535) return cudaErrorInvalidValue;
-  k_rope<DT, INTER, V><<<dim3((unsigned)blocks, (unsigned)gy), kRopeThreads, 0, st>>>(a);
+  k_rope<DT, INTER, WIDE><<<dim3((unsigned)blocks, (unsigned)gy), kRopeThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -247,11 +256,12 @@ extern "C" lkv_status lkv_rope_apply(const lkv_rope *rope, int32_t dtype, int32_
   a.tokens = tokens;
   cudaStream_t st = (cudaStream_t)stream;
   const bool bf = dtype == LKV_DTYPE_BF16, in = rope->layout == LKV_ROPE_INTERLEAVED;
-  const bool wide = rope->rotary_dim % 16 == 0;
+  // whether the pairs fill whole 16-byte vectors
+  const bool wide = rope->rotary_dim % ((bf ? 8 : 4) * (in ? 1 : 2)) == 0;
   cudaError_t e;
-  if (bf) e = in ? (wide ? launch_rope<1, 1, 8>(a, st) : launch_rope<1, 1, 1>(a, st))
-                 : (wide ? launch_rope<1, 0, 8>(a, st) : launch_rope<1, 0, 1>(a, st));
-  else e = in ? (wide ? launch_rope<0, 1, 8>(a, st) : launch_rope<0, 1, 1>(a, st))
-              : (wide ? launch_rope<0, 0, 8>(a, st) : launch_rope<0, 0, 1>(a, st));
+  if (bf) e = in ? (wide ? launch_rope<1, 1, 1>(a, st) : launch_rope<1, 1, 0>(a, st))
+                 : (wide ? launch_rope<1, 0, 1>(a, st) : launch_rope<1, 0, 0>(a, st));
+  else e = in ? (wide ? launch_rope<0, 1, 1>(a, st) : launch_rope<0, 1, 0>(a, st))
+              : (wide ? launch_rope<0, 0, 1>(a, st) : launch_rope<0, 0, 0>(a, st));
   return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_rope_apply", e);
 }
