@@ -36,30 +36,36 @@ bool overlaps_cache8(const lkv_cache8 *c, const void *p, int64_t bytes) {
 
 // ---------------------------------------------------------------- write
 
-// The sign of top * a - half * amax, both products taken with their rounding
-// errors (24-bit by 9-bit significands: an error has at most 9 bits and the
-// difference of two at most 11, so the sum below has the exact sign). fp64
-// would do too, at a sixty-fourth of the rate; bf16 inputs sit exactly halfway
-// often enough (one value in 600) for that to show.
+// The sign of top * a - half * amax. bf16 values: both products are exact
+// (8-bit by 9-bit significands). fp32 values: the products are taken with
+// their rounding errors (24-bit by 9-bit significands: an error has at most 9
+// bits and the difference of two at most 11, so the sum has the exact sign).
+// fp64 would do too, at a sixty-fourth of the rate; bf16 inputs sit exactly
+// halfway often enough (one value in 600) for that to show.
+template <int DT>
 __device__ __forceinline__ float halfway_sign(float top, float a, float half, float amax) {
-  const float p = top * a, r = half * amax;
+  const float p = top * a;
+  if (DT == 1) return __fmaf_rn(-half, amax, p);
+  const float r = half * amax;
   return (p - r) + (__fmaf_rn(top, a, -p) - __fmaf_rn(half, amax, -r));
 }
 
+template <int DT>
 __device__ __forceinline__ uint32_t int8_exact(float x, float inv, float amax) {
   const float a = fabsf(x);
   const float m = rintf(__fmaf_rn(a, inv, -0.5f));  // the halfway point is m + 1/2
-  const float d = halfway_sign(254.f, a, 2.f * m + 1.f, amax);
+  const float d = halfway_sign<DT>(254.f, a, 2.f * m + 1.f, amax);
   const int k = (int)m, up = d > 0.f || (d == 0.f && (k & 1));
   return (uint32_t)(x < 0.f ? -(k + up) : k + up);
 }
 
+template <int DT>
 __device__ __forceinline__ float e4m3_exact(float x, float inv, float amax) {
   const float a = fabsf(x), q = a * inv;
   // step of the code's binade: 2^(e - 3), 2^-9 below 2^-6
   const uint32_t step = q < 0x1p-6f ? (127u - 9u) << 23 : (__float_as_uint(q) & 0x7f800000u) - (3u << 23);
   const float m = rintf(__fmaf_rn(q, __uint_as_float((254u << 23) - step), -0.5f));
-  const float d = halfway_sign(448.f, a, (m + 0.5f) * __uint_as_float(step), amax);
+  const float d = halfway_sign<DT>(448.f, a, (m + 0.5f) * __uint_as_float(step), amax);
   const bool up = d > 0.f || (d == 0.f && ((int)m & 1));
   return copysignf((up ? m + 1.f : m) * __uint_as_float(step), x);
 }
@@ -70,58 +76,92 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// The codes of x[0..3] in a block of largest magnitude amax, decided exactly.
-// Magnitudes far from 1 are scaled by a power of two first (exactly, but for
-// values whose code is 0): no product overflows or loses bits.
-template <int CODE>
-__device__ __noinline__ uint32_t settle4(float x0, float x1, float x2, float x3, float amax) {
-  const float f = amax < 0x1p-60f ? 0x1p100f : amax > 0x1p60f ? 0x1p-60f : 1.f;
-  const float x[4] = {x0 * f, x1 * f, x2 * f, x3 * f};
-  amax *= f;
-  if constexpr (CODE == LKV_CODE_INT8) {
-    const float inv = __fdiv_rn(127.f, amax);
-    uint32_t r[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = int8_exact(x[e], inv, amax);
-    return __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
-  } else {
-    const float inv = __fdiv_rn(448.f, amax);
-    return e4m3x2(e4m3_exact(x[0], inv, amax), e4m3_exact(x[1], inv, amax)) |
-           (e4m3x2(e4m3_exact(x[2], inv, amax), e4m3_exact(x[3], inv, amax)) << 16);
-  }
+__device__ __forceinline__ uint32_t pack_low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// Four codes in one word; inv is 127 / amax or 448 / amax, rounded. x * inv is
-// off by at most 2 units in its last place; where that could change a code, or
-// always (`settle`), the lane settles its four exactly.
-template <int CODE>
-__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv, float amax, bool settle) {
-  if constexpr (CODE == LKV_CODE_INT8) {
-    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: a sum's low bits are the rounded integer
-    float far = 0.f;
-    uint32_t r[4];
+// The codes of x[0..3] in a block of largest magnitude amax, decided exactly;
+// inv is 127 / amax or 448 / amax, rounded.
+template <int DT, int CODE>
+__device__ __noinline__ uint32_t settle4(float x0, float x1, float x2, float x3, float inv, float amax) {
+  if constexpr (CODE == LKV_CODE_INT8)
+    return pack_low_bytes(int8_exact<DT>(x0, inv, amax), int8_exact<DT>(x1, inv, amax), int8_exact<DT>(x2, inv, amax),
+                          int8_exact<DT>(x3, inv, amax));
+  else
+    return e4m3x2(e4m3_exact<DT>(x0, inv, amax), e4m3_exact<DT>(x1, inv, amax)) |
+           (e4m3x2(e4m3_exact<DT>(x2, inv, amax), e4m3_exact<DT>(x3, inv, amax)) << 16);
+}
+
+// The same for magnitudes far from 1, scaled by a power of two (exactly, but
+// for values whose code is 0): no product overflows or loses bits.
+template <int DT, int CODE>
+__device__ __noinline__ uint32_t settle4_scaled(float x0, float x1, float x2, float x3, float amax) {
+  const float f = amax < 1.f ? 0x1p100f : 0x1p-60f;
+  return settle4<DT, CODE>(x0 * f, x1 * f, x2 * f, x3 * f, __fdiv_rn(CODE == LKV_CODE_INT8 ? 127.f : 448.f, amax * f), amax * f);
+}
+
+// Codes of N values, four in a word; inv is 127 / amax or 448 / amax, rounded.
+// x * inv is off by at most 2 units in its last place; where that could change
+// a code the lane decides exactly, as it does everywhere in blocks far from 1.
+template <int DT, int CODE, int N>
+__device__ __forceinline__ void codes(const float (&x)[N], float inv, float amax, bool far_from_one, uint32_t (&out)[N / 4]) {
+  bool settle = false;
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: a sum's low bits are the rounded integer
+  if constexpr (CODE == LKV_CODE_INT8 && DT == 1) {
+    // the remainder 127 x - k amax is exact (16 bits each): halfway or wrong if
+    // it is amax / 2 or more
+    float top = 0.f;
+    float s[N], r[N];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < N; ++e) {
+      s[e] = __fmaf_rn(x[e], inv, kMagic);
+      r[e] = __fmaf_rn(kMagic - s[e], amax, 127.f * x[e]);
+      top = fmaxf(top, fabsf(r[e]));
+    }
+    if (2.f * top >= amax) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const bool odd = __float_as_uint(s[e]) & 1u;
+        if (2.f * fabsf(r[e]) > amax || (2.f * fabsf(r[e]) == amax && odd)) s[e] += copysignf(1.f, r[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < N / 4; ++e)
+      out[e] = pack_low_bytes(__float_as_uint(s[4 * e]), __float_as_uint(s[4 * e + 1]), __float_as_uint(s[4 * e + 2]), __float_as_uint(s[4 * e + 3]));
+  } else if constexpr (CODE == LKV_CODE_INT8) {
+    float far = 0.f;
+    uint32_t r[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
       const float s = __fmaf_rn(x[e], inv, kMagic);
       r[e] = __float_as_uint(s);
       far = fmaxf(far, fabsf(__fmaf_rn(x[e], inv, kMagic - s)));
     }
-    // |x * inv| < 128 is off by less than 2^-15
-    if (far > 0.5f - 0x1p-14f || settle) return settle4<CODE>(x[0], x[1], x[2], x[3], amax);
-    return __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
+#pragma unroll
+    for (int e = 0; e < N / 4; ++e) out[e] = pack_low_bytes(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+    settle = far > 0.5f - 0x1p-14f;  // |x * inv| < 128 is off by less than 2^-15
   } else {
-    float q[4];
     uint32_t near = 0xffffffffu, small = 0xffffffffu;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      q[e] = x[e] * inv;
-      const uint32_t u = __float_as_uint(q[e]) & 0x7fffffffu;
-      near = min(near, (uint32_t)abs((int)(u & 0xfffffu) - 0x80000));  // the 20 bits behind a code
-      small = min(small, u - 1u);                                      // zero wraps to the top
+    for (int e = 0; e < N / 4; ++e) {
+      float q[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        q[k] = x[4 * e + k] * inv;
+        const uint32_t u = __float_as_uint(q[k]) & 0x7fffffffu;
+        near = min(near, (uint32_t)abs((int)(u & 0xfffffu) - 0x80000));  // the 20 bits behind a code
+        small = min(small, u - 1u);                                      // zero wraps to the top
+      }
+      out[e] = e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
     }
-    // below 2^-6 the codes are evenly spaced: settled exactly too
-    if (near <= 8u || small < 0x3c800000u || settle) return settle4<CODE>(x[0], x[1], x[2], x[3], amax);
-    return e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
+    settle = near <= 8u || small < 0x3c800000u;  // below 2^-6 the codes are evenly spaced: settled exactly too
+  }
+  if (far_from_one) {
+#pragma unroll
+    for (int e = 0; e < N / 4; ++e) out[e] = settle4_scaled<DT, CODE>(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3], amax);
+  } else if (settle) {
+#pragma unroll
+    for (int e = 0; e < N / 4; ++e) out[e] = settle4<DT, CODE>(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3], inv, amax);
   }
 }
 
@@ -136,7 +176,7 @@ struct BlockWriter {
   static constexpr int NL = kBlock / RPL;           // loads of a block
   const uint4 *src;      // new rows of the slice
   uint4 *tail;           // the slice's tail
-  uint8_t *codes;        // the slice's codes
+  uint8_t *codes_at;     // the slice's codes
   float *scale;          // the slice's scales
   int32_t *anomalies;
   int start, end, lane;
@@ -170,42 +210,43 @@ struct BlockWriter {
     return (w & 0x7fffffffu) > 0x7f800000u ? 0u : (w & 0x80000000u) | 0x7f7fffffu;
   }
 
-  static __device__ __forceinline__ void values4(const uint4 &w, int h, float (&x)[4]) {
-    if (DT == 1) {
-      const uint32_t a = h ? w.z : w.x, b = h ? w.w : w.y;
-      x[0] = __uint_as_float(a << 16); x[1] = __uint_as_float(a & 0xffff0000u);
-      x[2] = __uint_as_float(b << 16); x[3] = __uint_as_float(b & 0xffff0000u);
-    } else {
-      x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y);
-      x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
-    }
-  }
-
-  __device__ __forceinline__ void put(const uint4 (&w)[NL], int64_t block, float inv, float amax, bool settle) const {
-    uint8_t *to = codes + (block * kBlock + lane / LPR) * kHeadDim + (lane % LPR) * E;
+  __device__ __forceinline__ void put(const uint4 (&w)[NL], int64_t block, float inv, float amax, bool far_from_one) const {
+    uint8_t *to = codes_at + (block * kBlock + lane / LPR) * kHeadDim + (lane % LPR) * E;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      float x[4];
-      values4(w[i], 0, x);
-      const uint32_t c0 = codes4<CODE>(x, inv, amax, settle);
-      if constexpr (DT == 1) {
-        values4(w[i], 1, x);
-        *(uint2 *)(to + i * RPL * kHeadDim) = make_uint2(c0, codes4<CODE>(x, inv, amax, settle));
-      } else {
-        *(uint32_t *)(to + i * RPL * kHeadDim) = c0;
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      float x[E];
+      uint32_t c[E / 4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (DT == 1) {
+          x[2 * e] = __uint_as_float(u[e] << 16);
+          x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+        } else {
+          x[e] = __uint_as_float(u[e]);
+        }
       }
+      codes<DT, CODE>(x, inv, amax, far_from_one, c);
+      if constexpr (DT == 1) *(uint2 *)(to + i * RPL * kHeadDim) = make_uint2(c[0], c[1]);
+      else *(uint32_t *)(to + i * RPL * kHeadDim) = c[0];
     }
   }
 
   __device__ __forceinline__ void block(int j) const {
     uint4 w[NL];
     const int p0 = j * kBlock, sub = lane / LPR, chunk = lane % LPR;
+    if (p0 >= start && p0 + kBlock <= end) {  // all new
+      const uint4 *from = src + (int64_t)(p0 - start) * LPR + lane;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int r = i * RPL + sub, pos = p0 + r;
-      w[i] = make_uint4(0, 0, 0, 0);
-      if (pos < start) w[i] = tail[r * LPR + chunk];
-      else if (pos < end) w[i] = __ldcs(src + (int64_t)(pos - start) * LPR + chunk);
+      for (int i = 0; i < NL; ++i) w[i] = __ldcs(from + i * 32);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int r = i * RPL + sub, pos = p0 + r;
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (pos < start) w[i] = tail[r * LPR + chunk];
+        else if (pos < end) w[i] = __ldcs(src + (int64_t)(pos - start) * LPR + chunk);
+      }
     }
     float amax = amax_of(w);
     if (!(amax <= 0x1.fffffep127f)) {  // an infinity or a NaN
@@ -218,9 +259,9 @@ struct BlockWriter {
     constexpr float kTop = CODE == LKV_CODE_INT8 ? 127.f : 448.f;
     if (p0 + kBlock <= end) {
       if (amax > 0.f) {
-        put(w, j, __fdiv_rn(kTop, amax), amax, amax < 0x1p-110f);  // kTop / amax may overflow
+        put(w, j, __fdiv_rn(kTop, amax), amax, amax < 0x1p-60f || amax > 0x1p100f);
       } else {
-        uint4 *to = (uint4 *)(codes + (int64_t)j * kBlock * kHeadDim);
+        uint4 *to = (uint4 *)(codes_at + (int64_t)j * kBlock * kHeadDim);
 #pragma unroll
         for (int i = 0; i < kBlock * kHeadDim / 512; ++i) to[i * 32 + lane] = make_uint4(0, 0, 0, 0);
       }
@@ -284,7 +325,7 @@ __global__ void __launch_bounds__(kCacheThreads, DT == 1 ? 6 : 3) k_cache8_write
     const int64_t es = DT == 1 ? 2 : 4;
     w.src = (const uint4 *)((const char *)(kv ? a.v : a.k) + slice * a.n * kHeadDim * es);
     w.tail = (uint4 *)((char *)(kv ? c.v_tail : c.k_tail) + slice * kBlock * kHeadDim * es);
-    w.codes = (uint8_t *)(kv ? c.v_codes : c.k_codes) + slice * c.capacity * kHeadDim;
+    w.codes_at = (uint8_t *)(kv ? c.v_codes : c.k_codes) + slice * c.capacity * kHeadDim;
     w.scale = (kv ? c.v_scale : c.k_scale) + slice * (c.capacity / kBlock);
     w.anomalies = c.ticket + c.batch;
     w.start = start;
