@@ -109,6 +109,10 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
                :
                : "memory");
 }
+__device__ __forceinline__ void tmem_st4(uint32_t at, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float2 fma_2(float2 a, float2 b, float2 c) {
@@ -147,6 +151,90 @@ __device__ __forceinline__ bool rows_wait(uint64_t *bar, uint32_t phase, volatil
 // The same for a whole warp, uniformly.
 __device__ __forceinline__ bool rows_wait_warp(uint64_t *bar, uint32_t phase, volatile int *abort) {
   return __all_sync(0xffffffffu, rows_wait(bar, phase, abort));
+}
+
+// A row's softmax: reference, sum of w / u before and in this tile, the block
+// sum of weights past which the reference moves, and whether there is one.
+struct RowState {
+  float ref, l, sum, limit;
+  bool seen;
+};
+
+// The rare turn of the softmax, out of its loop's way: references of a warp's
+// rows move (kPShift below a row's largest y, up only once there is one), what
+// tensor memory holds of the tile's weights and of O follows, and blocks b and
+// b + 1 are weighed from their scores. hi, lo, si: which of their tokens the
+// row sees, unless all are (open).
+__device__ __noinline__ RowState move_reference(RowState z, uint32_t s_at, uint32_t o_at, const float4 *sc, float rc, bool open, const int (&hi)[2],
+                                                const int (&lo)[2], const int (&si)[2], int b, uint64_t *odone, uint32_t phase,
+                                                volatile int *abort) {
+  float far = -INFINITY;
+  auto scores = [&](int c, uint32_t(&x)[8]) {  // y of columns 8 c.. of the two blocks
+    tmem_ld8(s_at + 16 * b + 8 * c, x);
+    const int k = c >> 1;
+    const float f = rc * sc[k].x, at = sc[k].y - z.ref;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = 8 * (c & 1) + e;
+      const float v = __fmaf_rn(__uint_as_float(x[e]), f, at);
+      x[e] = __float_as_uint(open || (i <= hi[k] && (i > lo[k] || i < si[k])) ? v : -INFINITY);
+    }
+  };
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t x[8];
+    scores(c, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) far = fmaxf(far, __uint_as_float(x[e]));
+  }
+  float by = far - kPShift;
+  if (z.seen ? by < 0.f : far == -INFINITY) by = 0.f;
+  const float k = z.seen ? exp2f(-by) : 1.f;
+  z.seen |= far > -INFINITY;
+  z.limit = z.seen ? 0x1p15f : -1.f;
+  z.ref += by;
+  z.l *= k;
+  z.sum *= k;
+  if (__any_sync(0xffffffffu, k != 1.f)) {
+    tmem_wait_st();
+    const __half2 kh = __float2half2_rn(k);
+#pragma unroll 1
+    for (int d = 0; d < 8 * b; d += 8) {
+      uint32_t x[8];
+      tmem_ld8(s_at + d, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = h2_bits(__hmul2(*(const __half2 *)&x[e], kh));
+      tmem_st8(s_at + d, x);
+    }
+    if (odone) {  // the last product into O has to be done; if it is not in time the CTA gives up
+      rows_wait_warp(odone, phase, abort);
+      tmem_after();
+#pragma unroll 1
+      for (int d = 0; d < kHeadDim; d += 8) {
+        uint32_t x[8];
+        tmem_ld8(o_at + d, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * k);
+        tmem_st8(o_at + d, x);
+      }
+    }
+    tmem_wait_st();
+  }
+  float t[2] = {0.f, 0.f};
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {  // weights over columns whose scores have been read: 4 c.. behind 8 c..
+    uint32_t x[8], p[4];
+    scores(c, x);
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = ex2(__uint_as_float(x[e]));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = h2_bits(__floats2half2_rn(w[2 * e], w[2 * e + 1]));
+    t[c >> 1] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+    tmem_st4(s_at + 8 * b + 4 * c, p);
+  }
+  z.sum = __fmaf_rn(t[0], sc[0].z, __fmaf_rn(t[1], sc[1].z, z.sum));
+  return z;
 }
 
 template <int CODE>
@@ -502,94 +590,37 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
             if (!see(e)) y[e] = -INFINITY;
         }
         float t[2];
-        auto weigh = [&]() {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = ex2(y[e]);
+        for (int e = 0; e < 32; ++e) y[e] = ex2(y[e]);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float2 z = make_float2(y[16 * k], y[16 * k + 1]), z2 = make_float2(y[16 * k + 2], y[16 * k + 3]);
+        for (int k = 0; k < 2; ++k) {
+          float2 z = make_float2(y[16 * k], y[16 * k + 1]), z2 = make_float2(y[16 * k + 2], y[16 * k + 3]);
 #pragma unroll
-            for (int e = 4; e < 16; e += 4) {
-              z = add_2(z, make_float2(y[16 * k + e], y[16 * k + e + 1]));
-              z2 = add_2(z2, make_float2(y[16 * k + e + 2], y[16 * k + e + 3]));
-            }
-            z = add_2(z, z2);
-            t[k] = z.x + z.y;
+          for (int e = 4; e < 16; e += 4) {
+            z = add_2(z, make_float2(y[16 * k + e], y[16 * k + e + 1]));
+            z2 = add_2(z2, make_float2(y[16 * k + e + 2], y[16 * k + e + 3]));
           }
-        };
-        weigh();
+          z = add_2(z, z2);
+          t[k] = z.x + z.y;
+        }
         // a weight is at most its block's sum: below the limit none leaves fp16's range
         if (__any_sync(0xffffffffu, !(fmaxf(t[0], t[1]) <= limit))) {
-          // references move: kPShift below a row's largest y, up only once there is one
-          float far = -INFINITY;
-          auto again = [&](int c, uint32_t(&x)[8]) {  // y of columns 8 c.. of the two blocks, from the scores
-            tmem_ld8(s_at + 16 * b + 8 * c, x);
-            const float4 sc = scales[j & 3][b + (c >> 1)];
-            const float f = rc * sc.x, at = sc.y - ref;
+          tmem_wait32(r);  // the scores on their way, before registers change hands
+          const RowState z = move_reference(RowState{ref, l, sum, limit, seen}, s_at, o_at, &scales[j & 3][b], rc, open, hi, lo, si, b,
+                                            j > 0 ? &sy.odone[w] : nullptr, (j - 1) & 1, &abort_s);
+          ref = z.ref;
+          l = z.l;
+          sum = z.sum;
+          limit = z.limit;
+          seen = z.seen;
+        } else {
+          sum = __fmaf_rn(t[0], sc0.z, __fmaf_rn(t[1], sc1.z, sum));
+          uint32_t p[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float v = __fmaf_rn(__uint_as_float(x[e]), f, at);
-              x[e] = __float_as_uint(open || ((8 * (c & 1) + e) <= hi[c >> 1] && ((8 * (c & 1) + e) > lo[c >> 1] || (8 * (c & 1) + e) < si[c >> 1]))
-                                         ? v : -INFINITY);
-            }
-          };
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[8];
-            again(c, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) far = fmaxf(far, __uint_as_float(x[e]));
-          }
-          float by = far - kPShift;
-          if (seen ? by < 0.f : far == -INFINITY) by = 0.f;
-          const float k = seen ? exp2f(-by) : 1.f;
-          seen |= far > -INFINITY;
-          limit = seen ? 0x1p15f : -1.f;
-          ref += by;
-          l *= k;
-          sum *= k;
-          if (__any_sync(0xffffffffu, k != 1.f)) {
-            // what is in tensor memory: this tile's weights so far, and O
-            tmem_wait_st();
-            const __half2 kh = __float2half2_rn(k);
-#pragma unroll 1
-            for (int d = 0; d < 8 * b; d += 8) {
-              uint32_t x[8];
-              tmem_ld8(s_at + d, x);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = h2_bits(__hmul2(*(const __half2 *)&x[e], kh));
-              tmem_st8(s_at + d, x);
-            }
-            if (j > 0) {
-              ok &= rows_wait_warp(&sy.odone[w], (j - 1) & 1, &abort_s);
-              tmem_after();
-#pragma unroll 1
-              for (int d = 0; d < kHeadDim; d += 8) {
-                uint32_t x[8];
-                tmem_ld8(o_at + d, x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * k);
-                tmem_st8(o_at + d, x);
-              }
-            }
-            tmem_wait_st();
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[8];
-            again(c, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[8 * c + e] = __uint_as_float(x[e]);
-          }
-          weigh();
+          for (int e = 0; e < 16; ++e) p[e] = h2_bits(__floats2half2_rn(y[2 * e], y[2 * e + 1]));
+          tmem_st16(s_at + 8 * b, p);
         }
-        sum = __fmaf_rn(t[0], sc0.z, __fmaf_rn(t[1], sc1.z, sum));
-        uint32_t p[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) p[e] = h2_bits(__floats2half2_rn(y[2 * e], y[2 * e + 1]));
-        tmem_st16(s_at + 8 * b, p);
       }
-      if (!ok) break;
       l += sum;
       tmem_wait_st();
       tmem_before();
