@@ -82,11 +82,14 @@ __device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
                ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
       ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
       : "memory");
 }
 // 32 columns of the thread's lane; valid after tmem_wait32 on the same array.
@@ -153,6 +156,16 @@ __device__ __forceinline__ bool rows_wait_warp(uint64_t *bar, uint32_t phase, vo
   return __all_sync(0xffffffffu, rows_wait(bar, phase, abort));
 }
 
+// Which tokens of block unit u a row at position pos sees: those up to
+// see[0], and of them those above see[1] or below see[2].
+__device__ __forceinline__ void token_range(int u, int sb, int lo, int nb, int pos, int window, int sinks, int (&see)[3]) {
+  const int tok = (u < sb ? u : u - sb + lo) * kBlock;
+  see[0] = u < nb ? pos - tok : -1;
+  see[1] = window > 0 ? pos - window - tok : -1;
+  see[2] = sinks - tok;
+}
+__device__ __forceinline__ bool sees(const int (&see)[3], int i) { return i <= see[0] && (i > see[1] || i < see[2]); }
+
 // A row's softmax: reference, sum of w / u before and in this tile, the block
 // sum of weights past which the reference moves, and whether there is one.
 struct RowState {
@@ -162,26 +175,27 @@ struct RowState {
 
 // The rare turn of the softmax, out of its loop's way: references of a warp's
 // rows move (kPShift below a row's largest y, up only once there is one), what
-// tensor memory holds of the tile's weights and of O follows, and blocks b and
-// b + 1 are weighed from their scores. hi, lo, si: which of their tokens the
-// row sees, unless all are (open).
-__device__ __noinline__ RowState move_reference(RowState z, uint32_t s_at, uint32_t o_at, const float4 *sc, float rc, bool open, const int (&hi)[2],
-                                                const int (&lo)[2], const int (&si)[2], int b, uint64_t *odone, uint32_t phase,
+// tensor memory holds of the tile's weights and of O follows, and the four
+// blocks from b on are weighed from their scores. The row sees all of their
+// tokens (open) or what token_range says.
+__device__ __noinline__ RowState move_reference(RowState z, uint32_t s_at, uint32_t o_at, const float4 *scale, float rc, bool open, int u0, int sb,
+                                                int lo, int nb, int pos, int window, int sinks, int b, uint64_t *odone, uint32_t phase,
                                                 volatile int *abort) {
   float far = -INFINITY;
-  auto scores = [&](int c, uint32_t(&x)[8]) {  // y of columns 8 c.. of the two blocks
+  auto scores = [&](int c, uint32_t(&x)[8]) {  // y of columns 8 c.. of the four blocks
     tmem_ld8(s_at + 16 * b + 8 * c, x);
-    const int k = c >> 1;
-    const float f = rc * sc[k].x, at = sc[k].y - z.ref;
+    const float4 sc = scale[b + (c >> 1)];
+    const float f = rc * sc.x, at = sc.y - z.ref;
+    int see[3];
+    token_range(u0 + b + (c >> 1), sb, lo, nb, pos, window, sinks, see);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int i = 8 * (c & 1) + e;
       const float v = __fmaf_rn(__uint_as_float(x[e]), f, at);
-      x[e] = __float_as_uint(open || (i <= hi[k] && (i > lo[k] || i < si[k])) ? v : -INFINITY);
+      x[e] = __float_as_uint(open || sees(see, 8 * (c & 1) + e) ? v : -INFINITY);
     }
   };
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < 8; ++c) {
     uint32_t x[8];
     scores(c, x);
 #pragma unroll
@@ -220,9 +234,8 @@ __device__ __noinline__ RowState move_reference(RowState z, uint32_t s_at, uint3
     }
     tmem_wait_st();
   }
-  float t[2] = {0.f, 0.f};
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {  // weights over columns whose scores have been read: 4 c.. behind 8 c..
+  for (int c = 0; c < 8; ++c) {  // weights over columns whose scores have been read: 4 c.. behind 8 c..
     uint32_t x[8], p[4];
     scores(c, x);
     float w[8];
@@ -230,10 +243,9 @@ __device__ __noinline__ RowState move_reference(RowState z, uint32_t s_at, uint3
     for (int e = 0; e < 8; ++e) w[e] = ex2(__uint_as_float(x[e]));
 #pragma unroll
     for (int e = 0; e < 4; ++e) p[e] = h2_bits(__floats2half2_rn(w[2 * e], w[2 * e + 1]));
-    t[c >> 1] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+    z.sum = __fmaf_rn(((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7])), scale[b + (c >> 1)].z, z.sum);
     tmem_st4(s_at + 8 * b + 4 * c, p);
   }
-  z.sum = __fmaf_rn(t[0], sc[0].z, __fmaf_rn(t[1], sc[1].z, z.sum));
   return z;
 }
 
@@ -554,71 +566,66 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
       float sum = 0.f;
       uint32_t r[32];
       tmem_ld32(s_at, r);
-      // two blocks at a time: scores become weights, over the columns of
-      // blocks that have been read
+      // four blocks at a time, two by two: scores become weights, over the
+      // columns of blocks that have been read
 #pragma unroll 1
-      for (int b = 0; b < kRwBlocks; b += 2) {
-        const float4 sc0 = scales[j & 3][b], sc1 = scales[j & 3][b + 1];
-        // what a token of block b or b + 1 has to be for this row to see it
-        int hi[2] = {}, lo[2] = {}, si[2] = {};
-        auto see = [&](int e) { return (e & 15) <= hi[e >> 4] && ((e & 15) > lo[e >> 4] || (e & 15) < si[e >> 4]); };
-        if (!open) {
+      for (int b = 0; b < kRwBlocks; b += 4) {
+        uint32_t p[32];
+        float t[4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int u = u0 + b + k, tok = tile.block(u) * kBlock;
-            hi[k] = u < tile.nb ? pos - tok : -1;                     // up to it,
-            lo[k] = a.window > 0 ? pos - a.window - tok : -1;         // and above it
-            si[k] = a.sinks - tok;                                    // or below it
+        for (int g = 0; g < 2; ++g) {
+          const float4 sc0 = scales[j & 3][b + 2 * g], sc1 = scales[j & 3][b + 2 * g + 1];
+          float y[32];
+          tmem_wait32(r);
+          {
+            const float f0 = rc * sc0.x, at0 = sc0.y - ref, f1 = rc * sc1.x, at1 = sc1.y - ref;
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float f = e < 16 ? f0 : f1, at = e < 16 ? at0 : at1;
+              const float2 z = fma_2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), make_float2(f, f), make_float2(at, at));
+              y[e] = z.x;
+              y[e + 1] = z.y;
+            }
           }
-        }
-        float y[32];
-        tmem_wait32(r);
-        {
-          const float f0 = rc * sc0.x, at0 = sc0.y - ref, f1 = rc * sc1.x, at1 = sc1.y - ref;
+          if (g == 0 || b + 4 < kRwBlocks) tmem_ld32(s_at + 16 * (b + 2 * g + 2), r);
+          if (!open) {
+            int see[2][3];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float f = e < 16 ? f0 : f1, at = e < 16 ? at0 : at1;
-            const float2 z = fma_2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), make_float2(f, f), make_float2(at, at));
-            y[e] = z.x;
-            y[e + 1] = z.y;
+            for (int k = 0; k < 2; ++k) token_range(u0 + b + 2 * g + k, tile.sb, tile.lo, tile.nb, pos, a.window, a.sinks, see[k]);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!sees(see[e >> 4], e & 15)) y[e] = -INFINITY;
           }
-        }
-        if (b + 2 < kRwBlocks) tmem_ld32(s_at + 16 * (b + 2), r);
-        if (!open) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!see(e)) y[e] = -INFINITY;
-        }
-        float t[2];
+          for (int e = 0; e < 32; ++e) y[e] = ex2(y[e]);
+          float2 z[4];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = ex2(y[e]);
+          for (int k = 0; k < 4; ++k) {
+            z[k] = make_float2(y[8 * k], y[8 * k + 1]);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float2 z = make_float2(y[16 * k], y[16 * k + 1]), z2 = make_float2(y[16 * k + 2], y[16 * k + 3]);
+            for (int e = 2; e < 8; e += 2) z[k] = add_2(z[k], make_float2(y[8 * k + e], y[8 * k + e + 1]));
 #pragma unroll
-          for (int e = 4; e < 16; e += 4) {
-            z = add_2(z, make_float2(y[16 * k + e], y[16 * k + e + 1]));
-            z2 = add_2(z2, make_float2(y[16 * k + e + 2], y[16 * k + e + 3]));
+            for (int e = 0; e < 4; ++e) p[16 * g + 4 * k + e] = h2_bits(__floats2half2_rn(y[8 * k + 2 * e], y[8 * k + 2 * e + 1]));
           }
-          z = add_2(z, z2);
-          t[k] = z.x + z.y;
+          z[0] = add_2(z[0], z[1]);
+          z[2] = add_2(z[2], z[3]);
+          t[2 * g] = z[0].x + z[0].y;
+          t[2 * g + 1] = z[2].x + z[2].y;
         }
         // a weight is at most its block's sum: below the limit none leaves fp16's range
-        if (__any_sync(0xffffffffu, !(fmaxf(t[0], t[1]) <= limit))) {
+        if (__any_sync(0xffffffffu, !(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) <= limit))) {
           tmem_wait32(r);  // the scores on their way, before registers change hands
-          const RowState z = move_reference(RowState{ref, l, sum, limit, seen}, s_at, o_at, &scales[j & 3][b], rc, open, hi, lo, si, b,
-                                            j > 0 ? &sy.odone[w] : nullptr, (j - 1) & 1, &abort_s);
+          const RowState z = move_reference(RowState{ref, l, sum, limit, seen}, s_at, o_at, scales[j & 3], rc, open, u0, tile.sb, tile.lo, tile.nb,
+                                            pos, a.window, a.sinks, b, j > 0 ? &sy.odone[w] : nullptr, (j - 1) & 1, &abort_s);
           ref = z.ref;
           l = z.l;
           sum = z.sum;
           limit = z.limit;
           seen = z.seen;
         } else {
-          sum = __fmaf_rn(t[0], sc0.z, __fmaf_rn(t[1], sc1.z, sum));
-          uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) p[e] = h2_bits(__floats2half2_rn(y[2 * e], y[2 * e + 1]));
-          tmem_st16(s_at + 8 * b, p);
+          for (int k = 0; k < 4; ++k) sum = __fmaf_rn(t[k], scales[j & 3][b + k].z, sum);
+          tmem_st32(s_at + 8 * b, p);
         }
       }
       l += sum;
