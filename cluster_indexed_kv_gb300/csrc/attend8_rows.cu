@@ -133,7 +133,8 @@ __device__ __forceinline__ float2 add_2(float2 a, float2 b) {
 }
 
 struct RowsSync {
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], odone[2], scfull[4], drained;
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], odone[2], scfull[4], drained;
+  uint64_t pfull[2][2];  // [row tile][half of the tokens]
 };
 
 // Wait for the phase; false, and the abort flag raised, when it does not come
@@ -177,9 +178,11 @@ struct RowState {
 // rows move (kPShift below a row's largest y, up only once there is one), what
 // tensor memory holds of the tile's weights and of O follows, and the four
 // blocks from b on are weighed from their scores. The row sees all of their
-// tokens (open) or what token_range says.
+// tokens (open) or what token_range says. The step's first half finds O (if
+// there has been a product) at rest; its second half waits for the first
+// half's product (odone), which has also read that half's weights.
 __device__ __noinline__ RowState move_reference(RowState z, uint32_t s_at, uint32_t o_at, const float4 *scale, float rc, bool open, int u0, int sb,
-                                                int lo, int nb, int pos, int window, int sinks, int b, uint64_t *odone, uint32_t phase,
+                                                int lo, int nb, int pos, int window, int sinks, int b, bool has_o, uint64_t *odone,
                                                 volatile int *abort) {
   float far = -INFINITY;
   auto scores = [&](int c, uint32_t(&x)[8]) {  // y of columns 8 c.. of the four blocks
@@ -210,18 +213,9 @@ __device__ __noinline__ RowState move_reference(RowState z, uint32_t s_at, uint3
   z.l *= k;
   z.sum *= k;
   if (__any_sync(0xffffffffu, k != 1.f)) {
-    tmem_wait_st();
-    const __half2 kh = __float2half2_rn(k);
-#pragma unroll 1
-    for (int d = 0; d < 8 * b; d += 8) {
-      uint32_t x[8];
-      tmem_ld8(s_at + d, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = h2_bits(__hmul2(*(const __half2 *)&x[e], kh));
-      tmem_st8(s_at + d, x);
-    }
-    if (odone) {  // the last product into O has to be done; if it is not in time the CTA gives up
-      rows_wait_warp(odone, phase, abort);
+    // (if it is not in time the CTA gives up)
+    if (odone) rows_wait_warp(odone, 0, abort);
+    if (has_o) {
       tmem_after();
 #pragma unroll 1
       for (int d = 0; d < kHeadDim; d += 8) {
@@ -231,8 +225,8 @@ __device__ __noinline__ RowState move_reference(RowState z, uint32_t s_at, uint3
         for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * k);
         tmem_st8(o_at + d, x);
       }
+      tmem_wait_st();
     }
-    tmem_wait_st();
   }
 #pragma unroll 1
   for (int c = 0; c < 8; ++c) {  // weights over columns whose scores have been read: 4 c.. behind 8 c..
@@ -283,7 +277,8 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
       bar_init(&sy.vfull[i], 4);
       bar_init(&sy.vempty[i], 1);
       bar_init(&sy.sfull[i], 1);
-      bar_init(&sy.pfull[i], 4);
+      bar_init(&sy.pfull[i][0], 4);
+      bar_init(&sy.pfull[i][1], 4);
       bar_init(&sy.odone[i], 1);
     }
     for (int i = 0; i < 4; ++i) bar_init(&sy.scfull[i], 1);
@@ -500,13 +495,20 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
         }
         mma_commit(&sy.sfull[w]);
       };
-      auto pv = [&](int w, int st, bool first) {
+      // O += P V of a step's first and then second 64 tokens, each as soon as
+      // its weights are there
+      auto pv = [&](int w, int j) {
+        const uint64_t y = rw_desc(v_at + (j & 1) * kRwTile);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t at = (k >> 2) * kRwHalf + (k & 3) * 32;
-          mma_ts(tmem + 256 + w * 128, tmem + w * 128 + 8 * k, rw_desc(v_at + st * kRwTile + at), !first || k > 0);
+        for (int h = 0; h < 2; ++h) {
+          if (!rows_wait(&sy.pfull[w][h], j & 1, &abort_s)) return false;
+          tmem_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tmem + 256 + w * 128, tmem + w * 128 + 32 * h + 8 * k, y + ((h * kRwHalf + k * 32) >> 4), j > 0 || h > 0 || k > 0);
+          mma_commit(&sy.odone[w]);
         }
-        mma_commit(&sy.odone[w]);
+        return true;
       };
       bool ok = steps > 0 && rows_wait(&sy.kfull[0], 0, &abort_s);
       if (ok) {
@@ -517,10 +519,8 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
       }
       for (int j = 0; ok && j < steps; ++j) {
         const int st = j & 1, nx = (j + 1) & 1;
-        ok = rows_wait(&sy.vfull[st], (j >> 1) & 1, &abort_s) && rows_wait(&sy.pfull[0], j & 1, &abort_s);
+        ok = rows_wait(&sy.vfull[st], (j >> 1) & 1, &abort_s) && pv(0, j);
         if (!ok) break;
-        tmem_after();
-        pv(0, st, j == 0);
         if (j + 1 < steps) {
           ok = rows_wait(&sy.kfull[nx], ((j + 1) >> 1) & 1, &abort_s);
           if (!ok) break;
@@ -528,10 +528,8 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
           qk(0, nx);
         }
         if (two) {
-          ok = rows_wait(&sy.pfull[1], j & 1, &abort_s);
+          ok = pv(1, j);
           if (!ok) break;
-          tmem_after();
-          pv(1, st, j == 0);
         }
         mma_commit(&sy.vempty[st]);
         if (j + 1 < steps) {
@@ -616,7 +614,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
         if (__any_sync(0xffffffffu, !(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) <= limit))) {
           tmem_wait32(r);  // the scores on their way, before registers change hands
           const RowState z = move_reference(RowState{ref, l, sum, limit, seen}, s_at, o_at, scales[j & 3], rc, open, u0, tile.sb, tile.lo, tile.nb,
-                                            pos, a.window, a.sinks, b, j > 0 ? &sy.odone[w] : nullptr, (j - 1) & 1, &abort_s);
+                                            pos, a.window, a.sinks, b, j > 0 || b > 0, b > 0 ? &sy.odone[w] : nullptr, &abort_s);
           ref = z.ref;
           l = z.l;
           sum = z.sum;
@@ -627,14 +625,15 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
           for (int k = 0; k < 4; ++k) sum = __fmaf_rn(t[k], scales[j & 3][b + k].z, sum);
           tmem_st32(s_at + 8 * b, p);
         }
+        tmem_wait_st();
+        tmem_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sy.pfull[w][b >> 2]);
       }
       l += sum;
-      tmem_wait_st();
-      tmem_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive(&sy.pfull[w]);
     }
-    if (ok && steps > 0) ok = rows_wait_warp(&sy.odone[w], (steps - 1) & 1, &abort_s);
+    // the last two products into O (scores follow all products before them)
+    if (ok && steps > 0) ok = rows_wait_warp(&sy.odone[w], 0, &abort_s) && rows_wait_warp(&sy.odone[w], 1, &abort_s);
     tmem_after();
     const int row = r0 + (int)threadIdx.x;
     const float scale = valid && l != 0.f ? 1.f / l : 0.f, back = pow2f(unit);
