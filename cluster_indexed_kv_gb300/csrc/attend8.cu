@@ -6,7 +6,6 @@ namespace lkv {
 constexpr int kAtWarps = 6;
 constexpr int kAtThreads = 32 * kAtWarps;
 constexpr int kAtMaxCluster = 8;
-constexpr int kAtGroups = 512;      // (sequence, row tile) pairs that a streamed launch takes
 constexpr int kCodeBytes = kBlock * kHeadDim;      // one block of K or V
 constexpr int kTurnBytes = 2 * 2 * kCodeBytes;     // two blocks of both
 constexpr int kRingBytes = kAtWarps * 2 * kTurnBytes;
@@ -307,48 +306,6 @@ __device__ __forceinline__ float2 peer_f2(const void *p, uint32_t rank) {
   return v;
 }
 
-// 2^(m - top), 0 for a share that saw nothing
-__device__ __forceinline__ float share(float m, float top) { return m == -INFINITY ? 0.f : exp2f(m - top); }
-
-// A streamed launch's work: the blocks of all tiles in a row, (sequence, row
-// tile) by (sequence, row tile) and KV head by KV head, CTA i of P taking
-// those from total * i / P on (P the CTAs, but no more than blocks).
-struct Stream {
-  int64_t at[kAtGroups + 1];  // blocks before each (sequence, row tile)
-  int nb[kAtGroups];          // blocks of one of its tiles
-  __device__ void fill(const AttendArgs &a, int RT) {
-    const int G = a.c.batch * a.row_tiles;
-    for (int i = threadIdx.x; i < G; i += blockDim.x) nb[i] = Tile(a, i % a.c.batch, i / a.c.batch, RT).nb;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-      int64_t sum = 0;
-      for (int i0 = 0; i0 < G; i0 += 32) {
-        const int i = i0 + threadIdx.x;
-        int64_t x = i < G ? (int64_t)nb[i] * a.c.n_kv_heads : 0;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-          if ((int)threadIdx.x >= d) x += y;
-        }
-        if (i < G) at[i + 1] = sum + x;
-        sum += __shfl_sync(0xffffffffu, x, 31);
-      }
-      if (threadIdx.x == 0) at[0] = 0;
-    }
-    __syncthreads();
-  }
-  // the (sequence, row tile) that block x of the row belongs to
-  __device__ __forceinline__ int group(int64_t x, int G) const {
-    int lo = 0, hi = G;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (at[mid] <= x) lo = mid;
-      else hi = mid;
-    }
-    return lo;
-  }
-};
-
 template <int NT>
 struct AtSmem {
   static constexpr int RT = 8 * NT;
@@ -454,10 +411,8 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
 
   int64_t x0 = 0, x1 = 1;  // streamed: the CTA's share of the row of blocks
   if (a.streamed) {
-    stream.fill(a, RT);
-    const int64_t total = stream.at[G], P = min((int64_t)gridDim.x, total);
-    x0 = blockIdx.x < P ? total * blockIdx.x / P : 0;
-    x1 = blockIdx.x < P ? total * (blockIdx.x + 1) / P : 0;
+    stream.fill(a, RT, 1, 0);
+    stream.share(G, x0, x1);
   }
   launch_dependents();
   for (int64_t x = x0; x < x1;) {
@@ -465,7 +420,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
     int64_t slice;
     int rt, b0, b1;
     if (a.streamed) {
-      const int gi = stream.group(x, G), nb = stream.nb[gi];
+      const int gi = stream.group(x, G), nb = stream.nu[gi];
       const int64_t off = x - stream.at[gi];
       const int h = (int)(off / nb), b = gi % c.batch;
       rt = gi / c.batch;
@@ -717,22 +672,17 @@ __global__ void __launch_bounds__(kMergeThreads) k_attend8_merge(const __grid_co
   __shared__ float total_l, unit;
   __shared__ int range[3];
   const int G = a.c.batch * a.row_tiles, row = blockIdx.y;
-  stream.fill(a, RT);  // the lengths and counts are inputs: not the first kernel's
-  const int gi = blockIdx.x / a.c.n_kv_heads, h = blockIdx.x % a.c.n_kv_heads, nb = stream.nb[gi];
+  stream.fill(a, RT, 1, 0);  // the lengths and counts are inputs: not the first kernel's
+  const int gi = blockIdx.x / a.c.n_kv_heads, h = blockIdx.x % a.c.n_kv_heads;
   const int b = gi % a.c.batch, rt = gi / a.c.batch;
   const int64_t slice = (int64_t)b * a.c.n_kv_heads + h;
   if (threadIdx.x == 0) {
+    const int nb = stream.nu[gi];
     const int64_t total = stream.at[G], P = min((int64_t)ctas, total), p0 = stream.at[gi] + (int64_t)h * nb;
-    auto owner = [&](int64_t x) {
-      int i = (int)(x * P / total);
-      while (total * (i + 1) / P <= x) ++i;
-      while (total * i / P > x) --i;
-      return i;
-    };
     range[0] = range[1] = range[2] = 0;
     if (nb > 0) {  // CTAs range[0].. share the tile; the first one's part is its second if it began before
-      range[0] = owner(p0);
-      range[1] = owner(p0 + nb - 1) - range[0] + 1;
+      range[0] = stream.owner(p0, total, P);
+      range[1] = stream.owner(p0 + nb - 1, total, P) - range[0] + 1;
       range[2] = total * range[0] / P < p0;
     }
   }
@@ -798,19 +748,32 @@ static const char *plan_attend(const lkv_cache8 *c, int32_t group, int32_t n, in
                                AttendPlan *p) {
   const int64_t R = (int64_t)n * group, S = (int64_t)c->batch * c->n_kv_heads;
   if (R > 0x7fffffff - 256) return "too many rows";
-  p->rows = c->dtype == LKV_DTYPE_BF16 && R >= (getenv("XR") ? atoi(getenv("XR")) : 64);
-  p->ctas = 0;
-  if (p->rows) return nullptr;
   p->nt = R <= 8 ? 1 : 2;
   p->row_tiles = (int)((R + 8 * p->nt - 1) / (8 * p->nt));
   p->tiles = S * p->row_tiles;
-  // blocks that a tile's rows may see, at most
-  int64_t most = max_len > 0 && max_len < c->capacity ? max_len : c->capacity;
-  if (window > 0 && window < c->capacity) {
-    const int64_t seen = (int64_t)window + (sinks < c->capacity ? sinks : c->capacity) + (8 * p->nt + group - 1) / group;
-    if (seen < most) most = seen;
+  // tokens that a tile of `rows` rows may see, at most
+  auto most = [&](int rows) {
+    const int64_t len = max_len > 0 && max_len < c->capacity ? max_len : c->capacity;
+    const int64_t seen = (int64_t)window + (sinks < c->capacity ? sinks : c->capacity) + (rows + group - 1) / group;
+    return window > 0 && seen < len ? seen : len;
+  };
+  // Many rows go to the tensor memory's kernel where it is faster: its time
+  // against this kernel's, in its steps, of which this one takes 0.4 for 16 rows
+  // x 128 tokens on every SM and 3 to start. On a GB300, int8, 4 query heads,
+  // this kernel's and its time: 64 slices of 32K tokens, 16 tokens each 363 and
+  // 292 us; 8 slices, 16 tokens 58 and 73 us, 32 tokens 101 and 72; 8 slices of
+  // 4096 tokens, 64 tokens 33 and 42 us; 64 slices of 256 tokens, 64 tokens 39
+  // and 29 us.
+  p->rows = false;
+  p->ctas = 0;
+  if (c->dtype == LKV_DTYPE_BF16) {
+    const int64_t steps = (most(kRowsTile) + kRowsStep - 1) / kRowsStep + (window > 0);
+    const double time = rows_plan(*c, R, window > 0 ? 0 : n, steps, sms, &p->ctas);
+    p->rows = 0.4 * (double)(S * ((R + 15) / 16)) * steps / sms > time - 3;
+    if (p->rows) return nullptr;
+    p->ctas = 0;
   }
-  const int64_t blocks = (most + kBlock - 1) / kBlock + 1;
+  const int64_t blocks = (most(8 * p->nt) + kBlock - 1) / kBlock + 1;
   int64_t slots = (int64_t)sms * (c->dtype == LKV_DTYPE_FP32 && p->nt == 2 ? 1 : 2);  // CTAs that the GPU holds
   if (slots > kMaxCtas) slots = kMaxCtas;
   int64_t cluster = slots / p->tiles, most_cluster = blocks / (2 * kAtWarps);  // a turn for every warp
@@ -886,7 +849,7 @@ static lkv_status refuse_in(const char *where, const char *why) {
 }
 
 static int64_t plan_bytes(const AttendPlan &p) {
-  return !p.rows && p.ctas ? (int64_t)p.ctas * 2 * (p.nt == 1 ? AtSmem<1>::kSlot : AtSmem<2>::kSlot) * 4 : 0;
+  return p.rows ? rows_bytes(p.ctas) : p.ctas ? (int64_t)p.ctas * 2 * (p.nt == 1 ? AtSmem<1>::kSlot : AtSmem<2>::kSlot) * 4 : 0;
 }
 
 }  // namespace lkv
@@ -948,7 +911,7 @@ extern "C" lkv_status lkv_cache8_attend(const lkv_cache8 *c, const void *q, int3
   a.streamed = p.ctas > 0;
   a.ws = (float *)workspace;
   if (p.rows) {
-    e = launch_attend_rows(a, (cudaStream_t)stream);
+    e = launch_attend_rows(a, p.ctas, (cudaStream_t)stream);
     return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_attend", e);
   }
   CUtensorMap km, vm;

@@ -84,7 +84,7 @@ __device__ __forceinline__ void codes_across(uint32_t wa, uint32_t wb, int h, ui
 // the first `sb` (sinks), then lo..hi.
 struct Tile {
   int len, cnt, pmin, pmax, lo, hi, sb, nb;
-  __device__ __forceinline__ Tile() {}
+  Tile() = default;
   __device__ __forceinline__ Tile(const AttendArgs &a, int b, int rt, int RT) {
     len = min(max(a.c.lengths[b], 0), a.c.capacity);
     cnt = a.counts ? min(max(a.counts[b], 0), a.n) : a.n;
@@ -100,7 +100,70 @@ struct Tile {
   __device__ __forceinline__ int block(int u) const { return u < sb ? u : u - sb + lo; }
 };
 
-// The kernel for many rows (attend8_rows.cu): bf16 caches.
-cudaError_t launch_attend_rows(const AttendArgs &a, cudaStream_t st);
+constexpr int kAtGroups = 512;  // (sequence, row tile) pairs that a streamed launch takes
+
+// A streamed launch's work: the units (runs of `per` blocks, behind `start`
+// units that stand for what beginning a tile costs) of all tiles in a row, (sequence, row tile) by (sequence, row tile) and KV head by KV head, CTA
+// i of P taking those from total * i / P on (P the CTAs, but no more than units).
+struct Stream {
+  int64_t at[kAtGroups + 1];  // units before each (sequence, row tile)
+  int nu[kAtGroups];          // units of one of its tiles
+  __device__ void fill(const AttendArgs &a, int RT, int per, int start) {
+    const int G = a.c.batch * a.row_tiles;
+    for (int i = threadIdx.x; i < G; i += blockDim.x) nu[i] = start + (Tile(a, i % a.c.batch, i / a.c.batch, RT).nb + per - 1) / per;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      int64_t sum = 0;
+      for (int i0 = 0; i0 < G; i0 += 32) {
+        const int i = i0 + threadIdx.x;
+        int64_t x = i < G ? (int64_t)nu[i] * a.c.n_kv_heads : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+          if ((int)threadIdx.x >= d) x += y;
+        }
+        if (i < G) at[i + 1] = sum + x;
+        sum += __shfl_sync(0xffffffffu, x, 31);
+      }
+      if (threadIdx.x == 0) at[0] = 0;
+    }
+    __syncthreads();
+  }
+  // the CTA's share
+  __device__ __forceinline__ void share(int G, int64_t &x0, int64_t &x1) const {
+    const int64_t total = at[G], P = min((int64_t)gridDim.x, total);
+    x0 = blockIdx.x < P ? total * blockIdx.x / P : 0;
+    x1 = blockIdx.x < P ? total * (blockIdx.x + 1) / P : 0;
+  }
+  // the (sequence, row tile) that unit x of the row belongs to
+  __device__ __forceinline__ int group(int64_t x, int G) const {
+    int lo = 0, hi = G;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (at[mid] <= x) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+  // the CTA of P that unit x of the row belongs to
+  __device__ __forceinline__ int owner(int64_t x, int64_t total, int64_t P) const {
+    int i = (int)(x * P / total);
+    while (total * (i + 1) / P <= x) ++i;
+    while (total * i / P > x) --i;
+    return i;
+  }
+};
+
+// 2^(m - top), 0 for a share that saw nothing
+__device__ __forceinline__ float share(float m, float top) { return m == -INFINITY ? 0.f : exp2f(m - top); }
+
+// The kernel for many rows (attend8_rows.cu), for bf16 caches. How it splits a
+// call of `rows` rows a slice, the last of which see at most `steps` times 128
+// tokens and the first `tokens` tokens fewer: CTAs of a streamed launch, or 0;
+// returns the time that takes, in steps. Then the workspace, and the launch.
+constexpr int kRowsTile = 256, kRowsStep = 128;  // rows and tokens of a tile's step
+double rows_plan(const lkv_cache8 &c, int64_t rows, int64_t tokens, int64_t steps, int sms, int *ctas);
+int64_t rows_bytes(int ctas);
+cudaError_t launch_attend_rows(const AttendArgs &a, int ctas, cudaStream_t st);
 
 }  // namespace lkv
