@@ -6,6 +6,7 @@ namespace lkv {
 constexpr int kAtWarps = 6;
 constexpr int kAtThreads = 32 * kAtWarps;
 constexpr int kAtMaxCluster = 8;
+constexpr int kTailTurns = 4;       // turns that the partial block takes as long as (10,000 clocks, a turn 2500)
 constexpr int kCodeBytes = kBlock * kHeadDim;      // one block of K or V
 constexpr int kTurnBytes = 2 * 2 * kCodeBytes;     // two blocks of both
 constexpr int kRingBytes = kAtWarps * 2 * kTurnBytes;
@@ -213,21 +214,22 @@ struct Warp {
     return *(const float4 *)((const float *)tail + row * kHeadDim + d);
   }
 
-  // A power of two that brings the tail's largest magnitude below 1.
-  __device__ __forceinline__ int tail_exp(const void *tail, int rows) const {
-    float m = 0.f;
-    for (int row = 0; row < rows; ++row) {
-      const float4 x = tail4(tail, row, 4 * lane, rows);
-      m = fmaxf(m, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
-    }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    return min(max((int)(top >> 23) - 126, -100), 126);
-  }
+  static __device__ __forceinline__ int below(uint32_t bits) { return min(max((int)(bits >> 23) - 126, -100), 126); }
 
   // The last, partial block, from the tails in full precision: the same
   // products on fp16 values and (fp32 tails) their remainders.
   __device__ __noinline__ void tail_step(const void *kt, const void *vt, int rows, int block) {
-    const int ke = tail_exp(kt, rows), ve = max(tail_exp(vt, rows), unit - kUnitSpan);
+    // powers of two that bring the tails' largest magnitudes below 1; what is
+    // read again below comes from L1
+    float mk = 0.f, mv = 0.f;
+#pragma unroll
+    for (int row = 0; row < kBlock; ++row) {
+      const float4 x = tail4(kt, row, 4 * lane, rows), y = tail4(vt, row, 4 * lane, rows);
+      mk = fmaxf(mk, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+      mv = fmaxf(mv, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
+    }
+    const int ke = below(__reduce_max_sync(0xffffffffu, __float_as_uint(mk)));
+    const int ve = max(below(__reduce_max_sync(0xffffffffu, __float_as_uint(mv))), unit - kUnitSpan);
     raise_unit(ve);
     const float kf = pow2f(-ke), vf = pow2f(-ve);
     float s[1][2][4] = {};
@@ -367,6 +369,12 @@ __device__ __forceinline__ void put_out(const AttendArgs &a, int64_t slice, int 
 // as many CTAs as the GPU holds, whatever the sequences' lengths; a tile that
 // several CTAs share goes to the workspace in parts, and k_attend8_merge joins
 // them. No atomics in either: the same result each time.
+//
+// Bound by the codes' bytes (the products of a turn take a quarter of its copy's
+// time). On a GB300, 4 query heads, bf16: 64 slices of 33,000 tokens 89 us, 89%
+// of the measured copy rate; 8 of 131,579 tokens 53 us, 75% (a long merge); 256
+// slices of a window of 1024 tokens 19 us, 52%, and one of 2048 tokens 9 us:
+// those wait for a launch, lengths, queries, codes and the merges in turn.
 template <int DT, int CODE, int NT>
 __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
     k_attend8(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -430,21 +438,25 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
       b1 = (int)min((int64_t)nb, b0 + (x1 - x));
       x += b1 - b0;
     } else {
-      const int64_t id = blockIdx.x / parts, S = (int64_t)c.batch * c.n_kv_heads;
+      const uint32_t id = blockIdx.x / (uint32_t)parts, S = (uint32_t)c.batch * c.n_kv_heads;  // the grid is below 2^31
       slice = id % S;
       rt = a.row_tiles - 1 - (int)(id / S);  // the rows with most to see come first
-      tile = Tile(a, (int)(slice / c.n_kv_heads), rt, RT);
-      b0 = (int)((int64_t)tile.nb * part / parts);
-      b1 = (int)((int64_t)tile.nb * (part + 1) / parts);
+      tile = Tile(a, (int)((id % S) / c.n_kv_heads), rt, RT);
+      b0 = (int)((uint32_t)tile.nb * part / parts);  // at most 8 x 2^27
+      b1 = (int)((uint32_t)tile.nb * (part + 1) / parts);
       x = x1;
     }
     const int r0 = rt * RT, full = tile.len / kBlock;  // blocks before `full` are quantised
     const bool tail = tile.nb > 0 && tile.hi >= full && b1 == tile.nb && b1 > b0;  // the share ends in the partial one
     const int b2 = dead ? b0 : tail ? b1 - 1 : b1;
 
-    // the warp's turn i: units u = b0 + 2 (i kAtWarps + wid) and u + 1
+    // The warp's turn i: units unit_at(i) and the next. The turns go round the
+    // warps, kTailTurns rounds without the last warp, which takes the partial
+    // block.
+    const int late = tail ? kTailTurns : 0;
+    auto unit_at = [&](int i) { return b0 + 2 * (i * kAtWarps + wid + (wid == kAtWarps - 1 ? late * (kAtWarps - 1) : -min(i, late))); };
     auto issue = [&](int i) {
-      const int u = b0 + 2 * (i * kAtWarps + wid);
+      const int u = unit_at(i);
       if (u < b2 && w.lane == 0) {
         unsigned char *to = ring + (i & 1) * kTurnBytes;
         uint64_t *on = &bar[i & 1];
@@ -462,8 +474,25 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
     };
     issue(0);
     issue(1);
+    const char *const kt = (const char *)c.k_tail + slice * kBlock * kHeadDim * es, *const vt = (const char *)c.v_tail + slice * kBlock * kHeadDim * es;
+    if (tail && wid == kAtWarps - 1)
+      for (int64_t at = 128 * w.lane; at < kBlock * kHeadDim * es; at += 32 * 128) {
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(kt + at));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(vt + at));
+      }
 
     const float *ksc = c.k_scale + slice * (c.capacity / kBlock), *vsc = c.v_scale + slice * (c.capacity / kBlock);
+    // the scales of the warp's turns, 16 turns ahead
+    float ks_next = 0.f, vs_next = 0.f;
+    auto scales = [&](int i) {
+      const int mine = unit_at(i + (w.lane >> 1)) + (w.lane & 1);
+      vs_next = 0.f;
+      if (mine < b2) {
+        ks_next = ksc[tile.block(mine)];
+        vs_next = vsc[tile.block(mine)];
+      }
+    };
+    scales(0);
     w.pmin = tile.pmin;
     w.pmax = tile.pmax;
     w.open0 = a.window > 0 ? max(0, tile.pmax - a.window + kBlock) / kBlock : 0;
@@ -514,14 +543,11 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
 
     float ks = 0.f, vs = 1.f, lu = 0.f;
     int i = 0;
-    for (int u = b0 + 2 * wid; u < b2; u += 2 * kAtWarps, ++i) {
-      if ((i & 15) == 0) {  // the scales of the warp's next 16 turns
-        const int mine = u + (w.lane >> 1) * 2 * kAtWarps + (w.lane & 1);
-        vs = 0.f;
-        if (mine < b2) {
-          ks = ksc[tile.block(mine)];
-          vs = vsc[tile.block(mine)];
-        }
+    for (int u = unit_at(0); u < b2; u = unit_at(++i)) {
+      if ((i & 15) == 0) {
+        ks = ks_next;
+        vs = vs_next;
+        scales(i + 16);
         const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vs)));
         if (top > 0.f) w.raise_unit(min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126));
         vs = vs > 0.f ? fmaxf(vs * pow2f(-w.unit), pow2f(-kUnitSpan)) : 1.f;  // a block of zeros: any scale does
@@ -554,12 +580,11 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
       if (w.lane == 0) atomicOr(c.ticket + c.batch, kAnomTimeout);
       // copies still in flight land before the ring is used again
       for (int j = 0; j < 2; ++j)
-        if (b0 + 2 * ((i + j) * kAtWarps + wid) < b2) bar_wait(&bar[(i + j) & 1], (phase >> ((i + j) & 1)) & 1);
+        if (unit_at(i + j) < b2) bar_wait(&bar[(i + j) & 1], (phase >> ((i + j) & 1)) & 1);
     }
     if (tail && wid == kAtWarps - 1) {
       W z = w;  // a copy: w itself stays in registers
-      z.tail_step((const char *)c.k_tail + slice * kBlock * kHeadDim * es, (const char *)c.v_tail + slice * kBlock * kHeadDim * es,
-                  tile.len - full * kBlock, full);
+      z.tail_step(kt, vt, tile.len - full * kBlock, full);
       w = z;
     }
 
@@ -782,9 +807,9 @@ static const char *plan_attend(const lkv_cache8 *c, int32_t group, int32_t n, in
   // Streamed where whole tiles would leave over two fifths of the GPU idle (in
   // their last wave) and are long enough to pay for the second kernel. On a
   // GB300, int8 and 4 query heads: 8 KV heads of 131,579 tokens 131 us as 64
-  // CTAs in clusters, 56 us streamed; 2 of 8,000 tokens 14.4 and 10.1 us; 160
+  // CTAs in clusters, 53 us streamed; 2 of 8,000 tokens 14.4 and 10.1 us; 160
   // of 33,000 tokens 306 and 220 us; but 64 of 33,000 tokens (256 CTAs in
-  // clusters) 90 and 105 us.
+  // clusters) 89 and 105 us.
   const int64_t ctas = p->tiles * p->cluster, last = ctas <= slots ? ctas : ctas % slots;
   if (ctas < 3 * slots && last > 0 && last * 5 < slots * 3 && blocks >= 24 * p->cluster &&
       (int64_t)c->batch * p->row_tiles <= kAtGroups) {
