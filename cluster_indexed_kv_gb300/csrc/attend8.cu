@@ -370,8 +370,7 @@ __device__ __forceinline__ void put_out(const AttendArgs &a, int64_t slice, int 
 // several CTAs share goes to the workspace in parts, and k_attend8_merge joins
 // them. No atomics in either: the same result each time.
 //
-// Bound by the codes' bytes (the products of a turn take a quarter of its copy's
-// time). On a GB300, 4 query heads, bf16: 64 slices of 33,000 tokens 89 us, 89%
+// Bound by the codes' bytes. On a GB300, 4 query heads, bf16: 64 slices of 33,000 tokens 89 us, 89%
 // of the measured copy rate; 8 of 131,579 tokens 53 us, 75% (a long merge); 256
 // slices of a window of 1024 tokens 19 us, 52%, and one of 2048 tokens 9 us:
 // those wait for a launch, lengths, queries, codes and the merges in turn.
