@@ -18,6 +18,7 @@ _FORMATS = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
 _D = 128
 _BLOCK = _lib.LKV_CACHE8_BLOCK
 _SCALE = _D ** -0.5
+_INT32 = 2 ** 31 - 1
 
 
 def _tensor(t, name, shape, dtype, index) -> int:
@@ -55,6 +56,8 @@ class Rope:
     def __init__(self, *, rotary_dim: int = _D, layout: str = "half", base: float = 10000.0,
                  scaling: str = "none", factor: float = 1.0, orig_len: int = 0,
                  beta_fast: float = 32.0, beta_slow: float = 1.0):
+        if not 0 <= rotary_dim <= _INT32 or not 0 <= orig_len <= _INT32:
+            raise ValueError("rotary_dim and orig_len must be in 0..2^31 - 1")
         lay = {"half": _lib.LKV_ROPE_HALF, "interleaved": _lib.LKV_ROPE_INTERLEAVED}[layout]
         how = {"none": _lib.LKV_ROPE_NONE, "linear": _lib.LKV_ROPE_LINEAR, "ntk": _lib.LKV_ROPE_NTK,
                "yarn": _lib.LKV_ROPE_YARN}[scaling]
@@ -225,6 +228,8 @@ class Cache8:
             op = out.data_ptr()
         else:
             op = _tensor(out, "out", shape, dt, dev)
+        if window > _INT32 or sinks > _INT32 or max_len > _INT32:
+            raise ValueError("window, sinks and max_len must be below 2^31")
         sizes = (group, n, window, sinks, max_len)
         ws_bytes = self._ws_bytes.get(sizes)
         if ws_bytes is None:

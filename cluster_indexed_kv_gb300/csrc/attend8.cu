@@ -900,7 +900,8 @@ extern "C" lkv_status lkv_cache8_attend(const lkv_cache8 *c, const void *q, int3
                                         void *stream) {
   using namespace lkv;
   if (const char *m = check_attend(c, group, n, window, sinks, max_len)) return refuse_in("lkv_cache8_attend", m);
-  if (!(scale - scale == 0.f)) return refuse("lkv_cache8_attend: scale is not finite");
+  const float scale_log2 = scale * kLog2e;
+  if (!(scale_log2 - scale_log2 == 0.f)) return refuse("lkv_cache8_attend: scale, or its product with log2(e), is not finite");
   if (n == 0) return LKV_OK;
   if (!q || !out) return refuse("lkv_cache8_attend: null queries or output");
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(counts, 4) || !aligned(workspace, 16))
@@ -930,7 +931,7 @@ extern "C" lkv_status lkv_cache8_attend(const lkv_cache8 *c, const void *q, int3
   a.group = group;
   a.window = window >= c->capacity ? 0 : window;  // a window that reaches everything is none
   a.sinks = sinks < c->capacity ? sinks : c->capacity;
-  a.scale_log2 = scale * kLog2e;
+  a.scale_log2 = scale_log2;
   a.row_tiles = p.rows ? 0 : p.row_tiles;
   a.streamed = p.ctas > 0;
   a.ws = (float *)workspace;

@@ -591,7 +591,7 @@ lkv_status lkv_cache8_read(const lkv_cache8 *cache, const int32_t *first, int32_
  * memory of at least lkv_cache8_attend_workspace bytes for the same sizes
  * (NULL when that is 0), not shared by calls that may overlap.
  * out may not overlap q or the cache. Asynchronous on stream. Errors:
- * LKV_EINVAL (scale not finite too), LKV_ECUDA. */
+ * LKV_EINVAL (also when scale * log2(e) is not finite), LKV_ECUDA. */
 lkv_status lkv_cache8_attend(const lkv_cache8 *cache, const void *q, int32_t group, int32_t n,
                              const int32_t *counts, float scale, int32_t window, int32_t sinks,
                              int32_t max_len, void *out, void *workspace, int64_t workspace_bytes,

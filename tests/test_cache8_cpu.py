@@ -140,7 +140,7 @@ def test_cache_calls_refuse_bad_arguments():
 
     assert attend(q=None) == E and attend(out=None) == E and attend(q=q + 4) == E and attend(out=o + 8) == E
     assert attend(group=0) == E and attend(group=129) == E and attend(n=-1) == E and attend(n=(1 << 24) + 1) == E
-    assert attend(scale=float("nan")) == E and attend(scale=float("inf")) == E
+    assert attend(scale=float("nan")) == E and attend(scale=float("inf")) == E and attend(scale=3e38) == E
     assert attend(window=-1) == E and attend(sinks=-1) == E and attend(max_len=-1) == E
     assert attend(counts=A + 2) == E and attend(out=q) == E and attend(out=A) == E and attend(out=5 * A) == E
     assert attend(counts=o) == E
@@ -149,6 +149,12 @@ def test_cache_calls_refuse_bad_arguments():
     assert attend(n=0) == _lib.LKV_OK
     assert L.lkv_cache8_write(v, None, None, 0, None, None, None) == _lib.LKV_OK
     assert L.lkv_cache8_read(v, None, 0, None, None, None) == _lib.LKV_OK
+
+
+def test_rope_refuses_sizes_past_32_bits():
+    for kw in (dict(rotary_dim=2 ** 32 + 64), dict(scaling="yarn", factor=2.0, orig_len=2 ** 32 + 8)):
+        with pytest.raises(ValueError):
+            lkv.Rope(**kw)
 
 
 def test_python_wrappers_refuse_host_tensors():

@@ -154,3 +154,12 @@ def test_rows_behind_a_sequence_and_garbage():
             scale[i, :, full:] = float("nan")
             tail[i, :, (m - 1) % 16 + 1:] = float("inf")
     assert torch.equal(c.attend(q.cuda(), counts=i32(*counts)), want)
+
+
+def test_refuses_sizes_past_32_bits():
+    c = lkv.Cache8(batch=1, n_kv_heads=1, capacity=32, dtype=BF16)
+    q = torch.zeros(1, 1, 1, 128, dtype=BF16, device="cuda")
+    for kw in (dict(window=2 ** 32 + 5), dict(sinks=2 ** 31), dict(max_len=2 ** 40)):
+        with pytest.raises(ValueError):
+            c.attend(q, **kw)
+    assert (c.attend(q, window=2 ** 31 - 1, sinks=2 ** 31 - 1, max_len=2 ** 31 - 1) == 0).all()
