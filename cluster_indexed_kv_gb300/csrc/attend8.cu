@@ -785,7 +785,7 @@ static const char *plan_attend(const lkv_cache8 *c, int32_t group, int32_t n, in
   // against this kernel's, in its steps, of which this one takes 0.4 for 16 rows
   // x 128 tokens on every SM and 3 to start. On a GB300, int8, 4 query heads,
   // this kernel's and its time: 64 slices of 32K tokens, 16 tokens each 363 and
-  // 292 us; 8 slices, 16 tokens 58 and 73 us, 32 tokens 101 and 72; 8 slices of
+  // 277 us; 8 slices, 16 tokens 58 and 73 us, 32 tokens 101 and 72; 8 slices of
   // 4096 tokens, 64 tokens 33 and 42 us; 64 slices of 256 tokens, 64 tokens 39
   // and 29 us.
   p->rows = false;

@@ -27,12 +27,17 @@ namespace lkv {
 // then the launch is streamed, all tiles' steps shared out evenly over a CTA an
 // SM, and the parts of tiles that several CTAs share are joined (rows_plan).
 //
-// Bound, a step of 256 rows: the products take 2048 clocks, the exponentials
-// (16 a clock and SM) 2048, and shared memory about 2000 (Q, K and V tiles
-// read by the products, K and V written); it takes about 4000, the products'
-// own chain (S, weights, P V, the next S in the same columns) 3000 of them.
-// 2048 tokens over 32K, 32 query and 8 KV heads on a GB300: 1021 us, 1.04
-// PFLOP/s, 55% of the measured bf16 rate.
+// Bound, a step of 256 rows: the products take 2048 clocks; shared memory about
+// 2000 (Q, K and V tiles read by the products, K and V written), the
+// exponentials (32 a clock and SM) 1024. It takes about 4000: nothing is
+// saturated (tensor pipe 44%, issue slots 41%), the chain of a row tile is as
+// long as that: S 650, weights 2150 (450 of them the first read of S), the
+// last half's P V 300, and the barriers between them, with the other row tile's
+// products in between. 2048 tokens over 32K, 32 query and 8 KV heads on a
+// GB300: 1035 us, 1.03 PFLOP/s, 54% of the measured bf16 rate. Slower: a row
+// tile's first softmax thread issuing its products (no issuing warp, 168
+// registers, 1214 us); S in halves of 64 tokens, each with its barrier (1135);
+// a quarter of the exponentials as polynomials (1086).
 constexpr int kRwTok = kRowsStep;                // tokens of a K / V tile
 constexpr int kRwBlocks = kRwTok / kBlock;
 constexpr int kRwRows = kRowsTile / 2;           // rows of a row tile
@@ -462,21 +467,24 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
 
     if (warp >= kRwProducer && warp < kRwIssuer) {
       // ---------------------------------------------------------------- producers
-      const int pw = warp - kRwProducer, pt = pw * 32 + lane;
+      const int pw = warp - kRwProducer;
       const uint8_t *kc = (const uint8_t *)c.k_codes + slice * c.capacity * kHeadDim;
       const uint8_t *vc = (const uint8_t *)c.v_codes + slice * c.capacity * kHeadDim;
-      const int ks_row = lane >> 2, ks_j = lane & 3;      // K: 8 rows x 4 runs of 16 a load
-      const int tc = pt & 15, dc = pt >> 4;               // V: tokens 8 tc.., d 16 dc..
+      // K: 4 whole rows a load, 16 codes a lane: a load takes a pass for each
+      // 128-byte line (8 half rows a load: 296 against 284 us for 32 tokens over
+      // 32K, 64 slices). V: tokens 8 tc.., d 16 dc.., which fills its tile
+      // without bank conflicts.
+      const int kr_row = lane >> 3, kr_half = (lane >> 2) & 1, kr_run = lane & 3;
+      const int tc = (pw * 32 + lane) & 15, dc = (pw * 32 + lane) >> 4;
       const float kf = pow2f(-ke), vf = pow2f(-max(ve, unit - kUnitSpan));
       uint4 kr[8], vr[8];
       auto load_k = [&](int j) {
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const int u = j * kRwBlocks + 2 * pw + (it >> 1), b = tile.block(u);
+        for (int t = 0; t < 8; ++t) {
+          const int u = j * kRwBlocks + 2 * pw + (t >> 2), b = tile.block(u);
           const bool there = u < tile.nb && b < full;
-          const uint8_t *p = kc + ((int64_t)b * kBlock + 8 * (it & 1) + ks_row) * kHeadDim + 16 * ks_j;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) kr[2 * it + h] = there ? __ldg((const uint4 *)(p + 64 * h)) : make_uint4(0, 0, 0, 0);
+          const uint8_t *p = kc + ((int64_t)b * kBlock + 4 * (t & 3) + kr_row) * kHeadDim + 16 * (lane & 7);
+          kr[t] = there ? __ldg((const uint4 *)p) : make_uint4(0, 0, 0, 0);
         }
       };
       auto load_v = [&](int j) {
@@ -513,20 +521,19 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
         if (!rows_wait_warp(&sy.kempty[st], ((g >> 1) & 1) ^ 1, &abort_s)) break;
         unsigned char *const kt = area + 2 * kRwTile + st * kRwTile, *const vt = area + 4 * kRwTile + st * kRwTile;
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const int r = 32 * pw + 8 * it + ks_row;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 w = kr[2 * it + h];
-            uint32_t x[8];
-            codes_row<CODE>(w.x, x[0], x[1]);
-            codes_row<CODE>(w.y, x[2], x[3]);
-            codes_row<CODE>(w.z, x[4], x[5]);
-            codes_row<CODE>(w.w, x[6], x[7]);
-            unsigned char *to = kt + h * kRwHalf + r * 128;
-            *(uint4 *)(to + (((2 * ks_j) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-            *(uint4 *)(to + (((2 * ks_j + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
-          }
+        for (int t = 0; t < 8; ++t) {
+          // a run's 16-byte chunks go to places 2 run and 2 run + 1, the second
+          // half's in the other order: 8 lanes fill 8 places of a row at a time
+          const int r = 32 * pw + 4 * t + kr_row;
+          const uint4 w = kr_half ? make_uint4(kr[t].z, kr[t].w, kr[t].x, kr[t].y) : kr[t];
+          uint32_t x[8];
+          codes_row<CODE>(w.x, x[0], x[1]);
+          codes_row<CODE>(w.y, x[2], x[3]);
+          codes_row<CODE>(w.z, x[4], x[5]);
+          codes_row<CODE>(w.w, x[6], x[7]);
+          unsigned char *to = kt + kr_half * kRwHalf + r * 128;
+          *(uint4 *)(to + (((2 * kr_run + kr_half) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+          *(uint4 *)(to + (((2 * kr_run + 1 - kr_half) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
         }
         if (j + 1 < s1) load_k(j + 1);
         const bool ends = tail && (j + 1) * kRwBlocks >= tile.nb;  // the step's last block is the partial one
@@ -859,8 +866,8 @@ __global__ void __launch_bounds__(256) k_attend8_rows_merge(const __grid_constan
 // shares the steps out evenly, for 6% slower ones and what a second beginning,
 // storing parts and joining them cost: 14 steps. Measured, int8, 4 query heads
 // a KV head, a CTA a tile and streamed: 2048 tokens over 32K, 8 KV heads (256
-// tiles) 1131 and 1021 us, 4 KV heads 586 and 543; 64 tokens over 32K, 64
-// slices 575 and 325, 8 slices 564 and 78; 2048 over 4K, 4 KV heads 96 and 115;
+// tiles) 1131 and 1035 us, 4 KV heads 586 and 541; 64 tokens over 32K, 64
+// slices 575 and 300, 8 slices 564 and 78; 2048 over 4K, 4 KV heads 96 and 115;
 // 256 slices of a window of 1024, 64 tokens 111 and 145.
 double rows_plan(const lkv_cache8 &c, int64_t rows, int64_t tokens, int64_t steps, int sms, int *ctas) {
   const int64_t row_tiles = (rows + 2 * kRwRows - 1) / (2 * kRwRows), tiles = (int64_t)c.batch * c.n_kv_heads * row_tiles;
