@@ -19,6 +19,19 @@ _D = 128
 _BLOCK = _lib.LKV_CACHE8_BLOCK
 _SCALE = _D ** -0.5
 _INT32 = 2 ** 31 - 1
+# torch's allocation on the current CUDA device without its dispatcher, where
+# this build of torch has it: a small call costs less than its outputs did
+# (from call to call, 16 rows read back 11.7 -> 7.1 us, an attention 11.3 -> 8.1)
+_empty_here = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
+_empty_here = getattr(_empty_here, "_empty_strided_cuda", None)
+
+
+def _empty(shape, dtype, index) -> torch.Tensor:
+    """A new contiguous tensor of shape (a tuple) [B, H, n, 128] on CUDA device `index`."""
+    if _empty_here is not None and torch._C._cuda_getDevice() == index:
+        row = shape[2] * _D
+        return _empty_here(shape, (shape[1] * row, row, _D, 1), dtype)
+    return torch.empty(shape, dtype=dtype, device=f"cuda:{index}")
 
 
 def _tensor(t, name, shape, dtype, index) -> int:
@@ -84,7 +97,7 @@ class Rope:
             raise ValueError("q must be contiguous")
         pp = _tensor(positions, "positions", (batch, n), torch.int32, dev)
         if q_out is None:
-            q_out = torch.empty_like(q)
+            q_out = _empty((batch, heads, n, _D), dt, dev)
             qo = q_out.data_ptr()
         else:
             qo = _tensor(q_out, "q_out", q_shape, dt, dev)
@@ -97,7 +110,7 @@ class Rope:
             shape = (batch, kv_heads, n, _D)
             kp = _tensor(k, "k", shape, dt, dev)
             if k_out is None:
-                k_out = torch.empty_like(k)
+                k_out = _empty(shape, dt, dev)
                 ko = k_out.data_ptr()
             else:
                 ko = _tensor(k_out, "k_out", shape, dt, dev)
@@ -195,9 +208,9 @@ class Cache8:
         dev, dt = self._index, self.dtype
         shape = (self.batch, self.n_kv_heads, n, _D)
         if k_out is None:
-            k_out = torch.empty(shape, dtype=dt, device=self.device)
+            k_out = _empty(shape, dt, dev)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=dt, device=self.device)
+            v_out = _empty(shape, dt, dev)
         kp, vp = _tensor(k_out, "k_out", shape, dt, dev), _tensor(v_out, "v_out", shape, dt, dev)
         fp = None if first is None else _tensor(first, "first", (self.batch,), torch.int32, dev)
         _call(dev, self._read, self._at, fp, n, kp, vp)
@@ -224,7 +237,7 @@ class Cache8:
         qp = _tensor(q, "q", shape, dt, dev)
         cp = None if counts is None else _tensor(counts, "counts", (self.batch,), torch.int32, dev)
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty(shape, dt, dev)
             op = out.data_ptr()
         else:
             op = _tensor(out, "out", shape, dt, dev)

@@ -163,3 +163,23 @@ def test_refuses_sizes_past_32_bits():
         with pytest.raises(ValueError):
             c.attend(q, **kw)
     assert (c.attend(q, window=2 ** 31 - 1, sinks=2 ** 31 - 1, max_len=2 ** 31 - 1) == 0).all()
+
+
+def test_outputs_without_the_short_allocation(monkeypatch):
+    """A torch without it gives the same outputs, with the same layout."""
+    from cluster_indexed_kv_gb300 import cache8
+    g = gen(51)
+    x, y = rows(g, 2, 2, 40, BF16), rows(g, 2, 2, 40, BF16)
+    c, _, _ = make(x, y, "int8", BF16, 48, [40, 33])
+    q = torch.randn(2, 8, 3, 128, generator=g).to(BF16).cuda()
+    r, pos = lkv.Rope(), torch.arange(6, dtype=torch.int32, device="cuda").view(2, 3)
+    k = q[:, :2].contiguous()
+
+    def run():
+        return [*c.read(40), c.attend(q), *r.apply(q, pos, k), r.apply(q, pos)]
+
+    one = run()
+    monkeypatch.setattr(cache8, "_empty_here", None)
+    for a, b in zip(one, run()):
+        assert torch.equal(a, b) and a.stride() == b.stride() and a.dtype == b.dtype and a.device == b.device
+        assert a.is_contiguous()
