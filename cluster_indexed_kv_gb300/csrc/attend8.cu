@@ -412,6 +412,8 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
     }
   }
   __syncwarp();
+  wait_prerequisites();
+  if (a.streamed) launch_dependents();
   uint32_t phase = 0;      // parities of the two barriers
   bool dead = false;       // a copy did not arrive in time: the warp takes no more
   const int64_t es = DT == 1 ? 2 : 4;
@@ -421,7 +423,6 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
     stream.fill(a, RT, 1, 0);
     stream.share(G, x0, x1);
   }
-  launch_dependents();
   for (int64_t x = x0; x < x1;) {
     Tile tile;
     int64_t slice;
@@ -696,7 +697,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_attend8_merge(const __grid_co
   __shared__ float total_l, unit;
   __shared__ int range[3];
   const int G = a.c.batch * a.row_tiles, row = blockIdx.y;
-  stream.fill(a, RT, 1, 0);  // the lengths and counts are inputs: not the first kernel's
+  stream.fill(a, RT, 1, 0);  // the lengths and counts are inputs, written before the first kernel's wait was over
   const int gi = blockIdx.x / a.c.n_kv_heads, h = blockIdx.x % a.c.n_kv_heads;
   const int b = gi % a.c.batch, rt = gi / a.c.batch;
   const int64_t slice = (int64_t)b * a.c.n_kv_heads + h;
@@ -835,20 +836,20 @@ static cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, const
   cfg.blockDim = dim3(kAtThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = p.ctas ? 0 : 1;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.ctas ? 1 : 2;
   e = cudaLaunchKernelEx(&cfg, fn, a, km, vm);
   if (e != cudaSuccess || !p.ctas) return e;
   cfg.gridDim = dim3((unsigned)p.tiles, 8 * NT);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
   return cudaLaunchKernelEx(&cfg, k_attend8_merge<DT, NT>, a, p.ctas);
 }
 

@@ -301,6 +301,8 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = a.n * a.group, G = c.batch * a.row_tiles;
 
+  wait_prerequisites();
+  if constexpr (STREAMED) launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       bar_init(&sy.kfull[i], 4);
@@ -347,7 +349,6 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
       *(RowsJoin *)(a.ws + 2 * (int64_t)gridDim.x * kRwSlot + blockIdx.x * (sizeof(RowsJoin) / 4)) = join;
     }
     __syncthreads();
-    launch_dependents();
   }
   while (!STREAMED || seg.x < seg.end) {
     if (threadIdx.x == 0) {
@@ -894,19 +895,9 @@ cudaError_t launch_attend_rows(const AttendArgs &in, int ctas, cudaStream_t st) 
                                        : (ctas ? k_attend8_rows<LKV_CODE_E4M3, true> : k_attend8_rows<LKV_CODE_E4M3, false>);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRwSmem);
   if (e != cudaSuccess) return e;
-  fn<<<(unsigned)(ctas ? ctas : tiles), kRwThreads, kRwSmem, st>>>(a);
-  e = cudaGetLastError();
+  e = launch_next(fn, dim3((unsigned)(ctas ? ctas : tiles)), kRwThreads, kRwSmem, st, a);
   if (e != cudaSuccess || !ctas) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas, 2 * kRwRows / kRwMergeRows);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attend8_rows_merge, a);
+  return launch_next(k_attend8_rows_merge, dim3((unsigned)ctas, 2 * kRwRows / kRwMergeRows), 256, 0, st, a);
 }
 
 }  // namespace lkv

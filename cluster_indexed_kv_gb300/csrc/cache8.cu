@@ -301,6 +301,8 @@ struct WriteArgs {
 // Bound: bytes (2 or 4 in, 1 out a value).
 template <int DT, int CODE>
 __global__ void __launch_bounds__(kCacheThreads, DT == 1 ? 6 : 3) k_cache8_write(const __grid_constant__ WriteArgs a) {
+  wait_prerequisites();
+  launch_dependents();
   const int64_t task = (int64_t)blockIdx.x * kCacheWarps + threadIdx.x / 32;
   if (task >= a.tasks) return;
   const lkv_cache8 &c = a.c;
@@ -383,6 +385,7 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
 template <int DT, int CODE>
 __global__ void __launch_bounds__(kCacheThreads) k_cache8_read(const __grid_constant__ ReadArgs a) {
   constexpr int E = DT == 1 ? 8 : 4, LPR = kHeadDim / E, RPL = 32 / LPR, NL = kBlock / RPL;
+  wait_prerequisites();
   const int64_t task = (int64_t)blockIdx.x * kCacheWarps + threadIdx.x / 32;
   if (task >= a.tasks) return;
   const lkv_cache8 &c = a.c;
@@ -476,11 +479,10 @@ extern "C" lkv_status lkv_cache8_write(const lkv_cache8 *c, const void *k, const
   if (blocks > 0x7fffffff) return refuse("lkv_cache8_write: too many rows");
   cudaStream_t st = (cudaStream_t)stream;
   const bool bf = c->dtype == LKV_DTYPE_BF16, i8 = c->code == LKV_CODE_INT8;
-  if (bf && i8) k_cache8_write<1, LKV_CODE_INT8><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
-  else if (bf) k_cache8_write<1, LKV_CODE_E4M3><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
-  else if (i8) k_cache8_write<0, LKV_CODE_INT8><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
-  else k_cache8_write<0, LKV_CODE_E4M3><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
-  e = cudaGetLastError();
+  if (bf && i8) e = launch_next(k_cache8_write<1, LKV_CODE_INT8>, dim3((unsigned)blocks), kCacheThreads, 0, st, a);
+  else if (bf) e = launch_next(k_cache8_write<1, LKV_CODE_E4M3>, dim3((unsigned)blocks), kCacheThreads, 0, st, a);
+  else if (i8) e = launch_next(k_cache8_write<0, LKV_CODE_INT8>, dim3((unsigned)blocks), kCacheThreads, 0, st, a);
+  else e = launch_next(k_cache8_write<0, LKV_CODE_E4M3>, dim3((unsigned)blocks), kCacheThreads, 0, st, a);
   return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_write", e);
 }
 
@@ -512,12 +514,12 @@ extern "C" lkv_status lkv_cache8_read(const lkv_cache8 *c, const int32_t *first,
   const int64_t blocks = (a.tasks + kCacheWarps - 1) / kCacheWarps;
   if (blocks > 0x7fffffff) return refuse("lkv_cache8_read: too many rows");
   cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e;
   const bool bf = c->dtype == LKV_DTYPE_BF16, i8 = c->code == LKV_CODE_INT8;
-  if (bf && i8) k_cache8_read<1, LKV_CODE_INT8><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
-  else if (bf) k_cache8_read<1, LKV_CODE_E4M3><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
-  else if (i8) k_cache8_read<0, LKV_CODE_INT8><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
-  else k_cache8_read<0, LKV_CODE_E4M3><<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  if (bf && i8) e = launch_next(k_cache8_read<1, LKV_CODE_INT8>, dim3((unsigned)blocks), kCacheThreads, 0, st, a);
+  else if (bf) e = launch_next(k_cache8_read<1, LKV_CODE_E4M3>, dim3((unsigned)blocks), kCacheThreads, 0, st, a);
+  else if (i8) e = launch_next(k_cache8_read<0, LKV_CODE_INT8>, dim3((unsigned)blocks), kCacheThreads, 0, st, a);
+  else e = launch_next(k_cache8_read<0, LKV_CODE_E4M3>, dim3((unsigned)blocks), kCacheThreads, 0, st, a);
   return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_read", e);
 }
 

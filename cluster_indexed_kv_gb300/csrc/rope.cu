@@ -108,6 +108,8 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ R
   __shared__ uint64_t turn[64];
   if (threadIdx.x < 64) turn[threadIdx.x] = a.r.turn[threadIdx.x];
   __syncthreads();
+  wait_prerequisites();
+  launch_dependents();
   const int64_t id = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
   const int64_t tok = id / P::TPR;
   if (tok >= a.tokens) return;
@@ -173,8 +175,7 @@ static cudaError_t launch_rope(RopeArgs &a, cudaStream_t st) {
   a.per = (int)((all + want - 1) / want);
   const int gy = (all + a.per - 1) / a.per;
   if (gy > 65535) return cudaErrorInvalidValue;
-  k_rope<DT, INTER, WIDE><<<dim3((unsigned)blocks, (unsigned)gy), kRopeThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_next(k_rope<DT, INTER, WIDE>, dim3((unsigned)blocks, (unsigned)gy), kRopeThreads, 0, st, a);
 }
 
 }  // namespace lkv

@@ -51,11 +51,6 @@ __device__ __forceinline__ void tma_prefetch(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)map) : "memory");
 }
 
-// Programmatic dependent launch: the next kernel may start, and: everything
-// the previous kernel wrote is visible.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // cuTensorMapEncodeTiled through the runtime's driver entry point.
 inline PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

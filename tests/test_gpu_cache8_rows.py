@@ -183,3 +183,46 @@ def test_outputs_without_the_short_allocation(monkeypatch):
     for a, b in zip(one, run()):
         assert torch.equal(a, b) and a.stride() == b.stride() and a.dtype == b.dtype and a.device == b.device
         assert a.is_contiguous()
+
+
+@pytest.mark.parametrize("b,start,n,steps", [(1, 0, 6000, 12), (4, 8000, 1, 40), (16, 300, 48, 6)])
+def test_calls_back_to_back(b, start, n, steps):
+    """Rotate, write, attend and read in a row, each on what the one before it
+    has just made: launches may overlap, accesses may not."""
+    g = gen(61)
+    total = start + n * steps + 16
+    q = torch.randn(b, 8, n, 128, generator=g).to(BF16).cuda()
+    k, v = (torch.randn(b, 2, n, 128, generator=g).to(BF16).cuda() for _ in range(2))
+    k0, v0 = (torch.randn(b, 2, max(start, 1), 128, generator=g).to(BF16).cuda() for _ in range(2))
+    r = lkv.Rope()
+
+    def run(pause):
+        c = lkv.Cache8(batch=b, n_kv_heads=2, capacity=(total + 15) // 16 * 16, dtype=BF16)
+        got = []
+        if start:
+            c.write(k0, v0)
+        x, y, z = q, k, v
+        for i in range(steps):
+            pos = (torch.arange(n, dtype=torch.int32, device="cuda") + c.lengths[:, None]).to(torch.int32)
+            pause()
+            x, y = r.apply(x, pos, y)
+            pause()
+            c.write(y, z)
+            pause()
+            x = c.attend(x, window=0 if i % 2 else 700, sinks=3)
+            pause()
+            y, z = c.read(n, first=c.lengths - n)
+            pause()
+            got.append(x)
+        c.check()
+        return got + [y, z, c.k_codes, c.k_tail, c.lengths]
+
+    one = run(torch.cuda.synchronize)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(stream):
+            two = run(lambda: None)
+        torch.cuda.synchronize()
+        for a, b2 in zip(one, two):
+            assert torch.equal(a.view(torch.uint8), b2.view(torch.uint8))
