@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
       slice = id % S;
       rt = a.row_tiles - 1 - (int)(id / S);  // the rows with most to see come first
       tile = Tile(a, (int)((id % S) / c.n_kv_heads), rt, RT);
-      b0 = (int)((uint32_t)tile.nb * part / parts);  // at most 8 x 2^27
+      b0 = (int)((uint32_t)tile.nb * part / parts);  // at most 8 x 2^26
       b1 = (int)((uint32_t)tile.nb * (part + 1) / parts);
       x = x1;
     }

