@@ -34,7 +34,7 @@ namespace lkv {
 // long as that: S 650, weights 2150 (450 of them the first read of S), the
 // last half's P V 300, and the barriers between them, with the other row tile's
 // products in between. 2048 tokens over 32K, 32 query and 8 KV heads on a
-// GB300: 1035 us, 1.03 PFLOP/s, 54% of the measured bf16 rate. Slower: a row
+// GB300: 1030 us, 1.03 PFLOP/s, 54% of the measured bf16 rate. Slower: a row
 // tile's first softmax thread issuing its products (no issuing warp, 168
 // registers, 1214 us); S in halves of 64 tokens, each with its barrier (1135);
 // a quarter of the exponentials as polynomials (1086).
@@ -665,10 +665,12 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
       bool seen = !valid;
       bool ok = true;
       for (int g = done; ok && g < done + steps; ++g) {
-        ok = rows_wait_warp(&sy.scfull[g & 3], (g >> 2) & 1, &abort_s) && rows_wait_warp(&sy.sfull[w], g & 1, &abort_s);
+        ok = rows_wait_warp(&sy.scfull[g & 3], (g >> 2) & 1, &abort_s);
+        if (!ok) break;
+        const bool open = __float_as_int(scales[g & 3][0].w) >= first && __float_as_int(scales[g & 3][kRwBlocks - 1].w) <= last;
+        ok = rows_wait_warp(&sy.sfull[w], g & 1, &abort_s);
         if (!ok) break;
         tmem_after();
-        const bool open = __float_as_int(scales[g & 3][0].w) >= first && __float_as_int(scales[g & 3][kRwBlocks - 1].w) <= last;
         float sum = 0.f;
         uint32_t r[32];
         tmem_ld32(s_at, r);
@@ -867,7 +869,7 @@ __global__ void __launch_bounds__(256) k_attend8_rows_merge(const __grid_constan
 // shares the steps out evenly, for 6% slower ones and what a second beginning,
 // storing parts and joining them cost: 14 steps. Measured, int8, 4 query heads
 // a KV head, a CTA a tile and streamed: 2048 tokens over 32K, 8 KV heads (256
-// tiles) 1131 and 1035 us, 4 KV heads 586 and 541; 64 tokens over 32K, 64
+// tiles) 1131 and 1030 us, 4 KV heads 586 and 541; 64 tokens over 32K, 64
 // slices 575 and 300, 8 slices 564 and 78; 2048 over 4K, 4 KV heads 96 and 115;
 // 256 slices of a window of 1024, 64 tokens 111 and 145.
 double rows_plan(const lkv_cache8 &c, int64_t rows, int64_t tokens, int64_t steps, int sms, int *ctas) {
