@@ -510,7 +510,11 @@ lkv_status lkv_rope_init(const lkv_rope_params *params, lkv_rope *rope);
  * is fp32, rounded once. q_out may be q and k_out may be k (in place); any
  * other overlap of an output with an input or output is LKV_EINVAL. batch, n
  * and the head counts may be 0. *rope is read before the call returns.
- * Asynchronous on stream. Errors: LKV_EINVAL, LKV_ECUDA. */
+ * Asynchronous on stream. Errors: LKV_EINVAL, LKV_ECUDA.
+ * The kernels of lkv_rope_apply and lkv_cache8_write let a following kernel
+ * that is launched with programmatic stream serialization start before they
+ * end: such a kernel has to wait (griddepcontrol.wait) before it touches their
+ * tensors. Every other launch, copy and event comes after them as usual. */
 lkv_status lkv_rope_apply(const lkv_rope *rope, int32_t dtype, int32_t batch, int32_t n_heads,
                           int32_t n_kv_heads, int32_t n, const void *q, const void *k,
                           const int32_t *positions, void *q_out, void *k_out, void *stream);
