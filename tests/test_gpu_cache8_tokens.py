@@ -1,0 +1,122 @@
+"""Attention over the 8-bit cache, token by token: every output held to a bound
+of its own, and outputs that show a token lost or counted twice."""
+import pytest
+import torch
+
+import cluster_indexed_kv_gb300 as lkv
+from tests import _cache8_each as each
+from tests import _cache8_ref as ref
+from tests.test_gpu_cache8 import DTYPES, FMTS, gen, i32, make, rows
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    lkv.build()
+
+
+def check_each(c, k, v, lengths, q, *, counts=None, scale=None, window=0, sinks=0, max_len=0):
+    got = c.attend(q.cuda(), counts=None if counts is None else i32(*counts), scale=scale, window=window, sinks=sinks, max_len=max_len)
+    n = q.shape[2]
+    for b, length in enumerate(lengths):
+        kk, vv = (ref.values(a[0][b], a[1][b], a[2][b], length) for a in (k, v))
+        cnt = n if counts is None else min(max(counts[b], 0), n)
+        want, lim = each.attend(q[b].double(), kk, vv, each.units(v[1][b], v[2][b], length), cnt, 128 ** -0.5 if scale is None else scale,
+                                window, sinks, q.dtype)
+        err = (got[b].cpu().double() - want).abs()
+        assert torch.isfinite(got[b]).all() and (err <= lim).all(), \
+            f"sequence {b} of length {length}: off by {err.max():.3e}, {(err / lim.clamp_min(1e-300)).max():.2f} of the bound"
+
+
+# ---------------------------------------------------------------- every output by itself
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lengths,h,group,n,window,sinks", [
+    ([1, 17, 300, 640, 0], 2, 4, 1, 0, 0), ([333, 64, 500], 2, 3, 5, 0, 0), ([700, 650], 1, 8, 3, 100, 20), ([400, 31] * 32, 2, 4, 30, 0, 0),
+    ([260, 400] * 32, 2, 2, 64, 90, 5), ([900], 2, 4, 300, 0, 0)])
+def test_every_output(fmt, dtype, lengths, h, group, n, window, sinks):
+    g = gen(sum(lengths) + n)
+    b, top = len(lengths), max(lengths)
+    x, y = rows(g, b, h, top, dtype), rows(g, b, h, top, dtype)
+    c, k, v = make(x, y, fmt, dtype, (top + 15) // 16 * 16, lengths, garbage=g)
+    q = torch.randn(b, h * group, n, 128, generator=g).to(dtype)
+    check_each(c, k, v, lengths, q, window=window, sinks=sinks, counts=[min(n, m) for m in lengths])
+
+
+# ---------------------------------------------------------------- tokens counted
+
+COUNTED = [([40000, 3, 20011], 1, 4, 1, 0, 0), ([9000], 1, 1, 1, 0, 0), ([131000], 2, 4, 1, 0, 0), ([33001, 32964] * 4, 8, 4, 1, 0, 0),
+           ([30000, 29000], 2, 8, 2, 9000, 100), ([5000, 4999, 17, 0], 40, 1, 1, 0, 0), ([2100, 1033] * 8, 8, 2, 1, 1024, 4),
+           ([20001], 2, 4, 128, 0, 0), ([9000, 130, 20000], 1, 8, 100, 0, 0), ([30000, 5000], 2, 4, 200, 9000, 100), ([700, 640] * 32, 2, 4, 64, 0, 0),
+           ([1000, 555] * 32, 2, 4, 64, 300, 20)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lengths,h,group,n,window,sinks", COUNTED)
+def test_blocks_are_counted_once(fmt, dtype, lengths, h, group, n, window, sinks):
+    """Equal scores and values that name their block: an output is the count of
+    the visible tokens of its blocks times their height, over the count of all."""
+    if dtype == torch.float32 and n * group * len(lengths) * h > 4096:
+        pytest.skip("fp32 has one kernel: its other cases take it")
+    b, top = len(lengths), max(lengths)
+    y = each.one_hot(top, dtype).expand(b, h, top, 128)
+    c, k, v = make(torch.zeros(1, 1, top, 128, dtype=dtype).expand(b, h, top, 128), y, fmt, dtype, (top + 31) // 16 * 16, lengths, garbage=gen(2))
+    q = torch.randn(b, h * group, n, 128, generator=gen(3)).to(dtype)
+    got = c.attend(q.cuda(), window=window, sinks=sinks, counts=i32(*[min(n, m) for m in lengths])).cpu().double()
+    value = each.one_hot(top, torch.float64)
+    total = torch.cat((torch.zeros(1, 128, dtype=torch.float64), value.cumsum(0)))
+    for i, length in enumerate(lengths):
+        for r in range(min(n, length)):
+            pos = length - min(n, length) + r
+            low = max(0, pos + 1 - window) if window else 0
+            first = min(sinks, low)
+            want = (total[pos + 1] - total[low] + total[first]) / (pos + 1 - low + first)
+            err = (got[i, :, r] - want).abs()
+            assert (err <= each.one_hot_bound(want, dtype, length)).all(), \
+                f"sequence {i}, row {r}: channels {(err > each.one_hot_bound(want, dtype, length)).any(0).nonzero().flatten().tolist()[:8]}"
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lengths,h,group,n", [([40000, 20011], 2, 16, 1), ([131000], 8, 4, 1), ([33001] * 8, 8, 4, 1), ([20001], 2, 4, 32), ([700] * 64, 2, 4, 32)])
+def test_a_loud_token_is_found(fmt, dtype, lengths, h, group, n):
+    """Each row favours one token above all others, the first or the last of a
+    block, block after block: its output is that token's value."""
+    if dtype == torch.float32 and n > 1:
+        pytest.skip("fp32 has one kernel: its other cases take it")
+    b, top, per = len(lengths), max(lengths), n * group
+    g = gen(8)
+    small = torch.randn(b, 1, top, 128, generator=g).to(dtype)
+    zeros = torch.zeros(b, h, top, 128, dtype=dtype)
+    v = ref.held(small.expand(b, h, top, 128), fmt, dtype, (top + 15) // 16 * 16, lengths)
+    vv = [ref.values(v[0][i, :1], v[1][i, :1], v[2][i, :1], m)[0] for i, m in enumerate(lengths)]
+    for turn in range(3):
+        x, q = zeros.clone(), torch.zeros(b, h * group, n, 128, dtype=dtype)
+        hot = torch.zeros(b, h, per, dtype=torch.long)
+        for i, m in enumerate(lengths):
+            last = m - n  # every row sees it
+            blocks = torch.randperm(max(last // 16, 1), generator=g)
+            for j in range(h):
+                for r in range(per):
+                    z = ((j * per + r) + turn * h * per) % len(blocks)
+                    hot[i, j, r] = min(int(blocks[z]) * 16 + (15 if (r + turn) % 2 else 0), last) if r else last - turn
+                    x[i, j, hot[i, j, r], r % 128] = 64.0
+                    q[i, j * group + r % group, r // group, r % 128] = 64.0
+        k = ref.held(x, fmt, dtype, (top + 15) // 16 * 16, lengths)
+        c = lkv.Cache8.from_tensors(*(t.cuda() for pair in zip(k, v) for t in pair), i32(*lengths))
+        got = c.attend(q.cuda()).cpu().double()
+        for i in range(b):
+            for j in range(h):
+                for r in range(per):
+                    same = [s for s in range(r % 128, per, 128)]  # rows that share the channel share their tokens
+                    if len({int(hot[i, j, s]) for s in same}) > 1:
+                        continue
+                    want = vv[i][hot[i, j, r]]
+                    err = (got[i, j * group + r % group, r // group] - want).abs()
+                    # the weight of the token is 2^(y - reference): in fp16 off by 2^-11; the others' are below 2^-500
+                    lim = want.abs() * (2.0 ** -11 + 2.0 ** -16 + ref.half_step(dtype) * 1.01) + 2.0 ** -24 * vv[i].abs().max()
+                    assert (err <= lim).all(), f"sequence {i}, KV head {j}, row {r}: token {int(hot[i, j, r])}"
