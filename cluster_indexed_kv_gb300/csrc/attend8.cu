@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
         scales(i + 16);
         const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vs)));
         if (top > 0.f) w.raise_unit(min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126));
-        vs = vs > 0.f ? fmaxf(vs * pow2f(-w.unit), pow2f(-kUnitSpan)) : 1.f;  // a block of zeros: any scale does
+        vs = fmaxf(vs * pow2f(-w.unit), pow2f(-kUnitSpan));  // a scale of 0 too: its codes stand for zeros, whatever they are
         lu = log2f(vs);
         vs = 1.f / vs;
       }

@@ -12,7 +12,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 6.f;
 constexpr float kSlack = 8.f;
 constexpr int kNoUnit = -1000;
-constexpr int kUnitSpan = 90;  // V scales below 2^-90 of the largest are taken for that
+// V scales below 2^-90 of the largest are taken for that, 0 among them (a scale
+// of 0 may stand over codes that are not: those of values too small for it).
+constexpr int kUnitSpan = 90;
 
 struct AttendArgs {
   lkv_cache8 c;

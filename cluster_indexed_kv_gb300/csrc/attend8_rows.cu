@@ -510,8 +510,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
               float k = pow2f(ke), v = pow2f(max(ve, unit - kUnitSpan) - unit);
               if (b < full) {
                 k = ksc[b];
-                v = vsc[b];
-                v = v > 0.f ? fmaxf(v * pow2f(-unit), pow2f(-kUnitSpan)) : 1.f;
+                v = fmaxf(vsc[b] * pow2f(-unit), pow2f(-kUnitSpan));
               }
               s = make_float4(k, log2f(v), 1.f / v, __int_as_float(b * kBlock));
             }

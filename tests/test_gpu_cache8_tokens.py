@@ -1,5 +1,6 @@
 """Attention over the 8-bit cache, token by token: every output held to a bound
-of its own, and outputs that show a token lost or counted twice."""
+of its own, outputs that show a token lost or counted twice, and V units of any
+size beside one another."""
 import pytest
 import torch
 
@@ -28,6 +29,46 @@ def check_each(c, k, v, lengths, q, *, counts=None, scale=None, window=0, sinks=
         err = (got[b].cpu().double() - want).abs()
         assert torch.isfinite(got[b]).all() and (err <= lim).all(), \
             f"sequence {b} of length {length}: off by {err.max():.3e}, {(err / lim.clamp_min(1e-300)).max():.2f} of the bound"
+
+
+# ---------------------------------------------------------------- V units
+
+# A V scale of 0 stands for values of 0 whatever the codes are: by the
+# definition of reading back, code * scale.
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("b,n", [(3, 1), (64, 64)])
+def test_scale_of_zero_over_codes(fmt, dtype, b, n):
+    """In a cache made elsewhere; the many rows of 64 sequences go to their own kernel (bf16)."""
+    g = gen(b)
+    lengths = [200, 217, 96][:b] if b < 4 else torch.randint(70, 220, (b,), generator=g).tolist()
+    x, y = (torch.randn(b, 2, 224, 128, generator=g).to(dtype) for _ in range(2))
+    k, v = (ref.held(z, fmt, dtype, 224, lengths) for z in (x, y))
+    v[1][:, 0, 1] = 0
+    v[1][:, 1, 2:5] = 0
+    k[1][:, 1, 3] = 0
+    c = lkv.Cache8.from_tensors(*(t.cuda() for pair in zip(k, v) for t in pair), i32(*lengths))
+    q = torch.randn(b, 8, n, 128, generator=g).to(dtype)
+    check_each(c, k, v, lengths, q)
+    check_each(c, k, v, lengths, q, window=60, sinks=20)
+    if b < 4:  # every V scale: nothing but the tail is left
+        v[1][:] = 0
+        c.v_scale.zero_()
+        check_each(c, k, v, lengths, q)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_written_values_whose_scale_rounds_to_zero(fmt):
+    """fp32 values so small that amax / 127 rounds to 0 beside ordinary ones: read and attended alike."""
+    x = torch.randn(1, 2, 100, 128, generator=gen(4))
+    x[:, :, 16:48] = x[:, :, 16:48].clamp(-2, 2) * 1e-44
+    c = lkv.Cache8(batch=1, n_kv_heads=2, capacity=112, dtype=torch.float32, fmt=fmt)
+    c.write(x.cuda(), x.cuda())
+    arrays = ref.held(x, fmt, torch.float32, 112, [100])
+    assert (arrays[1][:, :, 1:3] == 0).all()
+    assert (c.read(100)[1][:, :, 16:48] == 0).all()
+    check_each(c, arrays, arrays, [100], torch.randn(1, 8, 2, 128, generator=gen(5)))
 
 
 # ---------------------------------------------------------------- every output by itself
