@@ -45,17 +45,34 @@ struct Warp {
   int pmin, pmax, window, sinks;
   int open0, open1;           // blocks [open0, open1) are visible to every row as a whole
 
-  // V scales up to 2^(e + 1) are to come: o counts in units of 2^(ref + unit), l in units of 2^ref.
+  // V scales up to 2^(e + 1) are to come: o counts in units of 2^(ref + unit), l
+  // in units of 2^ref. Weights carry the scales, so those of all scales known
+  // so far shrink as the unit grows: the references go down by as much, which
+  // leaves y and o as they are, as far as l (2^100, with room for weights over
+  // the smallest scales) allows; o takes the rest. Without that, tokens beside
+  // a block of far larger values lost their weights. Rows that are not there
+  // keep their reference: their y follows no score.
   __device__ __forceinline__ void raise_unit(int e) {
     if (e <= unit) return;
-    const float k = unit == kNoUnit ? 1.f : exp2f((float)(unit - e));
+    const int by = unit == kNoUnit ? 0 : e - unit;
     unit = e;
+    if (by == 0) return;
 #pragma unroll
-    for (int r = 0; r < NT; ++r)
+    for (int r = 0; r < NT; ++r) {
+      float m = l[r];
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int room = 226 - (int)(__float_as_uint(m) >> 23);  // l < 2^(e - 126) of its exponent field e
+      const int down = pos[r] < 0 ? 0 : max(0, min(by, room));
+      ref[r] -= (float)down;
+      l[r] *= pow2f(down);
+      const float k = exp2f((float)(down - by));
+      const float ka = __shfl_sync(0xffffffffu, k, 8 * t), kb = __shfl_sync(0xffffffffu, k, 8 * t + 4);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[r][i][c] *= k;
+      for (int i = 0; i < 8; ++i) {
+        o[r][i][0] *= ka; o[r][i][1] *= kb; o[r][i][2] *= ka; o[r][i][3] *= kb;
+      }
+    }
   }
 
   // Scores of NB blocks, masked, turned into weights; the reference moves if

@@ -71,6 +71,58 @@ def test_written_values_whose_scale_rounds_to_zero(fmt):
     check_each(c, arrays, arrays, [100], torch.randn(1, 8, 2, 128, generator=gen(5)))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("at,order,less", [(300, 40, 60), (300, 60, 30), (300, 20, 300), (511, 40, 50), (2, 80, 100), ("tail", 40, 60),
+                                           ("tail", 30, 35), ("tail", 80, 70)])
+def test_a_block_of_far_larger_values(dtype, fmt, at, order, less):
+    """One block, or the tail, holds values 2^order times the others' in tokens
+    that weigh 2^-less: what the other tokens before and after it add stays."""
+    n = 8192 + 5
+    x, y = torch.zeros(1, 1, n, 128), torch.randn(1, 1, n, 128, generator=gen(at if at != "tail" else 7)).abs() + 0.5
+    big = slice(n - 5, n) if at == "tail" else slice(16 * at, 16 * at + 16)
+    x[..., big, 0] = -1.0
+    y[..., big, :] *= 2.0 ** order
+    q = torch.zeros(1, 2, 1, 128)
+    q[..., 0] = round(less * 0.6931471805599453 * 128 ** 0.5)
+    c, k, v = make(x.to(dtype), y.to(dtype), fmt, dtype, 8208, [n])
+    for max_len in (16, 0):  # one CTA, and as many as the call would take
+        check_each(c, k, v, [n], q.to(dtype), max_len=max_len)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("at,order,less", [(100, 40, 60), (100, 60, 30), (2, 80, 100), ("tail", 40, 60), ("tail", 80, 70)])
+def test_many_rows_some_of_which_see_far_larger_values(dtype, at, order, less):
+    """The same for 64 tokens' rows: the tail's tokens are not seen by all of them, nor is the block by those of a window."""
+    n, count = 4096 + 5, 64
+    x, y = torch.zeros(1, 1, n, 128), torch.randn(1, 1, n, 128, generator=gen(6)).abs() + 0.5
+    big = slice(n - 5, n) if at == "tail" else slice(16 * at, 16 * at + 16)
+    x[..., big, 0] = -1.0
+    y[..., big, :] *= 2.0 ** order
+    q = torch.zeros(1, 4, count, 128)
+    q[..., 0] = round(less * 0.6931471805599453 * 128 ** 0.5)
+    c, k, v = make(x.to(dtype), y.to(dtype), "int8", dtype, 4112, [n])
+    check_each(c, k, v, [n], q.to(dtype))
+    check_each(c, k, v, [n], q.to(dtype), window=n - 16 * 101 - 30, sinks=64)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_units_that_climb(dtype):
+    """V units that rise by 2^7 every 64 blocks, over 2^84 in all, under weights
+    that fall as fast, or slower, or faster, or rise."""
+    n = 13 * 1024 - 3
+    block = torch.arange(n) // 1024
+    y = (torch.randn(1, 1, n, 128, generator=gen(1)).abs() + 0.5) * 2.0 ** (7.0 * block - 40)[:, None]
+    for step in (7, 5, 6.5, 8, 2, -2):
+        x = torch.zeros(1, 1, n, 128)
+        x[..., 0] = -block.float()
+        q = torch.zeros(1, 1, 1, 128)
+        q[..., 0] = round(step * 0.6931471805599453 * 128 ** 0.5)
+        c, k, v = make(x.to(dtype), y.to(dtype), "int8", dtype, 13 * 1024, [n])
+        for max_len in (16, 0):
+            check_each(c, k, v, [n], q.to(dtype), max_len=max_len)
+
+
 # ---------------------------------------------------------------- every output by itself
 
 @pytest.mark.parametrize("fmt", FMTS)
