@@ -25,12 +25,29 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// c += a * b, bf16 operands, fp32 accumulators
+__device__ __forceinline__ void mma16816_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// x and y (fp32) as three bf16 parts each: 24 bits, whatever their size
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t &p0, uint32_t &p1, uint32_t &p2) {
+  p0 = pack_bf16(x, y);
+  x -= __uint_as_float(p0 << 16);
+  y -= __uint_as_float(p0 & 0xffff0000u);
+  p1 = pack_bf16(x, y);
+  p2 = pack_bf16(x - __uint_as_float(p1 << 16), y - __uint_as_float(p1 & 0xffff0000u));
+}
+
 // A warp's part of a tile's attention (see k_attend8).
 template <int DT, int CODE, int NT>
 struct Warp {
   static constexpr int RT = 8 * NT;
   static constexpr bool SPLIT = DT == 0;      // fp32: operands with remainders
   static constexpr int QL = SPLIT && NT == 2 ? 2 : 1;
+  static constexpr int PW = SPLIT ? 4 : 2;    // words of a lane's four weights: fp32, or fp16 pairs
   uint32_t qa[QL][8][4];      // A fragments of the queries for the 8 steps over d
   float rc[NT];               // row g (+8): query scale * scale * log2(e)
   int pos[NT];                // its position, -1 for none
@@ -79,7 +96,7 @@ struct Warp {
   // needed. ks: the blocks' K scales, lu: log2 of their V scales, iu: 1 / those.
   template <int NB>
   __device__ __forceinline__ void weights(float (&s)[NB][2][4], const float (&ks)[NB], const float (&lu)[NB], const float (&iu)[NB],
-                                          const int (&block)[NB], uint32_t (&ph)[NB][NT][2], uint32_t (&pl)[NB][NT][2]) {
+                                          const int (&block)[NB], uint32_t (&pw)[NB][NT][PW]) {
     float y[NB][NT][4];
     float far = -INFINITY;
 #pragma unroll
@@ -147,13 +164,9 @@ struct Warp {
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[e] = ex2(y[n][r][e]);
         l[r] = __fmaf_rn((p[0] + p[1]) + (p[2] + p[3]), iu[n], l[r]);
-        if (SPLIT) {
-          split_h2(p[0], p[1], ph[n][r][0], pl[n][r][0]);
-          split_h2(p[2], p[3], ph[n][r][1], pl[n][r][1]);
-        } else {
-          ph[n][r][0] = h2_bits(__floats2half2_rn(p[0], p[1]));
-          ph[n][r][1] = h2_bits(__floats2half2_rn(p[2], p[3]));
-        }
+#pragma unroll
+        for (int e = 0; e < PW; ++e)
+          pw[n][r][e] = SPLIT ? __float_as_uint(p[e]) : h2_bits(__floats2half2_rn(p[2 * (e & 1)], p[2 * (e & 1) + 1]));
       }
   }
 
@@ -188,10 +201,11 @@ struct Warp {
         }
       }
     }
-    uint32_t ph[NB][NT][2], pl[NB][NT][2];
-    weights<NB>(s, ks, lu, iu, block, ph, pl);
+    uint32_t pw[NB][NT][PW];
+    weights<NB>(s, ks, lu, iu, block, pw);
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
+      Weights wn(pw[n]);
       uint4 v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -204,19 +218,42 @@ struct Warp {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t a[4];
-          codes_across<CODE>(w[0], w[1], h, a[0], a[1]);
-          codes_across<CODE>(w[2], w[3], h, a[2], a[3]);
-          accumulate(a, ph[n], pl[n], 2 * e + h);
+          codes_across<CODE, SPLIT>(w[0], w[1], h, a[0], a[1]);
+          codes_across<CODE, SPLIT>(w[2], w[3], h, a[2], a[3]);
+          accumulate(a, wn, 2 * e + h, SPLIT ? 3 : 1);
         }
       }
     }
   }
 
-  __device__ __forceinline__ void accumulate(const uint32_t (&a)[4], const uint32_t (&ph)[NT][2], const uint32_t (&pl)[NT][2], int i) {
+  // The weights of a block as operands of P V: fp16 for bf16 caches (off by 2^-11
+  // of themselves, or 2^-25 where they are small), in one product; three bf16
+  // parts for fp32 ones, which keep 24 bits of weights of any size.
+  struct Weights {
+    uint32_t b[SPLIT ? 3 : 1][NT][2];
+    __device__ __forceinline__ explicit Weights(const uint32_t (&w)[NT][PW]) {
+#pragma unroll
+      for (int r = 0; r < NT; ++r) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if constexpr (SPLIT)
+            split_bf16(__uint_as_float(w[r][2 * e]), __uint_as_float(w[r][2 * e + 1]), b[0][r][e], b[1][r][e], b[2][r][e]);
+          else
+            b[0][r][e] = w[r][e];
+        }
+      }
+    }
+  };
+
+  // o += values * weights, with the first `parts` parts of the weights
+  __device__ __forceinline__ void accumulate(const uint32_t (&a)[4], const Weights &w, int i, int parts) {
 #pragma unroll
     for (int r = 0; r < NT; ++r) {
-      mma16816(o[r][i], a, ph[r][0], ph[r][1]);
-      if (SPLIT) mma16816(o[r][i], a, pl[r][0], pl[r][1]);
+#pragma unroll
+      for (int z = 0; z < parts; ++z) {
+        if constexpr (SPLIT) mma16816_bf16(o[r][i], a, w.b[z][r][0], w.b[z][r][1]);
+        else mma16816(o[r][i], a, w.b[z][r][0], w.b[z][r][1]);
+      }
     }
   }
 
@@ -233,8 +270,9 @@ struct Warp {
 
   static __device__ __forceinline__ int below(uint32_t bits) { return min(max((int)(bits >> 23) - 126, -100), 126); }
 
-  // The last, partial block, from the tails in full precision: the same
-  // products on fp16 values and (fp32 tails) their remainders.
+  // The last, partial block, from the tails: the same products, scores on fp16
+  // values and (fp32 tails) their remainders, in units of the largest one; P V
+  // on fp16 values in such units, or (fp32) on three bf16 parts of them.
   __device__ __noinline__ void tail_step(const void *kt, const void *vt, int rows, int block) {
     // powers of two that bring the tails' largest magnitudes below 1; what is
     // read again below comes from L1
@@ -268,10 +306,11 @@ struct Warp {
         }
       }
     }
-    uint32_t ph[1][NT][2], pl[1][NT][2];
+    uint32_t pw[1][NT][PW];
     const float ks[1] = {pow2f(ke)}, lu[1] = {(float)(ve - unit)}, iu[1] = {pow2f(unit - ve)};
     const int at[1] = {block};
-    weights<1>(s, ks, lu, iu, at, ph, pl);
+    weights<1>(s, ks, lu, iu, at, pw);
+    const Weights w0(pw[0]);
     const int tok[4] = {t, t + 4, t + 8, t + 12};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -283,13 +322,19 @@ struct Warp {
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t a[4], b[4];
-        split_h2(h ? x[0].z : x[0].x, h ? x[1].z : x[1].x, a[0], b[0]);
-        split_h2(h ? x[0].w : x[0].y, h ? x[1].w : x[1].y, a[1], b[1]);
-        split_h2(h ? x[2].z : x[2].x, h ? x[3].z : x[3].x, a[2], b[2]);
-        split_h2(h ? x[2].w : x[2].y, h ? x[3].w : x[3].y, a[3], b[3]);
-        accumulate(a, ph[0], pl[0], 2 * e + h);
-        if (SPLIT) accumulate(b, ph[0], pl[0], 2 * e + h);
+        uint32_t a[3][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // d (+ 1) of tokens t and t + 4, then of t + 8 and t + 12
+          const float4 &y0 = x[j & 2], &y1 = x[(j & 2) + 1];
+          const float f0 = h ? (j & 1 ? y0.w : y0.z) : (j & 1 ? y0.y : y0.x), f1 = h ? (j & 1 ? y1.w : y1.z) : (j & 1 ? y1.y : y1.x);
+          if constexpr (SPLIT) split_bf16(f0, f1, a[0][j], a[1][j], a[2][j]);
+          else a[0][j] = h2_bits(__floats2half2_rn(f0, f1));
+        }
+        accumulate(a[0], w0, 2 * e + h, SPLIT ? 3 : 1);
+        if constexpr (SPLIT) {  // parts together below 2^-24 of a product are left out
+          accumulate(a[1], w0, 2 * e + h, 2);
+          accumulate(a[2], w0, 2 * e + h, 1);
+        }
       }
     }
   }
@@ -376,8 +421,10 @@ __device__ __forceinline__ void put_out(const AttendArgs &a, int64_t slice, int 
 // units of the largest one that the warp has met (u <= 2), whatever the
 // values' magnitude. The reference of a row only moves when a y passes it by
 // 2^8: the weights lie below 2^(8 + kPShift), fp16's range, and small ones
-// keep 2^-30 of the reference. For fp32 outputs the weights carry an fp16
-// remainder too (one more product a block).
+// are off by 2^-25, 2^-31 of the largest one or less: tokens that weigh less than
+// 2^-22 of it count with fewer bits than bf16 has.
+// For fp32 caches they are three bf16 parts (three products a block in place of
+// two on fp16 and a remainder, which lost weights below 2^-25 altogether).
 //
 // Small calls: a tile's blocks are shared by the CTAs of one cluster. Each CTA
 // merges its warps in shared memory, then every CTA of the cluster merges a

@@ -65,10 +65,21 @@ __device__ __forceinline__ void codes_row(uint32_t w, uint32_t &p01, uint32_t &p
   }
 }
 
-// Bytes 2 h and 2 h + 1 of two tokens' words as two fp16 pairs across the tokens.
-template <int CODE>
+// Bytes 2 h and 2 h + 1 of two tokens' words as two fp16 (or bf16) pairs across
+// the tokens: exact in either.
+template <int CODE, bool BF16 = false>
 __device__ __forceinline__ void codes_across(uint32_t wa, uint32_t wb, int h, uint32_t &even, uint32_t &odd) {
-  if constexpr (CODE == LKV_CODE_INT8) {
+  if constexpr (CODE == LKV_CODE_INT8 && BF16) {
+    // 0x4300 | x is 128 + x in bf16 for x below 128, and 256 for the sign bit alone
+    const uint32_t u = __byte_perm(wa, wb, h ? 0x7632 : 0x5410);
+    auto pair = [](uint32_t w) {
+      const uint32_t low = w & 0xff7fff7fu, off = w & 0xff80ff80u;
+      const __nv_bfloat162 d = __hsub2(*(const __nv_bfloat162 *)&low, *(const __nv_bfloat162 *)&off);
+      return *(const uint32_t *)&d;
+    };
+    even = pair(__byte_perm(u, 0x43434343u, 0x4240));
+    odd = pair(__byte_perm(u, 0x43434343u, 0x4341));
+  } else if constexpr (CODE == LKV_CODE_INT8) {
     const uint32_t u = __byte_perm(wa, wb, h ? 0x7632 : 0x5410) ^ 0x80808080u;
     const __half2 off = __float2half2_rn(1152.f);
     const uint32_t a = __byte_perm(u, 0x64646464u, 0x4240), b = __byte_perm(u, 0x64646464u, 0x4341);
@@ -79,6 +90,11 @@ __device__ __forceinline__ void codes_across(uint32_t wa, uint32_t wb, int h, ui
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(even), "=r"(odd) : "r"(u));
+    if constexpr (BF16) {
+      const float2 e2 = __half22float2(*(const __half2 *)&even), o2 = __half22float2(*(const __half2 *)&odd);
+      even = pack_bf16(e2.x, e2.y);
+      odd = pack_bf16(o2.x, o2.y);
+    }
   }
 }
 

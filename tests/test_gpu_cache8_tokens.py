@@ -123,6 +123,23 @@ def test_units_that_climb(dtype):
             check_each(c, k, v, [n], q.to(dtype), max_len=max_len)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("less", [20, 31, 40, 60])
+def test_one_token_far_above(dtype, less):
+    """A token of no value holds nearly all of the weight: the output is what
+    the 2^-less of the others sum to (fp32 to all of its bits)."""
+    n = 30000
+    y = torch.randn(1, 1, n, 128, generator=gen(9)).abs() + 0.5
+    y[:, :, 5] = 0
+    x = torch.zeros(1, 1, n, 128)
+    x[:, :, 5, 0] = 1.0
+    q = torch.zeros(1, 3, 1, 128)
+    q[..., 0] = round(less * 0.6931471805599453 * 128 ** 0.5)
+    c, k, v = make(x.to(dtype), y.to(dtype), "int8", dtype, 30016, [n])
+    for max_len in (16, 0):
+        check_each(c, k, v, [n], q.to(dtype), max_len=max_len)
+
+
 # ---------------------------------------------------------------- every output by itself
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -213,3 +230,29 @@ def test_a_loud_token_is_found(fmt, dtype, lengths, h, group, n):
                     # the weight of the token is 2^(y - reference): in fp16 off by 2^-11; the others' are below 2^-500
                     lim = want.abs() * (2.0 ** -11 + 2.0 ** -16 + ref.half_step(dtype) * 1.01) + 2.0 ** -24 * vv[i].abs().max()
                     assert (err <= lim).all(), f"sequence {i}, KV head {j}, row {r}: token {int(hot[i, j, r])}"
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("b,h,group,n", [(1, 4, 8, 1), (2, 1, 32, 1), (64, 2, 32, 8)])
+def test_every_code(fmt, dtype, b, h, group, n):
+    """Rows that favour one token each get that token's values: every code, in every type."""
+    code = (torch.arange(48 * 128) * 37 % 256).to(torch.uint8).view(48, 128)
+    if fmt == "e4m3":
+        code[code & 0x7f == 0x7f] = 0  # not a NaN
+    assert len(code[:32].unique()) >= 254
+    code = code.view(ref.CODE[fmt])
+    one = torch.zeros(48, 128)
+    one[torch.arange(32), torch.arange(32)] = 1.0
+    every = lambda x: x.expand(b, h, *x.shape).contiguous().cuda()  # noqa: E731
+    scale = torch.tensor([0.75, 0.125, 96.0])
+    c = lkv.Cache8.from_tensors(every(one.to(ref.CODE[fmt]).view(torch.int8)).view(ref.CODE[fmt]), every(code.view(torch.int8)).view(ref.CODE[fmt]),
+                                every(torch.full((3,), 64.0)), every(scale), every(torch.zeros(16, 128, dtype=dtype)),
+                                every(torch.zeros(16, 128, dtype=dtype)), i32(*[48] * b))
+    row = torch.arange(h * group) % 32
+    q = torch.zeros(b, h * group, n, 128, dtype=dtype)
+    q[:, torch.arange(h * group), :, row] = 64.0
+    want = (code.float().double() * scale.repeat_interleave(16)[:, None].double())[row][None, :, None]
+    err = (c.attend(q.cuda()).cpu().double() - want).abs()
+    # a weight in fp16 is off by 2^-11, exp2 and the logarithm of a scale by 2^-18; the others' weights are below 2^-500
+    assert (err <= want.abs() * (2.0 ** -11 + 2.0 ** -18 + ref.half_step(dtype) * 1.01)).all()
