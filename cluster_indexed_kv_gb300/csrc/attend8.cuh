@@ -118,6 +118,18 @@ struct Tile {
   __device__ __forceinline__ int block(int u) const { return u < sb ? u : u - sb + lo; }
 };
 
+// Which of a block's tokens (the first is token `tok`) a row at position pos
+// sees: those up to see[0], and of them those above see[1] or below see[2].
+// Nothing overflows for pos >= -1 and windows below and sinks up to a capacity of 2^30;
+// kNoToken, of a block that is not there, lies behind every position.
+constexpr int kNoToken = 1 << 30;
+__host__ __device__ __forceinline__ void token_range(int tok, int pos, int window, int sinks, int (&see)[3]) {
+  see[0] = pos - tok;
+  see[1] = window > 0 ? see[0] - window : -1;
+  see[2] = sinks - tok;
+}
+__host__ __device__ __forceinline__ bool sees(const int (&see)[3], int i) { return i <= see[0] && (i > see[1] || i < see[2]); }
+
 constexpr int kAtGroups = 512;  // (sequence, row tile) pairs that a streamed launch takes
 
 // A streamed launch's work: the units (runs of `per` blocks, behind `start`

@@ -169,15 +169,6 @@ __device__ __forceinline__ bool rows_wait_warp(uint64_t *bar, uint32_t phase, vo
 // The e of a largest magnitude (bits) < 2^e, within the fp32 scales' reach.
 __device__ __forceinline__ int exponent_of(uint32_t bits) { return min(max((int)(bits >> 23) - 126, -100), 126); }
 
-// Which of a block's tokens (the first is token `tok`) a row at position pos
-// sees: those up to see[0], and of them those above see[1] or below see[2].
-__device__ __forceinline__ void token_range(int tok, int pos, int window, int sinks, int (&see)[3]) {
-  see[0] = pos - tok;
-  see[1] = window > 0 ? see[0] - window : -1;
-  see[2] = sinks - tok;
-}
-__device__ __forceinline__ bool sees(const int (&see)[3], int i) { return i <= see[0] && (i > see[1] || i < see[2]); }
-
 // A row's softmax: reference, sum of w / u before and in this tile, the block
 // sum of weights past which the reference moves, and whether there is one.
 struct RowState {
@@ -404,7 +395,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
       // lanes a row; a thread's own row (the one it will weigh) keeps its unit
       const int row = r0 + (int)threadIdx.x, own = row / a.group, half = lane >> 4, run = lane & 15;
       valid = row < R && own < tile.cnt;
-      if (valid) pos = tile.len - tile.cnt + own;
+      if (valid) pos = max(tile.len - tile.cnt + own, -1);
 #pragma unroll 1
       for (int it = 0; it < 16; it += 8) {
         uint4 w[8];
@@ -505,7 +496,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
         if (pw == 0) {
           if (lane < kRwBlocks) {
             const int u = j * kRwBlocks + lane, b = tile.block(u);
-            float4 s = make_float4(0.f, 0.f, 1.f, __int_as_float(0x7fffffff));  // none: behind every position
+            float4 s = make_float4(0.f, 0.f, 1.f, __int_as_float(kNoToken));
             if (u < tile.nb) {
               float k = pow2f(ke), v = pow2f(max(ve, unit - kUnitSpan) - unit);
               if (b < full) {
