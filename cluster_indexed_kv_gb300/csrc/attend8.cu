@@ -750,10 +750,11 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
 // the eight sums are added in order.
 constexpr int kMergeThreads = 512;
 constexpr int kMergeGroups = kMergeThreads / 64;
+constexpr int kMergeEarly = 4;  // parts that a thread loads while the factors are made
 constexpr int kMaxCtas = 1024;
 
 template <int DT, int NT>
-__global__ void __launch_bounds__(kMergeThreads) k_attend8_merge(const __grid_constant__ AttendArgs a, int ctas) {
+__global__ void __launch_bounds__(kMergeThreads, 3) k_attend8_merge(const __grid_constant__ AttendArgs a, int ctas) {
   __shared__ Stream stream;
   constexpr int RT = 8 * NT, kSlot = AtSmem<NT>::kSlot;
   __shared__ float factor[kMaxCtas];
@@ -761,54 +762,75 @@ __global__ void __launch_bounds__(kMergeThreads) k_attend8_merge(const __grid_co
   __shared__ float total_l, unit;
   __shared__ int range[3];
   const int G = a.c.batch * a.row_tiles, row = blockIdx.y;
-  stream.fill(a, RT, 1, 0);  // the lengths and counts are inputs, written before the first kernel's wait was over
   const int gi = blockIdx.x / a.c.n_kv_heads, h = blockIdx.x % a.c.n_kv_heads;
   const int b = gi % a.c.batch, rt = gi / a.c.batch;
   const int64_t slice = (int64_t)b * a.c.n_kv_heads + h;
-  if (threadIdx.x == 0) {
-    const int nb = stream.nu[gi];
-    const int64_t total = stream.at[G], P = min((int64_t)ctas, total), p0 = stream.at[gi] + (int64_t)h * nb;
-    range[0] = range[1] = range[2] = 0;
-    if (nb > 0) {  // CTAs range[0].. share the tile; the first one's part is its second if it began before
-      range[0] = stream.owner(p0, total, P);
-      range[1] = stream.owner(p0 + nb - 1, total, P) - range[0] + 1;
-      range[2] = total * range[0] / P < p0;
-    }
-  }
-  __syncthreads();
-  const int i0 = range[0], np = range[1], second = range[2];
-  wait_prerequisites();  // by every CTA: this kernel's end stands for the first one's
-  if (np == 1 || rt * RT + row >= a.n * a.group) return;  // one CTA had it all, or the row is none
-  auto slot = [&](int j) { return a.ws + (2 * (int64_t)(i0 + j) + (j == 0 ? second : 0)) * kSlot; };
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    float top = -INFINITY, topt = -INFINITY, l = 0.f;
-    for (int j = lane; j < np; j += 32) {
-      top = fmaxf(top, slot(j)[RT * kHeadDim + row]);
-      topt = fmaxf(topt, slot(j)[RT * kHeadDim + RT + row]);
-    }
-#pragma unroll
-    for (int d = 16; d; d /= 2) {
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      topt = fmaxf(topt, __shfl_xor_sync(0xffffffffu, topt, d));
-    }
-    for (int j = lane; j < np; j += 32) {
-      factor[j] = share(slot(j)[RT * kHeadDim + row], top);
-      l += share(slot(j)[RT * kHeadDim + RT + row], topt) * slot(j)[RT * kHeadDim + 2 * RT + row];
-    }
-#pragma unroll
-    for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (lane == 0) {
-      total_l = l;
-      unit = top - topt;
-    }
-  }
-  __syncthreads();
   const int p = threadIdx.x & 63, grp = threadIdx.x >> 6;
+  auto slot = [&](int j) { return a.ws + (2 * (int64_t)(range[0] + j) + (j == 0 ? range[2] : 0)) * kSlot; };
+  auto part_at = [&](int j) { return *(const float2 *)(slot(j) + row * kHeadDim + 2 * p); };
+  float2 early[kMergeEarly];
+  int np;
+  // Which CTAs share the tile follows from the lengths and counts. They are
+  // read ahead of the wait, where nothing vouches for them yet, and again
+  // behind it: if they were others then, the second turn has them right.
+  // (Reading them behind the wait alone: 1 to 1.5 us a call.)
+  for (int turn = 0;; ++turn) {
+    stream.fill(a, RT, 1, 0);
+    if (threadIdx.x == 0) {
+      const int nb = stream.nu[gi];
+      const int64_t total = stream.at[G], P = min((int64_t)ctas, total), p0 = stream.at[gi] + (int64_t)h * nb;
+      range[0] = range[1] = range[2] = 0;
+      if (nb > 0) {  // CTAs range[0].. share the tile; the first one's part is its second if it began before
+        range[0] = stream.owner(p0, total, P);
+        range[1] = stream.owner(p0 + nb - 1, total, P) - range[0] + 1;
+        range[2] = total * range[0] / P < p0;
+      }
+    }
+    __syncthreads();
+    if (turn == 0) wait_prerequisites();  // by every CTA: this kernel's end stands for the first one's
+    np = range[1];
+    const bool others = threadIdx.x < G && stream.nu[threadIdx.x] != Tile(a, threadIdx.x % a.c.batch, threadIdx.x / a.c.batch, RT).nb;
+#pragma unroll
+    for (int k = 0; k < kMergeEarly; ++k)
+      early[k] = np > 1 && grp + k * kMergeGroups < np ? part_at(grp + k * kMergeGroups) : make_float2(0.f, 0.f);
+    if (threadIdx.x < 32 && np != 1) {
+      const int lane = threadIdx.x;
+      float top = -INFINITY, topt = -INFINITY, l = 0.f;
+      for (int j = lane; j < np; j += 32) {
+        top = fmaxf(top, slot(j)[RT * kHeadDim + row]);
+        topt = fmaxf(topt, slot(j)[RT * kHeadDim + RT + row]);
+      }
+#pragma unroll
+      for (int d = 16; d; d /= 2) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        topt = fmaxf(topt, __shfl_xor_sync(0xffffffffu, topt, d));
+      }
+      for (int j = lane; j < np; j += 32) {
+        factor[j] = share(slot(j)[RT * kHeadDim + row], top);
+        l += share(slot(j)[RT * kHeadDim + RT + row], topt) * slot(j)[RT * kHeadDim + 2 * RT + row];
+      }
+#pragma unroll
+      for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+      if (lane == 0) {
+        total_l = l;
+        unit = top - topt;
+      }
+    }
+    if (!__syncthreads_or(others) || turn == 1) break;
+  }
+  if (np == 1 || rt * RT + row >= a.n * a.group) return;  // one CTA had it all, or the row is none
   float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < kMergeEarly; ++k) {
+    if (grp + k * kMergeGroups < np) {
+      const float f = factor[grp + k * kMergeGroups];
+      s.x += f * early[k].x;
+      s.y += f * early[k].y;
+    }
+  }
 #pragma unroll 4
-  for (int j = grp; j < np; j += kMergeGroups) {
-    const float2 x2 = *(const float2 *)(slot(j) + row * kHeadDim + 2 * p);
+  for (int j = grp + kMergeEarly * kMergeGroups; j < np; j += kMergeGroups) {
+    const float2 x2 = part_at(j);
     const float f = factor[j];
     s.x += f * x2.x;
     s.y += f * x2.y;

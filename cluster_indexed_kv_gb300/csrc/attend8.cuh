@@ -104,8 +104,8 @@ struct Tile {
   int len, cnt, pmin, pmax, lo, hi, sb, nb;
   Tile() = default;
   __device__ __forceinline__ Tile(const AttendArgs &a, int b, int rt, int RT) {
-    len = min(max(a.c.lengths[b], 0), a.c.capacity);
-    cnt = a.counts ? min(max(a.counts[b], 0), a.n) : a.n;
+    len = min(max(__ldcg(a.c.lengths + b), 0), a.c.capacity);
+    cnt = a.counts ? min(max(__ldcg(a.counts + b), 0), a.n) : a.n;
     const int R = a.n * a.group, r0 = rt * RT;
     const int imin = r0 / a.group, imax = min((min(r0 + RT, R) - 1) / a.group, cnt - 1);
     pmin = len - cnt + imin;
@@ -175,12 +175,10 @@ struct Stream {
     }
     return lo;
   }
-  // the CTA of P that unit x of the row belongs to
+  // the CTA of P that unit x of the row belongs to: the last one that begins
+  // at or before it, total * i / P < x + 1
   __device__ __forceinline__ int owner(int64_t x, int64_t total, int64_t P) const {
-    int i = (int)(x * P / total);
-    while (total * (i + 1) / P <= x) ++i;
-    while (total * i / P > x) --i;
-    return i;
+    return (int)((P * (x + 1) - 1) / total);
   }
 };
 

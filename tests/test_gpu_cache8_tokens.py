@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import cluster_indexed_kv_gb300 as lkv
+from cluster_indexed_kv_gb300 import _lib
 from tests import _cache8_each as each
 from tests import _cache8_ref as ref
 from tests.test_gpu_cache8 import DTYPES, FMTS, gen, i32, make, rows
@@ -230,6 +231,43 @@ def test_a_loud_token_is_found(fmt, dtype, lengths, h, group, n):
                     # the weight of the token is 2^(y - reference): in fp16 off by 2^-11; the others' are below 2^-500
                     lim = want.abs() * (2.0 ** -11 + 2.0 ** -16 + ref.half_step(dtype) * 1.01) + 2.0 ** -24 * vv[i].abs().max()
                     assert (err <= lim).all(), f"sequence {i}, KV head {j}, row {r}: token {int(hot[i, j, r])}"
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_lengths_that_change_between_streamed_calls(dtype):
+    """Writes that take tokens back and add others, each followed at once by a
+    call whose split over CTAs follows from the lengths: the same bits as with
+    a pause after every call."""
+    b, h, cap = 3, 2, 40960
+    g = gen(17)
+    x, y = (torch.randn(b, h, cap, 128, generator=g).to(dtype).cuda() for _ in range(2))
+    c = lkv.Cache8(batch=b, n_kv_heads=h, capacity=cap, dtype=dtype)
+    c.write(x, y)
+    assert _lib.lkv_cache8_attend_workspace(c._at, 4, 1, 0, 0, 0) > 0, "not a streamed call"
+    q = torch.randn(b, 8, 1, 128, generator=g).to(dtype).cuda()
+    k1, v1 = x[:, :, :1].contiguous(), y[:, :, :1].contiguous()
+    # the last full block of each prefix holds what follows; the starts are multiples of 16, falling
+    starts = [i32(*(16 * max(0, 2500 - 60 * i - 700 * s) for s in range(b))) for i in range(30)]
+
+    def run(pause):
+        c.lengths.fill_(cap)
+        got = []
+        for s in starts:
+            c.write(k1, v1, start=s)
+            pause()
+            got.append(c.attend(q))
+            pause()
+            c.write(k1, v1)
+            pause()
+            got.append(c.attend(q))
+            pause()
+        return got
+
+    one = run(torch.cuda.synchronize)
+    for _ in range(3):
+        for m, n in zip(one, run(lambda: None)):
+            assert torch.equal(m, n)
+    c.check()
 
 
 @pytest.mark.parametrize("fmt", FMTS)
