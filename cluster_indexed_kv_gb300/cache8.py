@@ -50,6 +50,13 @@ def _tensor(t, name, shape, dtype, index) -> int:
     raise ValueError(f"{name} must be contiguous")
 
 
+def _range(**sizes) -> None:
+    """Refuse sizes that do not fit the call's int32; smaller ones below 0 are the call's to refuse."""
+    for name, value in sizes.items():
+        if not -_INT32 <= value <= _INT32:
+            raise ValueError(f"{name} must be in 0..2^31 - 1")
+
+
 def _call(index, fn, *args) -> None:
     """fn(*args, stream) on the device's current stream, with the device current."""
     if torch._C._cuda_getDevice() == index:
@@ -206,6 +213,8 @@ class Cache8:
         sequence as (k, v) [B, H_kv, n, 128] of the cache's dtype; zeros
         outside a sequence. The layout is the one Context.build_index takes."""
         dev, dt = self._index, self.dtype
+        if not 0 <= n <= _INT32:
+            raise ValueError("n must be in 0..2^31 - 1")
         shape = (self.batch, self.n_kv_heads, n, _D)
         if k_out is None:
             k_out = _empty(shape, dt, dev)
@@ -241,8 +250,8 @@ class Cache8:
             op = out.data_ptr()
         else:
             op = _tensor(out, "out", shape, dt, dev)
-        if window > _INT32 or sinks > _INT32 or max_len > _INT32:
-            raise ValueError("window, sinks and max_len must be below 2^31")
+        if not (0 <= window <= _INT32 and 0 <= sinks <= _INT32 and 0 <= max_len <= _INT32):
+            _range(window=window, sinks=sinks, max_len=max_len)
         sizes = (group, n, window, sinks, max_len)
         ws_bytes = self._ws_bytes.get(sizes)
         if ws_bytes is None:
