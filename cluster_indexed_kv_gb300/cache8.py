@@ -252,6 +252,13 @@ class Cache8:
             op = _tensor(out, "out", shape, dt, dev)
         if not (0 <= window <= _INT32 and 0 <= sinks <= _INT32 and 0 <= max_len <= _INT32):
             _range(window=window, sinks=sinks, max_len=max_len)
+        if max_len:
+            # the bound in steps of a 64th to a 128th of itself: a server's bound
+            # that grows with every token does not ask for the workspace each time
+            step = (1 << max(4, max_len.bit_length() - 7)) - 1
+            max_len = (max_len + step) & ~step
+            if max_len >= self.capacity:
+                max_len = 0
         sizes = (group, n, window, sinks, max_len)
         ws_bytes = self._ws_bytes.get(sizes)
         if ws_bytes is None:

@@ -34,3 +34,28 @@ def test_sizes_below_minus_2_31_are_refused():
     with pytest.raises(_lib.LKVError):
         c.attend(q, window=-1)
     c.check()
+
+
+def test_a_bound_that_grows_asks_for_few_workspaces(monkeypatch):
+    """max_len one larger each step, as a server passes it: the same outputs as
+    without a bound, and a size of workspace asked for now and then only."""
+    c = lkv.Cache8(batch=1, n_kv_heads=2, capacity=40960, dtype=BF16)
+    k, v = (torch.randn(1, 2, 8000, 128, device="cuda").to(BF16) for _ in range(2))
+    c.write(k, v)
+    q = torch.randn(1, 8, 1, 128, device="cuda").to(BF16)
+    asked = []
+    ask = _lib.lkv_cache8_attend_workspace
+    monkeypatch.setattr(_lib, "lkv_cache8_attend_workspace", lambda *a: asked.append(a[1:]) or ask(*a))
+    want = c.attend(q).float()
+    for m in range(8000, 9000):
+        got = c.attend(q, max_len=m)
+        if m % 100 == 0:  # another split sums in another order
+            assert (got.float() - want).abs().max() <= 2.0 ** -8 * want.abs().max()
+    assert len(asked) <= 1 + 1000 // 64 + 2
+    # a bound is never made smaller, and one past the capacity is none
+    for m in (1, 15, 16, 17, 127, 128, 129, 8191, 8192, 8193, 40959, 40960, 40961, 2 ** 31 - 1):
+        c._ws_bytes.clear()
+        c.attend(q, max_len=m)
+        bound = asked[-1][-1]
+        assert bound == 0 if m >= 40960 else bound == 0 or m <= bound <= m + max(15, m // 64)
+    c.check()
