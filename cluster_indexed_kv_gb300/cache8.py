@@ -2,7 +2,8 @@
 lkv_rope_*, lkv_cache8_*). ``Rope`` holds one table, ``Cache8`` one cache's
 tensors; the methods run on the current stream of the tensors' device, allocate
 only the outputs they return (and an attention's workspace, where it needs
-one), and can be captured into CUDA graphs.
+one), and can be captured into CUDA graphs. They have no backward pass: a tensor
+that requires a gradient is refused where gradients are recorded.
 """
 from __future__ import annotations
 
@@ -38,6 +39,8 @@ def _tensor(t, name, shape, dtype, index) -> int:
     """Data pointer of a contiguous tensor of this shape and type on CUDA device `index`."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape
             and t.is_contiguous()):
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} requires a gradient, and this call has none to give: use torch.no_grad() or {name}.detach()")
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -100,8 +103,7 @@ class Rope:
         if len(q_shape) != 4 or q_shape[3] != _D:
             raise ValueError(f"q must have shape [B, H, n, {_D}], got {tuple(q_shape)}")
         batch, heads, n, _ = q_shape
-        if not q.is_contiguous():
-            raise ValueError("q must be contiguous")
+        qp = _tensor(q, "q", q_shape, dt, dev)
         pp = _tensor(positions, "positions", (batch, n), torch.int32, dev)
         if q_out is None:
             q_out = _empty((batch, heads, n, _D), dt, dev)
@@ -123,7 +125,7 @@ class Rope:
                 ko = _tensor(k_out, "k_out", shape, dt, dev)
         elif k_out is not None:
             raise ValueError("k_out without k")
-        _call(dev, self._apply, self._at, _DTYPES[dt], batch, heads, kv_heads, n, q.data_ptr(), kp, pp,
+        _call(dev, self._apply, self._at, _DTYPES[dt], batch, heads, kv_heads, n, qp, kp, pp,
               qo, ko)
         return q_out if k is None else (q_out, k_out)
 

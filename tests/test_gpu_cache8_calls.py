@@ -59,3 +59,29 @@ def test_a_bound_that_grows_asks_for_few_workspaces(monkeypatch):
         bound = asked[-1][-1]
         assert bound == 0 if m >= 40960 else bound == 0 or m <= bound <= m + max(15, m // 64)
     c.check()
+
+
+def test_tensors_that_require_gradients():
+    """No call has a backward pass: where gradients are recorded it says so
+    rather than cut the graph; under no_grad, and detached, it runs."""
+    c, k, q = small()
+    pos = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    r = lkv.Rope()
+    leaf, kl, free = q.clone().requires_grad_(), k[:, :, :3].contiguous().requires_grad_(), k[:, :, :3].contiguous()
+    calls = [lambda: c.attend(leaf), lambda: c.attend(leaf * 2), lambda: r.apply(leaf, pos), lambda: r.apply(q, pos, kl), lambda: c.write(kl, free),
+             lambda: c.write(free, kl), lambda: r.apply(q, pos, q_out=leaf), lambda: c.attend(q, out=leaf),
+             lambda: c.read(3, k_out=kl, v_out=free.clone())]
+    before = c.lengths.tolist()
+    for call in calls:
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
+    assert c.lengths.tolist() == before and leaf.grad is None
+    want = c.attend(q)
+    with torch.no_grad():
+        assert torch.equal(c.attend(leaf), want)
+        r.apply(leaf, pos, kl)
+        c.write(kl, free)
+    with torch.inference_mode():
+        assert c.attend(leaf).shape == want.shape
+    assert c.attend(leaf.detach()).shape == want.shape
+    c.check()
