@@ -24,14 +24,34 @@ const char *check_cache8(const lkv_cache8 *c) {
   return nullptr;
 }
 
-bool overlaps_cache8(const lkv_cache8 *c, const void *p, int64_t bytes) {
+struct Extent { const void *at; int64_t bytes; };
+constexpr int kArrays = 8;
+static void extents(const lkv_cache8 *c, Extent (&e)[kArrays]) {
   const int64_t slices = (int64_t)c->batch * c->n_kv_heads, es = c->dtype == LKV_DTYPE_BF16 ? 2 : 4;
   const int64_t codes = slices * c->capacity * kHeadDim, scales = slices * (c->capacity / kBlock) * 4;
   const int64_t tail = slices * kBlock * kHeadDim * es;
-  return overlap(p, bytes, c->k_codes, codes) || overlap(p, bytes, c->v_codes, codes) ||
-         overlap(p, bytes, c->k_scale, scales) || overlap(p, bytes, c->v_scale, scales) ||
-         overlap(p, bytes, c->k_tail, tail) || overlap(p, bytes, c->v_tail, tail) ||
-         overlap(p, bytes, c->lengths, (int64_t)c->batch * 4) || overlap(p, bytes, c->ticket, ((int64_t)c->batch + 1) * 4);
+  e[0] = {c->k_codes, codes}; e[1] = {c->v_codes, codes};
+  e[2] = {c->k_scale, scales}; e[3] = {c->v_scale, scales};
+  e[4] = {c->k_tail, tail}; e[5] = {c->v_tail, tail};
+  e[6] = {c->lengths, (int64_t)c->batch * 4}; e[7] = {c->ticket, ((int64_t)c->batch + 1) * 4};
+}
+
+bool overlaps_cache8(const lkv_cache8 *c, const void *p, int64_t bytes) {
+  Extent e[kArrays];
+  extents(c, e);
+  for (const Extent &x : e)
+    if (overlap(p, bytes, x.at, x.bytes)) return true;
+  return false;
+}
+
+// Whether two of the cache's own arrays share memory.
+static bool arrays_overlap(const lkv_cache8 *c) {
+  Extent e[kArrays];
+  extents(c, e);
+  for (int i = 0; i < kArrays; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(e[i].at, e[i].bytes, e[j].at, e[j].bytes)) return true;
+  return false;
 }
 
 // ---------------------------------------------------------------- write
@@ -457,6 +477,7 @@ extern "C" lkv_status lkv_cache8_write(const lkv_cache8 *c, const void *k, const
   if (!k || !v) return refuse("lkv_cache8_write: null keys or values");
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4) || !aligned(counts, 4))
     return refuse("lkv_cache8_write: keys and values must be 16-byte aligned, start and counts 4-byte aligned");
+  if (arrays_overlap(c)) return refuse("lkv_cache8_write: two of the cache's arrays overlap");
   const int64_t slices = (int64_t)c->batch * c->n_kv_heads;
   const int64_t bytes = slices * n * kHeadDim * (c->dtype == LKV_DTYPE_BF16 ? 2 : 4), ib = (int64_t)c->batch * 4;
   if (overlaps_cache8(c, k, bytes) || overlaps_cache8(c, v, bytes) || overlaps_cache8(c, start, ib) ||

@@ -534,7 +534,8 @@ lkv_status lkv_rope_apply(const lkv_rope *rope, int32_t dtype, int32_t batch, in
  * infinity as the largest finite value of dtype, and lkv_cache8_status then
  * reports LKV_EINVAL. Calls that write a cache (lkv_cache8_write) may not
  * overlap on the GPU with any other call on it; calls that only read it
- * (lkv_cache8_read, lkv_cache8_attend) may overlap with one another. */
+ * (lkv_cache8_read, lkv_cache8_attend) may overlap with one another. No two of
+ * the arrays may share memory (lkv_cache8_write refuses it). */
 #define LKV_CACHE8_BLOCK 16
 enum { LKV_CODE_INT8 = 0, LKV_CODE_E4M3 = 1 };
 typedef struct lkv_cache8 {
