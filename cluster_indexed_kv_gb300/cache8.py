@@ -276,6 +276,9 @@ class Cache8:
         return out
 
     def check(self) -> None:
-        """Wait for the current stream; raise LKVError if a write since the
-        last check did not fit or held a value that is not finite."""
+        """Wait for the current stream; raise LKVError if, since the last
+        check, an attention gave up waiting for its copies (its output is not
+        complete), a write did not fit, or one held a value that is not finite.
+        Everything is reported once, in one error: the first of these that
+        there is."""
         _call(self._index, self._status, self._at)

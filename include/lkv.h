@@ -609,9 +609,9 @@ lkv_status lkv_cache8_attend_workspace(const lkv_cache8 *cache, int32_t group, i
                                        int64_t *bytes);
 
 /* Blocking: waits for stream, then reports and clears what calls on this
- * cache recorded: LKV_OK, LKV_ECAPACITY or LKV_EINVAL (writes), LKV_ETIMEOUT
- * (an attention whose copies did not arrive). May not be captured. Errors:
- * also LKV_ECUDA. */
+ * cache recorded: LKV_ETIMEOUT (an attention whose copies did not arrive: its
+ * output is not complete), else LKV_ECAPACITY, else LKV_EINVAL (writes), else
+ * LKV_OK. May not be captured. Errors: also LKV_ECUDA. */
 lkv_status lkv_cache8_status(const lkv_cache8 *cache, void *stream);
 
 /* Wait for the context's stream; report device-side anomalies. */

@@ -85,3 +85,21 @@ def test_tensors_that_require_gradients():
         assert c.attend(leaf).shape == want.shape
     assert c.attend(leaf.detach()).shape == want.shape
     c.check()
+
+
+def test_check_reports_an_attention_that_gave_up():
+    """The word that a kernel's bounded wait sets is set here by the host: it
+    comes before what writes recorded, once, and the cache goes on."""
+    c, k, q = small()
+    want = c.attend(q)
+    timeout, rest = 8, 1 | 2 | 4
+    for bits, status in ((timeout, _lib.LKV_ETIMEOUT), (timeout | rest, _lib.LKV_ETIMEOUT), (rest, _lib.LKV_ECAPACITY), (2 | 4, _lib.LKV_ECAPACITY),
+                         (1 | 4, _lib.LKV_EINVAL), (4, _lib.LKV_EINVAL)):
+        c._ticket[-1] = bits
+        with pytest.raises(_lib.LKVError) as e:
+            c.check()
+        assert e.value.status == status
+        c.check()
+        assert torch.equal(c.attend(q), want)
+        c.check()
+    assert c._ticket.tolist() == [0, 0, 0]
