@@ -298,35 +298,11 @@ def lkv_rope_init(rotary_dim, layout, scaling, orig_len, base, factor, beta_fast
     return table
 
 
-def lkv_rope_apply(table, dtype, batch, n_heads, n_kv_heads, n, q_ptr, k_ptr, pos_ptr, q_out_ptr,
-                   k_out_ptr, stream_ptr) -> None:
-    _check(load().lkv_rope_apply(table, dtype, batch, n_heads, n_kv_heads, n, q_ptr, k_ptr, pos_ptr,
-                                 q_out_ptr, k_out_ptr, stream_ptr), None)
-
-
-def lkv_cache8_write(cache, k_ptr, v_ptr, n, start_ptr, counts_ptr, stream_ptr) -> None:
-    _check(load().lkv_cache8_write(cache, k_ptr, v_ptr, n, start_ptr, counts_ptr, stream_ptr), None)
-
-
-def lkv_cache8_read(cache, first_ptr, n, k_ptr, v_ptr, stream_ptr) -> None:
-    _check(load().lkv_cache8_read(cache, first_ptr, n, k_ptr, v_ptr, stream_ptr), None)
-
-
-def lkv_cache8_attend(cache, q_ptr, group, n, counts_ptr, scale, window, sinks, max_len, out_ptr,
-                      ws_ptr, ws_bytes, stream_ptr) -> None:
-    _check(load().lkv_cache8_attend(cache, q_ptr, group, n, counts_ptr, scale, window, sinks, max_len,
-                                    out_ptr, ws_ptr, ws_bytes, stream_ptr), None)
-
-
 def lkv_cache8_attend_workspace(cache, group, n, window, sinks, max_len) -> int:
     n_bytes = C.c_int64(0)
     _check(load().lkv_cache8_attend_workspace(cache, group, n, window, sinks, max_len,
                                               C.byref(n_bytes)), None)
     return n_bytes.value
-
-
-def lkv_cache8_status(cache, stream_ptr) -> None:
-    _check(load().lkv_cache8_status(cache, stream_ptr), None)
 
 
 def lkv_diag_wait_timeout(ctx, limit_ns: int) -> None:

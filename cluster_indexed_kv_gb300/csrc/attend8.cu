@@ -59,7 +59,7 @@ struct Warp {
   int lane, g, t;
   int tk, cg;                 // the lane's token of 8 and its V chunk of 8 (see step)
   int koff, voff;
-  int pmin, pmax, window, sinks;
+  int window, sinks;
   int open0, open1;           // blocks [open0, open1) are visible to every row as a whole
 
   // V scales up to 2^(e + 1) are to come: o counts in units of 2^(ref + unit), l
@@ -557,8 +557,6 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
       }
     };
     scales(0);
-    w.pmin = tile.pmin;
-    w.pmax = tile.pmax;
     w.open0 = a.window > 0 ? max(0, tile.pmax - a.window + kBlock) / kBlock : 0;
     w.open1 = (tile.pmin + 1) / kBlock;
     w.limit = -INFINITY;
