@@ -402,7 +402,7 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
 }
 
 // A warp takes 16 rows, all its loads first: codes (8 or 4 bytes a lane) and
-// the rows' scales, then one rounded product a value. Bound: bytes (1 in, 2
+// the rows' scales, then a product in fp32 a value, rounded to the type. Bound: bytes (1 in, 2
 // or 4 out a value). On a GB300, 128K tokens of 8 KV heads to bf16: 115 us, the
 // measured copy rate; 777 rows of 2 sequences 4.8 us.
 template <int DT, int CODE>

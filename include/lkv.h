@@ -573,8 +573,8 @@ lkv_status lkv_cache8_write(const lkv_cache8 *cache, const void *k, const void *
                             const int32_t *start, const int32_t *counts, void *stream);
 
 /* Read rows first[b] .. first[b] + n - 1 of every (sequence, KV head) back
- * into k_out, v_out [B][H_kv][n][d] (dtype of the cache): code * scale
- * rounded once, the tail's rows as they are, and zeros for rows below 0 or at
+ * into k_out, v_out [B][H_kv][n][d] (dtype of the cache): code * scale in
+ * fp32, rounded to dtype, the tail's rows as they are, and zeros for rows below 0 or at
  * or past the length. first: device int32 [B] or NULL (from row 0). The
  * layout is the one lkv_build_index takes. Asynchronous on stream. Errors:
  * LKV_EINVAL, LKV_ECUDA. */

@@ -294,3 +294,18 @@ def test_every_code(fmt, dtype, b, h, group, n):
     err = (c.attend(q.cuda()).cpu().double() - want).abs()
     # a weight in fp16 is off by 2^-11, exp2 and the logarithm of a scale by 2^-18; the others' weights are below 2^-500
     assert (err <= want.abs() * (2.0 ** -11 + 2.0 ** -18 + ref.half_step(dtype) * 1.01)).all()
+
+
+# ---------------------------------------------------------------- read
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_read_is_the_product_in_fp32_rounded_to_the_type(fmt, dtype):
+    """Bit for bit."""
+    x = rows(gen(14), 2, 3, 333, dtype)
+    c = lkv.Cache8(batch=2, n_kv_heads=3, capacity=336, dtype=dtype, fmt=fmt)
+    c.write(x.cuda(), x.cuda())
+    want = (c.k_codes.float() * c.k_scale.repeat_interleave(16, 2)[..., None]).to(dtype)
+    for got in c.read(333):
+        assert torch.equal(got[:, :, :320], want[:, :, :320])
+        assert torch.equal(got[:, :, 320:], x[:, :, 320:].cuda())
