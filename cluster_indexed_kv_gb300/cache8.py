@@ -74,7 +74,11 @@ def _call(index, fn, *args) -> None:
 class Rope:
     """A table of rotary positions (lkv_rope_init): layout "half" pairs values
     (i, i + rotary_dim / 2), "interleaved" (2 i, 2 i + 1); scaling "none",
-    "linear", "ntk" or "yarn" stretches the positions by ``factor``."""
+    "linear", "ntk" or "yarn" stretches the positions by ``factor`` (YaRN with
+    the ramp over turns of its formula; checkpoints may want one over pair
+    indexes). ``table`` is what the calls read: for frequencies f_i of one's own,
+    ``table.turn[i] = round(f_i / (2 * math.pi) * 2 ** 64)`` for each pair, and
+    ``table.gain``."""
 
     def __init__(self, *, rotary_dim: int = _D, layout: str = "half", base: float = 10000.0,
                  scaling: str = "none", factor: float = 1.0, orig_len: int = 0,

@@ -474,7 +474,13 @@ lkv_status lkv_diag_wait_timeout(lkv_ctx *ctx, int64_t limit_ns);
  *   LKV_ROPE_YARN    f_i (g + (1 - g) / factor), g = (r - beta_slow) /
  *                    (beta_fast - beta_slow) clamped to 0..1, r = orig_len *
  *                    f_i / (2 pi) the turns of pair i in orig_len positions;
- *                    gain 0.1 ln(factor) + 1
+ *                    gain 0.1 ln(factor) + 1. This is the ramp over turns of
+ *                    the method's formula. Code that checkpoints were trained
+ *                    with may ramp over the pairs' index instead, between the
+ *                    pairs of beta_fast and beta_slow turns taken to whole
+ *                    numbers: other frequencies (up to 1.7 times these for
+ *                    128 values, base 10^6, factor 4, 32768 positions).
+ *                    Whoever needs those fills the table (lkv_rope below).
  * rotary_dim even, 2..128; base, factor >= 1 and finite; orig_len >= 1 and
  * beta_fast > beta_slow >= 0 (LKV_ROPE_YARN). */
 enum { LKV_ROPE_HALF = 0, LKV_ROPE_INTERLEAVED = 1 };
@@ -492,7 +498,9 @@ typedef struct lkv_rope_params {
 
 /* The table that lkv_rope_apply takes: turn[i] is f_i / (2 pi) in units of
  * 2^-64 turns, so that a position times turn[i], modulo 2^64, is the angle's
- * fraction of a turn however far the position is. */
+ * fraction of a turn however far the position is. A program with frequencies
+ * of its own may write the table itself: turn[i] = f_i / (2 pi) * 2^64, rounded,
+ * for i < rotary_dim / 2 (0 <= f_i < 2 pi), and the gain. */
 typedef struct lkv_rope {
   int32_t rotary_dim;
   int32_t layout;

@@ -1,10 +1,14 @@
 """The Python calls of rotary positions and the 8-bit cache: what they refuse
 and what they keep."""
+import math
+
 import pytest
 import torch
 
 import cluster_indexed_kv_gb300 as lkv
 from cluster_indexed_kv_gb300 import _lib
+from tests import _cache8_ref as ref
+from tests.test_gpu_rope import check
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -103,3 +107,32 @@ def test_check_reports_an_attention_that_gave_up():
         assert torch.equal(c.attend(q), want)
         c.check()
     assert c._ticket.tolist() == [0, 0, 0]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_frequencies_of_ones_own(dtype, layout):
+    """A table filled by the program: YaRN's ramp over pair indexes, which no scaling of Rope's gives."""
+    base, factor, orig, fast, slow = 1e6, 4.0, 32768, 32.0, 1.0
+
+    def pair(turns):
+        return 128 * math.log(orig / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+    low, high = math.floor(pair(fast)), math.ceil(pair(slow))
+    f = [base ** (-2 * i / 128) for i in range(64)]
+    keep = [1 - min(1.0, max(0.0, (i - low) / (high - low))) for i in range(64)]
+    f = [x * (g + (1 - g) / factor) for x, g in zip(f, keep)]
+    gain = 0.1 * math.log(factor) + 1
+    r = lkv.Rope(base=base, layout=layout)
+    for i, x in enumerate(f):
+        r.table.turn[i] = round(x / (2 * math.pi) * 2 ** 64)
+    r.table.gain = gain
+    g = torch.Generator().manual_seed(1)
+    q, k = (torch.randn(2, h, 40, 128, generator=g).to(dtype).cuda() for h in (8, 2))
+    pos = torch.randint(0, 1 << 17, (2, 40), generator=g, dtype=torch.int32).cuda()
+    q2, k2 = r.apply(q, pos, k)
+    rates = torch.tensor(f, dtype=torch.float64)
+    check(q2, q, pos, rates, gain, layout)
+    check(k2, k, pos, rates, gain, layout)
+    paper, _ = ref.rope_rates(128, base=base, scaling="yarn", factor=factor, orig_len=orig)
+    assert (rates / paper).max() > 1.3  # another ramp than scaling="yarn"
