@@ -597,8 +597,19 @@ lkv_status lkv_cache8_read(const lkv_cache8 *cache, const int32_t *first, int32_
  * own position; with window > 0 only those with j > position - window or
  * j < sinks (the first tokens stay visible). out = sum over them of
  * softmax(scale * q . k_j) v_j; a row that sees nothing (a position below 0),
- * and every row at or past counts[b], is zero. Scores, softmax and sums are
- * fp32. n = 1 is a decode step; any n is taken. max_len: an upper bound of the
+ * and every row at or past counts[b], is zero. Scores, exponentials, the
+ * softmax's totals and all sums are fp32; codes are exact. What is rounded on
+ * its way into a product:
+ *   - queries, and keys of the last, partial block, in units of the power of
+ *     two above the largest value of the row or block: 2^-25 of that unit
+ *     where they are small, and bf16 values not at all where they are above
+ *     2^-14 of it; fp32 values 2^-22 of themselves
+ *   - bf16 caches: the softmax's weights, 2^-11 of themselves, and 2^-31 of the
+ *     row's largest weight where they are below 2^-20 of it (weights times
+ *     their block's V scale); values of the partial block as its keys
+ *   - fp32 caches: weights and values of the partial block, 2^-24 of themselves
+ * V scales below 2^-90 of the largest may be taken for that.
+ * n = 1 is a decode step; any n is taken. max_len: an upper bound of the
  * lengths that the caller knows (0: the capacity); it steers how the work is
  * split, and results stay right when a length is above it. workspace: device
  * memory of at least lkv_cache8_attend_workspace bytes for the same sizes
