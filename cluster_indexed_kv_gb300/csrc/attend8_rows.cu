@@ -749,10 +749,11 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
             for (int e = 0; e < 16; e += 4) *(uint4 *)(slot + (d + e) * 2 * kRwRows + 4 * r) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
         }
+        // (a row whose scores are all NaN has no reference, but l and O, which are NaN, count)
         const bool any = valid && seen;
         slot[2 * kRwRows * kHeadDim + r] = any ? ref + (float)unit : -INFINITY;
         slot[2 * kRwRows * (kHeadDim + 1) + r] = any ? ref : -INFINITY;
-        slot[2 * kRwRows * (kHeadDim + 2) + r] = any ? l : 0.f;
+        slot[2 * kRwRows * (kHeadDim + 2) + r] = valid ? l : 0.f;
       } else {
         const float scale = valid && l != 0.f ? 1.f / l : 0.f, back = pow2f(unit);
         uint4 *out = (uint4 *)((uint16_t *)a.out + ((at.slice * a.group + row % a.group) * a.n + row / a.group) * kHeadDim);

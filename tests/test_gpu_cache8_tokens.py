@@ -309,3 +309,28 @@ def test_read_is_the_product_in_fp32_rounded_to_the_type(fmt, dtype):
     for got in c.read(333):
         assert torch.equal(got[:, :, :320], want[:, :, :320])
         assert torch.equal(got[:, :, 320:], x[:, :, 320:].cuda())
+
+
+# ---------------------------------------------------------------- NaN
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lengths,h,group,n", [([300, 17], 2, 4, 1), ([9000], 1, 4, 1), ([20011, 20000], 1, 4, 3), ([700] * 64, 2, 4, 64),
+                                               ([20001], 2, 4, 128)])
+def test_a_query_that_is_not_a_number(dtype, lengths, h, group, n):
+    """Its row of the output is NaN, however the call is split, and no other row is."""
+    b, top = len(lengths), max(lengths)
+    g = gen(n)
+    x, y = (torch.randn(b, h, top, 128, generator=g).to(dtype) for _ in range(2))
+    c, k, v = make(x, y, "int8", dtype, (top + 15) // 16 * 16, lengths)
+    q = torch.randn(b, h * group, n, 128, generator=g).to(dtype)
+    bad = torch.rand(b, h * group, n, generator=g) < 0.1
+    bad[0, 1, n - 1], bad[0, 0, n - 1] = True, False
+    q2 = q.clone()
+    q2[..., 77][bad] = float("nan")
+    got = c.attend(q2.cuda()).cpu()
+    assert got[bad].isnan().all()
+    for i, length in enumerate(lengths):
+        kk, vv = (ref.values(a[0][i], a[1][i], a[2][i], length) for a in (k, v))
+        want, lim = each.attend(q[i].double(), kk, vv, each.units(v[1][i], v[2][i], length), n, 128 ** -0.5, 0, 0, dtype)
+        assert ((got[i].double() - want).abs() <= lim)[~bad[i]].all()
+    c.check()
