@@ -435,9 +435,12 @@ __device__ __forceinline__ void put_out(const AttendArgs &a, int64_t slice, int 
 // them. No atomics in either: the same result each time.
 //
 // Bound by the codes' bytes. On a GB300, 4 query heads, bf16: 64 slices of 33,000 tokens 89 us, 89%
-// of the measured copy rate; 8 of 131,579 tokens 53 us, 75% (a long merge); 256
-// slices of a window of 1024 tokens 19 us, 52%, and one of 2048 tokens 9 us:
-// those wait for a launch, lengths, queries, codes and the merges in turn.
+// of the measured copy rate; 8 of 131,579 tokens 53 us, 75% (the merge is a
+// second kernel behind the first); 256 slices of a window of 1024 tokens 19.5 us,
+// 51% (one warp's partial block, and launch, lengths, queries and merges in
+// turn, as for one slice of 2048 tokens: 9 us). fp32 caches are bound by their
+// products: 64 slices of 33,000 tokens 116 us, 8 of 131,579 tokens 66 us, one
+// of 2048 tokens 9.6 us.
 template <int DT, int CODE, int NT>
 __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
     k_attend8(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -898,7 +901,10 @@ static const char *plan_attend(const lkv_cache8 *c, int32_t group, int32_t n, in
   if (ctas < 3 * slots && last > 0 && last * 5 < slots * 3 && blocks >= 24 * p->cluster &&
       (int64_t)c->batch * p->row_tiles <= kAtGroups) {
     // at least 16 blocks for each CTA; few tiles: a whole number of CTAs each,
-    // so that none begins two, and not the last ones (parts cost merging)
+    // so that none begins two, and not the last ones (parts cost merging). With
+    // 24, 27, 29 and 32 of 32 CTAs, us: 8 slices of 131,579 tokens 56.9, 52.8,
+    // 53.0, 53.6; 16 of 60,000 51.8, 48.9, 48.5, 48.8; 4 of 65,000 22.0, 19.8,
+    // 20.2, 20.0; one of 131,000 20.8, 20.1, 20.8, 20.9.
     int64_t most_ctas = p->tiles * blocks / 16;
     if (most_ctas < p->tiles) most_ctas = p->tiles;
     const int64_t full = slots * 27 / 32 < most_ctas ? slots * 27 / 32 : most_ctas;
