@@ -48,7 +48,14 @@ static thread_local std::string g_create_error;
 
 namespace lkv {
 // Error text of calls that have no context (read with lkv_last_error(NULL)).
-void set_unbound_error(const char *msg) { g_create_error = msg; }
+// Nothing is thrown: where there is no memory for the text, there is none.
+void set_unbound_error(const char *msg) {
+  try {
+    g_create_error = msg;
+  } catch (...) {
+    g_create_error.clear();
+  }
+}
 }  // namespace lkv
 
 static lkv_status fail(lkv_ctx *c, lkv_status s, const std::string &msg) {

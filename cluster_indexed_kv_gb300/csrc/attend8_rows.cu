@@ -34,7 +34,7 @@ namespace lkv {
 // long as that: S 650, weights 2150 (450 of them the first read of S), the
 // last half's P V 300, and the barriers between them, with the other row tile's
 // products in between. 2048 tokens over 32K, 32 query and 8 KV heads on a
-// GB300: 1030 us, 1.03 PFLOP/s, 54% of the measured bf16 rate. Slower: a row
+// GB300: 1020 to 1030 us, 1.04 PFLOP/s, 55% of the measured bf16 rate. Slower: a row
 // tile's first softmax thread issuing its products (no issuing warp, 168
 // registers, 1214 us); S in halves of 64 tokens, each with its barrier (1135);
 // a quarter of the exponentials as polynomials (1086).

@@ -637,7 +637,8 @@ lkv_status lkv_cache8_status(const lkv_cache8 *cache, void *stream);
 lkv_status lkv_sync(lkv_ctx *ctx);
 
 /* Text of the last error on this context ("" if none); valid until the next
- * call on the context. NULL ctx: the last lkv_create failure. */
+ * call on the context. NULL ctx: the last failure of lkv_create, or of a call
+ * that takes no context, on this thread. */
 const char *lkv_last_error(const lkv_ctx *ctx);
 
 #ifdef __cplusplus
