@@ -752,6 +752,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
 constexpr int kMergeThreads = 512;
 constexpr int kMergeGroups = kMergeThreads / 64;
 constexpr int kMergeEarly = 4;  // parts that a thread loads while the factors are made
+static_assert(kAtGroups <= kMergeThreads, "a thread checks one (sequence, row tile)");
 constexpr int kMaxCtas = 1024;
 
 template <int DT, int NT>
