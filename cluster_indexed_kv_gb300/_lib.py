@@ -23,12 +23,14 @@ EXPORTED = ("lkv_create", "lkv_destroy", "lkv_build_index", "lkv_load_index",
             "lkv_kmeans_static", "lkv_kmeans_static_status", "lkv_set_kmeans_filter",
             "lkv_diag_wait_timeout", "lkv_uva_read", "lkv_read_ceiling", "lkv_set_policy", "lkv_build_pages",
             "lkv_build_index_async", "lkv_build_paris", "lkv_paris_levels",
-            "lkv_rope_init", "lkv_rope_apply", "lkv_cache8_write", "lkv_cache8_read",
-            "lkv_cache8_attend", "lkv_cache8_attend_workspace", "lkv_cache8_status")
+            "lkv_rope_init", "lkv_rope_apply", "lkv_rope_apply_axes", "lkv_cache8_write", "lkv_cache8_read",
+            "lkv_cache8_attend", "lkv_cache8_attend_workspace", "lkv_cache8_take",
+            "lkv_cache8_take_workspace", "lkv_cache8_keep", "lkv_cache8_status")
 LKV_FILTER_TENSOR, LKV_FILTER_SIMT = 0, 1
 LKV_TRIGGER_ADAPTIVE, LKV_TRIGGER_EVERY, LKV_TRIGGER_INTERVAL = 0, 1, 2
 LKV_FILL_PREFIX, LKV_FILL_SKIP = 0, 1
 LKV_ROPE_HALF, LKV_ROPE_INTERLEAVED = 0, 1
+LKV_ROPE_AXES = 4
 LKV_ROPE_NONE, LKV_ROPE_LINEAR, LKV_ROPE_NTK, LKV_ROPE_YARN = range(4)
 LKV_CACHE8_BLOCK = 16
 LKV_CODE_INT8, LKV_CODE_E4M3 = 0, 1
@@ -155,6 +157,8 @@ def load(path: str = LIB_PATH):
         L.lkv_rope_init.restype = st
         L.lkv_rope_apply.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
         L.lkv_rope_apply.restype = st
+        L.lkv_rope_apply_axes.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+        L.lkv_rope_apply_axes.restype = st
         L.lkv_cache8_write.argtypes = [vp, vp, vp, i32, vp, vp, vp]
         L.lkv_cache8_write.restype = st
         L.lkv_cache8_read.argtypes = [vp, vp, i32, vp, vp, vp]
@@ -163,6 +167,12 @@ def load(path: str = LIB_PATH):
         L.lkv_cache8_attend.restype = st
         L.lkv_cache8_attend_workspace.argtypes = [vp, i32, i32, i32, i32, i32, C.POINTER(i64)]
         L.lkv_cache8_attend_workspace.restype = st
+        L.lkv_cache8_take.argtypes = [vp, vp, vp, vp, vp, i64, vp]
+        L.lkv_cache8_take.restype = st
+        L.lkv_cache8_take_workspace.argtypes = [vp, vp, C.POINTER(i64)]
+        L.lkv_cache8_take_workspace.restype = st
+        L.lkv_cache8_keep.argtypes = [vp, vp, vp, i32, vp, vp]
+        L.lkv_cache8_keep.restype = st
         L.lkv_cache8_status.argtypes = [vp, vp]
         L.lkv_cache8_status.restype = st
         L.lkv_sync.argtypes = [vp]
@@ -302,6 +312,12 @@ def lkv_cache8_attend_workspace(cache, group, n, window, sinks, max_len) -> int:
     n_bytes = C.c_int64(0)
     _check(load().lkv_cache8_attend_workspace(cache, group, n, window, sinks, max_len,
                                               C.byref(n_bytes)), None)
+    return n_bytes.value
+
+
+def lkv_cache8_take_workspace(cache, source) -> int:
+    n_bytes = C.c_int64(0)
+    _check(load().lkv_cache8_take_workspace(cache, source, C.byref(n_bytes)), None)
     return n_bytes.value
 
 

@@ -78,27 +78,55 @@ class Rope:
     the ramp over turns of its formula; checkpoints may want one over pair
     indexes). ``table`` is what the calls read: for frequencies f_i of one's own,
     ``table.turn[i] = round(f_i / (2 * math.pi) * 2 ** 64)`` for each pair, and
-    ``table.gain``."""
+    ``table.gain``.
+
+    Positions on several axes (time, height, width; at most 4): ``sections``
+    gives each axis a run of that many pairs, in order, which fill rotary_dim /
+    2; or ``axes`` names the axis of each pair. With own_base the frequencies
+    begin anew in each section, as if it were a rotation of 2 * section values."""
 
     def __init__(self, *, rotary_dim: int = _D, layout: str = "half", base: float = 10000.0,
                  scaling: str = "none", factor: float = 1.0, orig_len: int = 0,
-                 beta_fast: float = 32.0, beta_slow: float = 1.0):
+                 beta_fast: float = 32.0, beta_slow: float = 1.0, sections=None, axes=None,
+                 own_base: bool = False):
         if not 0 <= rotary_dim <= _INT32 or not 0 <= orig_len <= _INT32:
             raise ValueError("rotary_dim and orig_len must be in 0..2^31 - 1")
         lay = {"half": _lib.LKV_ROPE_HALF, "interleaved": _lib.LKV_ROPE_INTERLEAVED}[layout]
         how = {"none": _lib.LKV_ROPE_NONE, "linear": _lib.LKV_ROPE_LINEAR, "ntk": _lib.LKV_ROPE_NTK,
                "yarn": _lib.LKV_ROPE_YARN}[scaling]
-        self.table = _lib.lkv_rope_init(rotary_dim, lay, how, orig_len, base, factor, beta_fast,
-                                        beta_slow)
+        rest = (lay, how, orig_len, base, factor, beta_fast, beta_slow)
+        self.table = _lib.lkv_rope_init(rotary_dim, *rest)
+        self.n_axes = 0  # 0: positions are [B, n]
+        if sections is not None:
+            if axes is not None:
+                raise ValueError("sections or axes, not both")
+            sections = [int(s) for s in sections]
+            if any(s < 1 for s in sections) or sum(sections) != rotary_dim // 2:
+                raise ValueError(f"sections must be at least 1 each and {rotary_dim // 2} together, got {sections}")
+            axes = [a for a, s in enumerate(sections) for _ in range(s)]
+        elif own_base:
+            raise ValueError("own_base without sections")
+        if axes is not None:
+            axes = [int(a) for a in axes]
+            if len(axes) != rotary_dim // 2 or not all(0 <= a < _lib.LKV_ROPE_AXES for a in axes):
+                raise ValueError(f"axes must name one of at most {_lib.LKV_ROPE_AXES} axes for each of {rotary_dim // 2} pairs")
+            self.n_axes = max(axes) + 1
+            self._axis = (C.c_uint8 * len(axes))(*axes)
+        if own_base:
+            at = 0
+            for s in sections:
+                t = _lib.lkv_rope_init(2 * s, *rest)
+                self.table.turn[at:at + s] = t.turn[:s]
+                at += s
         self._at = C.addressof(self.table)
-        self._apply = _lib.load().lkv_rope_apply
+        self._apply, self._apply_axes = _lib.load().lkv_rope_apply, _lib.load().lkv_rope_apply_axes
 
     def apply(self, q: torch.Tensor, positions: torch.Tensor, k: torch.Tensor | None = None, *,
               q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
         """Rotate q [B, H, n, 128] and, if given, k [B, H_kv, n, 128] by
-        positions int32 [B, n]. Returns q_out, or (q_out, k_out) with k; the
-        outputs may be q and k themselves (in place), and are new tensors by
-        default."""
+        positions int32 [B, n], or [A, B, n] where the table has A axes.
+        Returns q_out, or (q_out, k_out) with k; the outputs may be q and k
+        themselves (in place), and are new tensors by default."""
         if not isinstance(q, torch.Tensor) or not q.is_cuda:
             raise ValueError("q must be a CUDA tensor")
         dt, dev, q_shape = q.dtype, q.get_device(), q.shape
@@ -108,7 +136,8 @@ class Rope:
             raise ValueError(f"q must have shape [B, H, n, {_D}], got {tuple(q_shape)}")
         batch, heads, n, _ = q_shape
         qp = _tensor(q, "q", q_shape, dt, dev)
-        pp = _tensor(positions, "positions", (batch, n), torch.int32, dev)
+        axes = self.n_axes
+        pp = _tensor(positions, "positions", (axes, batch, n) if axes else (batch, n), torch.int32, dev)
         if q_out is None:
             q_out = _empty((batch, heads, n, _D), dt, dev)
             qo = q_out.data_ptr()
@@ -129,8 +158,12 @@ class Rope:
                 ko = _tensor(k_out, "k_out", shape, dt, dev)
         elif k_out is not None:
             raise ValueError("k_out without k")
-        _call(dev, self._apply, self._at, _DTYPES[dt], batch, heads, kv_heads, n, qp, kp, pp,
-              qo, ko)
+        if axes:
+            _call(dev, self._apply_axes, self._at, self._axis, axes, _DTYPES[dt], batch, heads, kv_heads, n, qp, kp,
+                  pp, qo, ko)
+        else:
+            _call(dev, self._apply, self._at, _DTYPES[dt], batch, heads, kv_heads, n, qp, kp, pp,
+                  qo, ko)
         return q_out if k is None else (q_out, k_out)
 
 
@@ -197,6 +230,7 @@ class Cache8:
         lib = _lib.load()
         self._write, self._read = lib.lkv_cache8_write, lib.lkv_cache8_read
         self._attend, self._status = lib.lkv_cache8_attend, lib.lkv_cache8_status
+        self._take, self._keep = lib.lkv_cache8_take, lib.lkv_cache8_keep
 
     def write(self, k: torch.Tensor, v: torch.Tensor, *, start: torch.Tensor | None = None,
               counts: torch.Tensor | None = None) -> None:
@@ -230,6 +264,47 @@ class Cache8:
         fp = None if first is None else _tensor(first, "first", (self.batch,), torch.int32, dev)
         _call(dev, self._read, self._at, fp, n, kp, vp)
         return k_out, v_out
+
+    def _source(self, source) -> int:
+        """Address of the cache that a take or keep reads."""
+        if source is None:
+            return self._at
+        if not isinstance(source, Cache8):
+            raise TypeError("source must be a Cache8")
+        if source._index != self._index:
+            raise ValueError(f"source must be on cuda:{self._index}, got cuda:{source._index}")
+        return source._at
+
+    def take(self, source: Cache8 | None = None, sequences: torch.Tensor | None = None,
+             lengths: torch.Tensor | None = None) -> None:
+        """Sequence b becomes the first lengths[b] tokens (default: all) of
+        sequence sequences[b] (default: b; -1 leaves b as it is) of source, or
+        of this cache itself, whose sequences then take what the others held
+        before the call: samples of one prompt, beams put in order, sequences
+        moved together, cut back at any token, freed (length 0). sequences and
+        lengths are int32 [B]. Other batches and capacities of source fit."""
+        dev, batch = self._index, self.batch
+        at = self._source(source)
+        sp = None if sequences is None else _tensor(sequences, "sequences", (batch,), torch.int32, dev)
+        lp = None if lengths is None else _tensor(lengths, "lengths", (batch,), torch.int32, dev)
+        ws_bytes = _lib.lkv_cache8_take_workspace(self._at, at)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device) if ws_bytes else None
+        _call(dev, self._take, self._at, at, sp, lp, ws.data_ptr() if ws_bytes else None, ws_bytes)
+
+    def keep(self, blocks: torch.Tensor, counts: torch.Tensor, source: Cache8 | None = None) -> None:
+        """Whole blocks of 16 tokens stay, or come from source (of the same
+        batch), chosen for each KV head: block j < counts[b] of (b, h) becomes
+        block blocks[b, h, j], and the partial block follows. blocks int32
+        [B, H_kv, m], each list strictly ascending in its first counts[b]
+        entries; counts int32 [B], -1 to leave a sequence as it is."""
+        dev = self._index
+        at = self._source(source)
+        if not isinstance(blocks, torch.Tensor) or blocks.dim() != 3:
+            raise ValueError("blocks must be a tensor of shape [B, H_kv, m]")
+        m = blocks.shape[2]
+        bp = _tensor(blocks, "blocks", (self.batch, self.n_kv_heads, m), torch.int32, dev)
+        cp = _tensor(counts, "counts", (self.batch,), torch.int32, dev)
+        _call(dev, self._keep, self._at, at, bp, m, cp)
 
     def attend(self, q: torch.Tensor, *, counts: torch.Tensor | None = None, scale: float | None = None,
                window: int = 0, sinks: int = 0, max_len: int = 0,
@@ -281,8 +356,9 @@ class Cache8:
 
     def check(self) -> None:
         """Wait for the current stream; raise LKVError if, since the last
-        check, an attention gave up waiting for its copies (its output is not
-        complete), a write did not fit, or one held a value that is not finite.
+        check, an attention, take or keep gave up waiting for its copies (what
+        it made is not complete), a write, take or keep did not fit, or a write
+        held a value that is not finite.
         Everything is reported once, in one error: the first of these that
         there is."""
         _call(self._index, self._status, self._at)

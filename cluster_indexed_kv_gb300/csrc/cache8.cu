@@ -1,8 +1,6 @@
 // cache8.cu -- the 8-bit key/value cache: writing, reading back, status.
 #include "cache8.cuh"
 
-#include <cuda_fp16.h>
-
 namespace lkv {
 
 constexpr int kCacheThreads = 128;
@@ -45,12 +43,20 @@ bool overlaps_cache8(const lkv_cache8 *c, const void *p, int64_t bytes) {
 }
 
 // Whether two of the cache's own arrays share memory.
-static bool arrays_overlap(const lkv_cache8 *c) {
+bool cache8_arrays_overlap(const lkv_cache8 *c) {
   Extent e[kArrays];
   extents(c, e);
   for (int i = 0; i < kArrays; ++i)
     for (int j = 0; j < i; ++j)
       if (overlap(e[i].at, e[i].bytes, e[j].at, e[j].bytes)) return true;
+  return false;
+}
+
+bool caches_overlap(const lkv_cache8 *a, const lkv_cache8 *b) {
+  Extent e[kArrays];
+  extents(a, e);
+  for (const Extent &x : e)
+    if (overlaps_cache8(b, x.at, x.bytes)) return true;
   return false;
 }
 
@@ -386,21 +392,6 @@ struct ReadArgs {
   int64_t tasks;
 };
 
-template <int CODE>
-__device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
-  if constexpr (CODE == LKV_CODE_INT8) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = (float)(int8_t)(w >> (8 * e));
-  } else {
-    uint32_t lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi) : "r"(w));
-    const float2 a = __half22float2(*(__half2 *)&lo), b = __half22float2(*(__half2 *)&hi);
-    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-  }
-}
-
 // A warp takes 16 rows, all its loads first: codes (8 or 4 bytes a lane) and
 // the rows' scales, then a product in fp32 a value, rounded to the type. Bound: bytes (1 in, 2
 // or 4 out a value). On a GB300, 128K tokens of 8 KV heads to bf16: 115 us, the
@@ -477,7 +468,7 @@ extern "C" lkv_status lkv_cache8_write(const lkv_cache8 *c, const void *k, const
   if (!k || !v) return refuse("lkv_cache8_write: null keys or values");
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4) || !aligned(counts, 4))
     return refuse("lkv_cache8_write: keys and values must be 16-byte aligned, start and counts 4-byte aligned");
-  if (arrays_overlap(c)) return refuse("lkv_cache8_write: two of the cache's arrays overlap");
+  if (cache8_arrays_overlap(c)) return refuse("lkv_cache8_write: two of the cache's arrays overlap");
   const int64_t slices = (int64_t)c->batch * c->n_kv_heads;
   const int64_t bytes = slices * n * kHeadDim * (c->dtype == LKV_DTYPE_BF16 ? 2 : 4), ib = (int64_t)c->batch * 4;
   if (overlaps_cache8(c, k, bytes) || overlaps_cache8(c, v, bytes) || overlaps_cache8(c, start, ib) ||
@@ -562,15 +553,15 @@ extern "C" lkv_status lkv_cache8_status(const lkv_cache8 *c, void *stream) {
   if (e == cudaSuccess && bits) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_refuse("lkv_cache8_status", e);
   if (bits & kAnomTimeout) {
-    set_unbound_error("lkv_cache8: a device-side wait of an attention gave up; its output is not complete");
+    set_unbound_error("lkv_cache8: a device-side wait of an attention, take or keep gave up; what it made is not complete");
     return LKV_ETIMEOUT;
   }
   if (bits & kAnomCapacity) {
-    set_unbound_error("lkv_cache8: a write went past the capacity; that sequence was left as it was");
+    set_unbound_error("lkv_cache8: a write, take or keep went past the capacity; that sequence was left as it was");
     return LKV_ECAPACITY;
   }
   if (bits & kAnomRange)
-    return refuse("lkv_cache8: a write's start or count was out of range; that sequence was left as it was");
+    return refuse("lkv_cache8: a write's start or count, or what a take or keep named, was out of range; that sequence was left as it was");
   if (bits & kAnomNotFinite) return refuse("lkv_cache8: a NaN or an infinity was written");
   return LKV_OK;
 }

@@ -1,6 +1,8 @@
 // cache8.cuh -- shared by the calls that have no context: rotary positions
-// and the 8-bit cache (rope.cu, cache8.cu, attend8.cu).
+// and the 8-bit cache (rope.cu, cache8.cu, move8.cu, attend8.cu).
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include <cstdio>
 
@@ -13,10 +15,10 @@ constexpr int kBlock = LKV_CACHE8_BLOCK;  // tokens that share a scale
 
 // Anomalies of a cache, kept in ticket[batch] until lkv_cache8_status.
 enum : int32_t {
-  kAnomRange = 1,      // a write's start or count is not one the cache can take
-  kAnomCapacity = 2,   // a write past the capacity
+  kAnomRange = 1,      // a write's start or count is not one the cache can take, or what a take or keep names is not there
+  kAnomCapacity = 2,   // a write, take or keep past the capacity
   kAnomNotFinite = 4,  // a NaN or an infinity was written
-  kAnomTimeout = 8,    // a bounded wait in an attention gave up
+  kAnomTimeout = 8,    // a bounded wait in an attention, take or keep gave up
 };
 
 inline lkv_status refuse(const char *msg) {
@@ -49,6 +51,9 @@ inline cudaError_t sm_count(int *sms) {
 const char *check_cache8(const lkv_cache8 *c);
 // Whether [p, p + bytes) lies in one of the cache's arrays.
 bool overlaps_cache8(const lkv_cache8 *c, const void *p, int64_t bytes);
+// Whether two of the cache's own arrays share memory, and one of a's with one of b's.
+bool cache8_arrays_overlap(const lkv_cache8 *c);
+bool caches_overlap(const lkv_cache8 *a, const lkv_cache8 *b);
 
 // Programmatic dependent launch: the stream's next kernel may start; and:
 // everything the previous kernel wrote is visible, and it has ended. Every
@@ -80,6 +85,22 @@ inline cudaError_t launch_next(void (*fn)(Args), dim3 grid, int block, size_t sm
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 w = __floats2bfloat162_rn(lo, hi);
   return *(const uint32_t *)&w;
+}
+
+// Four codes as values.
+template <int CODE>
+__device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
+  if constexpr (CODE == LKV_CODE_INT8) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = (float)(int8_t)(w >> (8 * e));
+  } else {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+    const float2 a = __half22float2(*(__half2 *)&lo), b = __half22float2(*(__half2 *)&hi);
+    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+  }
 }
 
 }  // namespace lkv

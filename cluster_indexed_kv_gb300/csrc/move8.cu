@@ -1,0 +1,578 @@
+// move8.cu -- taking and keeping tokens of the 8-bit cache: lkv_cache8_take
+// (sequences copied, forked, put in order, cut back and freed) and
+// lkv_cache8_keep (blocks chosen for each KV head moved together).
+#include "cache8.cuh"
+#include "tma.cuh"
+
+namespace lkv {
+
+// Both kernels move whole blocks as they are, codes and scale, through shared
+// memory: a warp (a CTA is one) has kMoveStages stages, of which all but one are
+// being filled or emptied by bulk copies while it turns to the next. Nothing is
+// computed but the tail of a sequence that ends inside an older block.
+constexpr int kMoveStage = 16384;        // bytes of a stage's codes
+constexpr int kMoveStages = 4;
+constexpr int kMovePerSm = 3;            // CTAs that an SM's shared memory holds
+constexpr int kBlockBytes = kBlock * kHeadDim;
+constexpr int kTakeItems = 32;           // destinations of a CTA between two caches
+constexpr int kTakeInside = 1024;        // and within one, all of them: 16 bytes of each in a stage
+constexpr int32_t kKeepBad = 1 << 30;    // in a ticket: the sequence's lists are refused
+
+__device__ __forceinline__ void bulk_load(void *to, const void *from, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_at(to)), "l"(from), "r"(bytes), "r"(smem_at(bar)) : "memory");
+}
+__device__ __forceinline__ void bulk_store(void *to, const void *from, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(smem_at(from)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// a float to shared memory, by the thread's own groups
+__device__ __forceinline__ void word_load(float *to, const float *from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_at(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void word_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void word_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Bytes [from, to) of a block (multiples of 16) in shared memory as the rows of
+// a tail that lkv_cache8_read would give, by a whole warp.
+template <int DT, int CODE>
+__device__ __forceinline__ void to_tail(void *tail, const unsigned char *codes, int from, int to, float scale, int lane) {
+  for (int at = from + 4 * lane; at < to; at += 128) {
+    float x[4];
+    decode4<CODE>(*(const uint32_t *)(codes + at - from), x);
+    if (DT == 1)
+      *(uint2 *)((uint16_t *)tail + at) = make_uint2(pack_bf16(x[0] * scale, x[1] * scale), pack_bf16(x[2] * scale, x[3] * scale));
+    else
+      *(float4 *)((float *)tail + at) = make_float4(x[0] * scale, x[1] * scale, x[2] * scale, x[3] * scale);
+  }
+}
+
+// A tail as it is, by a whole warp.
+template <int DT>
+__device__ __forceinline__ void copy_tail(void *to, const void *from, int lane) {
+  constexpr int N = kBlock * kHeadDim * (DT == 1 ? 2 : 4) / 16;
+  uint4 w[N / 32];
+#pragma unroll
+  for (int i = 0; i < N / 32; ++i) w[i] = ((const uint4 *)from)[i * 32 + lane];
+#pragma unroll
+  for (int i = 0; i < N / 32; ++i) ((uint4 *)to)[i * 32 + lane] = w[i];
+}
+
+template <int DT>
+__device__ __forceinline__ char *tail_of(void *tails, int64_t slice) {
+  return (char *)tails + slice * kBlock * kHeadDim * (DT == 1 ? 2 : 4);
+}
+
+// ---------------------------------------------------------------- take
+
+struct TakeArgs {
+  lkv_cache8 to, from;            // from: lengths and tails are the snapshot's within one cache
+  const int32_t *sequences, *lengths;
+  int32_t items;                  // destinations of a CTA
+  int32_t inside;
+};
+
+// What a sequence becomes: its source (-1: it is left as it is), its length,
+// which slot of a stage holds the source's bytes (-1: none is needed), and its
+// last block where that is not the source's last one (-1: the source's tail is its own).
+struct TakeItem { int32_t from, len, slot, older; };
+// Which blocks of a source the stages hold.
+struct TakeSlot { int32_t from, lo, hi; };
+
+__host__ __device__ inline int64_t take_smem(int items) {
+  const int words = items > kMoveStage / kBlockBytes ? items : kMoveStage / kBlockBytes;
+  return 128 + kMoveStages * (int64_t)(kMoveStage + 4 * words) + items * (int64_t)(sizeof(TakeItem) + sizeof(TakeSlot));
+}
+
+// A CTA's tasks are columns: the same `unit` bytes of the codes of one KV head,
+// K or V, in every sequence of its group. It loads each distinct source's once,
+// and only when all of a column have arrived stores them, so that sequences of
+// one cache may take one another's tokens in any order: columns do not depend
+// on one another. (Tails and lengths do, and come from a snapshot there.)
+//
+// Bound by bytes. On a GB300, one prompt of 8191 tokens (8 KV heads, int8)
+// into 16 sequences: see the table of cases.
+template <int DT, int CODE>
+__global__ void __launch_bounds__(32) k_cache8_take(const __grid_constant__ TakeArgs a) {
+  extern __shared__ __align__(128) unsigned char area[];
+  __shared__ __align__(8) uint64_t full_bar[kMoveStages];
+  const int lane = threadIdx.x, group = blockIdx.y, H = a.to.n_kv_heads;
+  const int words = max(a.items, kMoveStage / kBlockBytes);
+  unsigned char *const stages = area;
+  float *const scales = (float *)(area + kMoveStages * kMoveStage);
+  TakeItem *const items = (TakeItem *)(scales + kMoveStages * words);
+  TakeSlot *const slots = (TakeSlot *)(items + a.items);
+  if (lane == 0) {
+    for (int i = 0; i < kMoveStages; ++i) bar_init(&full_bar[i], 32);
+    bar_init_fence();
+  }
+  __syncwarp();
+  wait_prerequisites();
+
+  // the plan: each CTA makes its group's again
+  const int first = group * a.items, count = min(a.items, a.to.batch - first);
+  int nslots = 0, most = 0;
+  for (int i0 = 0; i0 < count; i0 += 32) {
+    const int i = i0 + lane, b = first + i;
+    int from = -1, len = 0, lo = 0, hi = 0, older = -1, anomaly = 0;
+    if (i < count) {
+      from = a.sequences ? a.sequences[b] : b;
+      if (from < -1 || from >= a.from.batch) anomaly = kAnomRange;
+      else if (from >= 0) {
+        const int have = a.from.lengths[from];
+        len = a.lengths ? a.lengths[b] : have;
+        if (have < 0 || have > a.from.capacity || len < 0 || len > have) anomaly = kAnomRange;
+        else if (len > a.to.capacity) anomaly = kAnomCapacity;
+        else if (len > 0) {
+          const int last = (len - 1) / kBlock;
+          if (last != (have - 1) / kBlock) older = last;  // its tail comes from codes
+          if (a.inside && from == b) {
+            lo = max(older, 0);
+            hi = older + 1;
+          } else {
+            hi = max(older + 1, len / kBlock);
+          }
+        }
+      }
+      if (anomaly) from = -1;
+      if (blockIdx.x == 0) {
+        if (anomaly) atomicOr(a.to.ticket + a.to.batch, anomaly);
+        else if (from >= 0) a.to.lengths[b] = len;
+      }
+    }
+    const bool need = hi > lo;
+    const uint32_t same = __match_any_sync(0xffffffffu, need ? from : -2 - lane);
+    const int leader = __ffs(same) - 1;
+    for (uint32_t rest = __reduce_or_sync(0xffffffffu, same & ~(1u << leader)); rest; rest &= rest - 1) {
+      const int l2 = __ffs(rest) - 1;
+      const int lo2 = __shfl_sync(0xffffffffu, lo, l2), hi2 = __shfl_sync(0xffffffffu, hi, l2), of = __shfl_sync(0xffffffffu, leader, l2);
+      if (of == lane) {
+        lo = min(lo, lo2);
+        hi = max(hi, hi2);
+      }
+    }
+    const uint32_t lead = __ballot_sync(0xffffffffu, need && leader == lane);
+    const int slot = nslots + __popc(lead & ((1u << leader) - 1u));
+    if (i < count) items[i] = TakeItem{from, len, need ? slot : -1, older};
+    if (need && leader == lane) slots[slot] = TakeSlot{from, lo, hi};
+    nslots += __popc(lead);
+    most = max(most, (int)__reduce_max_sync(0xffffffffu, (uint32_t)hi));
+  }
+  __syncwarp();
+
+  // the widest columns that fit a stage, narrower where that leaves CTAs without work
+  int unit = kMoveStage;
+  while (unit > 16 && unit * nslots > kMoveStage) unit /= 2;
+  auto columns = [&] { return nslots ? ((int64_t)most * kBlockBytes + unit - 1) / unit : 0; };
+  while (unit > kBlockBytes && columns() * 2 * H < 4 * (int64_t)gridDim.x) unit /= 2;
+  const int64_t ncol = columns(), tasks = ncol * 2 * H;
+  const int blocks = max(1, unit / kBlockBytes);  // of a column
+  const int64_t slice_codes = (int64_t)a.from.capacity * kHeadDim, slice_scales = a.from.capacity / kBlock;
+
+  auto place = [&](int64_t task, int64_t &c0, int &h, int &kv) {
+    c0 = task % ncol * unit;
+    kv = (int)(task / ncol) & 1;
+    h = (int)(task / ncol) >> 1;
+  };
+  auto issue = [&](int64_t task, int st) {
+    if (task < tasks) {
+      int64_t c0;
+      int h, kv;
+      place(task, c0, h, kv);
+      uint32_t bytes = 0;
+      for (int j = lane; j < nslots; j += 32) {
+        const int64_t r0 = max(c0, (int64_t)slots[j].lo * kBlockBytes), r1 = min(c0 + unit, (int64_t)slots[j].hi * kBlockBytes);
+        if (r1 > r0) bytes += (uint32_t)(r1 - r0);
+      }
+      bar_expect(&full_bar[st], bytes);
+      for (int j = lane; j < nslots; j += 32) {
+        const TakeSlot s = slots[j];
+        const int64_t r0 = max(c0, (int64_t)s.lo * kBlockBytes), r1 = min(c0 + unit, (int64_t)s.hi * kBlockBytes);
+        if (r1 <= r0) continue;
+        const int64_t slice = (int64_t)s.from * H + h;
+        bulk_load(stages + st * kMoveStage + j * unit + (r0 - c0), (const char *)(kv ? a.from.v_codes : a.from.k_codes) + slice * slice_codes + r0,
+                  (uint32_t)(r1 - r0), &full_bar[st]);
+        const float *from = (kv ? a.from.v_scale : a.from.k_scale) + slice * slice_scales;
+        const int k0 = (int)(c0 / kBlockBytes);
+        for (int k = 0; k < blocks; ++k)
+          if (k0 + k >= s.lo && k0 + k < s.hi) word_load(scales + st * words + j * blocks + k, from + k0 + k);
+      }
+    }
+    word_commit();
+  };
+
+  const int64_t step = gridDim.x;
+  for (int i = 0; i < kMoveStages; ++i) issue(blockIdx.x + i * step, i);
+  uint32_t phase = 0;
+  bool dead = false;
+  int64_t task = blockIdx.x;
+  for (int i = 0; task < tasks; ++i, task += step) {
+    const int st = i % kMoveStages;
+    if (!__all_sync(0xffffffffu, bar_wait(&full_bar[st], (phase >> st) & 1))) {
+      dead = true;
+      break;
+    }
+    phase ^= 1u << st;
+    word_wait<kMoveStages - 2>();  // one group a stage, the stages behind this one but for the next to be filled
+    __syncwarp();
+    int64_t c0;
+    int h, kv;
+    place(task, c0, h, kv);
+    const int k0 = (int)(c0 / kBlockBytes);
+    for (int i0 = 0; i0 < count; i0 += 32) {
+      const int it = i0 + lane;
+      TakeItem x{-1, 0, -1, -1};
+      if (it < count) x = items[it];
+      const int b = first + it;
+      bool older = false;
+      if (x.slot >= 0) {
+        const int64_t slice = (int64_t)b * H + h;
+        const int fullb = x.len / kBlock;
+        if (!(a.inside && x.from == b)) {
+          const int64_t r1 = min(c0 + unit, (int64_t)fullb * kBlockBytes);
+          if (r1 > c0)
+            bulk_store((char *)(kv ? a.to.v_codes : a.to.k_codes) + slice * a.to.capacity * kHeadDim + c0, stages + st * kMoveStage + x.slot * unit,
+                       (uint32_t)(r1 - c0));
+          if (c0 % kBlockBytes == 0)
+            for (int k = 0; k < blocks; ++k)
+              if (k0 + k < fullb) (kv ? a.to.v_scale : a.to.k_scale)[slice * (a.to.capacity / kBlock) + k0 + k] = scales[st * words + x.slot * blocks + k];
+        }
+        older = x.older >= k0 && (int64_t)x.older * kBlockBytes < c0 + unit;
+      }
+      for (uint32_t rest = __ballot_sync(0xffffffffu, older); rest; rest &= rest - 1) {
+        const int l2 = __ffs(rest) - 1;
+        const int lb = __shfl_sync(0xffffffffu, x.older, l2), slot = __shfl_sync(0xffffffffu, x.slot, l2), b2 = first + i0 + l2;
+        const int64_t t0 = max(c0, (int64_t)lb * kBlockBytes), t1 = min(c0 + unit, (int64_t)(lb + 1) * kBlockBytes);
+        to_tail<DT, CODE>(tail_of<DT>(kv ? a.to.v_tail : a.to.k_tail, (int64_t)b2 * H + h), stages + st * kMoveStage + slot * unit + (t0 - c0),
+                          (int)(t0 - (int64_t)lb * kBlockBytes), (int)(t1 - (int64_t)lb * kBlockBytes), scales[st * words + slot * blocks + lb - k0], lane);
+      }
+    }
+    bulk_commit();
+    if (i > 0) {  // the stage before is empty once its stores have read it
+      bulk_wait_read<1>();
+      __syncwarp();
+      issue(task + (kMoveStages - 1) * step, (i - 1) % kMoveStages);
+    }
+  }
+  if (dead) {  // what is in flight lands before the warp ends
+    if (lane == 0) atomicOr(a.to.ticket + a.to.batch, kAnomTimeout);
+    for (int i = 0; i < kMoveStages; ++i) bar_wait(&full_bar[i], (phase >> i) & 1);
+  }
+  word_wait<0>();
+  bulk_wait_all();
+
+  // tails that are the source's own
+  for (int64_t t = blockIdx.x; t < (int64_t)count * 2 * H; t += step) {
+    const int it = (int)(t / (2 * H)), h = (int)(t % (2 * H)) >> 1, kv = (int)t & 1, b = first + it;
+    const TakeItem x = items[it];
+    if (x.from < 0 || x.len == 0 || x.older >= 0 || (a.inside && x.from == b)) continue;
+    copy_tail<DT>(tail_of<DT>(kv ? a.to.v_tail : a.to.k_tail, (int64_t)b * H + h), tail_of<DT>(kv ? a.from.v_tail : a.from.k_tail, (int64_t)x.from * H + h),
+                  lane);
+  }
+}
+
+// The lengths and tails of a cache as they are before its sequences take one another's.
+struct SnapArgs {
+  lkv_cache8 c;
+  uint4 *tails;        // K's, then V's
+  int32_t *lengths;
+  int64_t vectors;     // of one
+};
+__global__ void __launch_bounds__(256) k_cache8_snapshot(const __grid_constant__ SnapArgs a) {
+  wait_prerequisites();
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < a.c.batch) a.lengths[i] = a.c.lengths[i];
+  if (i < a.vectors) {
+    a.tails[i] = ((const uint4 *)a.c.k_tail)[i];
+    a.tails[a.vectors + i] = ((const uint4 *)a.c.v_tail)[i];
+  }
+}
+
+// ---------------------------------------------------------------- keep
+
+struct KeepArgs {
+  lkv_cache8 to, from;
+  const int32_t *blocks, *counts;
+  int32_t m;
+  int32_t inside;
+  int32_t split;      // CTAs of a (sequence, KV head) and tensor
+};
+
+// Whether a sequence's count and its lists can be kept: a CTA a (KV head,
+// sequence). What is wrong goes into the sequence's ticket, which is 0 at rest.
+__global__ void __launch_bounds__(256) k_cache8_keep_check(const __grid_constant__ KeepArgs a) {
+  wait_prerequisites();
+  const int h = blockIdx.x, b = blockIdx.y, count = a.counts[b], len = a.from.lengths[b];
+  if (count == -1) return;
+  int anomaly = 0;
+  if (count < 0 || count > a.m || len < 0 || len > a.from.capacity || count > len / kBlock) anomaly = kAnomRange;
+  else if ((int64_t)count * kBlock + len % kBlock > a.to.capacity) anomaly = kAnomCapacity;
+  else {
+    const int32_t *list = a.blocks + ((int64_t)b * a.to.n_kv_heads + h) * a.m;
+    const int full = len / kBlock;
+    for (int j = threadIdx.x; j < count; j += 256) {
+      const int x = list[j], before = j ? list[j - 1] : -1;
+      if (x <= before || x >= full) anomaly = kAnomRange;
+    }
+  }
+  if (anomaly) {
+    atomicOr(a.to.ticket + b, kKeepBad);
+    atomicOr(a.to.ticket + a.to.batch, anomaly);
+  }
+}
+
+// A CTA takes a run of a list between two caches; within one, a part (2048 /
+// split bytes) of every block of a list, in order: block j comes from one at or
+// behind j, so what a stage's stores overwrite has been loaded, and what later
+// stages load lies behind it. Lists of different heads and parts of blocks do
+// not depend on one another. The last CTA of a sequence sets its length.
+//
+// Bound by bytes: see the table of cases.
+template <int DT, int CODE>
+__global__ void __launch_bounds__(32) k_cache8_keep(const __grid_constant__ KeepArgs a) {
+  extern __shared__ __align__(128) unsigned char area[];
+  __shared__ __align__(8) uint64_t full_bar[kMoveStages];
+  __shared__ float scales[kMoveStages][kMoveStage / 256];
+  const int lane = threadIdx.x, H = a.to.n_kv_heads;
+  if (lane == 0) {
+    for (int i = 0; i < kMoveStages; ++i) bar_init(&full_bar[i], 32);
+    bar_init_fence();
+  }
+  __syncwarp();
+  wait_prerequisites();
+  const int part = (int)(blockIdx.x % a.split), kv = (int)(blockIdx.x / a.split) & 1;
+  const int64_t slice = blockIdx.x / a.split >> 1;
+  const int b = (int)(slice / H);
+  const int count = a.counts[b], len = __ldcg(a.from.lengths + b);
+  const bool bad = __ldcg(a.to.ticket + b) & kKeepBad, go = count >= 0 && !bad;
+  const int unit = a.inside ? kBlockBytes / a.split : kBlockBytes, at = a.inside ? part * unit : 0, per = kMoveStage / unit;
+  int j0 = 0, j1 = go ? count : 0;
+  if (go && !a.inside) {
+    j0 = (int)((int64_t)count * part / a.split);
+    j1 = (int)((int64_t)count * (part + 1) / a.split);
+  }
+  const int32_t *list = a.blocks + slice * a.m;
+  const char *from = (const char *)(kv ? a.from.v_codes : a.from.k_codes) + slice * a.from.capacity * kHeadDim + at;
+  char *to = (char *)(kv ? a.to.v_codes : a.to.k_codes) + slice * a.to.capacity * kHeadDim + at;
+  const float *from_scale = (kv ? a.from.v_scale : a.from.k_scale) + slice * (a.from.capacity / kBlock);
+  float *to_scale = (kv ? a.to.v_scale : a.to.k_scale) + slice * (a.to.capacity / kBlock);
+  const bool rest = len % kBlock != 0;                                   // a partial block follows
+  const int last = go && count > 0 && !rest ? list[count - 1] : -1;      // otherwise the last kept block is the last one
+  const bool older = last >= 0 && last != (len - 1) / kBlock;            // of which the source's tail is not
+
+  // two of a stage's blocks at most are a lane's; their numbers are read a stage ahead
+  int next[2];
+  auto fetch = [&](int64_t j) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) next[k] = lane + 32 * k < per && j + lane + 32 * k < j1 ? list[j + lane + 32 * k] : 0;
+  };
+  auto issue = [&](int64_t j, int st) {
+    if (j < j1) {
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (lane + 32 * k < per && j + lane + 32 * k < j1) bytes += unit;
+      bar_expect(&full_bar[st], bytes);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = lane + 32 * k;
+        if (i < per && j + i < j1) {
+          bulk_load(area + st * kMoveStage + i * unit, from + (int64_t)next[k] * kBlockBytes, unit, &full_bar[st]);
+          if (at == 0 || j + i == count - 1) word_load(&scales[st][i], from_scale + next[k]);
+        }
+      }
+      fetch(j + per);
+    }
+    word_commit();
+  };
+  fetch(j0);
+  for (int i = 0; i < kMoveStages; ++i) issue(j0 + (int64_t)i * per, i);
+  uint32_t phase = 0;
+  bool dead = false;
+  int i = 0;
+  for (int64_t j = j0; j < j1; j += per, ++i) {
+    const int st = i % kMoveStages;
+    if (!__all_sync(0xffffffffu, bar_wait(&full_bar[st], (phase >> st) & 1))) {
+      dead = true;
+      break;
+    }
+    phase ^= 1u << st;
+    word_wait<kMoveStages - 2>();  // one group a stage, the stages behind this one but for the next to be filled
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int x = lane + 32 * k;
+      if (x < per && j + x < j1) {
+        bulk_store(to + (j + x) * kBlockBytes, area + st * kMoveStage + x * unit, unit);
+        if (at == 0) to_scale[j + x] = scales[st][x];
+      }
+    }
+    if (older && count - 1 < min((int64_t)j1, j + per) && count > j)
+      to_tail<DT, CODE>(tail_of<DT>(kv ? a.to.v_tail : a.to.k_tail, slice), area + st * kMoveStage + (count - 1 - j) * unit, at, at + unit,
+                        scales[st][count - 1 - j], lane);
+    bulk_commit();
+    if (i > 0) {
+      bulk_wait_read<1>();
+      __syncwarp();
+      issue(j + (int64_t)(kMoveStages - 1) * per, (i - 1) % kMoveStages);
+    }
+  }
+  if (dead) {
+    if (lane == 0) atomicOr(a.to.ticket + a.to.batch, kAnomTimeout);
+    for (int k = 0; k < kMoveStages; ++k) bar_wait(&full_bar[k], (phase >> k) & 1);
+  }
+  word_wait<0>();
+  bulk_wait_all();
+  if (go && !a.inside && part == 0 && (rest || (last >= 0 && !older)))
+    copy_tail<DT>(tail_of<DT>(kv ? a.to.v_tail : a.to.k_tail, slice), tail_of<DT>(kv ? a.from.v_tail : a.from.k_tail, slice), lane);
+  __syncwarp();
+  // every CTA of the sequence has read its length when it arrives
+  if (lane == 0 && ((atomicAdd(a.to.ticket + b, 1) + 1) & ~kKeepBad) == 2 * H * a.split) {
+    a.to.ticket[b] = 0;
+    if (go) a.to.lengths[b] = count * kBlock + len % kBlock;
+  }
+}
+
+// What two caches of one call have to be; *inside: they are the same one.
+static const char *check_pair(const lkv_cache8 *to, const lkv_cache8 **from, bool *inside) {
+  if (const char *m = check_cache8(to)) return m;
+  if (!*from) *from = to;
+  if (const char *m = check_cache8(*from)) return m;
+  const lkv_cache8 *f = *from;
+  if (f->n_kv_heads != to->n_kv_heads || f->dtype != to->dtype || f->code != to->code)
+    return "the source has other KV heads, another dtype or another code";
+  *inside = f->k_codes == to->k_codes;
+  if (*inside) {
+    if (f->v_codes != to->v_codes || f->k_scale != to->k_scale || f->v_scale != to->v_scale || f->k_tail != to->k_tail ||
+        f->v_tail != to->v_tail || f->lengths != to->lengths || f->ticket != to->ticket || f->batch != to->batch || f->capacity != to->capacity)
+      return "the source shares some of the cache's arrays";
+    return cache8_arrays_overlap(to) ? "two of the cache's arrays overlap" : nullptr;
+  }
+  if (cache8_arrays_overlap(to)) return "two of the cache's arrays overlap";
+  if (caches_overlap(to, f)) return "the source shares some of the cache's arrays";
+  return nullptr;
+}
+
+static lkv_status refuse_in(const char *where, const char *why) {
+  char buf[192];
+  std::snprintf(buf, sizeof buf, "%s: %s", where, why);
+  return refuse(buf);
+}
+
+static int64_t snapshot_bytes(const lkv_cache8 *c) {
+  const int64_t tail = (int64_t)c->batch * c->n_kv_heads * kBlock * kHeadDim * (c->dtype == LKV_DTYPE_BF16 ? 2 : 4);
+  return 2 * tail + ((int64_t)c->batch * 4 + 15) / 16 * 16;
+}
+
+template <class Args>
+static cudaError_t launch_sized(void (*fn)(Args), dim3 grid, size_t smem, cudaStream_t st, const Args &a) {
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  return e != cudaSuccess ? e : launch_next(fn, grid, 32, smem, st, a);
+}
+
+}  // namespace lkv
+
+extern "C" lkv_status lkv_cache8_take_workspace(const lkv_cache8 *c, const lkv_cache8 *source, int64_t *bytes) {
+  using namespace lkv;
+  bool inside = false;
+  if (const char *m = check_pair(c, &source, &inside)) return refuse_in("lkv_cache8_take_workspace", m);
+  if (!bytes) return refuse("lkv_cache8_take_workspace: null result");
+  *bytes = inside ? snapshot_bytes(c) : 0;
+  return LKV_OK;
+}
+
+extern "C" lkv_status lkv_cache8_take(const lkv_cache8 *c, const lkv_cache8 *source, const int32_t *sequences,
+                                      const int32_t *lengths, void *workspace, int64_t workspace_bytes, void *stream) {
+  using namespace lkv;
+  bool inside = false;
+  if (const char *m = check_pair(c, &source, &inside)) return refuse_in("lkv_cache8_take", m);
+  if (inside && c->batch > kTakeInside) return refuse("lkv_cache8_take: at most 1024 sequences within one cache");
+  if (!aligned(sequences, 4) || !aligned(lengths, 4) || !aligned(workspace, 16))
+    return refuse("lkv_cache8_take: sequences and lengths must be 4-byte aligned, the workspace 16-byte aligned");
+  const int64_t ib = (int64_t)c->batch * 4;
+  if (overlaps_cache8(c, sequences, ib) || overlaps_cache8(c, lengths, ib))
+    return refuse("lkv_cache8_take: an input overlaps the cache's arrays");
+  const int64_t need = inside ? snapshot_bytes(c) : 0;
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return refuse("lkv_cache8_take: the workspace is smaller than lkv_cache8_take_workspace says");
+    if (overlaps_cache8(c, workspace, need) || overlap(workspace, need, sequences, ib) || overlap(workspace, need, lengths, ib))
+      return refuse("lkv_cache8_take: the workspace overlaps another tensor");
+  }
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_refuse("lkv_cache8_take", e);
+  cudaStream_t st = (cudaStream_t)stream;
+  TakeArgs a{};
+  a.to = *c;
+  a.from = *source;
+  a.sequences = sequences;
+  a.lengths = lengths;
+  a.inside = inside;
+  a.items = inside ? c->batch : c->batch < kTakeItems ? c->batch : kTakeItems;
+  if (inside) {
+    SnapArgs s{};
+    s.c = *c;
+    s.vectors = (int64_t)c->batch * c->n_kv_heads * kBlock * kHeadDim * (c->dtype == LKV_DTYPE_BF16 ? 2 : 4) / 16;
+    s.tails = (uint4 *)workspace;
+    s.lengths = (int32_t *)(s.tails + 2 * s.vectors);
+    e = launch_next(k_cache8_snapshot, dim3((unsigned)((s.vectors + 255) / 256)), 256, 0, st, s);
+    if (e != cudaSuccess) return cuda_refuse("lkv_cache8_take", e);
+    a.from.k_tail = s.tails;
+    a.from.v_tail = s.tails + s.vectors;
+    a.from.lengths = s.lengths;
+  }
+  const int groups = (c->batch + a.items - 1) / a.items;  // below 2^16: 2^20 sequences at most
+  const int wide = kMovePerSm * sms;
+  const dim3 grid((unsigned)((wide + groups - 1) / groups), (unsigned)groups);
+  const size_t smem = (size_t)take_smem(a.items);
+  const bool bf = c->dtype == LKV_DTYPE_BF16, i8 = c->code == LKV_CODE_INT8;
+  if (bf) e = i8 ? launch_sized(k_cache8_take<1, LKV_CODE_INT8>, grid, smem, st, a) : launch_sized(k_cache8_take<1, LKV_CODE_E4M3>, grid, smem, st, a);
+  else e = i8 ? launch_sized(k_cache8_take<0, LKV_CODE_INT8>, grid, smem, st, a) : launch_sized(k_cache8_take<0, LKV_CODE_E4M3>, grid, smem, st, a);
+  return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_take", e);
+}
+
+extern "C" lkv_status lkv_cache8_keep(const lkv_cache8 *c, const lkv_cache8 *source, const int32_t *blocks, int32_t m,
+                                      const int32_t *counts, void *stream) {
+  using namespace lkv;
+  bool inside = false;
+  if (const char *w = check_pair(c, &source, &inside)) return refuse_in("lkv_cache8_keep", w);
+  if (source->batch != c->batch) return refuse("lkv_cache8_keep: the source has another number of sequences");
+  if (m < 0) return refuse("lkv_cache8_keep: m must be >= 0");
+  if (!counts || (m > 0 && !blocks)) return refuse("lkv_cache8_keep: null blocks or counts");
+  if (!aligned(blocks, 4) || !aligned(counts, 4)) return refuse("lkv_cache8_keep: blocks and counts must be 4-byte aligned");
+  if (c->batch > 65535) return refuse("lkv_cache8_keep: at most 65535 sequences");
+  const int64_t slices = (int64_t)c->batch * c->n_kv_heads;
+  if (overlaps_cache8(c, blocks, slices * m * 4) || overlaps_cache8(c, counts, (int64_t)c->batch * 4))
+    return refuse("lkv_cache8_keep: an input overlaps the cache's arrays");
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_refuse("lkv_cache8_keep", e);
+  cudaStream_t st = (cudaStream_t)stream;
+  KeepArgs a{};
+  a.to = *c;
+  a.from = *source;
+  a.blocks = blocks;
+  a.counts = counts;
+  a.m = m;
+  a.inside = inside;
+  // CTAs for a GPU full of them: runs of lists, or parts of 256 bytes at least
+  const int64_t want = ((int64_t)kMovePerSm * sms + 2 * slices - 1) / (2 * slices);
+  a.split = 1;
+  if (inside)
+    while (a.split < 8 && a.split < want) a.split *= 2;
+  else
+    a.split = (int32_t)(want < (m + 7) / 8 ? want : (m + 7) / 8 < 1 ? 1 : (m + 7) / 8);
+  if (2 * slices * a.split > 0x7fffffff) return refuse("lkv_cache8_keep: too many sequences");
+  e = launch_next(k_cache8_keep_check, dim3((unsigned)c->n_kv_heads, (unsigned)c->batch), 256, 0, st, a);
+  if (e != cudaSuccess) return cuda_refuse("lkv_cache8_keep", e);
+  const dim3 grid((unsigned)(2 * slices * a.split));
+  const size_t smem = kMoveStages * kMoveStage;
+  const bool bf = c->dtype == LKV_DTYPE_BF16, i8 = c->code == LKV_CODE_INT8;
+  if (bf) e = i8 ? launch_sized(k_cache8_keep<1, LKV_CODE_INT8>, grid, smem, st, a) : launch_sized(k_cache8_keep<1, LKV_CODE_E4M3>, grid, smem, st, a);
+  else e = i8 ? launch_sized(k_cache8_keep<0, LKV_CODE_INT8>, grid, smem, st, a) : launch_sized(k_cache8_keep<0, LKV_CODE_E4M3>, grid, smem, st, a);
+  return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_keep", e);
+}

@@ -1,6 +1,8 @@
-// rope.cu -- rotary positions: lkv_rope_init and lkv_rope_apply.
+// rope.cu -- rotary positions: lkv_rope_init, lkv_rope_apply and lkv_rope_apply_axes.
 #include <cmath>
 #include <cstdio>
+#include <cstring>
+#include <type_traits>
 
 #include "../../include/lkv.h"
 #include "cache8.cuh"
@@ -35,6 +37,12 @@ struct RopeArgs {
   int32_t heads, kv_heads, n;
   int32_t per;       // heads (of q and k together) that a thread walks
   int64_t tokens;    // B * n
+};
+
+// Positions on several axes, [axes][B][n]: pair i turns by the one on axis[i].
+struct RopeAxesArgs : RopeArgs {
+  int32_t axes;
+  uint8_t axis[64];
 };
 
 // A thread's piece of a row: V values at o1 and, for NV = 2, at o2.
@@ -105,11 +113,16 @@ struct RopePiece {
   }
 };
 
-template <int DT, int INTER, int WIDE>
-__global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeArgs a) {
+template <int DT, int INTER, int WIDE, class Args>
+__global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ Args a) {
   using P = RopePiece<DT, INTER, WIDE>;
+  constexpr bool AXES = std::is_same_v<Args, RopeAxesArgs>;
   __shared__ uint64_t turn[64];
-  if (threadIdx.x < 64) turn[threadIdx.x] = a.r.turn[threadIdx.x];
+  __shared__ uint8_t axis[AXES ? 64 : 1];
+  if (threadIdx.x < 64) {
+    turn[threadIdx.x] = a.r.turn[threadIdx.x];
+    if constexpr (AXES) axis[threadIdx.x] = a.axis[threadIdx.x];
+  }
   __syncthreads();
   wait_prerequisites();
   launch_dependents();
@@ -132,10 +145,23 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ R
     p.o2 = p.o1 + (kHeadDim - rd) / 2;
   }
   if (p.rot) {
-    const int64_t pos = a.positions[tok];
+    const int32_t pos = a.positions[tok];
+    int32_t pos1 = 0, pos2 = 0, pos3 = 0;
+    if constexpr (AXES) {
+      static_assert(LKV_ROPE_AXES == 4);
+      if (a.axes > 1) pos1 = a.positions[a.tokens + tok];
+      if (a.axes > 2) pos2 = a.positions[2 * a.tokens + tok];
+      if (a.axes > 3) pos3 = a.positions[3 * a.tokens + tok];
+    }
 #pragma unroll
     for (int e = 0; e < P::PAIRS; ++e) {
-      const int32_t frac = (int32_t)(((uint64_t)pos * turn[t * P::PAIRS + e]) >> 32);
+      int64_t at = pos;
+      if constexpr (AXES) {
+        const int x = axis[t * P::PAIRS + e];
+        const int32_t low = x & 1 ? pos1 : pos, high = x & 1 ? pos3 : pos2;
+        at = x & 2 ? high : low;
+      }
+      const int32_t frac = (int32_t)(((uint64_t)at * turn[t * P::PAIRS + e]) >> 32);
       sincospif((float)frac * 0x1p-31f, &p.s[e], &p.c[e]);
       p.s[e] *= a.r.gain;
       p.c[e] *= a.r.gain;
@@ -164,8 +190,8 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ R
   if (g1 > a.heads) walk(a.k, a.k_out, a.kv_heads, max(g0, a.heads) - a.heads, g1 - a.heads);
 }
 
-template <int DT, int INTER, int WIDE>
-static cudaError_t launch_rope(RopeArgs &a, cudaStream_t st) {
+template <int DT, int INTER, int WIDE, class Args>
+static cudaError_t launch_rope(Args &a, cudaStream_t st) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
@@ -178,7 +204,7 @@ static cudaError_t launch_rope(RopeArgs &a, cudaStream_t st) {
   a.per = (int)((all + want - 1) / want);
   const int gy = (all + a.per - 1) / a.per;
   if (gy > 65535) return cudaErrorInvalidValue;
-  return launch_next(k_rope<DT, INTER, WIDE>, dim3((unsigned)blocks, (unsigned)gy), kRopeThreads, 0, st, a);
+  return launch_next(k_rope<DT, INTER, WIDE, Args>, dim3((unsigned)blocks, (unsigned)gy), kRopeThreads, 0, st, a);
 }
 
 }  // namespace lkv
@@ -226,46 +252,84 @@ extern "C" lkv_status lkv_rope_init(const lkv_rope_params *p, lkv_rope *rope) {
   return LKV_OK;
 }
 
-extern "C" lkv_status lkv_rope_apply(const lkv_rope *rope, int32_t dtype, int32_t batch, int32_t n_heads,
-                                     int32_t n_kv_heads, int32_t n, const void *q, const void *k,
-                                     const int32_t *positions, void *q_out, void *k_out, void *stream) {
-  using namespace lkv;
-  if (!rope) return refuse("lkv_rope_apply: null table");
+namespace lkv {
+
+template <class Args>
+static cudaError_t launch_rope(Args &a, int32_t dtype, cudaStream_t st) {
+  const bool bf = dtype == LKV_DTYPE_BF16, in = a.r.layout == LKV_ROPE_INTERLEAVED;
+  // whether the pairs fill whole 16-byte vectors
+  const bool wide = a.r.rotary_dim % ((bf ? 8 : 4) * (in ? 1 : 2)) == 0;
+  if (bf) return in ? (wide ? launch_rope<1, 1, 1>(a, st) : launch_rope<1, 1, 0>(a, st))
+                    : (wide ? launch_rope<1, 0, 1>(a, st) : launch_rope<1, 0, 0>(a, st));
+  return in ? (wide ? launch_rope<0, 1, 1>(a, st) : launch_rope<0, 1, 0>(a, st))
+            : (wide ? launch_rope<0, 0, 1>(a, st) : launch_rope<0, 0, 0>(a, st));
+}
+
+// Both calls: positions [axes][B][n], axis null for one axis.
+static lkv_status apply_rope(const char *where, const lkv_rope *rope, const uint8_t *axis, int32_t axes, int32_t dtype,
+                             int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t n, const void *q, const void *k,
+                             const int32_t *positions, void *q_out, void *k_out, cudaStream_t st) {
+  auto no = [&](const char *why) {
+    char buf[160];
+    std::snprintf(buf, sizeof buf, "%s: %s", where, why);
+    return refuse(buf);
+  };
+  if (!rope) return no("null table");
   if (rope->rotary_dim < 2 || rope->rotary_dim > kHeadDim || rope->rotary_dim % 2 != 0 ||
       (rope->layout != LKV_ROPE_HALF && rope->layout != LKV_ROPE_INTERLEAVED))
-    return refuse("lkv_rope_apply: the table was not filled by lkv_rope_init");
-  if (dtype != LKV_DTYPE_FP32 && dtype != LKV_DTYPE_BF16) return refuse("lkv_rope_apply: bad dtype");
-  if (batch < 0 || n < 0 || n_heads < 0 || n_kv_heads < 0) return refuse("lkv_rope_apply: negative size");
-  if (n_heads > 32768 || n_kv_heads > 32768) return refuse("lkv_rope_apply: at most 32768 heads");
+    return no("the table was not filled by lkv_rope_init");
+  if (axes < 1 || axes > LKV_ROPE_AXES) return no("axes must be 1..4");
+  if (axis)
+    for (int i = 0; i < rope->rotary_dim / 2; ++i)
+      if (axis[i] >= axes) return no("a pair's axis is not one of the axes");
+  if (dtype != LKV_DTYPE_FP32 && dtype != LKV_DTYPE_BF16) return no("bad dtype");
+  if (batch < 0 || n < 0 || n_heads < 0 || n_kv_heads < 0) return no("negative size");
+  if (n_heads > 32768 || n_kv_heads > 32768) return no("at most 32768 heads");
   const int64_t tokens = (int64_t)batch * n;
   if (tokens == 0 || n_heads + n_kv_heads == 0) return LKV_OK;
   if (!positions || (n_heads && (!q || !q_out)) || (n_kv_heads && (!k || !k_out)))
-    return refuse("lkv_rope_apply: null tensor");
+    return no("null tensor");
   if (!aligned(positions, 4) || (n_heads && (!aligned(q, 16) || !aligned(q_out, 16))) ||
       (n_kv_heads && (!aligned(k, 16) || !aligned(k_out, 16))))
-    return refuse("lkv_rope_apply: tensors must be 16-byte aligned, positions 4-byte aligned");
-  if (tokens > (int64_t(1) << 31)) return refuse("lkv_rope_apply: more than 2^31 tokens");
+    return no("tensors must be 16-byte aligned, positions 4-byte aligned");
+  if (tokens > (int64_t(1) << 31)) return no("more than 2^31 tokens");
   const int64_t es = dtype == LKV_DTYPE_BF16 ? 2 : 4;
   const int64_t qb = tokens * n_heads * kHeadDim * es, kb = tokens * n_kv_heads * kHeadDim * es;
-  const int64_t pb = tokens * 4;
+  const int64_t pb = tokens * axes * 4;
   if ((q_out != q && overlap(q_out, qb, q, qb)) || (k_out != k && overlap(k_out, kb, k, kb)) ||
       overlap(q_out, qb, k, kb) || overlap(k_out, kb, q, qb) || overlap(q_out, qb, k_out, kb) ||
       overlap(q_out, qb, positions, pb) || overlap(k_out, kb, positions, pb))
-    return refuse("lkv_rope_apply: an output overlaps another tensor (in place: the same pointer)");
-  RopeArgs a{};
+    return no("an output overlaps another tensor (in place: the same pointer)");
+  RopeAxesArgs a{};
   a.r = *rope;
   a.q = q; a.k = k; a.q_out = q_out; a.k_out = k_out;
   a.positions = positions;
   a.heads = n_heads; a.kv_heads = n_kv_heads; a.n = n;
   a.tokens = tokens;
-  cudaStream_t st = (cudaStream_t)stream;
-  const bool bf = dtype == LKV_DTYPE_BF16, in = rope->layout == LKV_ROPE_INTERLEAVED;
-  // whether the pairs fill whole 16-byte vectors
-  const bool wide = rope->rotary_dim % ((bf ? 8 : 4) * (in ? 1 : 2)) == 0;
   cudaError_t e;
-  if (bf) e = in ? (wide ? launch_rope<1, 1, 1>(a, st) : launch_rope<1, 1, 0>(a, st))
-                 : (wide ? launch_rope<1, 0, 1>(a, st) : launch_rope<1, 0, 0>(a, st));
-  else e = in ? (wide ? launch_rope<0, 1, 1>(a, st) : launch_rope<0, 1, 0>(a, st))
-              : (wide ? launch_rope<0, 0, 1>(a, st) : launch_rope<0, 0, 0>(a, st));
-  return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_rope_apply", e);
+  if (axis) {
+    a.axes = axes;
+    std::memcpy(a.axis, axis, rope->rotary_dim / 2);
+    e = launch_rope(a, dtype, st);
+  } else {
+    e = launch_rope(static_cast<RopeArgs &>(a), dtype, st);
+  }
+  return e == cudaSuccess ? LKV_OK : cuda_refuse(where, e);
+}
+
+}  // namespace lkv
+
+extern "C" lkv_status lkv_rope_apply(const lkv_rope *rope, int32_t dtype, int32_t batch, int32_t n_heads,
+                                     int32_t n_kv_heads, int32_t n, const void *q, const void *k,
+                                     const int32_t *positions, void *q_out, void *k_out, void *stream) {
+  return lkv::apply_rope("lkv_rope_apply", rope, nullptr, 1, dtype, batch, n_heads, n_kv_heads, n, q, k, positions, q_out,
+                         k_out, (cudaStream_t)stream);
+}
+
+extern "C" lkv_status lkv_rope_apply_axes(const lkv_rope *rope, const uint8_t *axis, int32_t axes, int32_t dtype,
+                                          int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t n, const void *q,
+                                          const void *k, const int32_t *positions, void *q_out, void *k_out, void *stream) {
+  if (!axis) return lkv::refuse("lkv_rope_apply_axes: null axes of the pairs");
+  return lkv::apply_rope("lkv_rope_apply_axes", rope, axis, axes, dtype, batch, n_heads, n_kv_heads, n, q, k, positions,
+                         q_out, k_out, (cudaStream_t)stream);
 }

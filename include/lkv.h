@@ -527,6 +527,17 @@ lkv_status lkv_rope_apply(const lkv_rope *rope, int32_t dtype, int32_t batch, in
                           int32_t n_kv_heads, int32_t n, const void *q, const void *k,
                           const int32_t *positions, void *q_out, void *k_out, void *stream);
 
+/* The same with positions on several axes (time, height and width of images
+ * and video): positions device int32 [axes][B][n], axes 1..LKV_ROPE_AXES, and
+ * pair i turns by its token's position on axis[i] times f_i. axis: host memory,
+ * rotary_dim / 2 entries below axes, read before the call returns. Frequencies
+ * that begin anew on each axis are the table's to hold (lkv_rope above). */
+#define LKV_ROPE_AXES 4
+lkv_status lkv_rope_apply_axes(const lkv_rope *rope, const uint8_t *axis, int32_t axes, int32_t dtype,
+                               int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t n, const void *q,
+                               const void *k, const int32_t *positions, void *q_out, void *k_out,
+                               void *stream);
+
 /* A key/value cache held in 8 bits: the caller's device arrays. Blocks of
  * LKV_CACHE8_BLOCK tokens of one (sequence, KV head) share a scale; token i
  * is row i. A block is quantised when its last token is written:
@@ -540,10 +551,11 @@ lkv_status lkv_rope_apply(const lkv_rope *rope, int32_t dtype, int32_t batch, in
  * full precision, so what the cache holds does not depend on how its tokens
  * were split over calls. Values have to be finite: a NaN is held as 0 and an
  * infinity as the largest finite value of dtype, and lkv_cache8_status then
- * reports LKV_EINVAL. Calls that write a cache (lkv_cache8_write) may not
- * overlap on the GPU with any other call on it; calls that only read it
- * (lkv_cache8_read, lkv_cache8_attend) may overlap with one another. No two of
- * the arrays may share memory (lkv_cache8_write refuses it). */
+ * reports LKV_EINVAL. Calls that write a cache (lkv_cache8_write, _take and
+ * _keep) may not overlap on the GPU with any other call on it; calls that only
+ * read it (lkv_cache8_read, _attend, _attend_shared; _take and _keep their
+ * source) may overlap with one another. No two of the arrays may share memory
+ * (calls that write refuse it). */
 #define LKV_CACHE8_BLOCK 16
 enum { LKV_CODE_INT8 = 0, LKV_CODE_E4M3 = 1 };
 typedef struct lkv_cache8 {
@@ -589,6 +601,46 @@ lkv_status lkv_cache8_write(const lkv_cache8 *cache, const void *k, const void *
 lkv_status lkv_cache8_read(const lkv_cache8 *cache, const int32_t *first, int32_t n, void *k_out,
                            void *v_out, void *stream);
 
+/* Sequence b of the cache becomes the first lengths[b] tokens of sequence
+ * sequences[b] of source: samples of one prompt, beams put in order, sequences
+ * moved together, cut back (drafts, at any position) and freed (length 0).
+ * sequences, lengths: device int32 [batch of cache], not part of cache's
+ * arrays; sequences NULL: b itself; -1 leaves sequence b as it is; lengths
+ * NULL: all of its tokens. Codes and scales are taken as they are; a sequence
+ * that ends in an older block than its source gets the rows of its last block,
+ * which the tail holds, as lkv_cache8_read gives them. source NULL or the same
+ * cache: every sequence takes what the others held before the call (at most
+ * 1024 sequences, and workspace: device memory of lkv_cache8_take_workspace
+ * bytes, not shared by calls that may overlap). Otherwise no array of the two
+ * may share memory, n_kv_heads, dtype and code are the same, and batch and
+ * capacity may differ. A sequence that asks for what is not there (a sequence
+ * or length out of range, more than the capacity) is left as it is, and
+ * lkv_cache8_status of cache reports LKV_EINVAL or LKV_ECAPACITY. The call
+ * writes cache and reads source (lkv_cache8 above). Asynchronous on stream.
+ * Errors: LKV_EINVAL, LKV_ECUDA. */
+lkv_status lkv_cache8_take(const lkv_cache8 *cache, const lkv_cache8 *source, const int32_t *sequences,
+                           const int32_t *lengths, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that lkv_cache8_take needs (0 between two caches), into
+ * *bytes. Errors: LKV_EINVAL. */
+lkv_status lkv_cache8_take_workspace(const lkv_cache8 *cache, const lkv_cache8 *source, int64_t *bytes);
+
+/* Whole blocks chosen for each KV head move together: block j < counts[b] of
+ * (sequence b, KV head h) becomes block blocks[b][h][j] of the same sequence
+ * and head of source, the last, partial block follows, and the length becomes
+ * 16 * counts[b] + length % 16. blocks: device int32 [B][H_kv][m], each list
+ * strictly ascending and below length / 16 in its first counts[b] entries;
+ * counts: device int32 [B], 0..m, or -1 to leave a sequence as it is. Neither
+ * is part of cache's arrays. source NULL or the same cache: in place;
+ * otherwise as for lkv_cache8_take, with the same batch (at most 65535). Where
+ * no partial block follows, the tail is what lkv_cache8_read gives for the last
+ * kept block. A sequence with a bad count or list is left as it is, and
+ * lkv_cache8_status of cache reports LKV_EINVAL or LKV_ECAPACITY. Rows keep
+ * what was rotated into them: positions do not change by moving. Asynchronous
+ * on stream. Errors: LKV_EINVAL, LKV_ECUDA. */
+lkv_status lkv_cache8_keep(const lkv_cache8 *cache, const lkv_cache8 *source, const int32_t *blocks,
+                           int32_t m, const int32_t *counts, void *stream);
+
 /* Causal attention of the last tokens of every sequence over the cache, which
  * holds them already: q [B][H][n][d], H = H_kv * group (group 1..128), and
  * out [B][H][n][d], both in the cache's dtype. Row i < counts[b] (counts:
@@ -628,9 +680,9 @@ lkv_status lkv_cache8_attend_workspace(const lkv_cache8 *cache, int32_t group, i
                                        int64_t *bytes);
 
 /* Blocking: waits for stream, then reports and clears what calls on this
- * cache recorded: LKV_ETIMEOUT (an attention whose copies did not arrive: its
- * output is not complete), else LKV_ECAPACITY, else LKV_EINVAL (writes), else
- * LKV_OK. May not be captured. Errors: also LKV_ECUDA. */
+ * cache recorded: LKV_ETIMEOUT (an attention, take or keep whose copies did not
+ * arrive: what it made is not complete), else LKV_ECAPACITY, else LKV_EINVAL
+ * (writes, takes, keeps), else LKV_OK. May not be captured. Errors: also LKV_ECUDA. */
 lkv_status lkv_cache8_status(const lkv_cache8 *cache, void *stream);
 
 /* Wait for the context's stream; report device-side anomalies. */
