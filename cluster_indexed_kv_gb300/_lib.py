@@ -25,7 +25,8 @@ EXPORTED = ("lkv_create", "lkv_destroy", "lkv_build_index", "lkv_load_index",
             "lkv_build_index_async", "lkv_build_paris", "lkv_paris_levels",
             "lkv_rope_init", "lkv_rope_apply", "lkv_rope_apply_axes", "lkv_cache8_write", "lkv_cache8_read",
             "lkv_cache8_attend", "lkv_cache8_attend_workspace", "lkv_cache8_take",
-            "lkv_cache8_take_workspace", "lkv_cache8_keep", "lkv_cache8_status")
+            "lkv_cache8_take_workspace", "lkv_cache8_keep", "lkv_cache8_attend_shared",
+            "lkv_cache8_attend_shared_workspace", "lkv_cache8_status")
 LKV_FILTER_TENSOR, LKV_FILTER_SIMT = 0, 1
 LKV_TRIGGER_ADAPTIVE, LKV_TRIGGER_EVERY, LKV_TRIGGER_INTERVAL = 0, 1, 2
 LKV_FILL_PREFIX, LKV_FILL_SKIP = 0, 1
@@ -173,6 +174,10 @@ def load(path: str = LIB_PATH):
         L.lkv_cache8_take_workspace.restype = st
         L.lkv_cache8_keep.argtypes = [vp, vp, vp, i32, vp, vp]
         L.lkv_cache8_keep.restype = st
+        L.lkv_cache8_attend_shared.argtypes = [vp, vp, vp, vp, i32, i32, vp, f32, i32, vp, vp, i64, vp]
+        L.lkv_cache8_attend_shared.restype = st
+        L.lkv_cache8_attend_shared_workspace.argtypes = [vp, vp, i32, i32, i32, C.POINTER(i64)]
+        L.lkv_cache8_attend_shared_workspace.restype = st
         L.lkv_cache8_status.argtypes = [vp, vp]
         L.lkv_cache8_status.restype = st
         L.lkv_sync.argtypes = [vp]
@@ -312,6 +317,12 @@ def lkv_cache8_attend_workspace(cache, group, n, window, sinks, max_len) -> int:
     n_bytes = C.c_int64(0)
     _check(load().lkv_cache8_attend_workspace(cache, group, n, window, sinks, max_len,
                                               C.byref(n_bytes)), None)
+    return n_bytes.value
+
+
+def lkv_cache8_attend_shared_workspace(cache, prefix, group, n, max_len) -> int:
+    n_bytes = C.c_int64(0)
+    _check(load().lkv_cache8_attend_shared_workspace(cache, prefix, group, n, max_len, C.byref(n_bytes)), None)
     return n_bytes.value
 
 

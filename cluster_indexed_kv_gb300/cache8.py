@@ -230,6 +230,7 @@ class Cache8:
         lib = _lib.load()
         self._write, self._read = lib.lkv_cache8_write, lib.lkv_cache8_read
         self._attend, self._status = lib.lkv_cache8_attend, lib.lkv_cache8_status
+        self._attend_shared = lib.lkv_cache8_attend_shared
         self._take, self._keep = lib.lkv_cache8_take, lib.lkv_cache8_keep
 
     def write(self, k: torch.Tensor, v: torch.Tensor, *, start: torch.Tensor | None = None,
@@ -316,30 +317,11 @@ class Cache8:
         1 / sqrt(128). window > 0: a token sees the `window` last ones up to
         itself and the `sinks` first ones. max_len: a bound of the lengths
         known to the caller (0: none); it only steers the split of the work."""
-        if not isinstance(q, torch.Tensor) or q.dim() != 4:
-            raise ValueError(f"q must be a tensor of shape [B, H, n, {_D}]")
-        dev, dt = self._index, self.dtype
-        _, heads, n, _ = q.shape
-        group = heads // self.n_kv_heads
-        if group * self.n_kv_heads != heads or heads == 0:
-            raise ValueError(f"q's {heads} heads are not a multiple of the cache's {self.n_kv_heads}")
-        shape = (self.batch, heads, n, _D)
-        qp = _tensor(q, "q", shape, dt, dev)
-        cp = None if counts is None else _tensor(counts, "counts", (self.batch,), torch.int32, dev)
-        if out is None:
-            out = _empty(shape, dt, dev)
-            op = out.data_ptr()
-        else:
-            op = _tensor(out, "out", shape, dt, dev)
+        dev = self._index
+        group, n, qp, cp, out, op = self._queries(q, counts, out)
         if not (0 <= window <= _INT32 and 0 <= sinks <= _INT32 and 0 <= max_len <= _INT32):
             _range(window=window, sinks=sinks, max_len=max_len)
-        if max_len:
-            # the bound in steps of a 64th to a 128th of itself: a server's bound
-            # that grows with every token does not ask for the workspace each time
-            step = (1 << max(4, max_len.bit_length() - 7)) - 1
-            max_len = (max_len + step) & ~step
-            if max_len >= self.capacity:
-                max_len = 0
+        max_len = self._bound(max_len)
         sizes = (group, n, window, sinks, max_len)
         ws_bytes = self._ws_bytes.get(sizes)
         if ws_bytes is None:
@@ -353,6 +335,64 @@ class Cache8:
         _call(dev, self._attend, self._at, qp, group, n, cp, _SCALE if scale is None else scale, window,
               sinks, max_len, op, ws.data_ptr() if ws_bytes else None, ws_bytes)
         return out
+
+    def attend_shared(self, q: torch.Tensor, prefix: Cache8, prefix_of: torch.Tensor | None = None, *,
+                      counts: torch.Tensor | None = None, scale: float | None = None, max_len: int = 0,
+                      out: torch.Tensor | None = None) -> torch.Tensor:
+        """Causal attention of sequences behind shared prefixes: sequence b's
+        tokens are those of sequence prefix_of[b] of the cache ``prefix`` (int32
+        [B]; default 0 for all; -1: none), then its own here. q, counts, scale
+        and out are attend's; q's rows are the sequence's last tokens. Each
+        prefix is read once for all sequences behind it. max_len bounds this
+        cache's lengths."""
+        dev = self._index
+        if not isinstance(prefix, Cache8):
+            raise TypeError("prefix must be a Cache8")
+        if prefix._index != dev:
+            raise ValueError(f"prefix must be on cuda:{dev}, got cuda:{prefix._index}")
+        group, n, qp, cp, out, op = self._queries(q, counts, out)
+        pp = None if prefix_of is None else _tensor(prefix_of, "prefix_of", (self.batch,), torch.int32, dev)
+        if not 0 <= max_len <= _INT32:
+            raise ValueError("max_len must be in 0..2^31 - 1")
+        max_len = self._bound(max_len)
+        sizes = (prefix.batch, group, n, max_len)
+        ws_bytes = self._ws_bytes.get(sizes)
+        if ws_bytes is None:
+            with torch.cuda.device(dev):
+                ws_bytes = _lib.lkv_cache8_attend_shared_workspace(self._at, prefix._at, group, n, max_len)
+            if len(self._ws_bytes) > 1000:
+                self._ws_bytes.clear()
+            self._ws_bytes[sizes] = ws_bytes
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device) if ws_bytes else None
+        _call(dev, self._attend_shared, self._at, prefix._at, pp, qp, group, n, cp, _SCALE if scale is None else scale,
+              max_len, op, ws.data_ptr() if ws_bytes else None, ws_bytes)
+        return out
+
+    def _queries(self, q, counts, out):
+        """Of an attention: group, n, addresses of q and counts, and the output with its address."""
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError(f"q must be a tensor of shape [B, H, n, {_D}]")
+        dev, dt = self._index, self.dtype
+        _, heads, n, _ = q.shape
+        group = heads // self.n_kv_heads
+        if group * self.n_kv_heads != heads or heads == 0:
+            raise ValueError(f"q's {heads} heads are not a multiple of the cache's {self.n_kv_heads}")
+        shape = (self.batch, heads, n, _D)
+        qp = _tensor(q, "q", shape, dt, dev)
+        cp = None if counts is None else _tensor(counts, "counts", (self.batch,), torch.int32, dev)
+        if out is None:
+            out = _empty(shape, dt, dev)
+            return group, n, qp, cp, out, out.data_ptr()
+        return group, n, qp, cp, out, _tensor(out, "out", shape, dt, dev)
+
+    def _bound(self, max_len: int) -> int:
+        """max_len in steps of a 64th to a 128th of itself (a server's bound that
+        grows with every token does not ask for the workspace each time), 0 from
+        the capacity on."""
+        if max_len:
+            step = (1 << max(4, max_len.bit_length() - 7)) - 1
+            max_len = (max_len + step) & ~step
+        return 0 if max_len >= self.capacity else max_len
 
     def check(self) -> None:
         """Wait for the current stream; raise LKVError if, since the last

@@ -1,0 +1,169 @@
+// attend8_shared.cuh -- attention behind shared prefixes: what its kernels share.
+//
+// The rows of all sequences behind one prefix are one list, sequence by
+// sequence (in the order of the batch), each token-major as elsewhere; runs of
+// part_rows of them are the prefix's row tiles. All tiles' work, prefix by
+// prefix, row tile by row tile and KV head by KV head, is one row of units (runs
+// of part_blocks blocks of a tile), of which each CTA takes an even share. What
+// it makes of a tile is a part: slot (CTA + tile) of the workspace, as each step
+// along the row goes to the next CTA, the next tile, or both.
+#pragma once
+
+#include "attend8.cuh"
+
+namespace lkv {
+
+constexpr int kSharedMost = 1024;  // sequences, and prefixes, that a call takes
+
+struct SharedArgs : AttendArgs {
+  lkv_cache8 p;               // the prefixes
+  const int32_t *prefix_of;   // null: all of prefix 0
+  int32_t part_rows, part_blocks;
+  int2 *seq;                  // [batch]: the first tile of the sequence's prefix (-1: none), its place behind that prefix
+  int2 *tile;                 // [tiles]: a tile's first CTA, and how many it has
+  float *parts;
+};
+
+// A part: o as [d / 4][row][4], then the exponents of the units of o and l, and l.
+__host__ __device__ constexpr int part_floats(int rows) { return rows * (kHeadDim + 3); }
+
+__device__ __forceinline__ int held(const lkv_cache8 &c, int b) { return min(max(__ldcg(c.lengths + b), 0), c.capacity); }
+
+// The prefixes' work, in shared memory.
+struct Prefixes {
+  int64_t *at;   // [G + 1]: units before each prefix's tiles
+  int *tiles;    // [G + 1]: tiles before
+  int *first;    // [G + 1]: sequences before, in `order`
+  int *nu;       // [G]: units of one of its tiles
+  int *order;    // [batch]: sequences, prefix by prefix
+
+  static __host__ __device__ int64_t bytes(int batch, int G) { return 20 * (int64_t)(G + 1) + 4 * (int64_t)batch; }
+  __device__ Prefixes(void *area, int G) {
+    at = (int64_t *)area;
+    tiles = (int *)(at + G + 1);
+    first = tiles + G + 1;
+    nu = first + G + 1;
+    order = nu + G + 1;
+  }
+  // the prefix of sequence b, -1 for none (or an empty one)
+  static __device__ __forceinline__ int of(const SharedArgs &a, int b) {
+    const int g = a.prefix_of ? __ldcg(a.prefix_of + b) : 0;
+    return g >= 0 && g < a.p.batch && held(a.p, g) > 0 ? g : -1;
+  }
+  __device__ void fill(const SharedArgs &a) {
+    const int G = a.p.batch, B = a.c.batch;
+    for (int g = threadIdx.x; g < G; g += blockDim.x) nu[g] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      const uint32_t below = (1u << lane) - 1u;
+      for (int turn = 0; turn < 2; ++turn) {  // how many sequences a prefix has, then their places
+        for (int b0 = 0; b0 < B; b0 += 32) {
+          const int b = b0 + lane, g = b < B ? of(a, b) : -1;
+          const uint32_t same = __match_any_sync(0xffffffffu, g >= 0 ? g : -2 - lane);
+          const int before = g >= 0 ? nu[g] : 0;
+          if (turn && g >= 0) order[before + __popc(same & below)] = b;
+          __syncwarp();
+          if (g >= 0 && (same & below) == 0) nu[g] = before + __popc(same);
+          __syncwarp();
+        }
+        if (turn) break;
+        int64_t units = 0;
+        int nt = 0, seqs = 0;
+        for (int g0 = 0; g0 < G; g0 += 32) {
+          const int g = g0 + lane;
+          const int have = g < G ? nu[g] : 0, len = have ? held(a.p, g) : 0;
+          const int rt = (int)(((int64_t)have * a.n * a.group + a.part_rows - 1) / a.part_rows);
+          const int run = a.part_blocks * kBlock, per = (len + run - 1) / run;
+          int64_t u = (int64_t)rt * a.c.n_kv_heads * per;
+          int t = rt * a.c.n_kv_heads, s = have;
+#pragma unroll
+          for (int d = 1; d < 32; d *= 2) {
+            const int64_t u2 = __shfl_up_sync(0xffffffffu, u, d);
+            const int t2 = __shfl_up_sync(0xffffffffu, t, d), s2 = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) {
+              u += u2;
+              t += t2;
+              s += s2;
+            }
+          }
+          if (g < G) {
+            at[g + 1] = units + u;
+            tiles[g + 1] = nt + t;
+            first[g + 1] = seqs + s;
+            nu[g] = seqs + s - have;  // where its sequences begin
+          }
+          units += __shfl_sync(0xffffffffu, u, 31);
+          nt += __shfl_sync(0xffffffffu, t, 31);
+          seqs += __shfl_sync(0xffffffffu, s, 31);
+        }
+        if (lane == 0) at[0] = tiles[0] = first[0] = 0;
+        __syncwarp();
+      }
+    }
+    __syncthreads();
+    for (int g = threadIdx.x; g < G; g += blockDim.x) {
+      const int t = tiles[g + 1] - tiles[g];
+      nu[g] = t ? (int)((at[g + 1] - at[g]) / t) : 0;
+    }
+    if (blockIdx.x == 0) {
+      for (int b = threadIdx.x; b < B; b += blockDim.x)
+        if (of(a, b) < 0) a.seq[b] = make_int2(-1, 0);
+      for (int i = threadIdx.x; i < first[G]; i += blockDim.x) {
+        const int b = order[i], g = of(a, b);
+        a.seq[b] = make_int2(tiles[g], i - first[g]);
+      }
+    }
+    __syncthreads();
+  }
+  // this CTA's units
+  __device__ __forceinline__ void share(int G, int64_t &x0, int64_t &x1) const {
+    const int64_t total = at[G], P = min((int64_t)gridDim.x, total);
+    x0 = blockIdx.x < P ? total * blockIdx.x / P : 0;
+    x1 = blockIdx.x < P ? total * (blockIdx.x + 1) / P : 0;
+  }
+  // a piece of unit x's tile: up to unit x1 of the row
+  struct Piece { int g, h, rt, tile, u0, u1; };
+  __device__ __forceinline__ Piece piece(const SharedArgs &a, int64_t x, int64_t x1) const {
+    int lo = 0, hi = a.p.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (at[mid] <= x) lo = mid;
+      else hi = mid;
+    }
+    const int64_t off = x - at[lo];
+    const int idx = (int)(off / nu[lo]);
+    Piece p;
+    p.g = lo;
+    p.h = idx % a.c.n_kv_heads;
+    p.rt = idx / a.c.n_kv_heads;
+    p.tile = tiles[lo] + idx;
+    p.u0 = (int)(off % nu[lo]);
+    p.u1 = (int)min((int64_t)nu[lo], p.u0 + (x1 - x));
+    return p;
+  }
+  // the tile that begins at unit x of the row, for whoever joins its parts (one thread of the CTA that has the unit)
+  __device__ __forceinline__ void announce(const SharedArgs &a, const Piece &p, int64_t x) const {
+    const int64_t total = at[a.p.batch], P = min((int64_t)gridDim.x, total), last = x + nu[p.g] - 1;
+    // the last CTA that begins at or before unit `last`
+    a.tile[p.tile] = make_int2((int)blockIdx.x, (int)((P * (last + 1) - 1) / total) - (int)blockIdx.x + 1);
+  }
+};
+
+// Row r of prefix g's list: where its query is (in rows of q, of KV head h) and
+// the last token of the prefix that it sees, len - 1 for all; at < 0: no row, or padding.
+struct PrefixRow { int64_t at; int pos; };
+__device__ __forceinline__ PrefixRow prefix_row(const SharedArgs &a, const Prefixes &p, int g, int h, int len, int64_t r) {
+  PrefixRow x{-1, -1};
+  const int per = a.n * a.group;
+  const int64_t m = r / per;
+  if (m >= p.first[g + 1] - p.first[g]) return x;
+  const int b = p.order[p.first[g] + (int)m], rest = (int)(r - m * per), i = rest / a.group;
+  const int mine = held(a.c, b), cnt = a.counts ? min(max(__ldcg(a.counts + b), 0), a.n) : a.n;
+  if (i >= cnt) return x;
+  x.pos = max(len + min(mine - cnt + i, -1), -1);
+  x.at = (((int64_t)b * a.c.n_kv_heads + h) * a.group + rest % a.group) * a.n + i;
+  return x;
+}
+
+}  // namespace lkv

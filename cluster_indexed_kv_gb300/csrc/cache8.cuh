@@ -26,6 +26,12 @@ inline lkv_status refuse(const char *msg) {
   return LKV_EINVAL;
 }
 
+inline lkv_status refuse_in(const char *where, const char *why) {
+  char buf[192];
+  std::snprintf(buf, sizeof buf, "%s: %s", where, why);
+  return refuse(buf);
+}
+
 inline lkv_status cuda_refuse(const char *where, cudaError_t e) {
   char buf[256];
   std::snprintf(buf, sizeof buf, "%s: %s", where, cudaGetErrorString(e));

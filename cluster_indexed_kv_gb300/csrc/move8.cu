@@ -457,12 +457,6 @@ static const char *check_pair(const lkv_cache8 *to, const lkv_cache8 **from, boo
   return nullptr;
 }
 
-static lkv_status refuse_in(const char *where, const char *why) {
-  char buf[192];
-  std::snprintf(buf, sizeof buf, "%s: %s", where, why);
-  return refuse(buf);
-}
-
 static int64_t snapshot_bytes(const lkv_cache8 *c) {
   const int64_t tail = (int64_t)c->batch * c->n_kv_heads * kBlock * kHeadDim * (c->dtype == LKV_DTYPE_BF16 ? 2 : 4);
   return 2 * tail + ((int64_t)c->batch * 4 + 15) / 16 * 16;

@@ -679,6 +679,33 @@ lkv_status lkv_cache8_attend_workspace(const lkv_cache8 *cache, int32_t group, i
                                        int32_t window, int32_t sinks, int32_t max_len,
                                        int64_t *bytes);
 
+/* Causal attention of the last tokens of sequences that share prefixes: the
+ * tokens of sequence b are those of sequence prefix_of[b] of the cache `prefix`
+ * (whole prompts, examples, documents), then its own in `cache`. The prefixes
+ * are read once for all sequences behind them. q, out, group, n, counts and
+ * scale are those of lkv_cache8_attend: row i < counts[b] is the token at
+ * position P + lengths[b] - counts[b] + i, P the prefix's length, and sees the
+ * tokens at or before it, of both; its own key and value are in the cache
+ * already. prefix_of: device int32 [B], NULL: prefix 0 for all; a value that
+ * names no sequence of `prefix` (-1) stands for no prefix. n_kv_heads, dtype
+ * and code of the caches are the same, batch and capacity need not be, and
+ * prefix may be cache itself; at most 1024 sequences in each. Precision as for
+ * lkv_cache8_attend. max_len: an upper bound of cache's lengths (0: its
+ * capacity), for the split of the work alone. workspace: device memory of at
+ * least lkv_cache8_attend_shared_workspace bytes for the same sizes, not shared
+ * by calls that may overlap. out may not overlap q or the caches. A wait that
+ * gave up is reported by lkv_cache8_status of cache. Asynchronous on stream.
+ * Errors: LKV_EINVAL (also when scale * log2(e) is not finite), LKV_ECUDA. */
+lkv_status lkv_cache8_attend_shared(const lkv_cache8 *cache, const lkv_cache8 *prefix,
+                                    const int32_t *prefix_of, const void *q, int32_t group, int32_t n,
+                                    const int32_t *counts, float scale, int32_t max_len, void *out,
+                                    void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that lkv_cache8_attend_shared needs for these sizes, into
+ * *bytes. Errors: LKV_EINVAL. */
+lkv_status lkv_cache8_attend_shared_workspace(const lkv_cache8 *cache, const lkv_cache8 *prefix,
+                                              int32_t group, int32_t n, int32_t max_len, int64_t *bytes);
+
 /* Blocking: waits for stream, then reports and clears what calls on this
  * cache recorded: LKV_ETIMEOUT (an attention, take or keep whose copies did not
  * arrive: what it made is not complete), else LKV_ECAPACITY, else LKV_EINVAL

@@ -1,5 +1,5 @@
-"""Host side of taking and keeping tokens of the 8-bit cache, and of rotary
-positions on several axes (no GPU): refusals before anything is launched."""
+"""Host side of taking and keeping tokens of the 8-bit cache, of attention behind
+shared prefixes and of rotary positions on several axes (no GPU): refusals before anything is launched."""
 import ctypes as C
 
 import pytest
@@ -73,6 +73,41 @@ def test_take_and_keep_refuse():
         assert take(source=C.addressof(y)) == E and keep(source=C.addressof(y)) == E
     y = _view(v_codes=A)
     assert take(to=C.addressof(y), source=None) == E and keep(to=C.addressof(y), source=None) == E
+
+
+@pytest.mark.parametrize("bad", BAD_VIEWS)
+def test_shared_attention_bad_views(bad):
+    L, out = _lib.load(), C.c_int64()
+    good, wrong = other(), _view(**bad)
+    g, w = C.addressof(good), C.addressof(wrong)
+    for c, p in ((w, g), (g, w), (w, w), (None, g), (g, None)):
+        assert L.lkv_cache8_attend_shared(c, p, 20 * A, 21 * A, 4, 1, None, 1.0, 0, 22 * A, 23 * A, 1 << 20, None) == E
+        assert L.lkv_cache8_attend_shared_workspace(c, p, 4, 1, 0, C.byref(out)) == E
+
+
+def test_shared_attention_refuses():
+    L, out = _lib.load(), C.c_int64()
+    c, p = _view(), other()
+    v, f = C.addressof(c), C.addressof(p)
+
+    def call(c=v, p=f, of=20 * A, q=21 * A, group=4, n=1, counts=None, scale=1.0, max_len=0, o=22 * A, ws=23 * A, bytes=1 << 20):
+        return L.lkv_cache8_attend_shared(c, p, of, q, group, n, counts, scale, max_len, o, ws, bytes, None)
+
+    assert L.lkv_cache8_attend_shared_workspace(v, f, 4, 1, 0, None) == E
+    for kw in (dict(group=0), dict(group=129), dict(n=-1), dict(n=(1 << 24) + 1), dict(max_len=-1), dict(scale=float("nan")), dict(scale=float("inf")),
+               dict(scale=3e38), dict(q=None), dict(o=None), dict(q=21 * A + 8), dict(o=22 * A + 8), dict(ws=23 * A + 8), dict(counts=24 * A + 2),
+               dict(of=20 * A + 1), dict(o=21 * A + 256), dict(o=20 * A), dict(counts=22 * A, o=22 * A)):
+        assert call(**kw) == E, kw
+    for x in (c, p):  # the output in a cache
+        for name in ARRAYS:
+            assert call(o=getattr(x, name)) == E, name
+    for kw in (dict(n_kv_heads=3), dict(dtype=0), dict(code=1), dict(batch=1025)):
+        x = other(**kw)
+        assert call(p=C.addressof(x)) == E and L.lkv_cache8_attend_shared_workspace(v, C.addressof(x), 4, 1, 0, C.byref(out)) == E
+    big = _view(batch=1025)
+    assert call(c=C.addressof(big)) == E
+    assert call(n=0) == _lib.LKV_OK
+    assert L.lkv_cache8_attend_shared_workspace(v, f, 4, 0, 0, C.byref(out)) == _lib.LKV_OK and out.value == 0
 
 
 def test_rope_axes_refuse():
