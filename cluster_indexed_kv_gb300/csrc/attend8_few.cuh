@@ -422,7 +422,7 @@ __device__ __forceinline__ const lkv_cache8 &keys_of(const ArgsOf<MODE> &a) {
 // 2^t) with its prefix's parts: values d and d + 1. row: of the sequence's rows.
 __device__ __forceinline__ void join_prefix(const SharedArgs &a, int64_t slice, int row, int d, float2 &o, float &l, float &m, float &t) {
   const int b = (int)(slice / a.c.n_kv_heads), h = (int)(slice % a.c.n_kv_heads);
-  const int2 sq = a.seq[b];
+  const int4 sq = a.seq[b];
   const int per = a.n * a.group;
   if (sq.x < 0 || row >= per) return;
   const int64_t pr = (int64_t)sq.y * per + row;
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
   // the prefixes' tables lie behind what the rings and merges use
   constexpr int kUsed = (int)sizeof(Sm) > kRingBytes ? (int)sizeof(Sm) : kRingBytes;
   static_assert(kUsed % 8 == 0, "the tables begin with 8-byte words");
-  [[maybe_unused]] Prefixes pre(area + kUsed, MODE == kPrefix ? G : 0);
+  [[maybe_unused]] Prefixes pre(area + kUsed, MODE == kPrefix ? G : 0, MODE == kPrefix ? G : 0);
 
   W w;
   w.lane = threadIdx.x & 31;
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
     }
   } else if constexpr (MODE == kPrefix) {
     pre.fill(a);
-    pre.share(G, x0, x1);
+    pre.share(x0, x1);
   }
   for (int64_t x = x0; x < x1;) {
     Tile tile;
@@ -565,8 +565,8 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
       piece = pre.piece(a, x, x1);
       if (threadIdx.x == 0 && piece.u0 == 0) pre.announce(a, piece, x);
       rt = piece.rt;
-      slice = (int64_t)piece.g * c.n_kv_heads + piece.h;
-      tile.len = held(c, piece.g);
+      slice = (int64_t)piece.list * c.n_kv_heads + piece.h;
+      tile.len = held(c, piece.list);
       tile.lo = tile.sb = tile.cnt = 0;
       tile.hi = (tile.len - 1) / kBlock;
       tile.nb = tile.hi + 1;
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
       w.pos[r] = valid ? tile.len - tile.cnt + i : -1;
       int64_t q_row = (slice * a.group + (valid ? row % a.group : 0)) * a.n + (valid ? i : 0);
       if constexpr (MODE == kPrefix) {
-        const PrefixRow pr = prefix_row(a, pre, piece.g, piece.h, tile.len, (int64_t)rt * RT + 8 * r + w.g);
+        const ListRow pr = list_row(a, pre, piece.list, piece.h, tile.len, (int64_t)rt * RT + 8 * r + w.g);
         valid = pr.at >= 0;
         w.pos[r] = pr.pos;
         q_row = max(pr.at, (int64_t)0);

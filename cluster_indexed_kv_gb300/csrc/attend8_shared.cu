@@ -5,12 +5,15 @@
 namespace lkv {
 
 // Two launches. The first takes each prefix's blocks once for the rows of all
-// sequences behind it and leaves parts (attend8_shared.cuh); the second takes
-// each sequence's own blocks and joins its rows with their parts.
+// sequences behind it and leaves parts (attend8_shared.cuh): in tensor memory's
+// tiles of 128 rows (bf16), or in tiles of 16. The second takes each sequence's
+// own blocks and joins its rows with their parts; where sequences have many rows
+// the first has taken their own blocks too, and the second joins parts alone.
 struct SharedPlan {
-  int nt;            // prefixes: row tiles of 8 nt rows
-  int ctas;          // prefixes: CTAs
-  int64_t tiles;     // prefixes: at most
+  int nt;            // row tiles of 8 nt rows, 16: the kernel for many rows
+  bool own_parts;    // the own tokens too
+  int ctas;
+  int64_t tiles;     // at most
   int own_nt, row_tiles, cluster;
   int64_t own_tiles;
   int64_t seq_at, tile_at, parts_at, bytes;  // the workspace
@@ -20,10 +23,12 @@ static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t
   const int64_t R = (int64_t)n * group, rows = c->batch * R, S = (int64_t)c->batch * c->n_kv_heads;
   if (rows > 0x7fffffff - 256) return "too many rows";
   const bool fp32 = c->dtype == LKV_DTYPE_FP32;
-  s->nt = rows <= 8 ? 1 : 2;
+  s->nt = !fp32 && rows > 16 ? 16 : rows <= 8 ? 1 : 2;
+  s->own_parts = s->nt == 16 && R > 32;
   const int part_rows = 8 * s->nt;
-  s->ctas = sms * (fp32 && s->nt == 2 ? 1 : 2);
+  s->ctas = s->nt == 16 ? sms : sms * (fp32 && s->nt == 2 ? 1 : 2);
   s->tiles = ((rows + part_rows - 1) / part_rows + (p->batch < c->batch ? p->batch : c->batch)) * c->n_kv_heads;
+  if (s->own_parts) s->tiles += S * ((R + part_rows - 1) / part_rows);
   s->own_nt = R <= 8 ? 1 : 2;
   s->row_tiles = (int)((R + 8 * s->own_nt - 1) / (8 * s->own_nt));
   s->own_tiles = S * s->row_tiles;
@@ -34,7 +39,7 @@ static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t
   s->cluster = (int)(cluster < 1 ? 1 : cluster > kAtMaxCluster ? kAtMaxCluster : cluster);
   if (s->tiles > 0x7fffffff || s->own_tiles * s->cluster > 0x7fffffff) return "too many rows";
   s->seq_at = 0;
-  s->tile_at = ((int64_t)c->batch * 8 + 15) / 16 * 16;
+  s->tile_at = (int64_t)c->batch * 16;
   s->parts_at = s->tile_at + (s->tiles * 8 + 15) / 16 * 16;
   s->bytes = s->parts_at + (s->ctas + s->tiles) * part_floats(part_rows) * 4;
   return nullptr;
@@ -44,7 +49,7 @@ template <int DT, int CODE, int NT, int MODE>
 static cudaError_t launch_part(const SharedArgs &a, unsigned grid, int cluster, const CUtensorMap &km, const CUtensorMap &vm, cudaStream_t st) {
   auto *fn = k_attend8<DT, CODE, NT, MODE>;
   const int used = (int)sizeof(AtSmem<NT>) > kRingBytes ? (int)sizeof(AtSmem<NT>) : kRingBytes;
-  const int smem = 1024 + used + (MODE == kPrefix ? (int)Prefixes::bytes(a.c.batch, a.p.batch) : 0);
+  const int smem = 1024 + used + (MODE == kPrefix ? (int)Prefixes::bytes(a.c.batch, a.p.batch, false) : 0);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -70,8 +75,9 @@ static cudaError_t launch_part(const SharedArgs &a, int nt, unsigned grid, int c
 
 template <int DT, int CODE>
 static cudaError_t launch_shared(const SharedArgs &a, const SharedPlan &s, const CUtensorMap (&maps)[4], cudaStream_t st) {
-  const cudaError_t e = launch_part<DT, CODE, kPrefix>(a, s.nt, (unsigned)s.ctas, 0, maps[0], maps[1], st);
+  const cudaError_t e = s.nt == 16 ? launch_shared_rows(a, s.ctas, st) : launch_part<DT, CODE, kPrefix>(a, s.nt, (unsigned)s.ctas, 0, maps[0], maps[1], st);
   if (e != cudaSuccess) return e;
+  if (s.own_parts) return launch_shared_join(a, st);
   return launch_part<DT, CODE, kOwn>(a, s.own_nt, (unsigned)(s.own_tiles * s.cluster), s.cluster, maps[2], maps[3], st);
 }
 
@@ -145,8 +151,9 @@ extern "C" lkv_status lkv_cache8_attend_shared(const lkv_cache8 *c, const lkv_ca
   a.scale_log2 = scale_log2;
   a.row_tiles = s.row_tiles;
   a.part_rows = 8 * s.nt;
-  a.part_blocks = 1;
-  a.seq = (int2 *)((char *)workspace + s.seq_at);
+  a.part_blocks = s.nt == 16 ? kSharedStep / kBlock : 1;
+  a.own_parts = s.own_parts;
+  a.seq = (int4 *)((char *)workspace + s.seq_at);
   a.tile = (int2 *)((char *)workspace + s.tile_at);
   a.parts = (float *)((char *)workspace + s.parts_at);
   const int64_t SP = (int64_t)prefix->batch * prefix->n_kv_heads;

@@ -6,7 +6,9 @@
 // prefix, row tile by row tile and KV head by KV head, is one row of units (runs
 // of part_blocks blocks of a tile), of which each CTA takes an even share. What
 // it makes of a tile is a part: slot (CTA + tile) of the workspace, as each step
-// along the row goes to the next CTA, the next tile, or both.
+// along the row goes to the next CTA, the next tile, or both. Calls of many rows
+// a sequence put the sequences' own tokens behind the prefixes in the same row,
+// as lists of one sequence each.
 #pragma once
 
 #include "attend8.cuh"
@@ -19,7 +21,8 @@ struct SharedArgs : AttendArgs {
   lkv_cache8 p;               // the prefixes
   const int32_t *prefix_of;   // null: all of prefix 0
   int32_t part_rows, part_blocks;
-  int2 *seq;                  // [batch]: the first tile of the sequence's prefix (-1: none), its place behind that prefix
+  int32_t own_parts;          // whether the sequences' own tokens are parts too
+  int4 *seq;                  // [batch]: the first tile of the sequence's prefix (-1: none), its place behind that prefix, its own first tile (-1: none)
   int2 *tile;                 // [tiles]: a tile's first CTA, and how many it has
   float *parts;
 };
@@ -29,21 +32,25 @@ __host__ __device__ constexpr int part_floats(int rows) { return rows * (kHeadDi
 
 __device__ __forceinline__ int held(const lkv_cache8 &c, int b) { return min(max(__ldcg(c.lengths + b), 0), c.capacity); }
 
-// The prefixes' work, in shared memory.
+// The work, in shared memory: list e < G is prefix e's, and list G + b
+// sequence b's own.
 struct Prefixes {
-  int64_t *at;   // [G + 1]: units before each prefix's tiles
-  int *tiles;    // [G + 1]: tiles before
+  int64_t *at;   // [lists + 1]: units before each list's tiles
+  int *tiles;    // [lists + 1]: tiles before
+  int *nu;       // [lists]: units of one of its tiles
   int *first;    // [G + 1]: sequences before, in `order`
-  int *nu;       // [G]: units of one of its tiles
   int *order;    // [batch]: sequences, prefix by prefix
+  int lists;
 
-  static __host__ __device__ int64_t bytes(int batch, int G) { return 20 * (int64_t)(G + 1) + 4 * (int64_t)batch; }
-  __device__ Prefixes(void *area, int G) {
+  static __host__ __device__ int64_t bytes(int batch, int G, bool own) {
+    return 16 * (int64_t)(G + (own ? batch : 0) + 1) + 4 * (int64_t)(G + 1 + batch);
+  }
+  __device__ Prefixes(void *area, int G, int lists_) : lists(lists_) {
     at = (int64_t *)area;
-    tiles = (int *)(at + G + 1);
-    first = tiles + G + 1;
-    nu = first + G + 1;
-    order = nu + G + 1;
+    tiles = (int *)(at + lists + 1);
+    nu = tiles + lists + 1;
+    first = nu + lists + 1;
+    order = first + G + 1;
   }
   // the prefix of sequence b, -1 for none (or an empty one)
   static __device__ __forceinline__ int of(const SharedArgs &a, int b) {
@@ -70,13 +77,21 @@ struct Prefixes {
         if (turn) break;
         int64_t units = 0;
         int nt = 0, seqs = 0;
-        for (int g0 = 0; g0 < G; g0 += 32) {
-          const int g = g0 + lane;
-          const int have = g < G ? nu[g] : 0, len = have ? held(a.p, g) : 0;
+        for (int e0 = 0; e0 < lists; e0 += 32) {
+          const int e = e0 + lane;
+          int have = 0, len = 0;  // sequences in the list, tokens that they see
+          if (e < G) {
+            have = nu[e];
+            len = have ? held(a.p, e) : 0;
+          } else if (e < lists) {
+            len = held(a.c, e - G);
+            have = len > 0;
+          }
           const int rt = (int)(((int64_t)have * a.n * a.group + a.part_rows - 1) / a.part_rows);
           const int run = a.part_blocks * kBlock, per = (len + run - 1) / run;
           int64_t u = (int64_t)rt * a.c.n_kv_heads * per;
-          int t = rt * a.c.n_kv_heads, s = have;
+          int t = rt * a.c.n_kv_heads, s = e < G ? have : 0;
+          const int mine = s;
 #pragma unroll
           for (int d = 1; d < 32; d *= 2) {
             const int64_t u2 = __shfl_up_sync(0xffffffffu, u, d);
@@ -87,11 +102,13 @@ struct Prefixes {
               s += s2;
             }
           }
-          if (g < G) {
-            at[g + 1] = units + u;
-            tiles[g + 1] = nt + t;
-            first[g + 1] = seqs + s;
-            nu[g] = seqs + s - have;  // where its sequences begin
+          if (e < lists) {
+            at[e + 1] = units + u;
+            tiles[e + 1] = nt + t;
+          }
+          if (e < G) {
+            first[e + 1] = seqs + s;
+            nu[e] = seqs + s - mine;  // where its sequences begin
           }
           units += __shfl_sync(0xffffffffu, u, 31);
           nt += __shfl_sync(0xffffffffu, t, 31);
@@ -102,30 +119,31 @@ struct Prefixes {
       }
     }
     __syncthreads();
-    for (int g = threadIdx.x; g < G; g += blockDim.x) {
-      const int t = tiles[g + 1] - tiles[g];
-      nu[g] = t ? (int)((at[g + 1] - at[g]) / t) : 0;
+    for (int e = threadIdx.x; e < lists; e += blockDim.x) {
+      const int t = tiles[e + 1] - tiles[e];
+      nu[e] = t ? (int)((at[e + 1] - at[e]) / t) : 0;
     }
     if (blockIdx.x == 0) {
+      auto own = [&](int b) { return lists > G && tiles[G + b + 1] > tiles[G + b] ? tiles[G + b] : -1; };
       for (int b = threadIdx.x; b < B; b += blockDim.x)
-        if (of(a, b) < 0) a.seq[b] = make_int2(-1, 0);
+        if (of(a, b) < 0) a.seq[b] = make_int4(-1, 0, own(b), 0);
       for (int i = threadIdx.x; i < first[G]; i += blockDim.x) {
         const int b = order[i], g = of(a, b);
-        a.seq[b] = make_int2(tiles[g], i - first[g]);
+        a.seq[b] = make_int4(tiles[g], i - first[g], own(b), 0);
       }
     }
     __syncthreads();
   }
   // this CTA's units
-  __device__ __forceinline__ void share(int G, int64_t &x0, int64_t &x1) const {
-    const int64_t total = at[G], P = min((int64_t)gridDim.x, total);
+  __device__ __forceinline__ void share(int64_t &x0, int64_t &x1) const {
+    const int64_t total = at[lists], P = min((int64_t)gridDim.x, total);
     x0 = blockIdx.x < P ? total * blockIdx.x / P : 0;
     x1 = blockIdx.x < P ? total * (blockIdx.x + 1) / P : 0;
   }
   // a piece of unit x's tile: up to unit x1 of the row
-  struct Piece { int g, h, rt, tile, u0, u1; };
+  struct Piece { int list, h, rt, tile, u0, u1; };
   __device__ __forceinline__ Piece piece(const SharedArgs &a, int64_t x, int64_t x1) const {
-    int lo = 0, hi = a.p.batch;
+    int lo = 0, hi = lists;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (at[mid] <= x) lo = mid;
@@ -134,7 +152,7 @@ struct Prefixes {
     const int64_t off = x - at[lo];
     const int idx = (int)(off / nu[lo]);
     Piece p;
-    p.g = lo;
+    p.list = lo;
     p.h = idx % a.c.n_kv_heads;
     p.rt = idx / a.c.n_kv_heads;
     p.tile = tiles[lo] + idx;
@@ -144,26 +162,32 @@ struct Prefixes {
   }
   // the tile that begins at unit x of the row, for whoever joins its parts (one thread of the CTA that has the unit)
   __device__ __forceinline__ void announce(const SharedArgs &a, const Piece &p, int64_t x) const {
-    const int64_t total = at[a.p.batch], P = min((int64_t)gridDim.x, total), last = x + nu[p.g] - 1;
+    const int64_t total = at[lists], P = min((int64_t)gridDim.x, total), last = x + nu[p.list] - 1;
     // the last CTA that begins at or before unit `last`
     a.tile[p.tile] = make_int2((int)blockIdx.x, (int)((P * (last + 1) - 1) / total) - (int)blockIdx.x + 1);
   }
 };
 
-// Row r of prefix g's list: where its query is (in rows of q, of KV head h) and
-// the last token of the prefix that it sees, len - 1 for all; at < 0: no row, or padding.
-struct PrefixRow { int64_t at; int pos; };
-__device__ __forceinline__ PrefixRow prefix_row(const SharedArgs &a, const Prefixes &p, int g, int h, int len, int64_t r) {
-  PrefixRow x{-1, -1};
-  const int per = a.n * a.group;
+// Row r of a list: where its query is (in rows of q, of KV head h) and the last
+// of the list's `len` tokens that it sees; at < 0: no row, or padding.
+struct ListRow { int64_t at; int pos; };
+__device__ __forceinline__ ListRow list_row(const SharedArgs &a, const Prefixes &p, int list, int h, int len, int64_t r) {
+  ListRow x{-1, -1};
+  const int per = a.n * a.group, G = a.p.batch;
   const int64_t m = r / per;
-  if (m >= p.first[g + 1] - p.first[g]) return x;
-  const int b = p.order[p.first[g] + (int)m], rest = (int)(r - m * per), i = rest / a.group;
+  if (m >= (list < G ? p.first[list + 1] - p.first[list] : 1)) return x;
+  const int b = list < G ? p.order[p.first[list] + (int)m] : list - G, rest = (int)(r - m * per), i = rest / a.group;
   const int mine = held(a.c, b), cnt = a.counts ? min(max(__ldcg(a.counts + b), 0), a.n) : a.n;
   if (i >= cnt) return x;
-  x.pos = max(len + min(mine - cnt + i, -1), -1);
+  x.pos = max(list < G ? len + min(mine - cnt + i, -1) : mine - cnt + i, -1);
   x.at = (((int64_t)b * a.c.n_kv_heads + h) * a.group + rest % a.group) * a.n + i;
   return x;
 }
+
+// The kernel for many rows of bf16 caches and the join of what it leaves
+// (attend8_shared_rows.cu): row tiles of kSharedRows, units of kSharedStep tokens.
+constexpr int kSharedRows = 128, kSharedStep = 128;
+cudaError_t launch_shared_rows(const SharedArgs &a, int ctas, cudaStream_t st);
+cudaError_t launch_shared_join(const SharedArgs &a, cudaStream_t st);
 
 }  // namespace lkv
