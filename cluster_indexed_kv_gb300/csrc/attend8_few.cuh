@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
   // the prefixes' tables lie behind what the rings and merges use
   constexpr int kUsed = (int)sizeof(Sm) > kRingBytes ? (int)sizeof(Sm) : kRingBytes;
   static_assert(kUsed % 8 == 0, "the tables begin with 8-byte words");
-  [[maybe_unused]] Prefixes pre(area + kUsed, MODE == kPrefix ? G : 0, MODE == kPrefix ? G : 0);
+  [[maybe_unused]] Prefixes pre(area + kUsed, MODE == kPrefix ? a.c.batch : 0, MODE == kPrefix ? G : 0, MODE == kPrefix ? G : 0);
 
   W w;
   w.lane = threadIdx.x & 31;
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
     }
   } else if constexpr (MODE == kPrefix) {
     pre.fill(a);
-    pre.share(x0, x1);
+    pre.share(a, x0, x1);
   }
   for (int64_t x = x0; x < x1;) {
     Tile tile;

@@ -21,6 +21,7 @@ struct SharedArgs : AttendArgs {
   lkv_cache8 p;               // the prefixes
   const int32_t *prefix_of;   // null: all of prefix 0
   int32_t part_rows, part_blocks;
+  int32_t least_units;        // that a CTA takes, at least
   int32_t own_parts;          // whether the sequences' own tokens are parts too
   int4 *seq;                  // [batch]: the first tile of the sequence's prefix (-1: none), its place behind that prefix, its own first tile (-1: none)
   int2 *tile;                 // [tiles]: a tile's first CTA, and how many it has
@@ -32,6 +33,12 @@ __host__ __device__ constexpr int part_floats(int rows) { return rows * (kHeadDi
 
 __device__ __forceinline__ int held(const lkv_cache8 &c, int b) { return min(max(__ldcg(c.lengths + b), 0), c.capacity); }
 
+// a / b, both >= 0, in 32 bits where they fit: most do, and several such
+// quotients stand between a CTA and its first copy.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // The work, in shared memory: list e < G is prefix e's, and list G + b
 // sequence b's own.
 struct Prefixes {
@@ -40,38 +47,49 @@ struct Prefixes {
   int *nu;       // [lists]: units of one of its tiles
   int *first;    // [G + 1]: sequences before, in `order`
   int *order;    // [batch]: sequences, prefix by prefix
+  int *of;       // [batch]: the sequence's prefix, -1 for none (or an empty one)
+  int *before;   // [batch]: its own tokens before its first row
+  int *rows;     // [batch]: tokens of its rows that are no padding
   int lists;
 
   static __host__ __device__ int64_t bytes(int batch, int G, bool own) {
-    return 16 * (int64_t)(G + (own ? batch : 0) + 1) + 4 * (int64_t)(G + 1 + batch);
+    return 16 * (int64_t)(G + (own ? batch : 0) + 1) + 4 * (int64_t)(G + 1 + 4 * batch);
   }
-  __device__ Prefixes(void *area, int G, int lists_) : lists(lists_) {
+  __device__ Prefixes(void *area, int batch, int G, int lists_) : lists(lists_) {
     at = (int64_t *)area;
     tiles = (int *)(at + lists + 1);
     nu = tiles + lists + 1;
     first = nu + lists + 1;
     order = first + G + 1;
-  }
-  // the prefix of sequence b, -1 for none (or an empty one)
-  static __device__ __forceinline__ int of(const SharedArgs &a, int b) {
-    const int g = a.prefix_of ? __ldcg(a.prefix_of + b) : 0;
-    return g >= 0 && g < a.p.batch && held(a.p, g) > 0 ? g : -1;
+    of = order + batch;
+    before = of + batch;
+    rows = before + batch;
   }
   __device__ void fill(const SharedArgs &a) {
     const int G = a.p.batch, B = a.c.batch;
-    for (int g = threadIdx.x; g < G; g += blockDim.x) nu[g] = 0;
+    for (int b = threadIdx.x; b < B; b += blockDim.x) {
+      const int g = a.prefix_of ? __ldcg(a.prefix_of + b) : 0, mine = held(a.c, b);
+      const int cnt = a.counts ? min(max(__ldcg(a.counts + b), 0), a.n) : a.n;
+      of[b] = g >= 0 && g < G && held(a.p, g) > 0 ? g : -1;
+      before[b] = mine - cnt;
+      rows[b] = cnt;
+    }
+    for (int e = threadIdx.x; e < lists; e += blockDim.x) {
+      nu[e] = 0;
+      at[e + 1] = e < G ? held(a.p, e) : held(a.c, e - G);
+    }
     __syncthreads();
     if (threadIdx.x < 32) {
       const int lane = threadIdx.x;
       const uint32_t below = (1u << lane) - 1u;
       for (int turn = 0; turn < 2; ++turn) {  // how many sequences a prefix has, then their places
         for (int b0 = 0; b0 < B; b0 += 32) {
-          const int b = b0 + lane, g = b < B ? of(a, b) : -1;
+          const int b = b0 + lane, g = b < B ? of[b] : -1;
           const uint32_t same = __match_any_sync(0xffffffffu, g >= 0 ? g : -2 - lane);
-          const int before = g >= 0 ? nu[g] : 0;
-          if (turn && g >= 0) order[before + __popc(same & below)] = b;
+          const int had = g >= 0 ? nu[g] : 0;
+          if (turn && g >= 0) order[had + __popc(same & below)] = b;
           __syncwarp();
-          if (g >= 0 && (same & below) == 0) nu[g] = before + __popc(same);
+          if (g >= 0 && (same & below) == 0) nu[g] = had + __popc(same);
           __syncwarp();
         }
         if (turn) break;
@@ -79,16 +97,9 @@ struct Prefixes {
         int nt = 0, seqs = 0;
         for (int e0 = 0; e0 < lists; e0 += 32) {
           const int e = e0 + lane;
-          int have = 0, len = 0;  // sequences in the list, tokens that they see
-          if (e < G) {
-            have = nu[e];
-            len = have ? held(a.p, e) : 0;
-          } else if (e < lists) {
-            len = held(a.c, e - G);
-            have = len > 0;
-          }
-          const int rt = (int)(((int64_t)have * a.n * a.group + a.part_rows - 1) / a.part_rows);
-          const int run = a.part_blocks * kBlock, per = (len + run - 1) / run;
+          const int len = e < lists ? (int)at[e + 1] : 0, have = e < G ? nu[e] : len > 0;  // tokens, and sequences that see them
+          const int rt = (int)quotient((int64_t)have * a.n * a.group + a.part_rows - 1, a.part_rows);
+          const int run = a.part_blocks * kBlock, per = (int)((uint32_t)(len + run - 1) / (uint32_t)run);
           int64_t u = (int64_t)rt * a.c.n_kv_heads * per;
           int t = rt * a.c.n_kv_heads, s = e < G ? have : 0;
           const int mine = s;
@@ -109,6 +120,8 @@ struct Prefixes {
           if (e < G) {
             first[e + 1] = seqs + s;
             nu[e] = seqs + s - mine;  // where its sequences begin
+          } else if (e < lists) {
+            nu[e] = per;
           }
           units += __shfl_sync(0xffffffffu, u, 31);
           nt += __shfl_sync(0xffffffffu, t, 31);
@@ -119,26 +132,30 @@ struct Prefixes {
       }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < lists; e += blockDim.x) {
-      const int t = tiles[e + 1] - tiles[e];
-      nu[e] = t ? (int)((at[e + 1] - at[e]) / t) : 0;
+    for (int g = threadIdx.x; g < G; g += blockDim.x) {
+      const int t = tiles[g + 1] - tiles[g];
+      nu[g] = t ? (int)quotient(at[g + 1] - at[g], t) : 0;
     }
     if (blockIdx.x == 0) {
       auto own = [&](int b) { return lists > G && tiles[G + b + 1] > tiles[G + b] ? tiles[G + b] : -1; };
       for (int b = threadIdx.x; b < B; b += blockDim.x)
-        if (of(a, b) < 0) a.seq[b] = make_int4(-1, 0, own(b), 0);
+        if (of[b] < 0) a.seq[b] = make_int4(-1, 0, own(b), 0);
       for (int i = threadIdx.x; i < first[G]; i += blockDim.x) {
-        const int b = order[i], g = of(a, b);
+        const int b = order[i], g = of[b];
         a.seq[b] = make_int4(tiles[g], i - first[g], own(b), 0);
       }
     }
     __syncthreads();
   }
+  // CTAs that take part
+  __device__ __forceinline__ int64_t takers(const SharedArgs &a) const {
+    return max((int64_t)1, min((int64_t)gridDim.x, quotient(at[lists], a.least_units)));
+  }
   // this CTA's units
-  __device__ __forceinline__ void share(int64_t &x0, int64_t &x1) const {
-    const int64_t total = at[lists], P = min((int64_t)gridDim.x, total);
-    x0 = blockIdx.x < P ? total * blockIdx.x / P : 0;
-    x1 = blockIdx.x < P ? total * (blockIdx.x + 1) / P : 0;
+  __device__ __forceinline__ void share(const SharedArgs &a, int64_t &x0, int64_t &x1) const {
+    const int64_t total = at[lists], P = takers(a);
+    x0 = blockIdx.x < P ? quotient(total * blockIdx.x, P) : 0;
+    x1 = blockIdx.x < P ? quotient(total * (blockIdx.x + 1), P) : 0;
   }
   // a piece of unit x's tile: up to unit x1 of the row
   struct Piece { int list, h, rt, tile, u0, u1; };
@@ -150,21 +167,21 @@ struct Prefixes {
       else hi = mid;
     }
     const int64_t off = x - at[lo];
-    const int idx = (int)(off / nu[lo]);
+    const int idx = (int)quotient(off, nu[lo]);
     Piece p;
     p.list = lo;
-    p.h = idx % a.c.n_kv_heads;
-    p.rt = idx / a.c.n_kv_heads;
+    p.rt = (int)((uint32_t)idx / (uint32_t)a.c.n_kv_heads);
+    p.h = idx - p.rt * a.c.n_kv_heads;
     p.tile = tiles[lo] + idx;
-    p.u0 = (int)(off % nu[lo]);
+    p.u0 = (int)(off - (int64_t)idx * nu[lo]);
     p.u1 = (int)min((int64_t)nu[lo], p.u0 + (x1 - x));
     return p;
   }
   // the tile that begins at unit x of the row, for whoever joins its parts (one thread of the CTA that has the unit)
   __device__ __forceinline__ void announce(const SharedArgs &a, const Piece &p, int64_t x) const {
-    const int64_t total = at[lists], P = min((int64_t)gridDim.x, total), last = x + nu[p.list] - 1;
+    const int64_t P = takers(a), last = x + nu[p.list] - 1;
     // the last CTA that begins at or before unit `last`
-    a.tile[p.tile] = make_int2((int)blockIdx.x, (int)((P * (last + 1) - 1) / total) - (int)blockIdx.x + 1);
+    a.tile[p.tile] = make_int2((int)blockIdx.x, (int)quotient(P * (last + 1) - 1, at[lists]) - (int)blockIdx.x + 1);
   }
 };
 
@@ -174,13 +191,13 @@ struct ListRow { int64_t at; int pos; };
 __device__ __forceinline__ ListRow list_row(const SharedArgs &a, const Prefixes &p, int list, int h, int len, int64_t r) {
   ListRow x{-1, -1};
   const int per = a.n * a.group, G = a.p.batch;
-  const int64_t m = r / per;
+  const int64_t m = quotient(r, per);
   if (m >= (list < G ? p.first[list + 1] - p.first[list] : 1)) return x;
-  const int b = list < G ? p.order[p.first[list] + (int)m] : list - G, rest = (int)(r - m * per), i = rest / a.group;
-  const int mine = held(a.c, b), cnt = a.counts ? min(max(__ldcg(a.counts + b), 0), a.n) : a.n;
-  if (i >= cnt) return x;
-  x.pos = max(list < G ? len + min(mine - cnt + i, -1) : mine - cnt + i, -1);
-  x.at = (((int64_t)b * a.c.n_kv_heads + h) * a.group + rest % a.group) * a.n + i;
+  const int b = list < G ? p.order[p.first[list] + (int)m] : list - G, rest = (int)(r - m * per);
+  const int i = (int)((uint32_t)rest / (uint32_t)a.group);
+  if (i >= p.rows[b]) return x;
+  x.pos = max(list < G ? len + min(p.before[b] + i, -1) : p.before[b] + i, -1);
+  x.at = (((int64_t)b * a.c.n_kv_heads + h) * a.group + rest - i * a.group) * a.n + i;
   return x;
 }
 

@@ -8,79 +8,67 @@ namespace lkv {
 constexpr uint32_t kShSmem = 5 * kRwTile + 1024;  // Q, K: 2, V: 2
 static_assert(kSharedRows == kRwRows && kSharedStep == kRwTok, "a tile is one of tensor memory's");
 
-// What a CTA is at. In shared memory, read again where it is needed after the
-// loop over steps, which has no registers left.
+// Warps: softmax of the even steps and of the odd ones, producers of K and of V,
+// and a fifth group with the issuing warp and the one that reads scales. The
+// launch's registers (96 a thread) are shared out anew: 136, 80 and 48 a thread
+// of these, 480 a lane of an SM's quarter in all.
+constexpr int kShSoft = 8, kShK = 8, kShV = 12, kShIssuer = 16, kShScales = 17, kShThreads = 20 * 32;
+template <int N>
+__device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ void group_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+// What a CTA is at.
 struct SharedPiece {
   Prefixes::Piece p;
-  int64_t x, end;
-  const uint8_t *codes[2];   // the list's cache: K's and V's codes, scales and tails of the KV head
+  int64_t x, end;             // of the row of units: where the CTA is, and its end
+  const uint8_t *codes[2];    // the list's cache: K's and V's codes, scales and tails of the KV head
   const float *scale[2];
   const uint16_t *tail[2];
-  int len, units;
+  int len;
+  int go;                     // whether there is a piece
+  int last;                   // the last token that a row sees
   uint32_t top, tail_top[2];  // largest V scale of the piece's blocks, largest magnitudes of the tails (bits)
-  int steps, done, unit;  // of the piece, of those before (the barriers' phases go on), exponent of its V scales' unit
+  int64_t at[kRwRows];        // the rows' queries, -1 for none
+  int pos[kRwRows];           // the last token that a row sees
+  float rc[kRwRows];          // query unit * scale * log2(e)
+  float ref[2][kRwRows], l[2][kRwRows];  // references and totals of the even and odd steps
 };
 
-// The rows of a piece's tile.
-struct PieceRows {
-  int64_t at[kRwRows];  // the rows' queries, -1 for none
-  int pos[kRwRows];
-  int last;             // the last token that a row sees
+// A piece's steps and units, as every warp forms them.
+struct Steps {
+  int s0, s1, nb, full, tail_rows;
+  bool tail;  // the partial block is among them, as the last
+  __device__ __forceinline__ explicit Steps(const SharedPiece &p) {
+    nb = (p.len + kBlock - 1) / kBlock;
+    full = p.len / kBlock;
+    tail_rows = p.len - full * kBlock;
+    // steps behind the last token that a row sees are nobody's
+    s0 = p.p.u0;
+    s1 = max(min(p.p.u1, (p.last + kRwTok) / kRwTok), s0);
+    tail = s1 > s0 && full < nb && s1 * kRwBlocks >= nb;
+  }
 };
-
-// The piece at seg.x and its rows, by all threads. Out of the way of the
-// registers that the loop over steps needs, as store_part is.
-static __device__ __noinline__ void begin_piece(const SharedArgs &a, void *tables, SharedPiece &seg, PieceRows &rows) {
-  const Prefixes pre(tables, a.p.batch, a.p.batch + (a.own_parts ? a.c.batch : 0));
-  if (threadIdx.x == 0) {
-    const Prefixes::Piece p = pre.piece(a, seg.x, seg.end);
-    if (p.u0 == 0) pre.announce(a, p, seg.x);
-    seg.p = p;
-    auto from = [&](const lkv_cache8 &c, int b) {
-      const int64_t slice = (int64_t)b * c.n_kv_heads + p.h, codes = slice * c.capacity * kHeadDim, tail = slice * kBlock * kHeadDim;
-      seg.len = held(c, b);
-      seg.codes[0] = (const uint8_t *)c.k_codes + codes;
-      seg.codes[1] = (const uint8_t *)c.v_codes + codes;
-      seg.scale[0] = c.k_scale + slice * (c.capacity / kBlock);
-      seg.scale[1] = c.v_scale + slice * (c.capacity / kBlock);
-      seg.tail[0] = (const uint16_t *)c.k_tail + tail;
-      seg.tail[1] = (const uint16_t *)c.v_tail + tail;
-    };
-    if (p.list < a.p.batch) from(a.p, p.list);
-    else from(a.c, p.list - a.p.batch);
-    seg.units = p.u1 - p.u0;
-    seg.top = seg.tail_top[0] = seg.tail_top[1] = 0;
-    rows.last = -1;
+// V scales count in units of 2^unit; tails in units of 2^ke and 2^ve.
+struct Units {
+  int ke, ve, unit;
+  __device__ __forceinline__ Units(const SharedPiece &p, bool tail) {
+    ke = exponent_of(p.tail_top[0]);
+    ve = exponent_of(p.tail_top[1]);
+    unit = max(max((int)(p.top >> 23) - 127, -126), tail ? ve : -126);
   }
-  __syncthreads();
-  if (threadIdx.x < kRwRows) {
-    const ListRow x = list_row(a, pre, seg.p.list, seg.p.h, seg.len, (int64_t)seg.p.rt * kRwRows + threadIdx.x);
-    rows.at[threadIdx.x] = x.at;
-    rows.pos[threadIdx.x] = x.pos;
-    const int top = __reduce_max_sync(0xffffffffu, x.at < 0 ? -1 : x.pos);
-    if (threadIdx.x % 32 == 0 && top >= 0) atomicMax(&rows.last, top);
-  }
-  __syncthreads();
-}
-
-// References and totals of a piece's even and odd steps.
-struct Halves { float ref[2][kRwRows], l[2][kRwRows]; };
+};
 
 // What both halves of the softmax have of a row goes into the piece's part: each
-// half's threads write 64 of the values of d. Out of the loop's way.
-static __device__ __noinline__ void store_part(const SharedArgs &a, const volatile SharedPiece &at, Halves &z, bool valid, bool seen, float ref, float l,
-                                        uint32_t tmem, volatile int *abort) {
+// half's threads write 64 of the values of d.
+__device__ __forceinline__ void store_part(const SharedArgs &a, const SharedPiece &z, int steps, int done, int unit, uint32_t tmem) {
   const int w = threadIdx.x >> 7, r = threadIdx.x & 127;
-  const bool has0 = at.steps > 1 || (at.done & 1) == 0, has1 = at.steps > 1 || (at.done & 1) == 1, has = w ? has1 : has0;
-  // (a row whose scores are all NaN has no reference, but l and O, which are NaN, count)
-  z.ref[w][r] = valid && seen && has ? ref : -INFINITY;
-  z.l[w][r] = valid && has ? l : 0.f;
-  tmem_before();
-  asm volatile("bar.sync 1, 256;" ::: "memory");
-  tmem_after();
-  if (!__any_sync(0xffffffffu, valid) || *abort) return;
-  float *const part = a.parts + ((int64_t)blockIdx.x + at.p.tile) * part_floats(kRwRows);
-  const float m0 = z.ref[0][r], m1 = z.ref[1][r], top = fmaxf(m0, m1), f0 = share(m0, top), f1 = share(m1, top);
+  const bool valid = z.at[r] >= 0, has0 = steps > 1 || (done & 1) == 0, has1 = steps > 1 || (done & 1) == 1;
+  if (!__any_sync(0xffffffffu, valid)) return;
+  float *const part = a.parts + ((int64_t)blockIdx.x + z.p.tile) * part_floats(kRwRows);
+  const float m0 = valid && has0 ? z.ref[0][r] : -INFINITY, m1 = valid && has1 ? z.ref[1][r] : -INFINITY;
+  const float top = fmaxf(m0, m1), f0 = share(m0, top), f1 = share(m1, top);
   const uint32_t o0 = tmem + ((uint32_t)(r & 96) << 16) + 256 + 64 * w, o1 = o0 + 128;
 #pragma unroll 1
   for (int d = 0; d < 64; d += 16) {
@@ -98,28 +86,27 @@ static __device__ __noinline__ void store_part(const SharedArgs &a, const volati
   }
   if (w == 0) {
     float *const p = part + kRwRows * kHeadDim + r;
-    p[0] = top == -INFINITY ? top : top + (float)at.unit;
+    p[0] = top == -INFINITY ? top : top + (float)unit;
     p[kRwRows] = top;
-    p[2 * kRwRows] = f0 * z.l[0][r] + f1 * z.l[1][r];
+    p[2 * kRwRows] = valid ? (has0 ? f0 * z.l[0][r] : 0.f) + (has1 ? f1 * z.l[1][r] : 0.f) : 0.f;
   }
 }
 
 template <int CODE>
-__global__ void __launch_bounds__(kRwThreads, 1) k_shared_rows(const __grid_constant__ SharedArgs a) {
+__global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_constant__ SharedArgs a) {
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) RowsSync sy;
+  __shared__ __align__(8) uint64_t scempty[4];
   __shared__ float4 scales[4][kRwBlocks];  // a block's K scale, log2 and reciprocal of its V scale's share of the unit, first token
   __shared__ uint32_t tmem_s;
   __shared__ volatile int abort_s;
   __shared__ __align__(16) uint16_t tails[2][kBlock * kHeadDim];  // K's and V's partial block, zeros behind its rows
   __shared__ SharedPiece seg;
-  __shared__ PieceRows rows;
-  __shared__ float rc_s[kRwRows];          // query unit * scale * log2(e)
-  __shared__ Halves half_s;
   const uint32_t base = (smem_at(raw) + 1023u) & ~1023u;
   unsigned char *const area = raw + (base - smem_at(raw));
   const uint32_t q_at = base, k_at = base + kRwTile, v_at = base + 3 * kRwTile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Prefixes pre(area + 5 * kRwTile, a.c.batch, a.p.batch, a.p.batch + (a.own_parts ? a.c.batch : 0));
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -133,273 +120,85 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_shared_rows(const __grid_cons
       bar_init(&sy.odone[i][0], 1);
       bar_init(&sy.odone[i][1], 1);
     }
-    for (int i = 0; i < 4; ++i) bar_init(&sy.scfull[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      bar_init(&sy.scfull[i], 1);
+      bar_init(&scempty[i], 1);
+    }
     bar_init(&sy.drained, 1);
     bar_init_fence();
     abort_s = 0;
   }
   wait_prerequisites();
   launch_dependents();
-  if (warp == kRwIssuer) {
+  if (warp == kShIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_at(&tmem_s)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  {
-    Prefixes pre(area + 5 * kRwTile, a.p.batch, a.p.batch + (a.own_parts ? a.c.batch : 0));
-    pre.fill(a);
-    if (threadIdx.x == 0) {
-      pre.share(seg.x, seg.end);
-      seg.done = 0;
-    }
-  }
+  const_cast<Prefixes &>(pre).fill(a);
+  if (threadIdx.x == 32 * kShK) pre.share(a, seg.x, seg.end);
+  tmem_before();
   __syncthreads();
+  tmem_after();
+  const uint32_t tmem = tmem_s;
+  int done = 0;  // steps of earlier pieces: the barriers' phases go on
 
-  while (seg.x < seg.end) {
-    begin_piece(a, area + 5 * kRwTile, seg, rows);
-    const int len = seg.len, nb = (len + kBlock - 1) / kBlock, full = len / kBlock;
-    // steps behind the last token that a row sees are nobody's
-    const int s0 = seg.p.u0, s1 = min(seg.p.u1, (rows.last + kRwTok) / kRwTok), steps = max(s1 - s0, 0), done = seg.done;
-    if (steps == 0) {
-      if (threadIdx.x < kRwRows) {
-        float *const slot = a.parts + ((int64_t)blockIdx.x + seg.p.tile) * part_floats(kRwRows);
-        slot[kRwRows * kHeadDim + threadIdx.x] = slot[kRwRows * (kHeadDim + 1) + threadIdx.x] = -INFINITY;
-        slot[kRwRows * (kHeadDim + 2) + threadIdx.x] = 0.f;
+  // Every warp passes the same four barriers a piece: (1) the piece before is
+  // done with, (2) the piece is named, (3) its rows are, (4) queries, units and
+  // tails are in place. Then each has its part of the steps.
+  if (warp < kShSoft) {
+    // ---------------------------------------------------------------- softmax
+    registers_up<136>();
+    // Four warps take the even steps, four the odd ones; both hold all rows,
+    // each with a reference, a total and an accumulator of its own.
+    const int w = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + w * 128, o_at = tmem + lanes + 256 + w * 128;
+    while (true) {
+      __syncthreads();
+      __syncthreads();
+      if (!seg.go) break;
+      if (w == 0) {
+        const ListRow x = list_row(a, pre, seg.p.list, seg.p.h, seg.len, (int64_t)seg.p.rt * kRwRows + row);
+        seg.at[row] = x.at;
+        seg.pos[row] = x.pos;
+        const int top = __reduce_max_sync(0xffffffffu, x.at < 0 ? -1 : x.pos);
+        if (lane == 0 && top >= 0) atomicMax(&seg.last, top);
       }
       __syncthreads();
-      if (threadIdx.x == 0) seg.x += seg.units;
+      {
+        // queries as fp16 in units of a power of two into the swizzled tile, 16 lanes a row, 16 rows a warp
+        const int half = lane >> 4, run = lane & 15;
+        uint4 q[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int64_t at = seg.at[warp * 16 + 2 * k + half];
+          q[k] = at >= 0 ? *(const uint4 *)((const uint16_t *)a.q + at * kHeadDim + 8 * run) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rr = warp * 16 + 2 * k + half;
+          uint32_t m = __vmaxu2(__vmaxu2(q[k].x & 0x7fff7fffu, q[k].y & 0x7fff7fffu), __vmaxu2(q[k].z & 0x7fff7fffu, q[k].w & 0x7fff7fffu));
+#pragma unroll
+          for (int d = 8; d > 0; d /= 2) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+          const int e = exponent_of(max(m << 16, m & 0xffff0000u));
+          const float f = pow2f(-e);
+          if (run == 0) seg.rc[rr] = pow2f(e) * a.scale_log2;
+          const uint32_t x[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+          uint32_t h[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            h[v] = h2_bits(__floats2half2_rn(__uint_as_float(x[v] << 16) * f, __uint_as_float(x[v] & 0xffff0000u) * f));
+          unsigned char *to = area + (run >> 3) * kRwHalf + rr * 128;
+          *(uint4 *)(to + (((run & 7) ^ (rr & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
       __syncthreads();
-      continue;
-    }
-    const bool tail = full < nb && s1 * kRwBlocks >= nb;  // the partial block is among them, as the last
-    const int tail_rows = len - full * kBlock, last = min(s1 * kRwBlocks, nb);
-    if (warp < kRwProducer) {
-      // queries as fp16 in units of a power of two into the swizzled tile, 16 lanes a row, 16 rows a warp
-      const int half = lane >> 4, run = lane & 15;
-      uint4 w[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t at = rows.at[warp * 16 + 2 * k + half];
-        w[k] = at >= 0 ? *(const uint4 *)((const uint16_t *)a.q + at * kHeadDim + 8 * run) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int rr = warp * 16 + 2 * k + half;
-        uint32_t m = __vmaxu2(__vmaxu2(w[k].x & 0x7fff7fffu, w[k].y & 0x7fff7fffu), __vmaxu2(w[k].z & 0x7fff7fffu, w[k].w & 0x7fff7fffu));
-#pragma unroll
-        for (int d = 8; d > 0; d /= 2) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const int e = exponent_of(max(m << 16, m & 0xffff0000u));
-        const float f = pow2f(-e);
-        if (run == 0) rc_s[rr] = pow2f(e) * a.scale_log2;
-        const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-        uint32_t h[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          h[v] = h2_bits(__floats2half2_rn(__uint_as_float(x[v] << 16) * f, __uint_as_float(x[v] & 0xffff0000u) * f));
-        unsigned char *to = area + (run >> 3) * kRwHalf + rr * 128;
-        *(uint4 *)(to + (((run & 7) ^ (rr & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    } else {
-      // the unit of the V scales, and the tails with their largest values
-      const int t = threadIdx.x - 32 * kRwProducer, stride = kRwThreads - 32 * kRwProducer;
-      const float *const vsc = seg.scale[1];
-      uint32_t top = 0;
-#pragma unroll 4
-      for (int u = s0 * kRwBlocks + t; u < min(last, full); u += stride) top = max(top, __float_as_uint(vsc[u]));
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0 && top) atomicMax(&seg.top, top);
-      if (tail) {
-        constexpr int kRun = kBlock * kHeadDim / 8;  // 16-byte runs of a tail: a multiple of a warp's 32
-#pragma unroll 4
-        for (int k = t; k < 2 * kRun; k += stride) {
-          const uint16_t *from = seg.tail[k / kRun];
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (k % kRun / 16 < tail_rows) w = *(const uint4 *)(from + k % kRun * 8);
-          *(uint4 *)(tails[k / kRun] + k % kRun * 8) = w;
-          uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-          m = __reduce_max_sync(0xffffffffu, max(m << 16, m & 0xffff0000u));
-          if (lane == 0) atomicMax(&seg.tail_top[k / kRun], m);
-        }
-      }
-    }
-    tmem_before();
-    __syncthreads();
-    tmem_after();
-    const uint32_t tmem = tmem_s;
-    const int ke = exponent_of(seg.tail_top[0]), ve = exponent_of(seg.tail_top[1]);
-    const int unit = max(max((int)(seg.top >> 23) - 127, -126), tail ? ve : -126);  // V scales count in units of 2^unit
-    if (threadIdx.x == 0) {
-      seg.steps = steps;
-      seg.unit = unit;
-    }
-
-    if (warp >= kRwProducer && warp < kRwIssuer) {
-      // ---------------------------------------------------------------- producers
-      const int pw = warp - kRwProducer;
-      const uint8_t *const kc = seg.codes[0], *const vc = seg.codes[1];
-      const float *const ksc = seg.scale[0], *const vsc = seg.scale[1];
-      const int kr_row = lane >> 3, kr_half = (lane >> 2) & 1, kr_run = lane & 3;
-      const int tc = (pw * 32 + lane) & 15, dc = (pw * 32 + lane) >> 4;
-      const float kf = pow2f(-ke), vf = pow2f(-max(ve, unit - kUnitSpan));
-      uint4 kr[8], vr[8];
-      auto load_k = [&](int j) {
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const int b = j * kRwBlocks + 2 * pw + (t >> 2);
-          const uint8_t *p = kc + ((int64_t)b * kBlock + 4 * (t & 3) + kr_row) * kHeadDim + 16 * (lane & 7);
-          kr[t] = b < full ? __ldg((const uint4 *)p) : make_uint4(0, 0, 0, 0);
-        }
-      };
-      auto load_v = [&](int j) {
-        const int b = j * kRwBlocks + (tc >> 1);
-        const uint8_t *p = vc + ((int64_t)b * kBlock + 8 * (tc & 1)) * kHeadDim + 16 * dc;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) vr[i] = b < full ? __ldg((const uint4 *)(p + i * kHeadDim)) : make_uint4(0, 0, 0, 0);
-      };
-      load_k(s0);
-      load_v(s0);
-      for (int g = done; g < done + steps; ++g) {
-        const int j = g - done + s0, st = g & 1;
-        if (pw == 0) {  // the blocks' scales
-          if (lane < kRwBlocks) {
-            const int b = j * kRwBlocks + lane;
-            float4 s = make_float4(0.f, 0.f, 1.f, __int_as_float(kNoToken));
-            if (b < nb) {
-              float k = pow2f(ke), v = pow2f(max(ve, unit - kUnitSpan) - unit);
-              if (b < full) {
-                k = ksc[b];
-                v = fmaxf(vsc[b] * pow2f(-unit), pow2f(-kUnitSpan));
-              }
-              s = make_float4(k, log2f(v), 1.f / v, __int_as_float(b * kBlock));
-            }
-            scales[g & 3][lane] = s;
-          }
-          __syncwarp();
-        }
-        if (!rows_wait_warp(&sy.kempty[st], ((g >> 1) & 1) ^ 1, &abort_s)) break;
-        unsigned char *const kt = area + kRwTile + st * kRwTile, *const vt = area + 3 * kRwTile + st * kRwTile;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          // a run's 16-byte chunks go to places 2 run and 2 run + 1, the second
-          // half's in the other order: 8 lanes fill 8 places of a row at a time
-          const int r = 32 * pw + 4 * t + kr_row;
-          const uint4 w = kr_half ? make_uint4(kr[t].z, kr[t].w, kr[t].x, kr[t].y) : kr[t];
-          uint32_t x[8];
-          codes_row<CODE>(w.x, x[0], x[1]);
-          codes_row<CODE>(w.y, x[2], x[3]);
-          codes_row<CODE>(w.z, x[4], x[5]);
-          codes_row<CODE>(w.w, x[6], x[7]);
-          unsigned char *to = kt + kr_half * kRwHalf + r * 128;
-          *(uint4 *)(to + (((2 * kr_run + kr_half) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-          *(uint4 *)(to + (((2 * kr_run + 1 - kr_half) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
-        }
-        if (j + 1 < s1) load_k(j + 1);
-        const bool ends = tail && (j + 1) * kRwBlocks >= nb;  // the step's last block is the partial one
-        const int tail_at = (nb - 1) % kRwBlocks * kBlock;
-        if (ends) {
-          __syncwarp();  // over the zeros of the rows' own warp
-          if (pw == tail_at / 32) {
-#pragma unroll 1
-            for (int r = 0; r < tail_rows; ++r) {
-              const int row = tail_at + r, d = 4 * lane;
-              const uint2 x = *(const uint2 *)(tails[0] + r * kHeadDim + d);
-              const uint32_t h0 = h2_bits(__floats2half2_rn(__uint_as_float(x.x << 16) * kf, __uint_as_float(x.x & 0xffff0000u) * kf));
-              const uint32_t h1 = h2_bits(__floats2half2_rn(__uint_as_float(x.y << 16) * kf, __uint_as_float(x.y & 0xffff0000u) * kf));
-              *(uint2 *)(kt + (d >> 6) * kRwHalf + row * 128 + ((((d & 63) >> 3) ^ (row & 7)) << 4) + (d & 7) * 2) = make_uint2(h0, h1);
-            }
-          }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          bar_arrive(&sy.kfull[st]);
-          if (pw == 0) bar_arrive(&sy.scfull[g & 3]);
-        }
-        if (!rows_wait_warp(&sy.vempty[st], ((g >> 1) & 1) ^ 1, &abort_s)) break;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = e == 0 ? vr[i].x : e == 1 ? vr[i].y : e == 2 ? vr[i].z : vr[i].w;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t x[4], y[4];  // d = 16 dc + 4 e + 2 h and the next: 8 tokens each
-#pragma unroll
-            for (int m = 0; m < 4; ++m) codes_across<CODE>(w[2 * m], w[2 * m + 1], h, x[m], y[m]);
-            const int d = 16 * dc + 4 * e + 2 * h;
-            unsigned char *to = vt + (tc >> 3) * kRwHalf + d * 128;
-            *(uint4 *)(to + (((tc & 7) ^ (d & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-            *(uint4 *)(to + 128 + (((tc & 7) ^ ((d + 1) & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-        }
-        if (j + 1 < s1) load_v(j + 1);
-        if (ends && (tc >> 1) == tail_at / kBlock) {  // this thread's 8 tokens and 16 values of d
-#pragma unroll 1
-          for (int e = 0; e < 16; ++e) {
-            const int d = 16 * dc + e, first = 8 * (tc & 1);
-            uint32_t x[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const int row = first + 2 * m;
-              const float lo = bf16_bits_to_f32(tails[1][row * kHeadDim + d]), hi = bf16_bits_to_f32(tails[1][(row + 1) * kHeadDim + d]);
-              x[m] = h2_bits(__floats2half2_rn(lo * vf, hi * vf));
-            }
-            *(uint4 *)(vt + (tc >> 3) * kRwHalf + d * 128 + (((tc & 7) ^ (d & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-          }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) bar_arrive(&sy.vfull[st]);
-      }
-    } else if (warp == kRwIssuer) {
-      // ---------------------------------------------------------------- products
-      if (lane == 0) {
-        auto qk = [&](int g) {
-          const int w = g & 1;
-          if (!rows_wait(&sy.kfull[w], (g >> 1) & 1, &abort_s)) return false;
-          tmem_after();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t at = (k >> 2) * kRwHalf + (k & 3) * 32;
-            mma_ss(tmem + w * 128, rw_desc(q_at + at), rw_desc(k_at + w * kRwTile + at), k > 0);
-          }
-          mma_commit(&sy.sfull[w]);
-          mma_commit(&sy.kempty[w]);
-          return true;
-        };
-        // O += P V of a step's first and then second 64 tokens, each as soon as its weights are there
-        auto pv = [&](int g) {
-          const int w = g & 1;
-          if (!rows_wait(&sy.vfull[w], (g >> 1) & 1, &abort_s)) return false;
-          const uint64_t y = rw_desc(v_at + w * kRwTile);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (!rows_wait(&sy.pfull[w][h], (g >> 1) & 1, &abort_s)) return false;
-            tmem_after();
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(tmem + 256 + w * 128, tmem + w * 128 + 32 * h + 8 * k, y + ((h * kRwHalf + k * 32) >> 4), g - done >= 2 || h > 0 || k > 0);
-            mma_commit(&sy.odone[w][h]);
-          }
-          mma_commit(&sy.vempty[w]);
-          return true;
-        };
-        const int end = done + steps;
-        bool ok = qk(done) && (steps < 2 || qk(done + 1));
-        for (int g = done; ok && g < end; ++g) ok = pv(g) && (g + 2 >= end || qk(g + 2));
-      }
-      __syncwarp();
-    } else {
-      // ---------------------------------------------------------------- softmax
-      // Four warps take the even steps, four the odd ones; both hold all rows,
-      // each with a reference, a total and an accumulator of its own.
-      const int w = warp >> 2;
-      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t s_at = tmem + lanes + w * 128, o_at = tmem + lanes + 256 + w * 128;
-      const bool valid = rows.at[threadIdx.x & 127] >= 0, any = __any_sync(0xffffffffu, valid);
-      const int pos = valid ? rows.pos[threadIdx.x & 127] : -1, end = done + steps;
-      const float rc = rc_s[threadIdx.x & 127];
+      const bool valid = seg.at[row] >= 0, any = __any_sync(0xffffffffu, valid);
+      const int pos = valid ? seg.pos[row] : -1;
+      const float rc = seg.rc[row];
       const int last_open = (int)__reduce_min_sync(0xffffffffu, (uint32_t)(valid ? pos + 1 : 0x7fffffff)) - kBlock;  // first token of the last whole block
+      const int end = done + Steps(seg).s1 - Steps(seg).s0;
       float ref = 0.f, l = 0.f, limit = valid ? -1.f : INFINITY;  // limit: of a block's sum of weights
       bool seen = !valid;
       bool ok = true;
@@ -413,6 +212,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_shared_rows(const __grid_cons
           }
         }
       }
+#pragma unroll 1
       for (; ok && g < end; g += 2) {
         ok = rows_wait_warp(&sy.scfull[g & 3], (g >> 2) & 1, &abort_s);
         if (!ok) break;
@@ -490,30 +290,279 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_shared_rows(const __grid_cons
         }
         l += sum;
       }
-      if (ok && any && steps > ((done ^ w) & 1)) ok = rows_wait_warp(&sy.odone[w][1], ((g - 2) >> 1) & 1, &abort_s);
-      store_part(a, seg, half_s, valid, seen, ref, l, tmem, &abort_s);
+      // the last step's product, if there was one
+      if (ok && any && end - done > ((done ^ w) & 1)) ok = rows_wait_warp(&sy.odone[w][1], ((g - 2) >> 1) & 1, &abort_s);
+      // (a row whose scores are all NaN has no reference, but l and O, which are NaN, count)
+      seg.ref[w][row] = seen ? ref : -INFINITY;
+      seg.l[w][row] = l;
+      tmem_before();
+      group_sync(1, 32 * kShSoft);
+      tmem_after();
+      {
+        const Steps st(seg);
+        if (st.s1 > st.s0 && !abort_s) {
+          store_part(a, seg, st.s1 - st.s0, done, Units(seg, st.tail).unit, tmem);
+        } else if (w == 0) {
+          float *const p = a.parts + ((int64_t)blockIdx.x + seg.p.tile) * part_floats(kRwRows) + kRwRows * kHeadDim + row;
+          p[0] = p[kRwRows] = -INFINITY;
+          p[2 * kRwRows] = 0.f;
+        }
+        done += st.s1 - st.s0;
+      }
     }
-    // the next piece's queries, scales and scores go over this one's
     tmem_before();
     __syncthreads();
-    tmem_after();
-    if (abort_s) break;
-    if (threadIdx.x == 0) {
-      seg.x += seg.units;
-      seg.done += seg.steps;
+  } else if (warp < kShIssuer) {
+    // ---------------------------------------------------------------- producers
+    registers_down<80>();
+    const int pw = warp & 3, kv = warp >= kShV;  // K's, and V's
+    while (true) {
+      __syncthreads();
+      if (threadIdx.x == 32 * kShK) {
+        seg.go = seg.x < seg.end && !abort_s;
+        if (seg.go) {
+          const Prefixes::Piece p = pre.piece(a, seg.x, seg.end);
+          if (p.u0 == 0) pre.announce(a, p, seg.x);
+          seg.p = p;
+          auto from = [&](const lkv_cache8 &c, int b) {
+            const int64_t slice = (int64_t)b * c.n_kv_heads + p.h, codes = slice * c.capacity * kHeadDim, tail = slice * kBlock * kHeadDim;
+            seg.len = held(c, b);
+            seg.codes[0] = (const uint8_t *)c.k_codes + codes;
+            seg.codes[1] = (const uint8_t *)c.v_codes + codes;
+            seg.scale[0] = c.k_scale + slice * (c.capacity / kBlock);
+            seg.scale[1] = c.v_scale + slice * (c.capacity / kBlock);
+            seg.tail[0] = (const uint16_t *)c.k_tail + tail;
+            seg.tail[1] = (const uint16_t *)c.v_tail + tail;
+          };
+          if (p.list < a.p.batch) from(a.p, p.list);
+          else from(a.c, p.list - a.p.batch);
+          seg.x += p.u1 - p.u0;
+          seg.top = seg.tail_top[0] = seg.tail_top[1] = 0;
+          seg.last = -1;
+        }
+      }
+      __syncthreads();
+      if (!seg.go) break;
+      __syncthreads();
+      const Steps z(seg);
+      const int s0 = z.s0, s1 = z.s1;
+      uint4 cr[8];
+      const uint8_t *const codes = seg.codes[kv];
+      const int tc = (pw * 32 + lane) & 15, dc = (pw * 32 + lane) >> 4;
+      // K: 4 whole rows a load, 16 codes a lane: a load takes a pass for each
+      // 128-byte line. V: tokens 8 tc.., d 16 dc.., which fills its tile without
+      // bank conflicts.
+      auto load = [&](int j) {
+        if (kv == 0) {
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const int b = j * kRwBlocks + 2 * pw + (t >> 2);
+            const uint8_t *p = codes + ((int64_t)b * kBlock + 4 * (t & 3) + (lane >> 3)) * kHeadDim + 16 * (lane & 7);
+            cr[t] = b < z.full ? __ldg((const uint4 *)p) : make_uint4(0, 0, 0, 0);
+          }
+        } else {
+          const int b = j * kRwBlocks + (tc >> 1);
+          const uint8_t *p = codes + ((int64_t)b * kBlock + 8 * (tc & 1)) * kHeadDim + 16 * dc;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) cr[i] = b < z.full ? __ldg((const uint4 *)(p + i * kHeadDim)) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      if (s1 > s0) load(s0);
+      {
+        // the unit of the V scales, and the tails with their largest values
+        const int t = threadIdx.x - 32 * kShK, stride = 32 * (kShIssuer - kShK);
+        const float *const vsc = seg.scale[1];
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int u = s0 * kRwBlocks + t; u < min(s1 * kRwBlocks, z.full); u += stride) top = max(top, __float_as_uint(vsc[u]));
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0 && top) atomicMax(&seg.top, top);
+        if (z.tail) {
+          constexpr int kRun = kBlock * kHeadDim / 8;  // 16-byte runs of a tail: as many as there are threads here
+          static_assert(kRun == 32 * (kShIssuer - kShK), "each takes a run of both");
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (t / 16 < z.tail_rows) x = *(const uint4 *)(seg.tail[k] + t * 8);
+            *(uint4 *)(tails[k] + t * 8) = x;
+            uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+            m = __reduce_max_sync(0xffffffffu, max(m << 16, m & 0xffff0000u));
+            if (lane == 0) atomicMax(&seg.tail_top[k], m);
+          }
+        }
+      }
+      __syncthreads();
+      const Units un(seg, z.tail);
+      const float tf = pow2f(kv ? -max(un.ve, un.unit - kUnitSpan) : -un.ke);
+      const int tail_at = (z.nb - 1) % kRwBlocks * kBlock;
+      for (int g = done; g < done + s1 - s0; ++g) {
+        const int j = g - done + s0, st = g & 1;
+        const bool ends = z.tail && (j + 1) * kRwBlocks >= z.nb;  // the step's last block is the partial one
+        if (!rows_wait_warp(kv ? &sy.vempty[st] : &sy.kempty[st], ((g >> 1) & 1) ^ 1, &abort_s)) break;
+        unsigned char *const to_tile = area + (1 + 2 * kv + st) * kRwTile;
+        if (kv == 0) {
+          const int kr_half = (lane >> 2) & 1, kr_run = lane & 3;
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            // a run's 16-byte chunks go to places 2 run and 2 run + 1, the second
+            // half's in the other order: 8 lanes fill 8 places of a row at a time
+            const int r = 32 * pw + 4 * t + (lane >> 3);
+            const uint4 c = kr_half ? make_uint4(cr[t].z, cr[t].w, cr[t].x, cr[t].y) : cr[t];
+            uint32_t x[8];
+            codes_row<CODE>(c.x, x[0], x[1]);
+            codes_row<CODE>(c.y, x[2], x[3]);
+            codes_row<CODE>(c.z, x[4], x[5]);
+            codes_row<CODE>(c.w, x[6], x[7]);
+            unsigned char *to = to_tile + kr_half * kRwHalf + r * 128;
+            *(uint4 *)(to + (((2 * kr_run + kr_half) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            *(uint4 *)(to + (((2 * kr_run + 1 - kr_half) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+          }
+          if (j + 1 < s1) load(j + 1);
+          if (ends) {
+            __syncwarp();  // over the zeros of the rows' own warp
+            if (pw == tail_at / 32) {
+#pragma unroll 1
+              for (int r = 0; r < z.tail_rows; ++r) {
+                const int at = tail_at + r, d = 4 * lane;
+                const uint2 x = *(const uint2 *)(tails[0] + r * kHeadDim + d);
+                const uint32_t h0 = h2_bits(__floats2half2_rn(__uint_as_float(x.x << 16) * tf, __uint_as_float(x.x & 0xffff0000u) * tf));
+                const uint32_t h1 = h2_bits(__floats2half2_rn(__uint_as_float(x.y << 16) * tf, __uint_as_float(x.y & 0xffff0000u) * tf));
+                *(uint2 *)(to_tile + (d >> 6) * kRwHalf + at * 128 + ((((d & 63) >> 3) ^ (at & 7)) << 4) + (d & 7) * 2) = make_uint2(h0, h1);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = e == 0 ? cr[i].x : e == 1 ? cr[i].y : e == 2 ? cr[i].z : cr[i].w;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t x[4], y[4];  // d = 16 dc + 4 e + 2 h and the next: 8 tokens each
+#pragma unroll
+              for (int m = 0; m < 4; ++m) codes_across<CODE>(c[2 * m], c[2 * m + 1], h, x[m], y[m]);
+              const int d = 16 * dc + 4 * e + 2 * h;
+              unsigned char *to = to_tile + (tc >> 3) * kRwHalf + d * 128;
+              *(uint4 *)(to + (((tc & 7) ^ (d & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+              *(uint4 *)(to + 128 + (((tc & 7) ^ ((d + 1) & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          }
+          if (j + 1 < s1) load(j + 1);
+          if (ends && (tc >> 1) == tail_at / kBlock) {  // this thread's 8 tokens and 16 values of d
+#pragma unroll 1
+            for (int e = 0; e < 16; ++e) {
+              const int d = 16 * dc + e, first = 8 * (tc & 1);
+              uint32_t x[4];
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                const int r = first + 2 * m;
+                const float lo = bf16_bits_to_f32(tails[1][r * kHeadDim + d]), hi = bf16_bits_to_f32(tails[1][(r + 1) * kHeadDim + d]);
+                x[m] = h2_bits(__floats2half2_rn(lo * tf, hi * tf));
+              }
+              *(uint4 *)(to_tile + (tc >> 3) * kRwHalf + d * 128 + (((tc & 7) ^ (d & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive(kv ? &sy.vfull[st] : &sy.kfull[st]);
+      }
+      done += s1 - s0;
     }
     __syncthreads();
-  }
-  if (warp == kRwIssuer) {
-    if (lane == 0) {  // every product has completed before the tensor memory is freed
-      mma_commit(&sy.drained);
-      bar_wait(&sy.drained, 0);
+  } else {
+    registers_down<48>();
+    while (true) {
+      __syncthreads();
+      __syncthreads();
+      if (!seg.go) break;
+      __syncthreads();
+      __syncthreads();
+      const Steps z(seg);
+      const int end = done + z.s1 - z.s0;
+      if (warp == kShIssuer) {
+        // -------------------------------------------------------------- products
+        if (lane == 0) {
+          tmem_after();
+          auto qk = [&](int g) {
+            const int w = g & 1;
+            if (!rows_wait(&sy.kfull[w], (g >> 1) & 1, &abort_s)) return false;
+            tmem_after();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t at = (k >> 2) * kRwHalf + (k & 3) * 32;
+              mma_ss(tmem + w * 128, rw_desc(q_at + at), rw_desc(k_at + w * kRwTile + at), k > 0);
+            }
+            mma_commit(&sy.sfull[w]);
+            mma_commit(&sy.kempty[w]);
+            return true;
+          };
+          // O += P V of a step's first and then second 64 tokens, each as soon as its weights are there
+          auto pv = [&](int g) {
+            const int w = g & 1;
+            if (!rows_wait(&sy.vfull[w], (g >> 1) & 1, &abort_s)) return false;
+            const uint64_t y = rw_desc(v_at + w * kRwTile);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!rows_wait(&sy.pfull[w][h], (g >> 1) & 1, &abort_s)) return false;
+              tmem_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts(tmem + 256 + w * 128, tmem + w * 128 + 32 * h + 8 * k, y + ((h * kRwHalf + k * 32) >> 4), g - done >= 2 || h > 0 || k > 0);
+              mma_commit(&sy.odone[w][h]);
+            }
+            mma_commit(&sy.vempty[w]);
+            mma_commit(&scempty[g & 3]);
+            return true;
+          };
+          bool ok = done == end || (qk(done) && (end - done < 2 || qk(done + 1)));
+          for (int g = done; ok && g < end; ++g) ok = pv(g) && (g + 2 >= end || qk(g + 2));
+        }
+        __syncwarp();
+      } else if (warp == kShScales) {
+        // -------------------------------------------------------------- scales
+        const Units un(seg, z.tail);
+        const float *const ksc = seg.scale[0], *const vsc = seg.scale[1];
+        float k = 0.f, v = 0.f;
+        auto load = [&](int g) {
+          const int b = (g - done + z.s0) * kRwBlocks + lane;
+          if (lane < kRwBlocks && b < z.full) {
+            k = ksc[b];
+            v = vsc[b];
+          }
+        };
+        if (end > done) load(done);
+        for (int g = done; g < end; ++g) {
+          const int b = (g - done + z.s0) * kRwBlocks + lane;
+          float4 s = make_float4(0.f, 0.f, 1.f, __int_as_float(kNoToken));
+          if (b < z.nb) {
+            const float kk = b < z.full ? k : pow2f(un.ke);
+            const float vv = b < z.full ? fmaxf(v * pow2f(-un.unit), pow2f(-kUnitSpan)) : pow2f(max(un.ve, un.unit - kUnitSpan) - un.unit);
+            s = make_float4(kk, log2f(vv), 1.f / vv, __int_as_float(b * kBlock));
+          }
+          if (g + 1 < end) load(g + 1);
+          if (!rows_wait_warp(&scempty[g & 3], ((g >> 2) & 1) ^ 1, &abort_s)) break;
+          if (lane < kRwBlocks) scales[g & 3][lane] = s;
+          __syncwarp();
+          if (lane == 0) bar_arrive(&sy.scfull[g & 3]);
+        }
+      }
+      done = end;
     }
-    __syncwarp();
+    __syncthreads();
     tmem_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_s), "r"(512) : "memory");
+    if (warp == kShIssuer) {
+      if (lane == 0) {  // every product has completed before the tensor memory is freed
+        mma_commit(&sy.drained);
+        bar_wait(&sy.drained, 0);
+        if (abort_s) atomicOr(a.c.ticket + a.c.batch, kAnomTimeout);
+      }
+      __syncwarp();
+      tmem_after();
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_s), "r"(512) : "memory");
+    }
   }
-  if (threadIdx.x == 0 && abort_s) atomicOr(a.c.ticket + a.c.batch, kAnomTimeout);
 }
 
 // Joins the parts of every row, of its prefix and of its own tokens: four rows a
@@ -572,7 +621,7 @@ cudaError_t launch_shared_rows(const SharedArgs &a, int ctas, cudaStream_t st) {
   auto *fn = a.c.code == LKV_CODE_INT8 ? k_shared_rows<LKV_CODE_INT8> : k_shared_rows<LKV_CODE_E4M3>;
   const size_t smem = kShSmem + (size_t)Prefixes::bytes(a.c.batch, a.p.batch, a.own_parts);
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  return e != cudaSuccess ? e : launch_next(fn, dim3((unsigned)ctas), kRwThreads, smem, st, a);
+  return e != cudaSuccess ? e : launch_next(fn, dim3((unsigned)ctas), kShThreads, smem, st, a);
 }
 
 cudaError_t launch_shared_join(const SharedArgs &a, cudaStream_t st) {
