@@ -418,40 +418,76 @@ __device__ __forceinline__ const lkv_cache8 &keys_of(const ArgsOf<MODE> &a) {
   else return a.c;
 }
 
-// Joins a row's result over its own tokens (o in units of 2^m, l in units of
-// 2^t) with its prefix's parts: values d and d + 1. row: of the sequence's rows.
-__device__ __forceinline__ void join_prefix(const SharedArgs &a, int64_t slice, int row, int d, float2 &o, float &l, float &m, float &t) {
-  const int b = (int)(slice / a.c.n_kv_heads), h = (int)(slice % a.c.n_kv_heads);
-  const int4 sq = a.seq[b];
-  const int per = a.n * a.group;
-  if (sq.x < 0 || row >= per) return;
-  const int64_t pr = (int64_t)sq.y * per + row;
-  const int tile = sq.x + (int)(pr / a.part_rows) * a.c.n_kv_heads + h, rr = (int)(pr % a.part_rows);
-  const int2 who = a.tile[tile];
-  const int rows = a.part_rows;
-  const float *part = a.parts + ((int64_t)who.x + tile) * part_floats(rows);
-  float top = m, topt = t;
-#pragma unroll 4
-  for (int j = 0; j < who.y; ++j) {
-    const float *p = part + (int64_t)j * part_floats(rows) + rows * kHeadDim + rr;
-    top = fmaxf(top, p[0]);
-    topt = fmaxf(topt, p[rows]);
-  }
-  const float f = share(m, top);
-  o.x = f == 0.f ? 0.f : o.x * f;
-  o.y = f == 0.f ? 0.f : o.y * f;
-  l *= share(t, topt);
-#pragma unroll 4
-  for (int j = 0; j < who.y; ++j) {
-    const float *p = part + (int64_t)j * part_floats(rows) + rows * kHeadDim + rr;
-    const float g = share(p[0], top);
-    const float2 x = *(const float2 *)(part + (int64_t)j * part_floats(rows) + (d >> 2) * 4 * rows + 4 * rr + (d & 2));
-    l += share(p[rows], topt) * p[2 * rows];
-    if (g != 0.f) {  // a part that saw nothing holds anything
-      o.x += g * x.x;
-      o.y += g * x.y;
+// What the prefix adds to a sequence's rows.
+template <int RT>
+struct PrefixSum {
+  float o[RT][kHeadDim];             // in units of 2^m
+  float m[RT], t[RT], l[RT];         // l in units of 2^t
+};
+
+// Row `row` of the sequence's (slice: sequence and KV head): the sum of its
+// prefix's parts, by a warp, into r of z. All but where the parts are is read at
+// once: the factors by a lane a part, the values by a lane four of d.
+template <int RT>
+__device__ __forceinline__ void sum_prefix(const SharedArgs &a, int64_t slice, int row, PrefixSum<RT> &z, int r, int lane) {
+  const int b = (int)((uint32_t)slice / (uint32_t)a.c.n_kv_heads), h = (int)((uint32_t)slice % (uint32_t)a.c.n_kv_heads);
+  const int per = a.n * a.group, rows = a.part_rows;
+  const int4 sq = row < per ? a.seq[b] : make_int4(-1, 0, 0, 0);
+  float top = -INFINITY, topt = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (sq.x >= 0) {
+    const int64_t pr = (int64_t)sq.y * per + row, rt = quotient(pr, rows);
+    const int tile = sq.x + (int)rt * a.c.n_kv_heads + h, rr = (int)(pr - rt * rows);
+    const int2 who = a.tile[tile];
+    const float *const part = a.parts + ((int64_t)who.x + tile) * part_floats(rows);
+    auto at = [&](int j) { return part + (int64_t)j * part_floats(rows); };
+    for (int j = lane; j < who.y; j += 32) {
+      top = fmaxf(top, at(j)[rows * kHeadDim + rr]);
+      topt = fmaxf(topt, at(j)[rows * (kHeadDim + 1) + rr]);
     }
+#pragma unroll
+    for (int d = 16; d; d /= 2) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      topt = fmaxf(topt, __shfl_xor_sync(0xffffffffu, topt, d));
+    }
+    for (int j0 = 0; j0 < who.y; j0 += 32) {
+      float f = 0.f;
+      if (j0 + lane < who.y) {
+        const float *p = at(j0 + lane) + rows * kHeadDim + rr;
+        f = share(p[0], top);
+        l += share(p[rows], topt) * p[2 * rows];
+      }
+      const int some = min(32, who.y - j0);
+#pragma unroll 8
+      for (int j = 0; j < some; ++j) {
+        const float g = __shfl_sync(0xffffffffu, f, j);
+        const float4 x = *(const float4 *)(at(j0 + j) + lane * 4 * rows + 4 * rr);
+        if (g != 0.f) {  // a part that saw nothing holds anything
+          o.x += g * x.x;
+          o.y += g * x.y;
+          o.z += g * x.z;
+          o.w += g * x.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
   }
+  *(float4 *)&z.o[r][4 * lane] = o;
+  if (lane == 0) {
+    z.m[r] = top;
+    z.t[r] = topt;
+    z.l[r] = l;
+  }
+}
+
+// A row's own result (o in units of 2^m, l of 2^t) and its prefix's, values d and d + 1.
+template <int RT>
+__device__ __forceinline__ void add_prefix(const PrefixSum<RT> &z, int r, int d, float2 &o, float &l, float &m, float &t) {
+  const float top = fmaxf(m, z.m[r]), topt = fmaxf(t, z.t[r]), f = share(m, top), g = share(z.m[r], top);
+  o.x = (f == 0.f ? 0.f : f * o.x) + (g == 0.f ? 0.f : g * z.o[r][d]);
+  o.y = (f == 0.f ? 0.f : f * o.y) + (g == 0.f ? 0.f : g * z.o[r][d + 1]);
+  l = share(t, topt) * l + share(z.t[r], topt) * z.l[r];
   m = top;
   t = topt;
 }
@@ -516,6 +552,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
   const int parts = streamed ? 1 : (int)cluster_size(), part = streamed ? 0 : (int)cluster_rank();
   const int G = MODE == kPrefix ? c.batch : c.batch * a.row_tiles;
   // the prefixes' tables lie behind what the rings and merges use
+  [[maybe_unused]] __shared__ __align__(16) std::conditional_t<MODE == kOwn, PrefixSum<RT>, int> prefix;
   constexpr int kUsed = (int)sizeof(Sm) > kRingBytes ? (int)sizeof(Sm) : kRingBytes;
   static_assert(kUsed % 8 == 0, "the tables begin with 8-byte words");
   [[maybe_unused]] Prefixes pre(area + kUsed, MODE == kPrefix ? a.c.batch : 0, MODE == kPrefix ? G : 0, MODE == kPrefix ? G : 0);
@@ -629,6 +666,10 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(kt + at));
         asm volatile("prefetch.global.L2 [%0];" ::"l"(vt + at));
       }
+
+    // while the first copies are on their way; a CTA of a cluster takes the rows that it will write
+    if constexpr (MODE == kOwn)
+      for (int row = part + parts * wid; row < RT; row += parts * kAtWarps) sum_prefix(a, slice, r0 + row, prefix, row, w.lane);
 
     const float *ksc = c.k_scale + slice * (c.capacity / kBlock), *vsc = c.v_scale + slice * (c.capacity / kBlock);
     // the scales of the warp's turns, 16 turns ahead
@@ -800,7 +841,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
         *(float2 *)(slot + (p >> 1) * 4 * RT + 4 * row + 2 * (p & 1)) = s;
       } else if (whole) {
         float m = sm.pm[row], t = sm.pt[row], l = sm.pl[row];
-        if constexpr (MODE == kOwn) join_prefix(a, slice, r0 + row, 2 * p, s, l, m, t);
+        if constexpr (MODE == kOwn) add_prefix(prefix, row, 2 * p, s, l, m, t);
         put_out<DT>(a, slice, tile.cnt, r0 + row, 2 * p, s, l, m - t);
       } else {
         *(float2 *)(slot ? slot + row * kHeadDim + 2 * p : &sm.part[row][2 * p]) = s;
@@ -820,8 +861,10 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
     }
     if (whole) return;
     cluster_barrier();
-    for (int it = threadIdx.x + part * kAtThreads; it < RT * 64; it += parts * kAtThreads) {
-      const int row = it >> 6, p = it & 63;
+    const int step = MODE == kOwn ? kAtThreads : parts * kAtThreads;
+    for (int it = threadIdx.x + (MODE == kOwn ? 0 : part * kAtThreads);; it += step) {
+      const int row = MODE == kOwn ? (it >> 6) * parts + part : it >> 6, p = it & 63;
+      if (row >= RT) break;
       float m[kAtMaxCluster], mt[kAtMaxCluster], top = -INFINITY, topt = -INFINITY, l = 0.f;
 #pragma unroll
       for (int j = 0; j < kAtMaxCluster; ++j) {
@@ -841,7 +884,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
         s.x += f * x2.x;
         s.y += f * x2.y;
       }
-      if constexpr (MODE == kOwn) join_prefix(a, slice, r0 + row, 2 * p, s, l, top, topt);
+      if constexpr (MODE == kOwn) add_prefix(prefix, row, 2 * p, s, l, top, topt);
       put_out<DT>(a, slice, tile.cnt, r0 + row, 2 * p, s, l, top - topt);
     }
     cluster_barrier();  // no CTA leaves while another reads its shared memory

@@ -152,6 +152,7 @@ extern "C" lkv_status lkv_cache8_attend_shared(const lkv_cache8 *c, const lkv_ca
   a.row_tiles = s.row_tiles;
   a.part_rows = 8 * s.nt;
   a.part_blocks = s.nt == 16 ? kSharedStep / kBlock : 1;
+  a.start_units = s.nt == 16 ? kSharedStart : 0;
   a.least_units = s.nt == 16 ? 2 : 16;
   a.own_parts = s.own_parts;
   a.seq = (int4 *)((char *)workspace + s.seq_at);

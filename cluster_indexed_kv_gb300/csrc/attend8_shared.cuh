@@ -21,6 +21,7 @@ struct SharedArgs : AttendArgs {
   lkv_cache8 p;               // the prefixes
   const int32_t *prefix_of;   // null: all of prefix 0
   int32_t part_rows, part_blocks;
+  int32_t start_units;        // that stand for what beginning a tile costs, before those of its blocks
   int32_t least_units;        // that a CTA takes, at least
   int32_t own_parts;          // whether the sequences' own tokens are parts too
   int4 *seq;                  // [batch]: the first tile of the sequence's prefix (-1: none), its place behind that prefix, its own first tile (-1: none)
@@ -99,7 +100,7 @@ struct Prefixes {
           const int e = e0 + lane;
           const int len = e < lists ? (int)at[e + 1] : 0, have = e < G ? nu[e] : len > 0;  // tokens, and sequences that see them
           const int rt = (int)quotient((int64_t)have * a.n * a.group + a.part_rows - 1, a.part_rows);
-          const int run = a.part_blocks * kBlock, per = (int)((uint32_t)(len + run - 1) / (uint32_t)run);
+          const int run = a.part_blocks * kBlock, per = a.start_units + (int)((uint32_t)(len + run - 1) / (uint32_t)run);
           int64_t u = (int64_t)rt * a.c.n_kv_heads * per;
           int t = rt * a.c.n_kv_heads, s = e < G ? have : 0;
           const int mine = s;
@@ -158,7 +159,7 @@ struct Prefixes {
     x1 = blockIdx.x < P ? quotient(total * (blockIdx.x + 1), P) : 0;
   }
   // a piece of unit x's tile: up to unit x1 of the row
-  struct Piece { int list, h, rt, tile, u0, u1; };
+  struct Piece { int list, h, rt, tile, u0, u1; };  // u0, u1: of its units, the start's among them
   __device__ __forceinline__ Piece piece(const SharedArgs &a, int64_t x, int64_t x1) const {
     int lo = 0, hi = lists;
     while (hi - lo > 1) {
@@ -204,6 +205,7 @@ __device__ __forceinline__ ListRow list_row(const SharedArgs &a, const Prefixes 
 // The kernel for many rows of bf16 caches and the join of what it leaves
 // (attend8_shared_rows.cu): row tiles of kSharedRows, units of kSharedStep tokens.
 constexpr int kSharedRows = 128, kSharedStep = 128;
+constexpr int kSharedStart = 4;  // steps' time that beginning a tile costs
 cudaError_t launch_shared_rows(const SharedArgs &a, int ctas, cudaStream_t st);
 cudaError_t launch_shared_join(const SharedArgs &a, cudaStream_t st);
 
