@@ -17,6 +17,27 @@ template <int N>
 __device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+// Products with shared-memory operands by the low words of their descriptors
+// (the address in 16-byte units): K-major as rw_desc, and V as it lies in the
+// cache, d along a row of 64 (128-byte swizzle), 8 tokens 1 KB and the other 64
+// values of d kRwHalf apart.
+constexpr uint32_t kShHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kShIdescV = kRwIdesc | (1u << 16);
+__device__ __forceinline__ void mma_ss2(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+               " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}"
+               ::"r"(d), "r"(a | (1u << 16)), "r"(b | (1u << 16)), "r"(kShHi), "r"(kRwIdesc), "r"(acc));
+}
+__device__ __forceinline__ void mma_ts2(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+               " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}"
+               ::"r"(d), "r"(a), "r"(b | ((kRwHalf >> 4) << 16)), "r"(kShHi), "r"(kShIdescV), "r"(acc));
+}
 __device__ __forceinline__ void group_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 // What a CTA is at.
@@ -105,7 +126,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
   const uint32_t base = (smem_at(raw) + 1023u) & ~1023u;
   unsigned char *const area = raw + (base - smem_at(raw));
   const uint32_t q_at = base, k_at = base + kRwTile, v_at = base + 3 * kRwTile;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // the warp: uniform for the compiler too
   const Prefixes pre(area + 5 * kRwTile, a.c.batch, a.p.batch, a.p.batch + (a.own_parts ? a.c.batch : 0));
 
   if (threadIdx.x == 0) {
@@ -347,24 +368,13 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       const Steps z(seg);
       const int s0 = z.s0, s1 = z.s1;
       uint4 cr[8];
-      const uint8_t *const codes = seg.codes[kv];
-      const int tc = (pw * 32 + lane) & 15, dc = (pw * 32 + lane) >> 4;
-      // K: 4 whole rows a load, 16 codes a lane: a load takes a pass for each
-      // 128-byte line. V: tokens 8 tc.., d 16 dc.., which fills its tile without
-      // bank conflicts.
+      const uint8_t *const codes = seg.codes[kv] + (32 * pw + (lane >> 3)) * kHeadDim + 16 * (lane & 7);
+      // 4 whole rows a load, 16 codes a lane: a load takes a pass for each 128-byte line
       auto load = [&](int j) {
-        if (kv == 0) {
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const int b = j * kRwBlocks + 2 * pw + (t >> 2);
-            const uint8_t *p = codes + ((int64_t)b * kBlock + 4 * (t & 3) + (lane >> 3)) * kHeadDim + 16 * (lane & 7);
-            cr[t] = b < z.full ? __ldg((const uint4 *)p) : make_uint4(0, 0, 0, 0);
-          }
-        } else {
-          const int b = j * kRwBlocks + (tc >> 1);
-          const uint8_t *p = codes + ((int64_t)b * kBlock + 8 * (tc & 1)) * kHeadDim + 16 * dc;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) cr[i] = b < z.full ? __ldg((const uint4 *)(p + i * kHeadDim)) : make_uint4(0, 0, 0, 0);
+        for (int t = 0; t < 8; ++t) {
+          const int b = j * kRwBlocks + 2 * pw + (t >> 2);
+          cr[t] = b < z.full ? __ldg((const uint4 *)(codes + ((int64_t)j * kRwTok + 4 * t) * kHeadDim)) : make_uint4(0, 0, 0, 0);
         }
       };
       if (s1 > s0) load(s0);
@@ -400,67 +410,33 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
         const bool ends = z.tail && (j + 1) * kRwBlocks >= z.nb;  // the step's last block is the partial one
         if (!rows_wait_warp(kv ? &sy.vempty[st] : &sy.kempty[st], ((g >> 1) & 1) ^ 1, &abort_s)) break;
         unsigned char *const to_tile = area + (1 + 2 * kv + st) * kRwTile;
-        if (kv == 0) {
-          const int kr_half = (lane >> 2) & 1, kr_run = lane & 3;
+        const int half = (lane >> 2) & 1, run = lane & 3;
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            // a run's 16-byte chunks go to places 2 run and 2 run + 1, the second
-            // half's in the other order: 8 lanes fill 8 places of a row at a time
-            const int r = 32 * pw + 4 * t + (lane >> 3);
-            const uint4 c = kr_half ? make_uint4(cr[t].z, cr[t].w, cr[t].x, cr[t].y) : cr[t];
-            uint32_t x[8];
-            codes_row<CODE>(c.x, x[0], x[1]);
-            codes_row<CODE>(c.y, x[2], x[3]);
-            codes_row<CODE>(c.z, x[4], x[5]);
-            codes_row<CODE>(c.w, x[6], x[7]);
-            unsigned char *to = to_tile + kr_half * kRwHalf + r * 128;
-            *(uint4 *)(to + (((2 * kr_run + kr_half) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-            *(uint4 *)(to + (((2 * kr_run + 1 - kr_half) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
-          }
-          if (j + 1 < s1) load(j + 1);
-          if (ends) {
-            __syncwarp();  // over the zeros of the rows' own warp
-            if (pw == tail_at / 32) {
+        for (int t = 0; t < 8; ++t) {
+          // a run's 16-byte chunks go to places 2 run and 2 run + 1, the second
+          // half's in the other order: 8 lanes fill 8 places of a row at a time
+          const int r = 32 * pw + 4 * t + (lane >> 3);
+          const uint4 c = half ? make_uint4(cr[t].z, cr[t].w, cr[t].x, cr[t].y) : cr[t];
+          uint32_t x[8];
+          codes_row<CODE>(c.x, x[0], x[1]);
+          codes_row<CODE>(c.y, x[2], x[3]);
+          codes_row<CODE>(c.z, x[4], x[5]);
+          codes_row<CODE>(c.w, x[6], x[7]);
+          unsigned char *to = to_tile + half * kRwHalf + r * 128;
+          *(uint4 *)(to + (((2 * run + half) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+          *(uint4 *)(to + (((2 * run + 1 - half) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+        }
+        if (j + 1 < s1) load(j + 1);
+        if (ends) {
+          __syncwarp();  // over the zeros of the rows' own warp
+          if (pw == tail_at / 32) {
 #pragma unroll 1
-              for (int r = 0; r < z.tail_rows; ++r) {
-                const int at = tail_at + r, d = 4 * lane;
-                const uint2 x = *(const uint2 *)(tails[0] + r * kHeadDim + d);
-                const uint32_t h0 = h2_bits(__floats2half2_rn(__uint_as_float(x.x << 16) * tf, __uint_as_float(x.x & 0xffff0000u) * tf));
-                const uint32_t h1 = h2_bits(__floats2half2_rn(__uint_as_float(x.y << 16) * tf, __uint_as_float(x.y & 0xffff0000u) * tf));
-                *(uint2 *)(to_tile + (d >> 6) * kRwHalf + at * 128 + ((((d & 63) >> 3) ^ (at & 7)) << 4) + (d & 7) * 2) = make_uint2(h0, h1);
-              }
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t c[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = e == 0 ? cr[i].x : e == 1 ? cr[i].y : e == 2 ? cr[i].z : cr[i].w;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t x[4], y[4];  // d = 16 dc + 4 e + 2 h and the next: 8 tokens each
-#pragma unroll
-              for (int m = 0; m < 4; ++m) codes_across<CODE>(c[2 * m], c[2 * m + 1], h, x[m], y[m]);
-              const int d = 16 * dc + 4 * e + 2 * h;
-              unsigned char *to = to_tile + (tc >> 3) * kRwHalf + d * 128;
-              *(uint4 *)(to + (((tc & 7) ^ (d & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-              *(uint4 *)(to + 128 + (((tc & 7) ^ ((d + 1) & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-          }
-          if (j + 1 < s1) load(j + 1);
-          if (ends && (tc >> 1) == tail_at / kBlock) {  // this thread's 8 tokens and 16 values of d
-#pragma unroll 1
-            for (int e = 0; e < 16; ++e) {
-              const int d = 16 * dc + e, first = 8 * (tc & 1);
-              uint32_t x[4];
-#pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                const int r = first + 2 * m;
-                const float lo = bf16_bits_to_f32(tails[1][r * kHeadDim + d]), hi = bf16_bits_to_f32(tails[1][(r + 1) * kHeadDim + d]);
-                x[m] = h2_bits(__floats2half2_rn(lo * tf, hi * tf));
-              }
-              *(uint4 *)(to_tile + (tc >> 3) * kRwHalf + d * 128 + (((tc & 7) ^ (d & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            for (int r = 0; r < z.tail_rows; ++r) {
+              const int at = tail_at + r, d = 4 * lane;
+              const uint2 x = *(const uint2 *)(tails[kv] + r * kHeadDim + d);
+              const uint32_t h0 = h2_bits(__floats2half2_rn(__uint_as_float(x.x << 16) * tf, __uint_as_float(x.x & 0xffff0000u) * tf));
+              const uint32_t h1 = h2_bits(__floats2half2_rn(__uint_as_float(x.y << 16) * tf, __uint_as_float(x.y & 0xffff0000u) * tf));
+              *(uint2 *)(to_tile + (d >> 6) * kRwHalf + at * 128 + ((((d & 63) >> 3) ^ (at & 7)) << 4) + (d & 7) * 2) = make_uint2(h0, h1);
             }
           }
         }
@@ -483,43 +459,54 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       const int end = done + z.s1 - z.s0;
       if (warp == kShIssuer) {
         // -------------------------------------------------------------- products
-        if (lane == 0) {
+        // The whole warp goes along, one lane issues: descriptors and addresses stay
+        // in uniform registers (a lane on its own took 1900 clocks a step to issue).
+        const int first = __shfl_sync(0xffffffffu, done, 0), stop = __shfl_sync(0xffffffffu, end, 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t q_lo = q_at >> 4, k_lo = k_at >> 4, v_lo = v_at >> 4;
+        const bool one = elect_one();
+        tmem_after();
+        auto qk = [&](int g) {
+          const int w = g & 1;
+          if (!rows_wait_warp(&sy.kfull[w], (g >> 1) & 1, &abort_s)) return false;
           tmem_after();
-          auto qk = [&](int g) {
-            const int w = g & 1;
-            if (!rows_wait(&sy.kfull[w], (g >> 1) & 1, &abort_s)) return false;
-            tmem_after();
+          if (one) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const uint32_t at = (k >> 2) * kRwHalf + (k & 3) * 32;
-              mma_ss(tmem + w * 128, rw_desc(q_at + at), rw_desc(k_at + w * kRwTile + at), k > 0);
+              const uint32_t at = ((k >> 2) * kRwHalf + (k & 3) * 32) >> 4;
+              mma_ss2(tm + w * 128, q_lo + at, k_lo + w * (kRwTile >> 4) + at, k > 0);
             }
             mma_commit(&sy.sfull[w]);
             mma_commit(&sy.kempty[w]);
-            return true;
-          };
-          // O += P V of a step's first and then second 64 tokens, each as soon as its weights are there
-          auto pv = [&](int g) {
-            const int w = g & 1;
-            if (!rows_wait(&sy.vfull[w], (g >> 1) & 1, &abort_s)) return false;
-            const uint64_t y = rw_desc(v_at + w * kRwTile);
+          }
+          __syncwarp();
+          return true;
+        };
+        // O += P V of a step's first and then second 64 tokens, each as soon as its weights are there
+        auto pv = [&](int g) {
+          const int w = g & 1;
+          if (!rows_wait_warp(&sy.vfull[w], (g >> 1) & 1, &abort_s)) return false;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!rows_wait(&sy.pfull[w][h], (g >> 1) & 1, &abort_s)) return false;
-              tmem_after();
+          for (int h = 0; h < 2; ++h) {
+            if (!rows_wait_warp(&sy.pfull[w][h], (g >> 1) & 1, &abort_s)) return false;
+            tmem_after();
+            if (one) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_ts(tmem + 256 + w * 128, tmem + w * 128 + 32 * h + 8 * k, y + ((h * kRwHalf + k * 32) >> 4), g - done >= 2 || h > 0 || k > 0);
+                mma_ts2(tm + 256 + w * 128, tm + w * 128 + 32 * h + 8 * k, v_lo + w * (kRwTile >> 4) + (4 * h + k) * (16 * 128 >> 4),
+                        g - first >= 2 || h > 0 || k > 0);
               mma_commit(&sy.odone[w][h]);
+              if (h) {
+                mma_commit(&sy.vempty[w]);
+                mma_commit(&scempty[g & 3]);
+              }
             }
-            mma_commit(&sy.vempty[w]);
-            mma_commit(&scempty[g & 3]);
-            return true;
-          };
-          bool ok = done == end || (qk(done) && (end - done < 2 || qk(done + 1)));
-          for (int g = done; ok && g < end; ++g) ok = pv(g) && (g + 2 >= end || qk(g + 2));
-        }
-        __syncwarp();
+            __syncwarp();
+          }
+          return true;
+        };
+        bool ok = first == stop || (qk(first) && (stop - first < 2 || qk(first + 1)));
+        for (int g = first; ok && g < stop; ++g) ok = pv(g) && (g + 2 >= stop || qk(g + 2));
       } else if (warp == kShScales) {
         // -------------------------------------------------------------- scales
         const Units un(seg, z.tail);
