@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
       if (threadIdx.x == 0 && piece.u0 == 0) pre.announce(a, piece, x);
       rt = piece.rt;
       slice = (int64_t)piece.list * c.n_kv_heads + piece.h;
-      tile.len = pre.len[piece.list];
+      tile.len = held(c, piece.list);
       tile.lo = tile.sb = tile.cnt = 0;
       tile.hi = (tile.len - 1) / kBlock;
       tile.nb = tile.hi + 1;

@@ -40,35 +40,34 @@ __device__ __forceinline__ void mma_ts2(uint32_t d, uint32_t a, uint32_t b, uint
 }
 __device__ __forceinline__ void group_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-// What warps of a piece tell one another.
+// What a CTA is at.
 struct SharedPiece {
-  // for the softmax's warps, which have no registers left for these: the piece's
-  // tile, how many steps, whether the partial block is in it, and where the next piece begins
-  int64_t next;
-  int tile, steps, tail;
+  Prefixes::Piece p;
+  int64_t x, end;             // of the row of units: where the CTA is, and its end
+  const uint8_t *codes[2];    // the list's cache: K's and V's codes, scales and tails of the KV head
+  const float *scale[2];
+  const uint16_t *tail[2];
+  int len;
+  int go;                     // whether there is a piece
   int last;                   // the last token that a row sees
   uint32_t top, tail_top[2];  // largest V scale of the piece's blocks, largest magnitudes of the tails (bits)
   int64_t at[kRwRows];        // the rows' queries, -1 for none
   int pos[kRwRows];           // the last token that a row sees
   float rc[kRwRows];          // query unit * scale * log2(e)
   float ref[2][kRwRows], l[2][kRwRows];  // references and totals of the even and odd steps
-  __device__ __forceinline__ void clear() {
-    last = -1;
-    top = tail_top[0] = tail_top[1] = 0;
-  }
 };
 
 // A piece's steps and units, as every warp forms them.
 struct Steps {
   int s0, s1, nb, full, tail_rows;
   bool tail;  // the partial block is among them, as the last
-  __device__ __forceinline__ Steps(const Prefixes::Piece &p, int len, int last) {
-    nb = (len + kBlock - 1) / kBlock;
-    full = len / kBlock;
-    tail_rows = len - full * kBlock;
+  __device__ __forceinline__ explicit Steps(const SharedPiece &p) {
+    nb = (p.len + kBlock - 1) / kBlock;
+    full = p.len / kBlock;
+    tail_rows = p.len - full * kBlock;
     // steps behind the last token that a row sees are nobody's
-    s0 = max(p.u0 - kSharedStart, 0);
-    s1 = max(min(p.u1 - kSharedStart, (last + kRwTok) / kRwTok), s0);
+    s0 = max(p.p.u0 - kSharedStart, 0);
+    s1 = max(min(p.p.u1 - kSharedStart, (p.last + kRwTok) / kRwTok), s0);
     tail = s1 > s0 && full < nb && s1 * kRwBlocks >= nb;
   }
 };
@@ -84,11 +83,11 @@ struct Units {
 
 // What both halves of the softmax have of a row goes into the piece's part: each
 // half's threads write 64 of the values of d.
-__device__ __forceinline__ void store_part(const SharedArgs &a, const SharedPiece &z, int tile, int steps, int done, int unit, uint32_t tmem) {
+__device__ __forceinline__ void store_part(const SharedArgs &a, const SharedPiece &z, int steps, int done, int unit, uint32_t tmem) {
   const int w = threadIdx.x >> 7, r = threadIdx.x & 127;
   const bool valid = z.at[r] >= 0, has0 = steps > 1 || (done & 1) == 0, has1 = steps > 1 || (done & 1) == 1;
   if (!__any_sync(0xffffffffu, valid)) return;
-  float *const part = a.parts + ((int64_t)blockIdx.x + tile) * part_floats(kRwRows);
+  float *const part = a.parts + ((int64_t)blockIdx.x + z.p.tile) * part_floats(kRwRows);
   const float m0 = valid && has0 ? z.ref[0][r] : -INFINITY, m1 = valid && has1 ? z.ref[1][r] : -INFINITY;
   const float top = fmaxf(m0, m1), f0 = share(m0, top), f1 = share(m1, top);
   const uint32_t o0 = tmem + ((uint32_t)(r & 96) << 16) + 256 + 64 * w, o1 = o0 + 128;
@@ -123,12 +122,12 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
   __shared__ uint32_t tmem_s;
   __shared__ volatile int abort_s;
   __shared__ __align__(16) uint16_t tails[2][kBlock * kHeadDim];  // K's and V's partial block, zeros behind its rows
-  __shared__ SharedPiece pieces[2];        // by turns
+  __shared__ SharedPiece seg;
   const uint32_t base = (smem_at(raw) + 1023u) & ~1023u;
   unsigned char *const area = raw + (base - smem_at(raw));
   const uint32_t q_at = base, k_at = base + kRwTile, v_at = base + 3 * kRwTile;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // the warp: uniform for the compiler too
-  Prefixes pre(area + 5 * kRwTile, a.c.batch, a.p.batch, a.p.batch + (a.own_parts ? a.c.batch : 0));
+  const Prefixes pre(area + 5 * kRwTile, a.c.batch, a.p.batch, a.p.batch + (a.own_parts ? a.c.batch : 0));
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -149,26 +148,24 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
     bar_init(&sy.drained, 1);
     bar_init_fence();
     abort_s = 0;
-    pieces[0].clear();
   }
+  wait_prerequisites();
+  launch_dependents();
   if (warp == kShIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_at(&tmem_s)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  wait_prerequisites();
-  launch_dependents();
-  pre.fill(a);
-  int64_t x, x_end;  // the CTA's share of the row of units, and where it is
-  pre.share(a, x, x_end);
+  const_cast<Prefixes &>(pre).fill(a);
+  if (threadIdx.x == 32 * kShK) pre.share(a, seg.x, seg.end);
   tmem_before();
   __syncthreads();
   tmem_after();
   const uint32_t tmem = tmem_s;
   int done = 0;  // steps of earlier pieces: the barriers' phases go on
 
-  // Every warp finds the pieces by itself and passes the same three barriers a
-  // piece: (1) the piece before is done with, (2) its rows are known, (3)
-  // queries, units and tails are in place. Then each has its part of the steps.
+  // Every warp passes the same four barriers a piece: (1) the piece before is
+  // done with, (2) the piece is named, (3) its rows are, (4) queries, units and
+  // tails are in place. Then each has its part of the steps.
   if (warp < kShSoft) {
     // ---------------------------------------------------------------- softmax
     registers_up<136>();
@@ -177,62 +174,52 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
     const int w = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + w * 128, o_at = tmem + lanes + 256 + w * 128;
-    for (int turn = 0; x < x_end; turn ^= 1) {
-      SharedPiece &seg = pieces[turn];
-      const Prefixes::Piece piece = pre.piece(a, x, x_end);
-      const int len = pre.len[piece.list];
-      x += piece.u1 - piece.u0;
-      // 16 rows a warp, 16 lanes a row
-      const int half = lane >> 4, run = lane & 15, r16 = warp * 16 + run;
-      const ListRow mine = list_row(a, pre, piece.list, piece.h, len, (int64_t)piece.rt * kRwRows + r16);
-      uint4 q[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t at = __shfl_sync(0xffffffffu, mine.at, 2 * k + half);
-        q[k] = at >= 0 ? *(const uint4 *)((const uint16_t *)a.q + at * kHeadDim + 8 * run) : make_uint4(0, 0, 0, 0);
+    while (true) {
+      __syncthreads();
+      __syncthreads();
+      if (!seg.go) break;
+      if (w == 0) {
+        const ListRow x = list_row(a, pre, seg.p.list, seg.p.h, seg.len, (int64_t)seg.p.rt * kRwRows + row);
+        seg.at[row] = x.at;
+        seg.pos[row] = x.pos;
+        const int top = __reduce_max_sync(0xffffffffu, x.at < 0 ? -1 : x.pos);
+        if (lane == 0 && top >= 0) atomicMax(&seg.last, top);
       }
       __syncthreads();
-      if (abort_s) break;
-      if (half == 0) {
-        seg.at[r16] = mine.at;
-        seg.pos[r16] = mine.pos;
-      }
-      const int top = __reduce_max_sync(0xffffffffu, mine.at < 0 ? -1 : mine.pos);
-      if (lane == 0 && top >= 0) atomicMax(&seg.last, top);
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        const Steps z(piece, len, seg.last);
-        pieces[turn ^ 1].clear();
-        seg.next = x;
-        seg.tile = piece.tile;
-        seg.steps = z.s1 - z.s0;
-        seg.tail = z.tail;
-      }
-      // queries as fp16 in units of a power of two into the swizzled tile
+      {
+        // queries as fp16 in units of a power of two into the swizzled tile, 16 lanes a row, 16 rows a warp
+        const int half = lane >> 4, run = lane & 15;
+        uint4 q[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int rr = warp * 16 + 2 * k + half;
-        uint32_t m = __vmaxu2(__vmaxu2(q[k].x & 0x7fff7fffu, q[k].y & 0x7fff7fffu), __vmaxu2(q[k].z & 0x7fff7fffu, q[k].w & 0x7fff7fffu));
+        for (int k = 0; k < 8; ++k) {
+          const int64_t at = seg.at[warp * 16 + 2 * k + half];
+          q[k] = at >= 0 ? *(const uint4 *)((const uint16_t *)a.q + at * kHeadDim + 8 * run) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-        for (int d = 8; d > 0; d /= 2) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const int e = exponent_of(max(m << 16, m & 0xffff0000u));
-        const float f = pow2f(-e);
-        if (run == 0) seg.rc[rr] = pow2f(e) * a.scale_log2;
-        const uint32_t v[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
-        uint32_t h[4];
+        for (int k = 0; k < 8; ++k) {
+          const int rr = warp * 16 + 2 * k + half;
+          uint32_t m = __vmaxu2(__vmaxu2(q[k].x & 0x7fff7fffu, q[k].y & 0x7fff7fffu), __vmaxu2(q[k].z & 0x7fff7fffu, q[k].w & 0x7fff7fffu));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          h[i] = h2_bits(__floats2half2_rn(__uint_as_float(v[i] << 16) * f, __uint_as_float(v[i] & 0xffff0000u) * f));
-        unsigned char *to = area + (run >> 3) * kRwHalf + rr * 128;
-        *(uint4 *)(to + (((run & 7) ^ (rr & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          for (int d = 8; d > 0; d /= 2) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+          const int e = exponent_of(max(m << 16, m & 0xffff0000u));
+          const float f = pow2f(-e);
+          if (run == 0) seg.rc[rr] = pow2f(e) * a.scale_log2;
+          const uint32_t x[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+          uint32_t h[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            h[v] = h2_bits(__floats2half2_rn(__uint_as_float(x[v] << 16) * f, __uint_as_float(x[v] & 0xffff0000u) * f));
+          unsigned char *to = area + (run >> 3) * kRwHalf + rr * 128;
+          *(uint4 *)(to + (((run & 7) ^ (rr & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncthreads();
       const bool valid = seg.at[row] >= 0, any = __any_sync(0xffffffffu, valid);
       const int pos = valid ? seg.pos[row] : -1;
       const float rc = seg.rc[row];
       const int last_open = (int)__reduce_min_sync(0xffffffffu, (uint32_t)(valid ? pos + 1 : 0x7fffffff)) - kBlock;  // first token of the last whole block
-      const int end = done + seg.steps;
+      const int end = done + Steps(seg).s1 - Steps(seg).s0;
       float ref = 0.f, l = 0.f, limit = valid ? -1.f : INFINITY;  // limit: of a block's sum of weights
       bool seen = !valid;
       bool ok = true;
@@ -333,17 +320,15 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       group_sync(1, 32 * kShSoft);
       tmem_after();
       {
-        const volatile SharedPiece &z = seg;
-        const int steps = z.steps, tile = z.tile;
-        if (steps > 0 && !abort_s) {
-          store_part(a, seg, tile, steps, done, Units(seg, z.tail).unit, tmem);
+        const Steps st(seg);
+        if (st.s1 > st.s0 && !abort_s) {
+          store_part(a, seg, st.s1 - st.s0, done, Units(seg, st.tail).unit, tmem);
         } else if (w == 0) {
-          float *const p = a.parts + ((int64_t)blockIdx.x + tile) * part_floats(kRwRows) + kRwRows * kHeadDim + row;
+          float *const p = a.parts + ((int64_t)blockIdx.x + seg.p.tile) * part_floats(kRwRows) + kRwRows * kHeadDim + row;
           p[0] = p[kRwRows] = -INFINITY;
           p[2 * kRwRows] = 0.f;
         }
-        done += steps;
-        x = z.next;
+        done += st.s1 - st.s0;
       }
     }
     tmem_before();
@@ -352,25 +337,38 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
     // ---------------------------------------------------------------- producers
     registers_down<80>();
     const int pw = warp & 3, kv = warp >= kShV;  // K's, and V's
-    for (int turn = 0; x < x_end; turn ^= 1) {
-      SharedPiece &seg = pieces[turn];
-      const Prefixes::Piece piece = pre.piece(a, x, x_end);
-      const int len = pre.len[piece.list];
-      if (threadIdx.x == 32 * kShK && piece.u0 == 0) pre.announce(a, piece, x);
-      x += piece.u1 - piece.u0;
-      // the list's cache: codes of K or V, V's scales, and both tails
-      const bool own = piece.list >= a.p.batch;
-      const int64_t slice = (int64_t)(own ? piece.list - a.p.batch : piece.list) * a.c.n_kv_heads + piece.h;
-      const int capacity = own ? a.c.capacity : a.p.capacity;
-      const float *const vsc = (own ? a.c.v_scale : a.p.v_scale) + slice * (capacity / kBlock);
-      const uint8_t *const codes = (const uint8_t *)(kv ? (own ? a.c.v_codes : a.p.v_codes) : (own ? a.c.k_codes : a.p.k_codes)) +
-                                   slice * capacity * kHeadDim + (32 * pw + (lane >> 3)) * kHeadDim + 16 * (lane & 7);
+    while (true) {
       __syncthreads();
-      if (abort_s) break;
+      if (threadIdx.x == 32 * kShK) {
+        seg.go = seg.x < seg.end && !abort_s;
+        if (seg.go) {
+          const Prefixes::Piece p = pre.piece(a, seg.x, seg.end);
+          if (p.u0 == 0) pre.announce(a, p, seg.x);
+          seg.p = p;
+          auto from = [&](const lkv_cache8 &c, int b) {
+            const int64_t slice = (int64_t)b * c.n_kv_heads + p.h, codes = slice * c.capacity * kHeadDim, tail = slice * kBlock * kHeadDim;
+            seg.len = held(c, b);
+            seg.codes[0] = (const uint8_t *)c.k_codes + codes;
+            seg.codes[1] = (const uint8_t *)c.v_codes + codes;
+            seg.scale[0] = c.k_scale + slice * (c.capacity / kBlock);
+            seg.scale[1] = c.v_scale + slice * (c.capacity / kBlock);
+            seg.tail[0] = (const uint16_t *)c.k_tail + tail;
+            seg.tail[1] = (const uint16_t *)c.v_tail + tail;
+          };
+          if (p.list < a.p.batch) from(a.p, p.list);
+          else from(a.c, p.list - a.p.batch);
+          seg.x += p.u1 - p.u0;
+          seg.top = seg.tail_top[0] = seg.tail_top[1] = 0;
+          seg.last = -1;
+        }
+      }
       __syncthreads();
-      const Steps z(piece, len, seg.last);
+      if (!seg.go) break;
+      __syncthreads();
+      const Steps z(seg);
       const int s0 = z.s0, s1 = z.s1;
       uint4 cr[8];
+      const uint8_t *const codes = seg.codes[kv] + (32 * pw + (lane >> 3)) * kHeadDim + 16 * (lane & 7);
       // 4 whole rows a load, 16 codes a lane: a load takes a pass for each 128-byte line
       auto load = [&](int j) {
 #pragma unroll
@@ -383,6 +381,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       {
         // the unit of the V scales, and the tails with their largest values
         const int t = threadIdx.x - 32 * kShK, stride = 32 * (kShIssuer - kShK);
+        const float *const vsc = seg.scale[1];
         uint32_t top = 0;
 #pragma unroll 4
         for (int u = s0 * kRwBlocks + t; u < min(s1 * kRwBlocks, z.full); u += stride) top = max(top, __float_as_uint(vsc[u]));
@@ -393,11 +392,10 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
           static_assert(kRun == 32 * (kShIssuer - kShK), "each takes a run of both");
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            uint4 y = make_uint4(0, 0, 0, 0);
-            const void *from = k ? (own ? a.c.v_tail : a.p.v_tail) : (own ? a.c.k_tail : a.p.k_tail);
-            if (t / 16 < z.tail_rows) y = *(const uint4 *)((const uint16_t *)from + slice * kBlock * kHeadDim + t * 8);
-            *(uint4 *)(tails[k] + t * 8) = y;
-            uint32_t m = __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu), __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu));
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (t / 16 < z.tail_rows) x = *(const uint4 *)(seg.tail[k] + t * 8);
+            *(uint4 *)(tails[k] + t * 8) = x;
+            uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
             m = __reduce_max_sync(0xffffffffu, max(m << 16, m & 0xffff0000u));
             if (lane == 0) atomicMax(&seg.tail_top[k], m);
           }
@@ -451,17 +449,14 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
     __syncthreads();
   } else {
     registers_down<48>();
-    for (int turn = 0; x < x_end; turn ^= 1) {
-      SharedPiece &seg = pieces[turn];
-      const Prefixes::Piece piece = pre.piece(a, x, x_end);
-      const int len = pre.len[piece.list];
-      x += piece.u1 - piece.u0;
+    while (true) {
       __syncthreads();
-      if (abort_s) break;
       __syncthreads();
-      const Steps z(piece, len, seg.last);
+      if (!seg.go) break;
+      __syncthreads();
+      __syncthreads();
+      const Steps z(seg);
       const int end = done + z.s1 - z.s0;
-      __syncthreads();
       if (warp == kShIssuer) {
         // -------------------------------------------------------------- products
         // The whole warp goes along, one lane issues: descriptors and addresses stay
@@ -515,10 +510,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       } else if (warp == kShScales) {
         // -------------------------------------------------------------- scales
         const Units un(seg, z.tail);
-        const bool own = piece.list >= a.p.batch;
-        const int64_t at = (int64_t)(own ? piece.list - a.p.batch : piece.list) * a.c.n_kv_heads + piece.h;
-        const float *const ksc = (own ? a.c.k_scale : a.p.k_scale) + at * ((own ? a.c.capacity : a.p.capacity) / kBlock);
-        const float *const vsc = (own ? a.c.v_scale : a.p.v_scale) + at * ((own ? a.c.capacity : a.p.capacity) / kBlock);
+        const float *const ksc = seg.scale[0], *const vsc = seg.scale[1];
         // four steps' blocks at a time, a lane each, read four steps ahead (one step at a time: 3250 clocks a step)
         float k = 0.f, v = 0.f;
         auto load = [&](int g) {
