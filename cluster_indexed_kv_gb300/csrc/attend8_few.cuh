@@ -426,8 +426,9 @@ struct PrefixSum {
 };
 
 // Row `row` of the sequence's (slice: sequence and KV head): the sum of its
-// prefix's parts, by a warp, into r of z. All but where the parts are is read at
-// once: the factors by a lane a part, the values by a lane four of d.
+// prefix's parts, by a warp, into r of z: a lane takes four values of d, and
+// a part's exponents and total. What few parts there are is read at once.
+constexpr int kSumEarly = 12;
 template <int RT>
 __device__ __forceinline__ void sum_prefix(const SharedArgs &a, int64_t slice, int row, PrefixSum<RT> &z, int r, int lane) {
   const int b = (int)((uint32_t)slice / (uint32_t)a.c.n_kv_heads), h = (int)((uint32_t)slice % (uint32_t)a.c.n_kv_heads);
@@ -441,34 +442,47 @@ __device__ __forceinline__ void sum_prefix(const SharedArgs &a, int64_t slice, i
     const int2 who = a.tile[tile];
     const float *const part = a.parts + ((int64_t)who.x + tile) * part_floats(rows);
     auto at = [&](int j) { return part + (int64_t)j * part_floats(rows); };
-    for (int j = lane; j < who.y; j += 32) {
-      top = fmaxf(top, at(j)[rows * kHeadDim + rr]);
-      topt = fmaxf(topt, at(j)[rows * (kHeadDim + 1) + rr]);
-    }
-#pragma unroll
-    for (int d = 16; d; d /= 2) {
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      topt = fmaxf(topt, __shfl_xor_sync(0xffffffffu, topt, d));
-    }
-    for (int j0 = 0; j0 < who.y; j0 += 32) {
-      float f = 0.f;
-      if (j0 + lane < who.y) {
-        const float *p = at(j0 + lane) + rows * kHeadDim + rr;
-        f = share(p[0], top);
-        l += share(p[rows], topt) * p[2 * rows];
-      }
+    for (int j0 = 0; j0 < who.y; j0 += 32) {  // 32 parts: a lane's own one's exponents, and its values of the first few
       const int some = min(32, who.y - j0);
-#pragma unroll 8
-      for (int j = 0; j < some; ++j) {
-        const float g = __shfl_sync(0xffffffffu, f, j);
-        const float4 x = *(const float4 *)(at(j0 + j) + lane * 4 * rows + 4 * rr);
-        if (g != 0.f) {  // a part that saw nothing holds anything
-          o.x += g * x.x;
-          o.y += g * x.y;
-          o.z += g * x.z;
-          o.w += g * x.w;
-        }
+      float4 x[kSumEarly];
+#pragma unroll
+      for (int j = 0; j < kSumEarly; ++j)
+        if (j < some) x[j] = *(const float4 *)(at(j0 + j) + lane * 4 * rows + 4 * rr);
+      float m = -INFINITY, t = -INFINITY, mine = 0.f;
+      if (lane < some) {
+        const float *p = at(j0 + lane) + rows * kHeadDim + rr;
+        m = p[0];
+        t = p[rows];
+        mine = p[2 * rows];
       }
+      float above = fmaxf(top, m), abovet = fmaxf(topt, t);
+#pragma unroll
+      for (int d = 16; d; d /= 2) {
+        above = fmaxf(above, __shfl_xor_sync(0xffffffffu, above, d));
+        abovet = fmaxf(abovet, __shfl_xor_sync(0xffffffffu, abovet, d));
+      }
+      const float k = share(top, above), f = share(m, above);
+      o.x = k == 0.f ? 0.f : k * o.x;
+      o.y = k == 0.f ? 0.f : k * o.y;
+      o.z = k == 0.f ? 0.f : k * o.z;
+      o.w = k == 0.f ? 0.f : k * o.w;
+      l = share(topt, abovet) * l + share(t, abovet) * mine;
+      top = above;
+      topt = abovet;
+      auto add = [&](int j, const float4 &v) {
+        const float g = __shfl_sync(0xffffffffu, f, j);
+        if (g != 0.f) {  // a part that saw nothing holds anything
+          o.x += g * v.x;
+          o.y += g * v.y;
+          o.z += g * v.z;
+          o.w += g * v.w;
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < kSumEarly; ++j)
+        if (j < some) add(j, x[j]);
+#pragma unroll 8
+      for (int j = kSumEarly; j < some; ++j) add(j, *(const float4 *)(at(j0 + j) + lane * 4 * rows + 4 * rr));
     }
 #pragma unroll
     for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
@@ -603,7 +617,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
       if (threadIdx.x == 0 && piece.u0 == 0) pre.announce(a, piece, x);
       rt = piece.rt;
       slice = (int64_t)piece.list * c.n_kv_heads + piece.h;
-      tile.len = held(c, piece.list);
+      tile.len = pre.len[piece.list];
       tile.lo = tile.sb = tile.cnt = 0;
       tile.hi = (tile.len - 1) / kBlock;
       tile.nb = tile.hi + 1;

@@ -46,6 +46,7 @@ struct Prefixes {
   int64_t *at;   // [lists + 1]: units before each list's tiles
   int *tiles;    // [lists + 1]: tiles before
   int *nu;       // [lists]: units of one of its tiles
+  int *len;      // [lists]: tokens
   int *first;    // [G + 1]: sequences before, in `order`
   int *order;    // [batch]: sequences, prefix by prefix
   int *of;       // [batch]: the sequence's prefix, -1 for none (or an empty one)
@@ -54,13 +55,14 @@ struct Prefixes {
   int lists;
 
   static __host__ __device__ int64_t bytes(int batch, int G, bool own) {
-    return 16 * (int64_t)(G + (own ? batch : 0) + 1) + 4 * (int64_t)(G + 1 + 4 * batch);
+    return 20 * (int64_t)(G + (own ? batch : 0) + 1) + 4 * (int64_t)(G + 1 + 4 * batch);
   }
   __device__ Prefixes(void *area, int batch, int G, int lists_) : lists(lists_) {
     at = (int64_t *)area;
     tiles = (int *)(at + lists + 1);
     nu = tiles + lists + 1;
-    first = nu + lists + 1;
+    len = nu + lists + 1;
+    first = len + lists + 1;
     order = first + G + 1;
     of = order + batch;
     before = of + batch;
@@ -68,16 +70,17 @@ struct Prefixes {
   }
   __device__ void fill(const SharedArgs &a) {
     const int G = a.p.batch, B = a.c.batch;
+    // everything that is read, at once
     for (int b = threadIdx.x; b < B; b += blockDim.x) {
       const int g = a.prefix_of ? __ldcg(a.prefix_of + b) : 0, mine = held(a.c, b);
       const int cnt = a.counts ? min(max(__ldcg(a.counts + b), 0), a.n) : a.n;
-      of[b] = g >= 0 && g < G && held(a.p, g) > 0 ? g : -1;
+      of[b] = g;
       before[b] = mine - cnt;
       rows[b] = cnt;
     }
     for (int e = threadIdx.x; e < lists; e += blockDim.x) {
       nu[e] = 0;
-      at[e + 1] = e < G ? held(a.p, e) : held(a.c, e - G);
+      len[e] = e < G ? held(a.p, e) : held(a.c, e - G);
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -85,7 +88,10 @@ struct Prefixes {
       const uint32_t below = (1u << lane) - 1u;
       for (int turn = 0; turn < 2; ++turn) {  // how many sequences a prefix has, then their places
         for (int b0 = 0; b0 < B; b0 += 32) {
-          const int b = b0 + lane, g = b < B ? of[b] : -1;
+          const int b = b0 + lane;
+          int g = b < B ? of[b] : -1;
+          if (g < 0 || g >= G || len[g] == 0) g = -1;
+          if (turn == 0 && b < B) of[b] = g;
           const uint32_t same = __match_any_sync(0xffffffffu, g >= 0 ? g : -2 - lane);
           const int had = g >= 0 ? nu[g] : 0;
           if (turn && g >= 0) order[had + __popc(same & below)] = b;
@@ -98,9 +104,9 @@ struct Prefixes {
         int nt = 0, seqs = 0;
         for (int e0 = 0; e0 < lists; e0 += 32) {
           const int e = e0 + lane;
-          const int len = e < lists ? (int)at[e + 1] : 0, have = e < G ? nu[e] : len > 0;  // tokens, and sequences that see them
+          const int tokens = e < lists ? len[e] : 0, have = e < G ? nu[e] : tokens > 0;  // and sequences that see them
           const int rt = (int)quotient((int64_t)have * a.n * a.group + a.part_rows - 1, a.part_rows);
-          const int run = a.part_blocks * kBlock, per = a.start_units + (int)((uint32_t)(len + run - 1) / (uint32_t)run);
+          const int run = a.part_blocks * kBlock, per = a.start_units + (int)((uint32_t)(tokens + run - 1) / (uint32_t)run);
           int64_t u = (int64_t)rt * a.c.n_kv_heads * per;
           int t = rt * a.c.n_kv_heads, s = e < G ? have : 0;
           const int mine = s;

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
   unsigned char *const area = raw + (base - smem_at(raw));
   const uint32_t q_at = base, k_at = base + kRwTile, v_at = base + 3 * kRwTile;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // the warp: uniform for the compiler too
-  const Prefixes pre(area + 5 * kRwTile, a.c.batch, a.p.batch, a.p.batch + (a.own_parts ? a.c.batch : 0));
+  Prefixes pre(area + 5 * kRwTile, a.c.batch, a.p.batch, a.p.batch + (a.own_parts ? a.c.batch : 0));
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -149,13 +149,13 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
     bar_init_fence();
     abort_s = 0;
   }
-  wait_prerequisites();
-  launch_dependents();
   if (warp == kShIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_at(&tmem_s)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  const_cast<Prefixes &>(pre).fill(a);
+  wait_prerequisites();
+  launch_dependents();
+  pre.fill(a);
   if (threadIdx.x == 32 * kShK) pre.share(a, seg.x, seg.end);
   tmem_before();
   __syncthreads();
@@ -347,8 +347,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
           seg.p = p;
           auto from = [&](const lkv_cache8 &c, int b) {
             const int64_t slice = (int64_t)b * c.n_kv_heads + p.h, codes = slice * c.capacity * kHeadDim, tail = slice * kBlock * kHeadDim;
-            seg.len = held(c, b);
-            seg.codes[0] = (const uint8_t *)c.k_codes + codes;
+                seg.codes[0] = (const uint8_t *)c.k_codes + codes;
             seg.codes[1] = (const uint8_t *)c.v_codes + codes;
             seg.scale[0] = c.k_scale + slice * (c.capacity / kBlock);
             seg.scale[1] = c.v_scale + slice * (c.capacity / kBlock);
@@ -357,6 +356,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
           };
           if (p.list < a.p.batch) from(a.p, p.list);
           else from(a.c, p.list - a.p.batch);
+          seg.len = pre.len[p.list];
           seg.x += p.u1 - p.u0;
           seg.top = seg.tail_top[0] = seg.tail_top[1] = 0;
           seg.last = -1;
@@ -558,55 +558,50 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
   }
 }
 
-// Joins the parts of every row, of its prefix and of its own tokens: four rows a
-// CTA, a thread 4 values of one.
-__global__ void __launch_bounds__(128) k_shared_join(const __grid_constant__ SharedArgs a) {
+// Joins the parts of every row, of its prefix and of its own tokens: a warp
+// takes 4 neighbouring rows (of one token, mostly) and 32 values of d, its
+// lanes 4 values each, as parts keep them.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) k_shared_join(const __grid_constant__ SharedArgs a) {
   wait_prerequisites();
-  const int per = a.n * a.group, runs = (per + 3) / 4, d = 4 * (threadIdx.x >> 2);
-  const int slice = (int)(blockIdx.x / (unsigned)runs), row = (int)(blockIdx.x % (unsigned)runs) * 4 + (threadIdx.x & 3);
-  const int b = slice / a.c.n_kv_heads, h = slice % a.c.n_kv_heads;
-  if (row >= per) return;
-  const int cnt = a.counts ? min(max(a.counts[b], 0), a.n) : a.n;
+  const int lane = threadIdx.x & 31, per = a.n * a.group;
+  const uint32_t runs = (uint32_t)(per + 3) / 4, id = blockIdx.x * (kJoinWarps / 4) + threadIdx.x / 128;
+  const int slice = (int)(id / runs), row = (int)(id % runs) * 4 + (lane & 3), d = 4 * ((threadIdx.x / 32 % 4) * 8 + lane / 4);
+  if (slice >= a.c.batch * a.c.n_kv_heads || row >= per) return;
+  const int b = (int)((uint32_t)slice / (uint32_t)a.c.n_kv_heads), h = slice - b * a.c.n_kv_heads;
+  const int i = (int)((uint32_t)row / (uint32_t)a.group), cnt = a.counts ? min(max(__ldcg(a.counts + b), 0), a.n) : a.n;
   float top = -INFINITY, topt = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (row / a.group < cnt) {
+  if (i < cnt) {
     const int4 sq = a.seq[b];
-    const float *part[2];
-    int rr[2], np[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int first = k ? sq.z : sq.x;
       if (first < 0) continue;
       const int64_t pr = (k ? 0 : (int64_t)sq.y * per) + row;
-      const int tile = first + (int)(pr / kSharedRows) * a.c.n_kv_heads + h;
+      const int tile = first + (int)(pr / kSharedRows) * a.c.n_kv_heads + h, rr = (int)(pr % kSharedRows);
       const int2 who = a.tile[tile];
-      rr[k] = (int)(pr % kSharedRows);
-      np[k] = who.y;
-      part[k] = a.parts + ((int64_t)who.x + tile) * part_floats(kSharedRows);
-      for (int j = 0; j < np[k]; ++j) {
-        const float *p = part[k] + (int64_t)j * part_floats(kSharedRows) + kSharedRows * kHeadDim + rr[k];
-        top = fmaxf(top, p[0]);
-        topt = fmaxf(topt, p[kSharedRows]);
+      const float *part = a.parts + ((int64_t)who.x + tile) * part_floats(kSharedRows);
+#pragma unroll 4
+      for (int j = 0; j < who.y; ++j, part += part_floats(kSharedRows)) {
+        const float *p = part + kSharedRows * kHeadDim + rr;
+        const float m = p[0], t = p[kSharedRows], mine = p[2 * kSharedRows];
+        const float4 x = *(const float4 *)(part + d * kSharedRows + 4 * rr);
+        const float above = fmaxf(top, m), abovet = fmaxf(topt, t), f = share(top, above), g = share(m, above);
+        l = share(topt, abovet) * l + share(t, abovet) * mine;
+        // a part that saw nothing holds anything
+        o.x = (f == 0.f ? 0.f : f * o.x) + (g == 0.f ? 0.f : g * x.x);
+        o.y = (f == 0.f ? 0.f : f * o.y) + (g == 0.f ? 0.f : g * x.y);
+        o.z = (f == 0.f ? 0.f : f * o.z) + (g == 0.f ? 0.f : g * x.z);
+        o.w = (f == 0.f ? 0.f : f * o.w) + (g == 0.f ? 0.f : g * x.w);
+        top = above;
+        topt = abovet;
       }
     }
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      for (int j = 0; j < np[k]; ++j) {
-        const float *s = part[k] + (int64_t)j * part_floats(kSharedRows), *p = s + kSharedRows * kHeadDim + rr[k];
-        const float f = share(p[0], top);
-        l += share(p[kSharedRows], topt) * p[2 * kSharedRows];
-        const float4 x = *(const float4 *)(s + d * kSharedRows + 4 * rr[k]);
-        if (f != 0.f) {  // a part that saw nothing holds anything
-          o.x += f * x.x;
-          o.y += f * x.y;
-          o.z += f * x.z;
-          o.w += f * x.w;
-        }
-      }
   }
   const bool none = l == 0.f;
   const float scale = none ? 0.f : 1.f / l, back = none ? 0.f : exp2f(top - topt);
-  uint16_t *out = (uint16_t *)a.out + (((int64_t)slice * a.group + row % a.group) * a.n + row / a.group) * kHeadDim + d;
+  uint16_t *out = (uint16_t *)a.out + (((int64_t)slice * a.group + row - i * a.group) * a.n + i) * kHeadDim + d;
   *(uint2 *)out = none ? make_uint2(0, 0) : make_uint2(pack_bf16(o.x * scale * back, o.y * scale * back), pack_bf16(o.z * scale * back, o.w * scale * back));
 }
 
@@ -620,7 +615,7 @@ cudaError_t launch_shared_rows(const SharedArgs &a, int ctas, cudaStream_t st) {
 cudaError_t launch_shared_join(const SharedArgs &a, cudaStream_t st) {
   const int64_t runs = ((int64_t)a.n * a.group + 3) / 4 * a.c.batch * a.c.n_kv_heads;
   if (runs > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_next(k_shared_join, dim3((unsigned)runs), 128, 0, st, a);
+  return launch_next(k_shared_join, dim3((unsigned)((runs + kJoinWarps / 4 - 1) / (kJoinWarps / 4))), 32 * kJoinWarps, 0, st, a);
 }
 
 }  // namespace lkv
