@@ -447,7 +447,7 @@ __device__ __forceinline__ void sum_prefix(const SharedArgs &a, int64_t slice, i
       float4 x[kSumEarly];
 #pragma unroll
       for (int j = 0; j < kSumEarly; ++j)
-        if (j < some) x[j] = *(const float4 *)(at(j0 + j) + lane * 4 * rows + 4 * rr);
+        if (j < some) x[j] = *(const float4 *)(at(j0 + j) + part_place(rr, 4 * lane));
       float m = -INFINITY, t = -INFINITY, mine = 0.f;
       if (lane < some) {
         const float *p = at(j0 + lane) + rows * kHeadDim + rr;
@@ -482,7 +482,7 @@ __device__ __forceinline__ void sum_prefix(const SharedArgs &a, int64_t slice, i
       for (int j = 0; j < kSumEarly; ++j)
         if (j < some) add(j, x[j]);
 #pragma unroll 8
-      for (int j = kSumEarly; j < some; ++j) add(j, *(const float4 *)(at(j0 + j) + lane * 4 * rows + 4 * rr));
+      for (int j = kSumEarly; j < some; ++j) add(j, *(const float4 *)(at(j0 + j) + part_place(rr, 4 * lane)));
     }
 #pragma unroll
     for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
         s.y += f * x2.y;
       }
       if constexpr (MODE == kPrefix) {
-        *(float2 *)(slot + (p >> 1) * 4 * RT + 4 * row + 2 * (p & 1)) = s;
+        *(float2 *)(slot + part_place(row, 2 * p) + 2 * (p & 1)) = s;
       } else if (whole) {
         float m = sm.pm[row], t = sm.pt[row], l = sm.pl[row];
         if constexpr (MODE == kOwn) add_prefix(prefix, row, 2 * p, s, l, m, t);

@@ -21,7 +21,7 @@ struct SharedPlan {
 
 static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t group, int32_t n, int32_t max_len, int sms, SharedPlan *s) {
   const int64_t R = (int64_t)n * group, rows = c->batch * R, S = (int64_t)c->batch * c->n_kv_heads;
-  if (rows > 0x7fffffff - 256) return "too many rows";
+  if (rows * c->n_kv_heads > 0x7fffffff - 256) return "too many rows";
   const bool fp32 = c->dtype == LKV_DTYPE_FP32;
   s->nt = !fp32 && rows > 16 ? 16 : rows <= 8 ? 1 : 2;
   s->own_parts = s->nt == 16 && R > 32;

@@ -29,8 +29,13 @@ struct SharedArgs : AttendArgs {
   float *parts;
 };
 
-// A part: o as [d / 4][row][4], then the exponents of the units of o and l, and l.
+// A part: the rows of o, then the exponents of the units of o and l, and l of
+// each. Four values of d go together, those of row r at place (d / 4) ^ (r % 32):
+// a thread a row fills shared memory so without bank conflicts, and a warp still
+// reads a row as one run. (As [d / 4][row][4], which a thread a row writes as
+// whole runs, joining 8 rows took 10 us.)
 __host__ __device__ constexpr int part_floats(int rows) { return rows * (kHeadDim + 3); }
+__host__ __device__ __forceinline__ int part_place(int row, int d) { return row * kHeadDim + (((d >> 2) ^ (row & 31)) << 2); }
 
 __device__ __forceinline__ int held(const lkv_cache8 &c, int b) { return min(max(__ldcg(c.lengths + b), 0), c.capacity); }
 

@@ -82,28 +82,36 @@ struct Units {
 };
 
 // What both halves of the softmax have of a row goes into the piece's part: each
-// half's threads write 64 of the values of d.
-__device__ __forceinline__ void store_part(const SharedArgs &a, const SharedPiece &z, int steps, int done, int unit, uint32_t tmem) {
+// half's threads bring 64 of the values of d into `stage`, from where one copy
+// takes them; the rows' exponents and totals go straight to the part.
+__device__ __forceinline__ void store_part(const SharedArgs &a, const SharedPiece &z, int steps, int done, int unit, uint32_t tmem, float *stage) {
   const int w = threadIdx.x >> 7, r = threadIdx.x & 127;
   const bool valid = z.at[r] >= 0, has0 = steps > 1 || (done & 1) == 0, has1 = steps > 1 || (done & 1) == 1;
-  if (!__any_sync(0xffffffffu, valid)) return;
-  float *const part = a.parts + ((int64_t)blockIdx.x + z.p.tile) * part_floats(kRwRows);
   const float m0 = valid && has0 ? z.ref[0][r] : -INFINITY, m1 = valid && has1 ? z.ref[1][r] : -INFINITY;
   const float top = fmaxf(m0, m1), f0 = share(m0, top), f1 = share(m1, top);
   const uint32_t o0 = tmem + ((uint32_t)(r & 96) << 16) + 256 + 64 * w, o1 = o0 + 128;
+  if (__any_sync(0xffffffffu, valid)) {
 #pragma unroll 1
-  for (int d = 0; d < 64; d += 16) {
-    uint32_t u[16], v[16];
-    if (has0) tmem_ld16(o0 + d, u);
-    if (has1) tmem_ld16(o1 + d, v);
-    if (has0) tmem_wait16(u);
-    if (has1) tmem_wait16(v);
-    float o[16];
+    for (int d = 0; d < 64; d += 16) {
+      uint32_t u[16], v[16];
+      if (has0) tmem_ld16(o0 + d, u);
+      if (has1) tmem_ld16(o1 + d, v);
+      if (has0) tmem_wait16(u);
+      if (has1) tmem_wait16(v);
+      float o[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      o[e] = (has0 && f0 != 0.f ? f0 * __uint_as_float(u[e]) : 0.f) + (has1 && f1 != 0.f ? f1 * __uint_as_float(v[e]) : 0.f);
+      for (int e = 0; e < 16; ++e)
+        o[e] = (has0 && f0 != 0.f ? f0 * __uint_as_float(u[e]) : 0.f) + (has1 && f1 != 0.f ? f1 * __uint_as_float(v[e]) : 0.f);
 #pragma unroll
-    for (int e = 0; e < 16; e += 4) *(float4 *)(part + (64 * w + d + e) * kRwRows + 4 * r) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      for (int e = 0; e < 16; e += 4) *(float4 *)(stage + part_place(r, 64 * w + d + e)) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  group_sync(1, 32 * kShSoft);
+  float *const part = a.parts + ((int64_t)blockIdx.x + z.p.tile) * part_floats(kRwRows);
+  if (threadIdx.x == 0) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(part), "r"(smem_at(stage)), "r"(kRwRows * kHeadDim * 4) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
   if (w == 0) {
     float *const p = part + kRwRows * kHeadDim + r;
@@ -214,6 +222,8 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
+      // the producers write where the part before is copied from
+      if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       __syncthreads();
       const bool valid = seg.at[row] >= 0, any = __any_sync(0xffffffffu, valid);
       const int pos = valid ? seg.pos[row] : -1;
@@ -321,8 +331,8 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       tmem_after();
       {
         const Steps st(seg);
-        if (st.s1 > st.s0 && !abort_s) {
-          store_part(a, seg, st.s1 - st.s0, done, Units(seg, st.tail).unit, tmem);
+        if (st.s1 > st.s0) {
+          store_part(a, seg, st.s1 - st.s0, done, Units(seg, st.tail).unit, tmem, (float *)(area + kRwTile));
         } else if (w == 0) {
           float *const p = a.parts + ((int64_t)blockIdx.x + seg.p.tile) * part_floats(kRwRows) + kRwRows * kHeadDim + row;
           p[0] = p[kRwRows] = -INFINITY;
@@ -331,6 +341,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
         done += st.s1 - st.s0;
       }
     }
+    if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     tmem_before();
     __syncthreads();
   } else if (warp < kShIssuer) {
@@ -558,16 +569,15 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
   }
 }
 
-// Joins the parts of every row, of its prefix and of its own tokens: a warp
-// takes 4 neighbouring rows (of one token, mostly) and 32 values of d, its
-// lanes 4 values each, as parts keep them.
+// Joins the parts of every row, of its prefix and of its own tokens: a warp a
+// row, a lane four values of d.
 constexpr int kJoinWarps = 8;
 __global__ void __launch_bounds__(32 * kJoinWarps) k_shared_join(const __grid_constant__ SharedArgs a) {
   wait_prerequisites();
   const int lane = threadIdx.x & 31, per = a.n * a.group;
-  const uint32_t runs = (uint32_t)(per + 3) / 4, id = blockIdx.x * (kJoinWarps / 4) + threadIdx.x / 128;
-  const int slice = (int)(id / runs), row = (int)(id % runs) * 4 + (lane & 3), d = 4 * ((threadIdx.x / 32 % 4) * 8 + lane / 4);
-  if (slice >= a.c.batch * a.c.n_kv_heads || row >= per) return;
+  const uint32_t id = blockIdx.x * kJoinWarps + threadIdx.x / 32;
+  const int slice = (int)(id / (uint32_t)per), row = (int)(id % (uint32_t)per), d = 4 * lane;
+  if (slice >= a.c.batch * a.c.n_kv_heads) return;
   const int b = (int)((uint32_t)slice / (uint32_t)a.c.n_kv_heads), h = slice - b * a.c.n_kv_heads;
   const int i = (int)((uint32_t)row / (uint32_t)a.group), cnt = a.counts ? min(max(__ldcg(a.counts + b), 0), a.n) : a.n;
   float top = -INFINITY, topt = -INFINITY, l = 0.f;
@@ -586,7 +596,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_shared_join(const __grid_co
       for (int j = 0; j < who.y; ++j, part += part_floats(kSharedRows)) {
         const float *p = part + kSharedRows * kHeadDim + rr;
         const float m = p[0], t = p[kSharedRows], mine = p[2 * kSharedRows];
-        const float4 x = *(const float4 *)(part + d * kSharedRows + 4 * rr);
+        const float4 x = *(const float4 *)(part + part_place(rr, d));
         const float above = fmaxf(top, m), abovet = fmaxf(topt, t), f = share(top, above), g = share(m, above);
         l = share(topt, abovet) * l + share(t, abovet) * mine;
         // a part that saw nothing holds anything
@@ -613,9 +623,9 @@ cudaError_t launch_shared_rows(const SharedArgs &a, int ctas, cudaStream_t st) {
 }
 
 cudaError_t launch_shared_join(const SharedArgs &a, cudaStream_t st) {
-  const int64_t runs = ((int64_t)a.n * a.group + 3) / 4 * a.c.batch * a.c.n_kv_heads;
-  if (runs > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_next(k_shared_join, dim3((unsigned)((runs + kJoinWarps / 4 - 1) / (kJoinWarps / 4))), 32 * kJoinWarps, 0, st, a);
+  const int64_t rows = (int64_t)a.n * a.group * a.c.batch * a.c.n_kv_heads;
+  if (rows > 0x7fffffff) return cudaErrorInvalidValue;
+  return launch_next(k_shared_join, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), 32 * kJoinWarps, 0, st, a);
 }
 
 }  // namespace lkv
