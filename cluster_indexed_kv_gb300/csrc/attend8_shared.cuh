@@ -91,7 +91,9 @@ struct Prefixes {
     if (threadIdx.x < 32) {
       const int lane = threadIdx.x;
       const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 1
       for (int turn = 0; turn < 2; ++turn) {  // how many sequences a prefix has, then their places
+#pragma unroll 1
         for (int b0 = 0; b0 < B; b0 += 32) {
           const int b = b0 + lane;
           int g = b < B ? of[b] : -1;
@@ -107,6 +109,7 @@ struct Prefixes {
         if (turn) break;
         int64_t units = 0;
         int nt = 0, seqs = 0;
+#pragma unroll 1
         for (int e0 = 0; e0 < lists; e0 += 32) {
           const int e = e0 + lane;
           const int tokens = e < lists ? len[e] : 0, have = e < G ? nu[e] : tokens > 0;  // and sequences that see them
@@ -115,7 +118,7 @@ struct Prefixes {
           int64_t u = (int64_t)rt * a.c.n_kv_heads * per;
           int t = rt * a.c.n_kv_heads, s = e < G ? have : 0;
           const int mine = s;
-#pragma unroll
+#pragma unroll 1
           for (int d = 1; d < 32; d *= 2) {
             const int64_t u2 = __shfl_up_sync(0xffffffffu, u, d);
             const int t2 = __shfl_up_sync(0xffffffffu, t, d), s2 = __shfl_up_sync(0xffffffffu, s, d);
