@@ -428,7 +428,7 @@ struct PrefixSum {
 // Row `row` of the sequence's (slice: sequence and KV head): the sum of its
 // prefix's parts, by a warp, into r of z: a lane takes four values of d, and
 // a part's exponents and total. What few parts there are is read at once.
-constexpr int kSumEarly = 4;
+constexpr int kSumEarly = 12;
 template <int RT>
 __device__ __forceinline__ void sum_prefix(const SharedArgs &a, int64_t slice, int row, PrefixSum<RT> &z, int r, int lane) {
   const int b = (int)((uint32_t)slice / (uint32_t)a.c.n_kv_heads), h = (int)((uint32_t)slice % (uint32_t)a.c.n_kv_heads);
@@ -439,19 +439,21 @@ __device__ __forceinline__ void sum_prefix(const SharedArgs &a, int64_t slice, i
   if (sq.x >= 0) {
     const int64_t pr = (int64_t)sq.y * per + row, rt = quotient(pr, rows);
     const int tile = sq.x + (int)rt * a.c.n_kv_heads + h, rr = (int)(pr - rt * rows);
-    const Parts parts(a, tile);
-    for (int j0 = 0; j0 < parts.n; j0 += 32) {  // 32 parts: a lane's own one's exponents, and its values of the first few
-      const int some = min(32, parts.n - j0);
+    const int2 who = a.tile[tile];
+    const float *const part = a.parts + ((int64_t)who.x + tile) * part_floats(rows);
+    auto at = [&](int j) { return part + (int64_t)j * part_floats(rows); };
+    for (int j0 = 0; j0 < who.y; j0 += 32) {  // 32 parts: a lane's own one's exponents, and its values of the first few
+      const int some = min(32, who.y - j0);
       float4 x[kSumEarly];
 #pragma unroll
       for (int j = 0; j < kSumEarly; ++j)
-        if (j < some) x[j] = parts.values(j0 + j, rr, 4 * lane);
+        if (j < some) x[j] = *(const float4 *)(at(j0 + j) + part_place(rr, 4 * lane));
       float m = -INFINITY, t = -INFINITY, mine = 0.f;
       if (lane < some) {
-        const float3 p = parts.sums(j0 + lane, rr);
-        m = p.x;
-        t = p.y;
-        mine = p.z;
+        const float *p = at(j0 + lane) + rows * kHeadDim + rr;
+        m = p[0];
+        t = p[rows];
+        mine = p[2 * rows];
       }
       float above = fmaxf(top, m), abovet = fmaxf(topt, t);
 #pragma unroll
@@ -479,8 +481,8 @@ __device__ __forceinline__ void sum_prefix(const SharedArgs &a, int64_t slice, i
 #pragma unroll
       for (int j = 0; j < kSumEarly; ++j)
         if (j < some) add(j, x[j]);
-#pragma unroll 4
-      for (int j = kSumEarly; j < some; ++j) add(j, parts.values(j0 + j, rr, 4 * lane));
+#pragma unroll 8
+      for (int j = kSumEarly; j < some; ++j) add(j, *(const float4 *)(at(j0 + j) + part_place(rr, 4 * lane)));
     }
 #pragma unroll
     for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
@@ -612,7 +614,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
     [[maybe_unused]] Prefixes::Piece piece{};
     if constexpr (MODE == kPrefix) {
       piece = pre.piece(a, x, x1);
-      if (threadIdx.x == 0 && piece.u0 == 0) pre.announce(a, piece, x, false);
+      if (threadIdx.x == 0 && piece.u0 == 0) pre.announce(a, piece, x);
       rt = piece.rt;
       slice = (int64_t)piece.list * c.n_kv_heads + piece.h;
       tile.len = pre.len[piece.list];

@@ -16,7 +16,6 @@
 namespace lkv {
 
 constexpr int kSharedMost = 1024;  // sequences, and prefixes, that a call takes
-constexpr int kTwice = 1 << 30;
 
 struct SharedArgs : AttendArgs {
   lkv_cache8 p;               // the prefixes
@@ -26,7 +25,7 @@ struct SharedArgs : AttendArgs {
   int32_t least_units;        // that a CTA takes, at least
   int32_t own_parts;          // whether the sequences' own tokens are parts too
   int4 *seq;                  // [batch]: the first tile of the sequence's prefix (-1: none), its place behind that prefix, its own first tile (-1: none)
-  int2 *tile;                 // [tiles]: a tile's first CTA, and how many it has (kTwice: its rows stand twice in each part)
+  int2 *tile;                 // [tiles]: a tile's first CTA, and how many it has
   float *parts;
 };
 
@@ -193,36 +192,11 @@ struct Prefixes {
     p.u1 = (int)min((int64_t)nu[lo], p.u0 + (x1 - x));
     return p;
   }
-  // rows of a piece's list from its tile on
-  __device__ __forceinline__ int64_t rows_left(const SharedArgs &a, const Piece &p) const {
-    const int64_t seqs = p.list < a.p.batch ? first[p.list + 1] - first[p.list] : 1;
-    return seqs * a.n * a.group - (int64_t)p.rt * a.part_rows;
-  }
   // the tile that begins at unit x of the row, for whoever joins its parts (one thread of the CTA that has the unit)
-  __device__ __forceinline__ void announce(const SharedArgs &a, const Piece &p, int64_t x, bool twice) const {
+  __device__ __forceinline__ void announce(const SharedArgs &a, const Piece &p, int64_t x) const {
     const int64_t P = takers(a), last = x + nu[p.list] - 1;
     // the last CTA that begins at or before unit `last`
-    a.tile[p.tile] = make_int2((int)blockIdx.x, ((int)quotient(P * (last + 1) - 1, at[lists]) - (int)blockIdx.x + 1) | (twice ? kTwice : 0));
-  }
-};
-
-// A tile's parts: how many, and where part j's row begins (`row` of the tile).
-struct Parts {
-  const float *at;
-  int n, rows, twice;
-  __device__ __forceinline__ Parts(const SharedArgs &a, int tile) : rows(a.part_rows) {
-    const int2 who = a.tile[tile];
-    twice = who.y >> 30 & 1;
-    n = (who.y & (kTwice - 1)) << twice;
-    at = a.parts + ((int64_t)who.x + tile) * part_floats(rows);
-  }
-  __device__ __forceinline__ int row_of(int j, int row) const { return twice ? row + (j & 1) * (rows / 2) : row; }
-  __device__ __forceinline__ const float *part(int j) const { return at + (int64_t)(j >> twice) * part_floats(rows); }
-  __device__ __forceinline__ float4 values(int j, int row, int d) const { return *(const float4 *)(part(j) + part_place(row_of(j, row), d)); }
-  // the exponents of the units of o and l, and l
-  __device__ __forceinline__ float3 sums(int j, int row) const {
-    const float *p = part(j) + rows * kHeadDim + row_of(j, row);
-    return make_float3(p[0], p[rows], p[2 * rows]);
+    a.tile[p.tile] = make_int2((int)blockIdx.x, (int)quotient(P * (last + 1) - 1, at[lists]) - (int)blockIdx.x + 1);
   }
 };
 
@@ -245,7 +219,7 @@ __device__ __forceinline__ ListRow list_row(const SharedArgs &a, const Prefixes 
 // The kernel for many rows of bf16 caches and the join of what it leaves
 // (attend8_shared_rows.cu): row tiles of kSharedRows, units of kSharedStep tokens.
 constexpr int kSharedRows = 128, kSharedStep = 128;
-constexpr int kSharedStart = 7;  // steps' time that beginning a tile costs
+constexpr int kSharedStart = 4;  // steps' time that beginning a tile costs
 cudaError_t launch_shared_rows(const SharedArgs &a, int ctas, cudaStream_t st);
 cudaError_t launch_shared_join(const SharedArgs &a, cudaStream_t st);
 

@@ -49,7 +49,6 @@ struct SharedPiece {
   const uint16_t *tail[2];
   int len;
   int go;                     // whether there is a piece
-  int twice;                  // whether its rows stand twice in the tile
   int last;                   // the last token that a row sees
   uint32_t top, tail_top[2];  // largest V scale of the piece's blocks, largest magnitudes of the tails (bits)
   int64_t at[kRwRows];        // the rows' queries, -1 for none
@@ -188,7 +187,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       __syncthreads();
       if (!seg.go) break;
       if (w == 0) {
-        const ListRow x = list_row(a, pre, seg.p.list, seg.p.h, seg.len, (int64_t)seg.p.rt * kRwRows + (seg.twice ? row % (kRwRows / 2) : row));
+        const ListRow x = list_row(a, pre, seg.p.list, seg.p.h, seg.len, (int64_t)seg.p.rt * kRwRows + row);
         seg.at[row] = x.at;
         seg.pos[row] = x.pos;
         const int top = __reduce_max_sync(0xffffffffu, x.at < 0 ? -1 : x.pos);
@@ -231,8 +230,6 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       const float rc = seg.rc[row];
       const int last_open = (int)__reduce_min_sync(0xffffffffu, (uint32_t)(valid ? pos + 1 : 0x7fffffff)) - kBlock;  // first token of the last whole block
       const int end = done + Steps(seg).s1 - Steps(seg).s0;
-      // rows that stand twice: each time for 64 of a step's tokens, the others weigh nothing
-      const int mine = seg.twice ? (warp & 2) * 2 : -1;  // the first block of those
       float ref = 0.f, l = 0.f, limit = valid ? -1.f : INFINITY;  // limit: of a block's sum of weights
       bool seen = !valid;
       bool ok = true;
@@ -257,22 +254,12 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
         tmem_after();
         float sum = 0.f;
         uint32_t x[32];
-        tmem_ld32(s_at + (mine > 0 ? 64 : 0), x);
+        tmem_ld32(s_at, x);
         // four blocks at a time, two by two: scores become weights, over the
         // columns of blocks that have been read
 #pragma unroll 1
         for (int b = 0; b < kRwBlocks; b += 4) {
           uint32_t p[32];
-          if (mine >= 0 && mine != b) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) p[e] = 0;
-            tmem_st32(s_at + 8 * b, p);
-            tmem_wait_st();
-            tmem_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(&sy.pfull[w][b >> 2]);
-            continue;
-          }
           float t[4];
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
@@ -289,7 +276,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
                 y[e + 1] = z.y;
               }
             }
-            if (v == 0 || (b + 4 < kRwBlocks && mine < 0)) tmem_ld32(s_at + 16 * (b + 2 * v + 2), x);
+            if (v == 0 || b + 4 < kRwBlocks) tmem_ld32(s_at + 16 * (b + 2 * v + 2), x);
             if (!open) {
               const int see0 = pos - __float_as_int(sc0.w), see1 = pos - __float_as_int(sc1.w);
 #pragma unroll
@@ -367,8 +354,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
         seg.go = seg.x < seg.end && !abort_s;
         if (seg.go) {
           const Prefixes::Piece p = pre.piece(a, seg.x, seg.end);
-          seg.twice = pre.rows_left(a, p) <= kRwRows / 2;
-          if (p.u0 == 0) pre.announce(a, p, seg.x, seg.twice);
+          if (p.u0 == 0) pre.announce(a, p, seg.x);
           seg.p = p;
           auto from = [&](const lkv_cache8 &c, int b) {
             const int64_t slice = (int64_t)b * c.n_kv_heads + p.h, codes = slice * c.capacity * kHeadDim, tail = slice * kBlock * kHeadDim;
@@ -604,12 +590,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_shared_join(const __grid_co
       if (first < 0) continue;
       const int64_t pr = (k ? 0 : (int64_t)sq.y * per) + row;
       const int tile = first + (int)(pr / kSharedRows) * a.c.n_kv_heads + h, rr = (int)(pr % kSharedRows);
-      const Parts parts(a, tile);
+      const int2 who = a.tile[tile];
+      const float *part = a.parts + ((int64_t)who.x + tile) * part_floats(kSharedRows);
 #pragma unroll 4
-      for (int j = 0; j < parts.n; ++j) {
-        const float3 p = parts.sums(j, rr);
-        const float m = p.x, t = p.y, mine = p.z;
-        const float4 x = parts.values(j, rr, d);
+      for (int j = 0; j < who.y; ++j, part += part_floats(kSharedRows)) {
+        const float *p = part + kSharedRows * kHeadDim + rr;
+        const float m = p[0], t = p[kSharedRows], mine = p[2 * kSharedRows];
+        const float4 x = *(const float4 *)(part + part_place(rr, d));
         const float above = fmaxf(top, m), abovet = fmaxf(topt, t), f = share(top, above), g = share(m, above);
         l = share(topt, abovet) * l + share(t, abovet) * mine;
         // a part that saw nothing holds anything
