@@ -428,7 +428,7 @@ struct PrefixSum {
 // Row `row` of the sequence's (slice: sequence and KV head): the sum of its
 // prefix's parts, by a warp, into r of z: a lane takes four values of d, and
 // a part's exponents and total. What few parts there are is read at once.
-constexpr int kSumEarly = 12;
+constexpr int kSumEarly = 4;
 template <int RT>
 __device__ __forceinline__ void sum_prefix(const SharedArgs &a, int64_t slice, int row, PrefixSum<RT> &z, int r, int lane) {
   const int b = (int)((uint32_t)slice / (uint32_t)a.c.n_kv_heads), h = (int)((uint32_t)slice % (uint32_t)a.c.n_kv_heads);
@@ -481,7 +481,7 @@ __device__ __forceinline__ void sum_prefix(const SharedArgs &a, int64_t slice, i
 #pragma unroll
       for (int j = 0; j < kSumEarly; ++j)
         if (j < some) add(j, x[j]);
-#pragma unroll 8
+#pragma unroll 4
       for (int j = kSumEarly; j < some; ++j) add(j, *(const float4 *)(at(j0 + j) + part_place(rr, 4 * lane)));
     }
 #pragma unroll

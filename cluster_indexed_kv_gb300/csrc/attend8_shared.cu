@@ -24,7 +24,7 @@ static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t
   if (rows * c->n_kv_heads > 0x7fffffff - 256) return "too many rows";
   const bool fp32 = c->dtype == LKV_DTYPE_FP32;
   s->nt = !fp32 && rows > 16 ? 16 : rows <= 8 ? 1 : 2;
-  s->own_parts = s->nt == 16 && R > 32;
+  s->own_parts = s->nt == 16 && R > 16;
   const int part_rows = 8 * s->nt;
   s->ctas = s->nt == 16 ? sms : sms * (fp32 && s->nt == 2 ? 1 : 2);
   s->tiles = ((rows + part_rows - 1) / part_rows + (p->batch < c->batch ? p->batch : c->batch)) * c->n_kv_heads;

@@ -219,7 +219,7 @@ __device__ __forceinline__ ListRow list_row(const SharedArgs &a, const Prefixes 
 // The kernel for many rows of bf16 caches and the join of what it leaves
 // (attend8_shared_rows.cu): row tiles of kSharedRows, units of kSharedStep tokens.
 constexpr int kSharedRows = 128, kSharedStep = 128;
-constexpr int kSharedStart = 4;  // steps' time that beginning a tile costs
+constexpr int kSharedStart = 7;  // steps' time that beginning a tile costs
 cudaError_t launch_shared_rows(const SharedArgs &a, int ctas, cudaStream_t st);
 cudaError_t launch_shared_join(const SharedArgs &a, cudaStream_t st);
 
