@@ -570,13 +570,14 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
 }
 
 // Joins the parts of every row, of its prefix and of its own tokens: a warp a
-// row, a lane four values of d.
-constexpr int kJoinWarps = 8;
+// row, a lane four values of d. Where the parts of both lie is read at once, and
+// then kJoinAtOnce parts at a time.
+constexpr int kJoinWarps = 8, kJoinAtOnce = 4;
 __global__ void __launch_bounds__(32 * kJoinWarps) k_shared_join(const __grid_constant__ SharedArgs a) {
   wait_prerequisites();
-  const int lane = threadIdx.x & 31, per = a.n * a.group;
+  const int lane = threadIdx.x & 31, per = a.n * a.group, d = 4 * lane;
   const uint32_t id = blockIdx.x * kJoinWarps + threadIdx.x / 32;
-  const int slice = (int)(id / (uint32_t)per), row = (int)(id % (uint32_t)per), d = 4 * lane;
+  const int slice = (int)(id / (uint32_t)per), row = (int)(id % (uint32_t)per);
   if (slice >= a.c.batch * a.c.n_kv_heads) return;
   const int b = (int)((uint32_t)slice / (uint32_t)a.c.n_kv_heads), h = slice - b * a.c.n_kv_heads;
   const int i = (int)((uint32_t)row / (uint32_t)a.group), cnt = a.counts ? min(max(__ldcg(a.counts + b), 0), a.n) : a.n;
@@ -584,29 +585,55 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_shared_join(const __grid_co
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   if (i < cnt) {
     const int4 sq = a.seq[b];
+    // the row in the prefix's list, and in its own
+    const int64_t there = (int64_t)sq.y * per + row, rt = quotient(there, kSharedRows);
+    const int tile0 = sq.x + (int)rt * a.c.n_kv_heads + h, tile1 = sq.z + row / kSharedRows * a.c.n_kv_heads + h;
+    const int2 none = make_int2(0, 0), who0 = sq.x >= 0 ? a.tile[tile0] : none, who1 = sq.z >= 0 ? a.tile[tile1] : none;
+    const float *const at0 = a.parts + ((int64_t)who0.x + tile0) * part_floats(kSharedRows);
+    const float *const at1 = a.parts + ((int64_t)who1.x + tile1 - who0.y) * part_floats(kSharedRows);
+    const int r0 = (int)(there - rt * kSharedRows), r1 = row % kSharedRows, n = who0.y + who1.y;
+    for (int j0 = 0; j0 < n; j0 += kJoinAtOnce) {
+      float4 x[kJoinAtOnce];
+      float m[kJoinAtOnce], t[kJoinAtOnce], mine[kJoinAtOnce];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int first = k ? sq.z : sq.x;
-      if (first < 0) continue;
-      const int64_t pr = (k ? 0 : (int64_t)sq.y * per) + row;
-      const int tile = first + (int)(pr / kSharedRows) * a.c.n_kv_heads + h, rr = (int)(pr % kSharedRows);
-      const int2 who = a.tile[tile];
-      const float *part = a.parts + ((int64_t)who.x + tile) * part_floats(kSharedRows);
-#pragma unroll 4
-      for (int j = 0; j < who.y; ++j, part += part_floats(kSharedRows)) {
-        const float *p = part + kSharedRows * kHeadDim + rr;
-        const float m = p[0], t = p[kSharedRows], mine = p[2 * kSharedRows];
-        const float4 x = *(const float4 *)(part + part_place(rr, d));
-        const float above = fmaxf(top, m), abovet = fmaxf(topt, t), f = share(top, above), g = share(m, above);
-        l = share(topt, abovet) * l + share(t, abovet) * mine;
-        // a part that saw nothing holds anything
-        o.x = (f == 0.f ? 0.f : f * o.x) + (g == 0.f ? 0.f : g * x.x);
-        o.y = (f == 0.f ? 0.f : f * o.y) + (g == 0.f ? 0.f : g * x.y);
-        o.z = (f == 0.f ? 0.f : f * o.z) + (g == 0.f ? 0.f : g * x.z);
-        o.w = (f == 0.f ? 0.f : f * o.w) + (g == 0.f ? 0.f : g * x.w);
-        top = above;
-        topt = abovet;
+      for (int k = 0; k < kJoinAtOnce; ++k) {
+        const int j = j0 + k, r = j < who0.y ? r0 : r1;
+        const float *part = (j < who0.y ? at0 : at1) + (int64_t)j * part_floats(kSharedRows);
+        m[k] = t[k] = -INFINITY;
+        mine[k] = 0.f;
+        if (j < n) {
+          x[k] = *(const float4 *)(part + part_place(r, d));
+          const float *p = part + kSharedRows * kHeadDim + r;
+          m[k] = p[0];
+          t[k] = p[kSharedRows];
+          mine[k] = p[2 * kSharedRows];
+        }
       }
+      float above = top, abovet = topt;
+#pragma unroll
+      for (int k = 0; k < kJoinAtOnce; ++k) {
+        above = fmaxf(above, m[k]);
+        abovet = fmaxf(abovet, t[k]);
+      }
+      const float f = share(top, above);
+      o.x = f == 0.f ? 0.f : f * o.x;
+      o.y = f == 0.f ? 0.f : f * o.y;
+      o.z = f == 0.f ? 0.f : f * o.z;
+      o.w = f == 0.f ? 0.f : f * o.w;
+      l *= share(topt, abovet);
+#pragma unroll
+      for (int k = 0; k < kJoinAtOnce; ++k) {
+        const float g = share(m[k], above);
+        l += share(t[k], abovet) * mine[k];
+        if (g != 0.f) {  // a part that saw nothing holds anything
+          o.x += g * x[k].x;
+          o.y += g * x[k].y;
+          o.z += g * x[k].z;
+          o.w += g * x[k].w;
+        }
+      }
+      top = above;
+      topt = abovet;
     }
   }
   const bool none = l == 0.f;
