@@ -569,7 +569,10 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
   [[maybe_unused]] __shared__ __align__(16) std::conditional_t<MODE == kOwn, PrefixSum<RT>, int> prefix;
   constexpr int kUsed = (int)sizeof(Sm) > kRingBytes ? (int)sizeof(Sm) : kRingBytes;
   static_assert(kUsed % 8 == 0, "the tables begin with 8-byte words");
-  [[maybe_unused]] Prefixes pre(area + kUsed, MODE == kPrefix ? a.c.batch : 0, MODE == kPrefix ? G : 0, MODE == kPrefix ? G : 0);
+  [[maybe_unused]] auto pre = [&] {
+    if constexpr (MODE == kPrefix) return Prefixes(a, area + kUsed);
+    else return 0;
+  }();
 
   W w;
   w.lane = threadIdx.x & 31;
@@ -617,7 +620,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
       if (threadIdx.x == 0 && piece.u0 == 0) pre.announce(a, piece, x);
       rt = piece.rt;
       slice = (int64_t)piece.list * c.n_kv_heads + piece.h;
-      tile.len = pre.len[piece.list];
+      tile.len = pre.len(piece.list);
       tile.lo = tile.sb = tile.cnt = 0;
       tile.hi = (tile.len - 1) / kBlock;
       tile.nb = tile.hi + 1;

@@ -48,46 +48,53 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 // The work, in shared memory: list e < G is prefix e's, and list G + b
 // sequence b's own.
 struct Prefixes {
-  int64_t *at;   // [lists + 1]: units before each list's tiles
-  int *tiles;    // [lists + 1]: tiles before
-  int *nu;       // [lists]: units of one of its tiles
-  int *len;      // [lists]: tokens
-  int *first;    // [G + 1]: sequences before, in `order`
-  int *order;    // [batch]: sequences, prefix by prefix
-  int *of;       // [batch]: the sequence's prefix, -1 for none (or an empty one)
-  int *before;   // [batch]: its own tokens before its first row
-  int *rows;     // [batch]: tokens of its rows that are no padding
-  int lists;
+  int64_t *at;       // [lists + 1]: units before each list's tiles
+  int *tiles;        // [lists + 1]: tiles before
+  int *plen;         // [G]: the prefixes' tokens
+  int *pnu;          // [G]: units of one of a prefix's tiles
+  int *first;        // [G + 1]: sequences before, in `order`
+  int *before;       // [batch]: a sequence's own tokens before its first row
+  int *rows;         // [batch]: tokens of its rows that are no padding
+  int16_t *order;    // [batch]: sequences, prefix by prefix
+  int16_t *of;       // [batch]: the sequence's prefix, -1 for none (or an empty one)
+  int G, lists, run, start;
 
   static __host__ __device__ int64_t bytes(int batch, int G, bool own) {
-    return 20 * (int64_t)(G + (own ? batch : 0) + 1) + 4 * (int64_t)(G + 1 + 4 * batch);
+    return 12 * (int64_t)(G + (own ? batch : 0) + 2) + 12 * (int64_t)(G + 1) + 12 * (int64_t)batch;
   }
-  __device__ Prefixes(void *area, int batch, int G, int lists_) : lists(lists_) {
+  __device__ Prefixes(const SharedArgs &a, void *area) : G(a.p.batch), lists(a.p.batch + (a.own_parts ? a.c.batch : 0)),
+                                                          run(a.part_blocks * kBlock), start(a.start_units) {
+    const int B = a.c.batch;
     at = (int64_t *)area;
     tiles = (int *)(at + lists + 1);
-    nu = tiles + lists + 1;
-    len = nu + lists + 1;
-    first = len + lists + 1;
-    order = first + G + 1;
-    of = order + batch;
-    before = of + batch;
-    rows = before + batch;
+    plen = tiles + lists + 1;
+    pnu = plen + G;
+    first = pnu + G;
+    before = first + G + 1;
+    rows = before + B;
+    order = (int16_t *)(rows + B);
+    of = order + B;
   }
+  // a list's tokens, and the units of one of its tiles
+  __device__ __forceinline__ int len(int list) const { return list < G ? plen[list] : before[list - G] + rows[list - G]; }
+  __device__ __forceinline__ int units(int tokens) const { return start + (int)((uint32_t)(tokens + run - 1) / (uint32_t)run); }
+  __device__ __forceinline__ int nu(int list) const { return list < G ? pnu[list] : units(len(list)); }
   __device__ void fill(const SharedArgs &a) {
-    const int G = a.p.batch, B = a.c.batch;
+    const int B = a.c.batch;
     // everything that is read, at once
     for (int b = threadIdx.x; b < B; b += blockDim.x) {
       const int g = a.prefix_of ? __ldcg(a.prefix_of + b) : 0, mine = held(a.c, b);
       const int cnt = a.counts ? min(max(__ldcg(a.counts + b), 0), a.n) : a.n;
-      of[b] = g;
+      of[b] = (int16_t)(g >= 0 && g < G ? g : -1);
       before[b] = mine - cnt;
       rows[b] = cnt;
     }
-    for (int e = threadIdx.x; e < lists; e += blockDim.x) {
-      nu[e] = 0;
-      len[e] = e < G ? held(a.p, e) : held(a.c, e - G);
+    for (int g = threadIdx.x; g < G; g += blockDim.x) {
+      pnu[g] = 0;
+      plen[g] = held(a.p, g);
     }
     __syncthreads();
+    // (loops are kept short: code that runs once costs its fetching, 10,000 clocks of it when these were unrolled)
     if (threadIdx.x < 32) {
       const int lane = threadIdx.x;
       const uint32_t below = (1u << lane) - 1u;
@@ -97,25 +104,23 @@ struct Prefixes {
         for (int b0 = 0; b0 < B; b0 += 32) {
           const int b = b0 + lane;
           int g = b < B ? of[b] : -1;
-          if (g < 0 || g >= G || len[g] == 0) g = -1;
-          if (turn == 0 && b < B) of[b] = g;
+          if (g >= 0 && plen[g] == 0) of[b] = g = -1;
           const uint32_t same = __match_any_sync(0xffffffffu, g >= 0 ? g : -2 - lane);
-          const int had = g >= 0 ? nu[g] : 0;
-          if (turn && g >= 0) order[had + __popc(same & below)] = b;
+          const int had = g >= 0 ? pnu[g] : 0;
+          if (turn && g >= 0) order[had + __popc(same & below)] = (int16_t)b;
           __syncwarp();
-          if (g >= 0 && (same & below) == 0) nu[g] = had + __popc(same);
+          if (g >= 0 && (same & below) == 0) pnu[g] = had + __popc(same);
           __syncwarp();
         }
         if (turn) break;
-        int64_t units = 0;
+        int64_t sum = 0;
         int nt = 0, seqs = 0;
 #pragma unroll 1
         for (int e0 = 0; e0 < lists; e0 += 32) {
           const int e = e0 + lane;
-          const int tokens = e < lists ? len[e] : 0, have = e < G ? nu[e] : tokens > 0;  // and sequences that see them
+          const int tokens = e < lists ? len(e) : 0, have = e < G ? pnu[e] : tokens > 0;  // and sequences that see them
           const int rt = (int)quotient((int64_t)have * a.n * a.group + a.part_rows - 1, a.part_rows);
-          const int run = a.part_blocks * kBlock, per = a.start_units + (int)((uint32_t)(tokens + run - 1) / (uint32_t)run);
-          int64_t u = (int64_t)rt * a.c.n_kv_heads * per;
+          int64_t u = (int64_t)rt * a.c.n_kv_heads * units(tokens);
           int t = rt * a.c.n_kv_heads, s = e < G ? have : 0;
           const int mine = s;
 #pragma unroll 1
@@ -129,16 +134,14 @@ struct Prefixes {
             }
           }
           if (e < lists) {
-            at[e + 1] = units + u;
+            at[e + 1] = sum + u;
             tiles[e + 1] = nt + t;
           }
           if (e < G) {
             first[e + 1] = seqs + s;
-            nu[e] = seqs + s - mine;  // where its sequences begin
-          } else if (e < lists) {
-            nu[e] = per;
+            pnu[e] = seqs + s - mine;  // where its sequences begin
           }
-          units += __shfl_sync(0xffffffffu, u, 31);
+          sum += __shfl_sync(0xffffffffu, u, 31);
           nt += __shfl_sync(0xffffffffu, t, 31);
           seqs += __shfl_sync(0xffffffffu, s, 31);
         }
@@ -147,10 +150,7 @@ struct Prefixes {
       }
     }
     __syncthreads();
-    for (int g = threadIdx.x; g < G; g += blockDim.x) {
-      const int t = tiles[g + 1] - tiles[g];
-      nu[g] = t ? (int)quotient(at[g + 1] - at[g], t) : 0;
-    }
+    for (int g = threadIdx.x; g < G; g += blockDim.x) pnu[g] = units(plen[g]);
     if (blockIdx.x == 0) {
       auto own = [&](int b) { return lists > G && tiles[G + b + 1] > tiles[G + b] ? tiles[G + b] : -1; };
       for (int b = threadIdx.x; b < B; b += blockDim.x)
@@ -182,19 +182,19 @@ struct Prefixes {
       else hi = mid;
     }
     const int64_t off = x - at[lo];
-    const int idx = (int)quotient(off, nu[lo]);
+    const int per = nu(lo), idx = (int)quotient(off, per);
     Piece p;
     p.list = lo;
     p.rt = (int)((uint32_t)idx / (uint32_t)a.c.n_kv_heads);
     p.h = idx - p.rt * a.c.n_kv_heads;
     p.tile = tiles[lo] + idx;
-    p.u0 = (int)(off - (int64_t)idx * nu[lo]);
-    p.u1 = (int)min((int64_t)nu[lo], p.u0 + (x1 - x));
+    p.u0 = (int)(off - (int64_t)idx * per);
+    p.u1 = (int)min((int64_t)per, p.u0 + (x1 - x));
     return p;
   }
   // the tile that begins at unit x of the row, for whoever joins its parts (one thread of the CTA that has the unit)
   __device__ __forceinline__ void announce(const SharedArgs &a, const Piece &p, int64_t x) const {
-    const int64_t P = takers(a), last = x + nu[p.list] - 1;
+    const int64_t P = takers(a), last = x + nu(p.list) - 1;
     // the last CTA that begins at or before unit `last`
     a.tile[p.tile] = make_int2((int)blockIdx.x, (int)quotient(P * (last + 1) - 1, at[lists]) - (int)blockIdx.x + 1);
   }

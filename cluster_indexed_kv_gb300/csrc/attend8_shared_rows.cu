@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
   unsigned char *const area = raw + (base - smem_at(raw));
   const uint32_t q_at = base, k_at = base + kRwTile, v_at = base + 3 * kRwTile;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // the warp: uniform for the compiler too
-  Prefixes pre(area + 5 * kRwTile, a.c.batch, a.p.batch, a.p.batch + (a.own_parts ? a.c.batch : 0));
+  Prefixes pre(a, area + 5 * kRwTile);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
           };
           if (p.list < a.p.batch) from(a.p, p.list);
           else from(a.c, p.list - a.p.batch);
-          seg.len = pre.len[p.list];
+          seg.len = pre.len(p.list);
           seg.x += p.u1 - p.u0;
           seg.top = seg.tail_top[0] = seg.tail_top[1] = 0;
           seg.last = -1;

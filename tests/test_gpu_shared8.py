@@ -173,21 +173,58 @@ def test_many_prefixes(dtype):
     check(c, p, to, own, pre, torch.randn(b, 2, 1, 128, generator=g).to(dtype))
 
 
-def test_the_most_sequences_and_prefixes():
+@pytest.mark.parametrize("n", [1, 17])
+def test_the_most_sequences_and_prefixes(n):
     g = gen(7)
     b = 1024
-    pre, own, to = [17] * b, [2] * b, [(i * 5) % b if i % 3 else 7 for i in range(b)]
+    pre, own, to = [17] * b, [n + 1] * b, [(i * 5) % b if i % 3 else 7 for i in range(b)]
     p, c = cache(g, 1, pre, "int8", BF16), cache(g, 1, own, "int8", BF16)
-    q = torch.randn(b, 1, 1, 128, generator=g).to(BF16)
+    q = torch.randn(b, 1, n, 128, generator=g).to(BF16)
     got = c[0].attend_shared(q.cuda(), p[0], i32(*to))
     for i in range(0, b, 41):
-        want, lim = sh.attend(q[i].double(), [sh.sequence(*p[1:], to[i], 17), sh.sequence(*c[1:], i, 2)], 1, 128 ** -0.5, BF16)
+        want, lim = sh.attend(q[i].double(), [sh.sequence(*p[1:], to[i], 17), sh.sequence(*c[1:], i, n + 1)], n, 128 ** -0.5, BF16)
         assert ((got[i].cpu().double() - want).abs() <= lim).all(), i
     more = lkv.Cache8(batch=1025, n_kv_heads=1, capacity=16, dtype=BF16)
     with pytest.raises(_lib.LKVError):
         c[0].attend_shared(q.cuda(), more)
     with pytest.raises(_lib.LKVError):
-        more.attend_shared(torch.zeros(1025, 1, 1, 128, dtype=BF16, device="cuda"), p[0])
+        more.attend_shared(torch.zeros(1025, 1, n, 128, dtype=BF16, device="cuda"), p[0])
+
+
+@pytest.mark.parametrize("n", [1, 9, 20])
+def test_offsets_past_32_bits(n):
+    """A prefix whose codes take over 2^32 bytes: the heads at its end, attended and taken."""
+    h, length = 136, (1 << 18) - 5
+    capacity = 1 << 18
+    g = torch.Generator(device="cuda").manual_seed(n)
+    codes = [torch.randint(-127, 128, (1, h, capacity, 128), dtype=torch.int8, device="cuda", generator=g) for _ in range(2)]
+    scale = [torch.full((1, h, capacity // 16), 2.0 ** -7, device="cuda") for _ in range(2)]
+    tail = [torch.randn(1, h, 16, 128, device="cuda", generator=g).to(BF16) for _ in range(2)]
+    p = lkv.Cache8.from_tensors(*codes, *scale, *tail, i32(length))
+    c = cache(gen(n), h, [n + 3, n], "int8", BF16)
+    q = torch.randn(2, h * 4, n, 128, generator=gen(n)).to(BF16)
+    got = c[0].attend_shared(q.cuda(), p)
+    for x in (0, h - 1):
+        k, v = ([t[:, x:x + 1].cpu() for t in (codes[i], scale[i], tail[i])] for i in (0, 1))
+        one, two = ([t[:, x:x + 1] for t in y] for y in c[1:])
+        for b, own in enumerate((n + 3, n)):
+            want, lim = sh.attend(q[b, 4 * x:4 * x + 4].double(), [sh.sequence(k, v, 0, length), sh.sequence(one, two, b, own)], n, 128 ** -0.5, BF16)
+            assert ((got[b, 4 * x:4 * x + 4].cpu().double() - want).abs() <= lim).all(), (x, b)
+    if n > 1:
+        return
+    d = lkv.Cache8(batch=1, n_kv_heads=h, capacity=capacity, dtype=BF16)
+    d.take(p, lengths=i32(length - 16))
+    for x in (0, h - 1):
+        for y, z in ((d.k_codes, codes[0]), (d.v_codes, codes[1])):
+            assert torch.equal(y[0, x, :length // 16 * 16 - 16], z[0, x, :length // 16 * 16 - 16])
+    blocks = torch.arange(1, capacity // 16 - 1, 2, dtype=torch.int32, device="cuda").expand(1, h, -1).contiguous()
+    kept = blocks.shape[2]
+    d.keep(blocks, i32(kept))
+    for x in (0, h - 1):
+        for y, z in ((d.k_codes, codes[0]), (d.v_codes, codes[1])):
+            assert torch.equal(y[0, x, :kept * 16].view(kept, 2048), z[0, x].view(-1, 2048)[blocks[0, x].long()])
+    d.check()
+    c[0].check()
 
 
 @pytest.mark.parametrize("n", [1, 20])
