@@ -219,7 +219,9 @@ __device__ __forceinline__ ListRow list_row(const SharedArgs &a, const Prefixes 
 // The kernel for many rows of bf16 caches and the join of what it leaves
 // (attend8_shared_rows.cu): row tiles of kSharedRows, units of kSharedStep tokens.
 constexpr int kSharedRows = 128, kSharedStep = 128;
-constexpr int kSharedStart = 7;  // steps' time that beginning a tile costs
+// Steps' time that beginning a tile costs. With 4, 7, 10 and 14: 8 x 256 tokens
+// behind 16K 635, 573, 581 and 596 us; 32 x 5 behind 8K 62, 59, 64 and 73.
+constexpr int kSharedStart = 7;
 cudaError_t launch_shared_rows(const SharedArgs &a, int ctas, cudaStream_t st);
 cudaError_t launch_shared_join(const SharedArgs &a, cudaStream_t st);
 

@@ -5,6 +5,36 @@
 
 namespace lkv {
 
+// A CTA takes pieces of 128-row tiles (attend8_shared.cuh), 128 tokens (8 blocks,
+// a step) at a time. With one row tile, steps take the place that row tiles have
+// in attend8_rows.cu: even and odd steps have four softmax warps each, a
+// reference, a total and an accumulator of their own, and while one half weighs
+// its step the tensor cores work for the other.
+//   - Four warps turn K's codes into fp16 tiles (exact), four V's, both as they
+//     lie in the cache, a row a token (128-byte swizzle); the next step's codes are
+//     in registers meanwhile. The product with V takes its tile with d along the
+//     rows, so nothing is transposed (which took half of a step's work).
+//   - One warp issues: S = Q K^T, and O += P V with P in tensor memory over S.
+//   - One warp reads the blocks' scales, four steps ahead.
+//   - Weights, references and units are those of attend8_rows.cu. At a piece's end
+//     the halves are added, row by row, and one copy takes the part to memory.
+// Tensor memory: S and O of both halves, all 512 columns.
+//
+// Bound, a step of 128 rows: products 1024 clocks; shared memory 1280 (Q, K and V
+// read by the products, K and V written); bytes 1390 at the measured copy rate.
+// It takes 2130 (8 x 256 tokens behind 16K) to 2450 (a step of 16 or 32 samples): the
+// chain of a half, weights 2850 and then P V and the next S 1000 to 1400, is two
+// steps long. Tensor pipe 39% active, issue slots 49%, LSU data pipe 44%. Beside
+// the steps a piece costs its beginning (5000 clocks: tables, rows, queries, each
+// a round trip or two) and its end (4000). On a GB300, 8 KV heads, 4 query heads: 32
+// samples of a 32K prompt, 14 steps a CTA, 33 us; 8 x 256 tokens behind 16K 535 us,
+// 1.03 PFLOP/s, 53% of the measured bf16 rate. Measured before: K, V and scales by
+// the same four warps 2870 us; warps with one role each 751; V as it lies and a
+// whole warp along with the issuing lane 637 (a lane on its own took 1900 clocks a
+// step to issue); 7 steps counted for a tile's beginning, 535. Slower: rows that
+// fill half a tile twice in it, each time for half of a step's tokens (half the
+// weights a warp, but the products' queue grows as long; 3% faster there, 4%
+// slower elsewhere); every warp finding its pieces by itself (registers: 680).
 constexpr uint32_t kShSmem = 5 * kRwTile + 1024;  // Q, K: 2, V: 2
 static_assert(kSharedRows == kRwRows && kSharedStep == kRwTok, "a tile is one of tensor memory's");
 
@@ -471,7 +501,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       if (warp == kShIssuer) {
         // -------------------------------------------------------------- products
         // The whole warp goes along, one lane issues: descriptors and addresses stay
-        // in uniform registers (a lane on its own took 1900 clocks a step to issue).
+        // in uniform registers.
         const int first = __shfl_sync(0xffffffffu, done, 0), stop = __shfl_sync(0xffffffffu, end, 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint32_t q_lo = q_at >> 4, k_lo = k_at >> 4, v_lo = v_at >> 4;
@@ -522,7 +552,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
         // -------------------------------------------------------------- scales
         const Units un(seg, z.tail);
         const float *const ksc = seg.scale[0], *const vsc = seg.scale[1];
-        // four steps' blocks at a time, a lane each, read four steps ahead (one step at a time: 3250 clocks a step)
+        // four steps' blocks at a time, a lane each, read four steps ahead
         float k = 0.f, v = 0.f;
         auto load = [&](int g) {
           const int b = (g - done + z.s0) * kRwBlocks + lane;
@@ -571,7 +601,8 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
 
 // Joins the parts of every row, of its prefix and of its own tokens: a warp a
 // row, a lane four values of d. Where the parts of both lie is read at once, and
-// then kJoinAtOnce parts at a time.
+// then kJoinAtOnce parts at a time. Bound by round trips: 65,536 rows of 2 to 3
+// parts 35 us, 100 MB (a part after another 42 us).
 constexpr int kJoinWarps = 8, kJoinAtOnce = 4;
 __global__ void __launch_bounds__(32 * kJoinWarps) k_shared_join(const __grid_constant__ SharedArgs a) {
   wait_prerequisites();

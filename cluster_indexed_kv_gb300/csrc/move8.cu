@@ -94,8 +94,10 @@ __host__ __device__ inline int64_t take_smem(int items) {
 // one cache may take one another's tokens in any order: columns do not depend
 // on one another. (Tails and lengths do, and come from a snapshot there.)
 //
-// Bound by bytes. On a GB300, one prompt of 8191 tokens (8 KV heads, int8)
-// into 16 sequences: see the table of cases.
+// Bound by bytes. On a GB300, 8 KV heads: one prompt of 8191 tokens into 16
+// sequences 49 us, 85% of the measured copy rate; 8 sequences of 32768 into
+// another cache 182 us (87%), and round within their own 190 us; 24 beams of 517
+// tokens put in order 9.5 us, two launches' latency.
 template <int DT, int CODE>
 __global__ void __launch_bounds__(32) k_cache8_take(const __grid_constant__ TakeArgs a) {
   extern __shared__ __align__(128) unsigned char area[];
@@ -325,65 +327,74 @@ __global__ void __launch_bounds__(256) k_cache8_keep_check(const __grid_constant
   }
 }
 
-// A CTA takes a run of a list between two caches; within one, a part (2048 /
-// split bytes) of every block of a list, in order: block j comes from one at or
-// behind j, so what a stage's stores overwrite has been loaded, and what later
-// stages load lies behind it. Lists of different heads and parts of blocks do
-// not depend on one another. The last CTA of a sequence sets its length.
+// What the kernels of a keep know of their (sequence, KV head) and tensor.
+struct KeepLane {
+  int64_t slice;
+  int b, kv, part, count, len, last;
+  bool go, older;
+  const int32_t *list;
+  const char *from;
+  char *to;
+  const float *from_scale;
+  float *to_scale;
+  __device__ __forceinline__ explicit KeepLane(const KeepArgs &a) {
+    part = (int)(blockIdx.x % a.split);
+    kv = (int)(blockIdx.x / a.split) & 1;
+    slice = blockIdx.x / a.split >> 1;
+    b = (int)(slice / a.to.n_kv_heads);
+    count = a.counts[b];
+    len = __ldcg(a.from.lengths + b);
+    go = count >= 0 && !(__ldcg(a.to.ticket + b) & kKeepBad);
+    list = a.blocks + slice * a.m;
+    from = (const char *)(kv ? a.from.v_codes : a.from.k_codes) + slice * a.from.capacity * kHeadDim;
+    to = (char *)(kv ? a.to.v_codes : a.to.k_codes) + slice * a.to.capacity * kHeadDim;
+    from_scale = (kv ? a.from.v_scale : a.from.k_scale) + slice * (a.from.capacity / kBlock);
+    to_scale = (kv ? a.to.v_scale : a.to.k_scale) + slice * (a.to.capacity / kBlock);
+    // where no partial block follows, the last kept block is the last one; older: the source's tail is not its
+    last = go && count > 0 && len % kBlock == 0 ? list[count - 1] : -1;
+    older = last >= 0 && last != (len - 1) / kBlock;
+  }
+  // Every CTA of the sequence has read its length when it arrives (one thread); the last sets it.
+  __device__ __forceinline__ void arrive(const KeepArgs &a) const {
+    if (((atomicAdd(a.to.ticket + b, 1) + 1) & ~kKeepBad) != 2 * a.to.n_kv_heads * a.split) return;
+    a.to.ticket[b] = 0;
+    if (go) a.to.lengths[b] = count * kBlock + len % kBlock;
+  }
+};
+
+// Between two caches: a CTA (a warp) takes a run of a list.
 //
-// Bound by bytes: see the table of cases.
+// Bound by bytes. On a GB300, half the blocks of 8 x 32768 tokens (8 KV heads,
+// int8): 98 us, 80% of the measured copy rate, the check of the lists among it;
+// of one such sequence 16 us.
 template <int DT, int CODE>
 __global__ void __launch_bounds__(32) k_cache8_keep(const __grid_constant__ KeepArgs a) {
   extern __shared__ __align__(128) unsigned char area[];
   __shared__ __align__(8) uint64_t full_bar[kMoveStages];
-  __shared__ float scales[kMoveStages][kMoveStage / 256];
-  const int lane = threadIdx.x, H = a.to.n_kv_heads;
+  __shared__ float scales[kMoveStages][32];
+  constexpr int per = kMoveStage / kBlockBytes;  // blocks of a stage, a lane each
+  const int lane = threadIdx.x;
   if (lane == 0) {
     for (int i = 0; i < kMoveStages; ++i) bar_init(&full_bar[i], 32);
     bar_init_fence();
   }
   __syncwarp();
   wait_prerequisites();
-  const int part = (int)(blockIdx.x % a.split), kv = (int)(blockIdx.x / a.split) & 1;
-  const int64_t slice = blockIdx.x / a.split >> 1;
-  const int b = (int)(slice / H);
-  const int count = a.counts[b], len = __ldcg(a.from.lengths + b);
-  const bool bad = __ldcg(a.to.ticket + b) & kKeepBad, go = count >= 0 && !bad;
-  const int unit = a.inside ? kBlockBytes / a.split : kBlockBytes, at = a.inside ? part * unit : 0, per = kMoveStage / unit;
-  int j0 = 0, j1 = go ? count : 0;
-  if (go && !a.inside) {
-    j0 = (int)((int64_t)count * part / a.split);
-    j1 = (int)((int64_t)count * (part + 1) / a.split);
+  const KeepLane z(a);
+  int j0 = 0, j1 = 0;
+  if (z.go) {
+    j0 = (int)((int64_t)z.count * z.part / a.split);
+    j1 = (int)((int64_t)z.count * (z.part + 1) / a.split);
   }
-  const int32_t *list = a.blocks + slice * a.m;
-  const char *from = (const char *)(kv ? a.from.v_codes : a.from.k_codes) + slice * a.from.capacity * kHeadDim + at;
-  char *to = (char *)(kv ? a.to.v_codes : a.to.k_codes) + slice * a.to.capacity * kHeadDim + at;
-  const float *from_scale = (kv ? a.from.v_scale : a.from.k_scale) + slice * (a.from.capacity / kBlock);
-  float *to_scale = (kv ? a.to.v_scale : a.to.k_scale) + slice * (a.to.capacity / kBlock);
-  const bool rest = len % kBlock != 0;                                   // a partial block follows
-  const int last = go && count > 0 && !rest ? list[count - 1] : -1;      // otherwise the last kept block is the last one
-  const bool older = last >= 0 && last != (len - 1) / kBlock;            // of which the source's tail is not
-
-  // two of a stage's blocks at most are a lane's; their numbers are read a stage ahead
-  int next[2];
-  auto fetch = [&](int64_t j) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) next[k] = lane + 32 * k < per && j + lane + 32 * k < j1 ? list[j + lane + 32 * k] : 0;
-  };
+  int next;  // a lane's block of the stage to come: read a stage ahead
+  auto fetch = [&](int64_t j) { next = lane < per && j + lane < j1 ? z.list[j + lane] : 0; };
   auto issue = [&](int64_t j, int st) {
     if (j < j1) {
-      uint32_t bytes = 0;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (lane + 32 * k < per && j + lane + 32 * k < j1) bytes += unit;
-      bar_expect(&full_bar[st], bytes);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int i = lane + 32 * k;
-        if (i < per && j + i < j1) {
-          bulk_load(area + st * kMoveStage + i * unit, from + (int64_t)next[k] * kBlockBytes, unit, &full_bar[st]);
-          if (at == 0 || j + i == count - 1) word_load(&scales[st][i], from_scale + next[k]);
-        }
+      const bool mine = lane < per && j + lane < j1;
+      bar_expect(&full_bar[st], mine ? kBlockBytes : 0);
+      if (mine) {
+        bulk_load(area + st * kMoveStage + lane * kBlockBytes, z.from + (int64_t)next * kBlockBytes, kBlockBytes, &full_bar[st]);
+        word_load(&scales[st][lane], z.from_scale + next);
       }
       fetch(j + per);
     }
@@ -401,19 +412,15 @@ __global__ void __launch_bounds__(32) k_cache8_keep(const __grid_constant__ Keep
       break;
     }
     phase ^= 1u << st;
-    word_wait<kMoveStages - 2>();  // one group a stage, the stages behind this one but for the next to be filled
+    word_wait<kMoveStages - 2>();
     __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int x = lane + 32 * k;
-      if (x < per && j + x < j1) {
-        bulk_store(to + (j + x) * kBlockBytes, area + st * kMoveStage + x * unit, unit);
-        if (at == 0) to_scale[j + x] = scales[st][x];
-      }
+    if (lane < per && j + lane < j1) {
+      bulk_store(z.to + (j + lane) * kBlockBytes, area + st * kMoveStage + lane * kBlockBytes, kBlockBytes);
+      z.to_scale[j + lane] = scales[st][lane];
     }
-    if (older && count - 1 < min((int64_t)j1, j + per) && count > j)
-      to_tail<DT, CODE>(tail_of<DT>(kv ? a.to.v_tail : a.to.k_tail, slice), area + st * kMoveStage + (count - 1 - j) * unit, at, at + unit,
-                        scales[st][count - 1 - j], lane);
+    const int64_t at = z.count - 1 - j;  // of the last kept block, in this stage
+    if (z.older && at >= 0 && at < per && z.count <= j1)
+      to_tail<DT, CODE>(tail_of<DT>(z.kv ? a.to.v_tail : a.to.k_tail, z.slice), area + st * kMoveStage + at * kBlockBytes, 0, kBlockBytes, scales[st][at], lane);
     bulk_commit();
     if (i > 0) {
       bulk_wait_read<1>();
@@ -427,14 +434,75 @@ __global__ void __launch_bounds__(32) k_cache8_keep(const __grid_constant__ Keep
   }
   word_wait<0>();
   bulk_wait_all();
-  if (go && !a.inside && part == 0 && (rest || (last >= 0 && !older)))
-    copy_tail<DT>(tail_of<DT>(kv ? a.to.v_tail : a.to.k_tail, slice), tail_of<DT>(kv ? a.from.v_tail : a.from.k_tail, slice), lane);
+  if (z.go && z.part == 0 && (z.len % kBlock != 0 || (z.last >= 0 && !z.older)))
+    copy_tail<DT>(tail_of<DT>(z.kv ? a.to.v_tail : a.to.k_tail, z.slice), tail_of<DT>(z.kv ? a.from.v_tail : a.from.k_tail, z.slice), lane);
   __syncwarp();
-  // every CTA of the sequence has read its length when it arrives
-  if (lane == 0 && ((atomicAdd(a.to.ticket + b, 1) + 1) & ~kKeepBad) == 2 * H * a.split) {
-    a.to.ticket[b] = 0;
-    if (go) a.to.lengths[b] = count * kBlock + len % kBlock;
+  if (lane == 0) z.arrive(a);
+}
+
+// Within one cache: a CTA takes the same `unit` bytes of every block of a list,
+// in order, kInsideLoads of 16 a thread at a time. Block j comes from one at or
+// behind j, so what a run of blocks overwrites lies before what later runs read,
+// and its own sources have been read when every thread is at the barrier. Lists
+// of different heads and parts of blocks do not depend on one another.
+//
+// Bound by bytes, or by what few CTAs keep on their way. On a GB300, half the
+// blocks of 8 x 32768 tokens 128 us, 62% of the measured copy rate; of one such
+// sequence 21 us (67 us with bulk copies of 256 bytes, which the copy engine
+// takes as long for as for 2 KB).
+constexpr int kInsideThreads = 256, kInsideLoads = 4;
+constexpr int kInsideBytes = kInsideThreads * kInsideLoads * 16;  // of a run
+template <int DT, int CODE>
+__global__ void __launch_bounds__(kInsideThreads) k_cache8_keep_inside(const __grid_constant__ KeepArgs a) {
+  wait_prerequisites();
+  const KeepLane z(a);
+  const int unit = kBlockBytes / a.split, at = z.part * unit, chunks = unit / 16, per = kInsideBytes / unit;  // 16-byte chunks of a unit, blocks of a run
+  const int count = z.go ? z.count : 0;
+  // the thread's k-th chunk of a run: block block(k), bytes byte(k) of it
+  auto block = [&](int k) { return (k * kInsideThreads + (int)threadIdx.x) / chunks; };
+  auto byte = [&](int k) { return at + (k * kInsideThreads + (int)threadIdx.x) % chunks * 16; };
+  const bool scales = z.part == 0 && (int)threadIdx.x < per;
+  uint4 x[kInsideLoads], y[kInsideLoads];
+  float sx = 0.f, sy = 0.f;
+  auto load = [&](int64_t j, uint4 (&w)[kInsideLoads], float &s) {
+#pragma unroll
+    for (int k = 0; k < kInsideLoads; ++k) {
+      w[k] = make_uint4(0, 0, 0, 0);
+      if (j + block(k) < count) w[k] = __ldcg((const uint4 *)(z.from + (int64_t)z.list[j + block(k)] * kBlockBytes + byte(k)));
+    }
+    if (scales && j + threadIdx.x < count) s = __ldcg(z.from_scale + z.list[j + threadIdx.x]);
+  };
+  auto store = [&](int64_t j, const uint4 (&w)[kInsideLoads], float s) {
+#pragma unroll
+    for (int k = 0; k < kInsideLoads; ++k) {
+      if (j + block(k) >= count) continue;
+      *(uint4 *)(z.to + (j + block(k)) * kBlockBytes + byte(k)) = w[k];
+      if (z.older && j + block(k) == count - 1) {  // the last kept block's values into the tail
+        const float scale = __ldcg(z.from_scale + z.last);
+        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v[4];
+          decode4<CODE>(u[e], v);
+          char *tail = tail_of<DT>(z.kv ? a.to.v_tail : a.to.k_tail, z.slice) + (byte(k) + 4 * e) * (DT == 1 ? 2 : 4);
+          if (DT == 1) *(uint2 *)tail = make_uint2(pack_bf16(v[0] * scale, v[1] * scale), pack_bf16(v[2] * scale, v[3] * scale));
+          else *(float4 *)tail = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
+        }
+      }
+    }
+    if (scales && j + threadIdx.x < count) z.to_scale[j + threadIdx.x] = s;
+  };
+  if (count > 0) load(0, x, sx);
+  for (int64_t j = 0; j < count; j += 2 * per) {
+    load(j + per, y, sy);
+    __syncthreads();
+    store(j, x, sx);
+    load(j + 2 * per, x, sx);
+    __syncthreads();
+    store(j + per, y, sy);
   }
+  __syncthreads();
+  if (threadIdx.x == 0) z.arrive(a);
 }
 
 // What two caches of one call have to be; *inside: they are the same one.
@@ -553,11 +621,13 @@ extern "C" lkv_status lkv_cache8_keep(const lkv_cache8 *c, const lkv_cache8 *sou
   a.counts = counts;
   a.m = m;
   a.inside = inside;
-  // CTAs for a GPU full of them: runs of lists, or parts of 256 bytes at least
+  // CTAs for a GPU full of them: runs of 8 blocks of a list at least, or parts
+  // of 128 bytes of its blocks, no more than the GPU holds at once (of 8 x 32768
+  // tokens in place, 256 CTAs and 512: 128 and 157 us)
   const int64_t want = ((int64_t)kMovePerSm * sms + 2 * slices - 1) / (2 * slices);
   a.split = 1;
   if (inside)
-    while (a.split < 8 && a.split < want) a.split *= 2;
+    while (a.split < 16 && 2 * slices * 2 * a.split <= 2 * sms) a.split *= 2;
   else
     a.split = (int32_t)(want < (m + 7) / 8 ? want : (m + 7) / 8 < 1 ? 1 : (m + 7) / 8);
   if (2 * slices * a.split > 0x7fffffff) return refuse("lkv_cache8_keep: too many sequences");
@@ -566,6 +636,12 @@ extern "C" lkv_status lkv_cache8_keep(const lkv_cache8 *c, const lkv_cache8 *sou
   const dim3 grid((unsigned)(2 * slices * a.split));
   const size_t smem = kMoveStages * kMoveStage;
   const bool bf = c->dtype == LKV_DTYPE_BF16, i8 = c->code == LKV_CODE_INT8;
+  if (inside) {
+    auto *fn = bf ? (i8 ? k_cache8_keep_inside<1, LKV_CODE_INT8> : k_cache8_keep_inside<1, LKV_CODE_E4M3>)
+                  : (i8 ? k_cache8_keep_inside<0, LKV_CODE_INT8> : k_cache8_keep_inside<0, LKV_CODE_E4M3>);
+    e = launch_next(fn, grid, kInsideThreads, 0, st, a);
+    return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_keep", e);
+  }
   if (bf) e = i8 ? launch_sized(k_cache8_keep<1, LKV_CODE_INT8>, grid, smem, st, a) : launch_sized(k_cache8_keep<1, LKV_CODE_E4M3>, grid, smem, st, a);
   else e = i8 ? launch_sized(k_cache8_keep<0, LKV_CODE_INT8>, grid, smem, st, a) : launch_sized(k_cache8_keep<0, LKV_CODE_E4M3>, grid, smem, st, a);
   return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_keep", e);

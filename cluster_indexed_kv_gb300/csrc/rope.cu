@@ -26,7 +26,9 @@ namespace lkv {
 // Bound: the tensors' bytes, once in and once out. On a GB300, 40 heads x 32K
 // tokens of bf16 take 100 us, 98% of the measured copy rate, in either layout
 // (148 us before each thread kept eight vectors' loads in flight); one token of
-// 8 sequences 1.9 us.
+// 8 sequences 1.9 us. Positions on several axes cost a select a pair: 40 heads x
+// 32K tokens on three axes 102 us, 97% of the copy rate; 32 heads x 5476 patches
+// in fp32 28.6 us, 92%.
 constexpr int kRopeThreads = 128;
 
 struct RopeArgs {
