@@ -2,6 +2,7 @@
 // caches: the prefixes' part, and for many rows a sequence the own tokens' too.
 #include "attend8_rows.cuh"
 #include "attend8_shared.cuh"
+#include "tma.cuh"
 
 namespace lkv {
 
@@ -140,8 +141,8 @@ __device__ __forceinline__ void store_part(const SharedArgs &a, const SharedPiec
   group_sync(1, 32 * kShSoft);
   float *const part = a.parts + ((int64_t)blockIdx.x + z.p.tile) * part_floats(kRwRows);
   if (threadIdx.x == 0) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(part), "r"(smem_at(stage)), "r"(kRwRows * kHeadDim * 4) : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    bulk_store(part, stage, kRwRows * kHeadDim * 4);
+    bulk_commit();
   }
   if (w == 0) {
     float *const p = part + kRwRows * kHeadDim + r;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       // the producers write where the part before is copied from
-      if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      if (threadIdx.x == 0) bulk_wait_read<0>();
       __syncthreads();
       const bool valid = seg.at[row] >= 0, any = __any_sync(0xffffffffu, valid);
       const int pos = valid ? seg.pos[row] : -1;
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
         done += st.s1 - st.s0;
       }
     }
-    if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (threadIdx.x == 0) bulk_wait_all();
     tmem_before();
     __syncthreads();
   } else if (warp < kShIssuer) {
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
     __syncthreads();
     tmem_after();
     if (warp == kShIssuer) {
-      if (lane == 0) {  // every product has completed before the tensor memory is freed
+      if (elect_one()) {  // every product (of this lane, as elected before) has completed before the tensor memory is freed
         mma_commit(&sy.drained);
         bar_wait(&sy.drained, 0);
         if (abort_s) atomicOr(a.c.ticket + a.c.batch, kAnomTimeout);

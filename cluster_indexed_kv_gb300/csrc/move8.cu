@@ -18,17 +18,6 @@ constexpr int kTakeItems = 32;           // destinations of a CTA between two ca
 constexpr int kTakeInside = 1024;        // and within one, all of them: 16 bytes of each in a stage
 constexpr int32_t kKeepBad = 1 << 30;    // in a ticket: the sequence's lists are refused
 
-__device__ __forceinline__ void bulk_load(void *to, const void *from, uint32_t bytes, uint64_t *bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(smem_at(to)), "l"(from), "r"(bytes), "r"(smem_at(bar)) : "memory");
-}
-__device__ __forceinline__ void bulk_store(void *to, const void *from, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(smem_at(from)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // a float to shared memory, by the thread's own groups
 __device__ __forceinline__ void word_load(float *to, const float *from) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_at(to)), "l"(from) : "memory");

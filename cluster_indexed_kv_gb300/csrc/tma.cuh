@@ -1,4 +1,4 @@
-// tma.cuh -- mbarriers and tensor copies of the 8-bit cache's attention.
+// tma.cuh -- mbarriers, tensor copies and bulk copies of the 8-bit cache's kernels.
 #pragma once
 
 #include <cuda.h>
@@ -46,6 +46,20 @@ __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int x,
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
       ::"r"(smem_at(dst)), "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(smem_at(bar)) : "memory");
 }
+
+// Copies of whole 16 bytes between shared and global memory; a store belongs to
+// the thread's group that the next bulk_commit ends.
+__device__ __forceinline__ void bulk_load(void *to, const void *from, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_at(to)), "l"(from), "r"(bytes), "r"(smem_at(bar)) : "memory");
+}
+__device__ __forceinline__ void bulk_store(void *to, const void *from, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(smem_at(from)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)map) : "memory");

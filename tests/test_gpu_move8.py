@@ -100,6 +100,17 @@ def test_take_of_what_is_not_there(inside):
         checked(d, bad)
 
 
+def test_take_of_each_ones_own_from_a_smaller_cache():
+    """Without a list, sequences that the source does not have are refused."""
+    src, dst = mv.filled(2, 1, 64, "int8", BF16, [50, 3], 1), mv.filled(4, 1, 64, "int8", BF16, [3, 4, 5, 6], 2)
+    s, d = upload(src), upload(dst)
+    want, bad = mv.take(dst, src, None, None)
+    assert bad == {2, 3}
+    d.take(s)
+    mv.same(download(d), want)
+    checked(d, bad)
+
+
 def test_take_past_the_capacity_is_reported_as_that():
     src, dst = mv.filled(1, 1, 64, "int8", BF16, [50], 1), mv.filled(2, 1, 32, "int8", BF16, [3, 4], 2)
     s, d = upload(src), upload(dst)

@@ -53,6 +53,11 @@ CASES = [  # prefixes' lengths, own lengths, prefix_of, KV heads, group, n
     ([1000], [70, 65], None, 1, 4, 65),
     ([513, 40], [9] * 40, [b % 3 for b in range(40)], 1, 3, 2),
     ([130], [300, 150], None, 2, 16, 129),
+    ([300], [20] * 16, None, 1, 1, 1),           # 16 rows, and 17
+    ([300], [20] * 17, None, 1, 1, 1),
+    ([300, 200], [20] * 7, [0, 1, 0, 1, 0, 1, 0], 2, 2, 4),   # 8 rows a sequence, and 9
+    ([300, 200], [20] * 7, [0, 1, 0, 1, 0, 1, 0], 2, 3, 3),
+    ([4000, 128, 127], [700, 256, 255, 129], [0, 1, 2, 0], 1, 128, 1),
 ]
 
 
