@@ -22,20 +22,24 @@ namespace lkv {
 // Tensor memory: S and O of both halves, all 512 columns.
 //
 // Bound, a step of 128 rows: products 1024 clocks; shared memory 1280 (Q, K and V
-// read by the products, K and V written); bytes 1390 at the measured copy rate.
-// It takes 2130 (8 x 256 tokens behind 16K) to 2450 (a step of 16 or 32 samples): the
-// chain of a half, weights 2850 and then P V and the next S 1000 to 1400, is two
-// steps long. Tensor pipe 39% active, issue slots 49%, LSU data pipe 44%. Beside
-// the steps a piece costs its beginning (5000 clocks: tables, rows, queries, each
-// a round trip or two) and its end (4000). On a GB300, 8 KV heads, 4 query heads: 32
-// samples of a 32K prompt, 14 steps a CTA, 33 us; 8 x 256 tokens behind 16K 535 us,
-// 1.03 PFLOP/s, 53% of the measured bf16 rate. Measured before: K, V and scales by
-// the same four warps 2870 us; warps with one role each 751; V as it lies and a
-// whole warp along with the issuing lane 637 (a lane on its own took 1900 clocks a
-// step to issue); 7 steps counted for a tile's beginning, 535. Slower: rows that
-// fill half a tile twice in it, each time for half of a step's tokens (half the
-// weights a warp, but the products' queue grows as long; 3% faster there, 4%
-// slower elsewhere); every warp finding its pieces by itself (registers: 680).
+// read by the products, K and V written), 1540 with the codes that pass through the
+// same memory on their way in; bytes 1390 at the measured copy rate. It takes 2130
+// (8 x 256 tokens behind 16K) to 2400 (a step of 16 or 32 samples): the chain of a
+// half, weights 2850 and then P V and the next S 1000 to 1400, is two steps long,
+// and the producers work 1500 to 1800 of the time. Tensor pipe 39% active, issue
+// slots 49%, LSU data pipe 44%. Beside the steps a piece costs its beginning (5000
+// clocks: tables, rows, queries, each a round trip or two) and its end (3000 to
+// 4000). On a GB300, 8 KV heads, 4 query heads: 32 samples of a 32K prompt, 14 steps a
+// CTA, 30 us; 8 x 256 tokens behind 16K 535 us, 1.03 PFLOP/s, 53% of the measured
+// bf16 rate. Measured before, the latter: K, V and scales by the same four warps
+// 2870 us; warps with one role each 751; V as it lies and a whole warp along with
+// the issuing lane 637 (a lane on its own took 1900 clocks a step to issue); 7
+// steps counted for a tile's beginning, 535. Slower: the scores of 64 tokens at a
+// time, over columns that the other half's weights do not need (the wait for S
+// goes, but Q is read twice: a call 599 against 570); rows that fill half a tile
+// twice in it, each time for half of a step's tokens (half the weights a warp, but
+// the products' queue grows as long; 3% faster there, 4% slower elsewhere); every
+// warp finding its pieces by itself (registers: 680 against 637).
 constexpr uint32_t kShSmem = 5 * kRwTile + 1024;  // Q, K: 2, V: 2
 static_assert(kSharedRows == kRwRows && kSharedStep == kRwTok, "a tile is one of tensor memory's");
 

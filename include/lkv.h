@@ -519,7 +519,7 @@ lkv_status lkv_rope_init(const lkv_rope_params *params, lkv_rope *rope);
  * other overlap of an output with an input or output is LKV_EINVAL. batch, n
  * and the head counts may be 0. *rope is read before the call returns.
  * Asynchronous on stream. Errors: LKV_EINVAL, LKV_ECUDA.
- * The kernels of lkv_rope_apply and lkv_cache8_write let a following kernel
+ * The kernels of lkv_rope_apply(_axes) and lkv_cache8_write let a following kernel
  * that is launched with programmatic stream serialization start before they
  * end: such a kernel has to wait (griddepcontrol.wait) before it touches their
  * tensors. Every other launch, copy and event comes after them as usual. */
