@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
           seg.p = p;
           auto from = [&](const lkv_cache8 &c, int b) {
             const int64_t slice = (int64_t)b * c.n_kv_heads + p.h, codes = slice * c.capacity * kHeadDim, tail = slice * kBlock * kHeadDim;
-                seg.codes[0] = (const uint8_t *)c.k_codes + codes;
+            seg.codes[0] = (const uint8_t *)c.k_codes + codes;
             seg.codes[1] = (const uint8_t *)c.v_codes + codes;
             seg.scale[0] = c.k_scale + slice * (c.capacity / kBlock);
             seg.scale[1] = c.v_scale + slice * (c.capacity / kBlock);
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       const uint8_t *const codes = seg.codes[kv] + (32 * pw + (lane >> 3)) * kHeadDim + 16 * (lane & 7);
       // 4 whole rows a load, 16 codes a lane: a load takes a pass for each 128-byte
       // line. What is read for one row tile alone passes by the caches (16 samples
-      // of 131K tokens 97 -> 86 us), what others read too stays (8 x 256
+      // of 131K tokens 97 -> 88 us), what others read too stays (8 x 256
       // tokens behind 16K, 64 row tiles a KV head: 582 us where it does not, 570).
       const bool once = seg.once;
       auto load = [&](int j) {

@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdio>
+#include <type_traits>
 
 #include "../../include/lkv.h"
 #include "lkv_internal.cuh"
@@ -73,8 +74,8 @@ bool caches_overlap(const lkv_cache8 *a, const lkv_cache8 *b);
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-template <class Args>
-inline cudaError_t launch_next(void (*fn)(Args), dim3 grid, int block, size_t smem, cudaStream_t st, const Args &args) {
+template <class... Args>
+inline cudaError_t launch_next(void (*fn)(Args...), dim3 grid, int block, size_t smem, cudaStream_t st, const std::common_type_t<Args> &...args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
@@ -85,7 +86,7 @@ inline cudaError_t launch_next(void (*fn)(Args), dim3 grid, int block, size_t sm
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, args);
+  return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

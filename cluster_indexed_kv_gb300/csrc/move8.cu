@@ -59,18 +59,52 @@ __device__ __forceinline__ char *tail_of(void *tails, int64_t slice) {
 // ---------------------------------------------------------------- take
 
 struct TakeArgs {
-  lkv_cache8 to, from;            // from: lengths and tails are the snapshot's within one cache
+  lkv_cache8 to, from;            // from: within one cache, lengths are those before the call
   const int32_t *sequences, *lengths;
+  void *new_tails[2];             // within one cache: the sequences' tails, made before any is written
   int32_t items;                  // destinations of a CTA
   int32_t inside;
 };
 
-// What a sequence becomes: its source (-1: it is left as it is), its length,
-// which slot of a stage holds the source's bytes (-1: none is needed), and its
-// last block where that is not the source's last one (-1: the source's tail is its own).
-struct TakeItem { int32_t from, len, slot, older; };
-// Which blocks of a source the stages hold.
-struct TakeSlot { int32_t from, lo, hi; };
+// What a sequence becomes: its source (-1: it is left as it is), how much of it,
+// and what is wrong with that.
+struct Taken {
+  int from, len, have, anomaly;
+  __device__ __forceinline__ Taken(const TakeArgs &a, int b) : from(a.sequences ? a.sequences[b] : b), len(0), have(0), anomaly(0) {
+    if (from < -1 || from >= a.from.batch) {
+      anomaly = kAnomRange;
+    } else if (from >= 0) {
+      have = a.from.lengths[from];
+      len = a.lengths ? a.lengths[b] : have;
+      if (have < 0 || have > a.from.capacity || len < 0 || len > have) anomaly = kAnomRange;
+      else if (len > a.to.capacity) anomaly = kAnomCapacity;
+    }
+    if (anomaly) from = -1;
+  }
+  // its last block, where that is not the source's last one (-1: the source's tail is its own)
+  __device__ __forceinline__ int older() const { return len > 0 && (len - 1) / kBlock != (have - 1) / kBlock ? (len - 1) / kBlock : -1; }
+  // whether its tail changes
+  __device__ __forceinline__ bool moves(const TakeArgs &a, int b) const { return from >= 0 && len > 0 && !(a.inside && from == b && older() < 0); }
+};
+
+// The tail of a sequence that is to be `x`, by a whole warp: the source's own, or
+// its last block's rows as lkv_cache8_read gives them.
+template <int DT, int CODE>
+__device__ __forceinline__ void make_tail(const TakeArgs &a, const Taken &x, int h, int kv, void *to, int lane) {
+  const int64_t slice = (int64_t)x.from * a.from.n_kv_heads + h;
+  const int older = x.older();
+  if (older < 0) {
+    copy_tail<DT>(to, tail_of<DT>(kv ? a.from.v_tail : a.from.k_tail, slice), lane);
+  } else {
+    const unsigned char *codes = (const unsigned char *)(kv ? a.from.v_codes : a.from.k_codes) + (slice * a.from.capacity + (int64_t)older * kBlock) * kHeadDim;
+    to_tail<DT, CODE>(to, codes, 0, kBlockBytes, (kv ? a.from.v_scale : a.from.k_scale)[slice * (a.from.capacity / kBlock) + older], lane);
+  }
+}
+
+// A sequence of the plan: its source, its length, and which slot of a stage holds the source's bytes (-1: none is needed).
+struct TakeItem { int32_t from, len, slot; };
+// How many blocks of a source the stages hold.
+struct TakeSlot { int32_t from, hi; };
 
 __host__ __device__ inline int64_t take_smem(int items) {
   const int words = items > kMoveStage / kBlockBytes ? items : kMoveStage / kBlockBytes;
@@ -81,12 +115,13 @@ __host__ __device__ inline int64_t take_smem(int items) {
 // K or V, in every sequence of its group. It loads each distinct source's once,
 // and only when all of a column have arrived stores them, so that sequences of
 // one cache may take one another's tokens in any order: columns do not depend
-// on one another. (Tails and lengths do, and come from a snapshot there.)
+// on one another. Tails and lengths do: there they are made by a kernel before
+// this one, from the cache as it was.
 //
 // Bound by bytes. On a GB300, 8 KV heads: one prompt of 8191 tokens into 16
-// sequences 49 us, 85% of the measured copy rate; 8 sequences of 32768 into
-// another cache 182 us (87%), and round within their own 190 us; 24 beams of 517
-// tokens put in order 9.5 us, two launches' latency.
+// sequences 48 us, 87% of the measured copy rate; 8 sequences of 32768 into
+// another cache 175 us (91%), and round within their own 185 us; 24 beams of 517
+// tokens put in order 10.3 us, two launches' latency.
 template <int DT, int CODE>
 __global__ void __launch_bounds__(32) k_cache8_take(const __grid_constant__ TakeArgs a) {
   extern __shared__ __align__(128) unsigned char area[];
@@ -109,47 +144,29 @@ __global__ void __launch_bounds__(32) k_cache8_take(const __grid_constant__ Take
   int nslots = 0, most = 0;
   for (int i0 = 0; i0 < count; i0 += 32) {
     const int i = i0 + lane, b = first + i;
-    int from = -1, len = 0, lo = 0, hi = 0, older = -1, anomaly = 0;
+    int from = -1, len = 0, hi = 0;
     if (i < count) {
-      from = a.sequences ? a.sequences[b] : b;
-      if (from < -1 || from >= a.from.batch) anomaly = kAnomRange;
-      else if (from >= 0) {
-        const int have = a.from.lengths[from];
-        len = a.lengths ? a.lengths[b] : have;
-        if (have < 0 || have > a.from.capacity || len < 0 || len > have) anomaly = kAnomRange;
-        else if (len > a.to.capacity) anomaly = kAnomCapacity;
-        else if (len > 0) {
-          const int last = (len - 1) / kBlock;
-          if (last != (have - 1) / kBlock) older = last;  // its tail comes from codes
-          if (a.inside && from == b) {
-            lo = max(older, 0);
-            hi = older + 1;
-          } else {
-            hi = max(older + 1, len / kBlock);
-          }
-        }
-      }
-      if (anomaly) from = -1;
+      const Taken x(a, b);
+      from = x.from;
+      len = x.len;
+      if (from >= 0 && !(a.inside && from == b)) hi = len / kBlock;
       if (blockIdx.x == 0) {
-        if (anomaly) atomicOr(a.to.ticket + a.to.batch, anomaly);
+        if (x.anomaly) atomicOr(a.to.ticket + a.to.batch, x.anomaly);
         else if (from >= 0) a.to.lengths[b] = len;
       }
     }
-    const bool need = hi > lo;
+    const bool need = hi > 0;
     const uint32_t same = __match_any_sync(0xffffffffu, need ? from : -2 - lane);
     const int leader = __ffs(same) - 1;
     for (uint32_t rest = __reduce_or_sync(0xffffffffu, same & ~(1u << leader)); rest; rest &= rest - 1) {
       const int l2 = __ffs(rest) - 1;
-      const int lo2 = __shfl_sync(0xffffffffu, lo, l2), hi2 = __shfl_sync(0xffffffffu, hi, l2), of = __shfl_sync(0xffffffffu, leader, l2);
-      if (of == lane) {
-        lo = min(lo, lo2);
-        hi = max(hi, hi2);
-      }
+      const int hi2 = __shfl_sync(0xffffffffu, hi, l2), of = __shfl_sync(0xffffffffu, leader, l2);
+      if (of == lane) hi = max(hi, hi2);
     }
     const uint32_t lead = __ballot_sync(0xffffffffu, need && leader == lane);
     const int slot = nslots + __popc(lead & ((1u << leader) - 1u));
-    if (i < count) items[i] = TakeItem{from, len, need ? slot : -1, older};
-    if (need && leader == lane) slots[slot] = TakeSlot{from, lo, hi};
+    if (i < count) items[i] = TakeItem{from, len, need ? slot : -1};
+    if (need && leader == lane) slots[slot] = TakeSlot{from, hi};
     nslots += __popc(lead);
     most = max(most, (int)__reduce_max_sync(0xffffffffu, (uint32_t)hi));
   }
@@ -176,21 +193,22 @@ __global__ void __launch_bounds__(32) k_cache8_take(const __grid_constant__ Take
       place(task, c0, h, kv);
       uint32_t bytes = 0;
       for (int j = lane; j < nslots; j += 32) {
-        const int64_t r0 = max(c0, (int64_t)slots[j].lo * kBlockBytes), r1 = min(c0 + unit, (int64_t)slots[j].hi * kBlockBytes);
-        if (r1 > r0) bytes += (uint32_t)(r1 - r0);
+        const int64_t r1 = min(c0 + unit, (int64_t)slots[j].hi * kBlockBytes);
+        if (r1 > c0) bytes += (uint32_t)(r1 - c0);
       }
       bar_expect(&full_bar[st], bytes);
       for (int j = lane; j < nslots; j += 32) {
         const TakeSlot s = slots[j];
-        const int64_t r0 = max(c0, (int64_t)s.lo * kBlockBytes), r1 = min(c0 + unit, (int64_t)s.hi * kBlockBytes);
-        if (r1 <= r0) continue;
+        const int64_t r1 = min(c0 + unit, (int64_t)s.hi * kBlockBytes);
+        if (r1 <= c0) continue;
         const int64_t slice = (int64_t)s.from * H + h;
-        bulk_load(stages + st * kMoveStage + j * unit + (r0 - c0), (const char *)(kv ? a.from.v_codes : a.from.k_codes) + slice * slice_codes + r0,
-                  (uint32_t)(r1 - r0), &full_bar[st]);
+        bulk_load(stages + st * kMoveStage + j * unit, (const char *)(kv ? a.from.v_codes : a.from.k_codes) + slice * slice_codes + c0, (uint32_t)(r1 - c0),
+                  &full_bar[st]);
+        if (c0 % kBlockBytes) continue;  // a block's scale goes with its first bytes
         const float *from = (kv ? a.from.v_scale : a.from.k_scale) + slice * slice_scales;
         const int k0 = (int)(c0 / kBlockBytes);
         for (int k = 0; k < blocks; ++k)
-          if (k0 + k >= s.lo && k0 + k < s.hi) word_load(scales + st * words + j * blocks + k, from + k0 + k);
+          if (k0 + k < s.hi) word_load(scales + st * words + j * blocks + k, from + k0 + k);
       }
     }
     word_commit();
@@ -214,33 +232,17 @@ __global__ void __launch_bounds__(32) k_cache8_take(const __grid_constant__ Take
     int h, kv;
     place(task, c0, h, kv);
     const int k0 = (int)(c0 / kBlockBytes);
-    for (int i0 = 0; i0 < count; i0 += 32) {
-      const int it = i0 + lane;
-      TakeItem x{-1, 0, -1, -1};
-      if (it < count) x = items[it];
-      const int b = first + it;
-      bool older = false;
-      if (x.slot >= 0) {
-        const int64_t slice = (int64_t)b * H + h;
-        const int fullb = x.len / kBlock;
-        if (!(a.inside && x.from == b)) {
-          const int64_t r1 = min(c0 + unit, (int64_t)fullb * kBlockBytes);
-          if (r1 > c0)
-            bulk_store((char *)(kv ? a.to.v_codes : a.to.k_codes) + slice * a.to.capacity * kHeadDim + c0, stages + st * kMoveStage + x.slot * unit,
-                       (uint32_t)(r1 - c0));
-          if (c0 % kBlockBytes == 0)
-            for (int k = 0; k < blocks; ++k)
-              if (k0 + k < fullb) (kv ? a.to.v_scale : a.to.k_scale)[slice * (a.to.capacity / kBlock) + k0 + k] = scales[st * words + x.slot * blocks + k];
-        }
-        older = x.older >= k0 && (int64_t)x.older * kBlockBytes < c0 + unit;
-      }
-      for (uint32_t rest = __ballot_sync(0xffffffffu, older); rest; rest &= rest - 1) {
-        const int l2 = __ffs(rest) - 1;
-        const int lb = __shfl_sync(0xffffffffu, x.older, l2), slot = __shfl_sync(0xffffffffu, x.slot, l2), b2 = first + i0 + l2;
-        const int64_t t0 = max(c0, (int64_t)lb * kBlockBytes), t1 = min(c0 + unit, (int64_t)(lb + 1) * kBlockBytes);
-        to_tail<DT, CODE>(tail_of<DT>(kv ? a.to.v_tail : a.to.k_tail, (int64_t)b2 * H + h), stages + st * kMoveStage + slot * unit + (t0 - c0),
-                          (int)(t0 - (int64_t)lb * kBlockBytes), (int)(t1 - (int64_t)lb * kBlockBytes), scales[st * words + slot * blocks + lb - k0], lane);
-      }
+    for (int it = lane; it < count; it += 32) {
+      const TakeItem x = items[it];
+      if (x.slot < 0) continue;
+      const int64_t slice = (int64_t)(first + it) * H + h;
+      const int full = x.len / kBlock;
+      const int64_t r1 = min(c0 + unit, (int64_t)full * kBlockBytes);
+      if (r1 <= c0) continue;
+      bulk_store((char *)(kv ? a.to.v_codes : a.to.k_codes) + slice * a.to.capacity * kHeadDim + c0, stages + st * kMoveStage + x.slot * unit, (uint32_t)(r1 - c0));
+      if (c0 % kBlockBytes == 0)
+        for (int k = 0; k < blocks; ++k)
+          if (k0 + k < full) (kv ? a.to.v_scale : a.to.k_scale)[slice * (a.to.capacity / kBlock) + k0 + k] = scales[st * words + x.slot * blocks + k];
     }
     bulk_commit();
     if (i > 0) {  // the stage before is empty once its stores have read it
@@ -256,31 +258,30 @@ __global__ void __launch_bounds__(32) k_cache8_take(const __grid_constant__ Take
   word_wait<0>();
   bulk_wait_all();
 
-  // tails that are the source's own
   for (int64_t t = blockIdx.x; t < (int64_t)count * 2 * H; t += step) {
-    const int it = (int)(t / (2 * H)), h = (int)(t % (2 * H)) >> 1, kv = (int)t & 1, b = first + it;
-    const TakeItem x = items[it];
-    if (x.from < 0 || x.len == 0 || x.older >= 0 || (a.inside && x.from == b)) continue;
-    copy_tail<DT>(tail_of<DT>(kv ? a.to.v_tail : a.to.k_tail, (int64_t)b * H + h), tail_of<DT>(kv ? a.from.v_tail : a.from.k_tail, (int64_t)x.from * H + h),
-                  lane);
+    const int b = first + (int)(t / (2 * H)), h = (int)(t % (2 * H)) >> 1, kv = (int)t & 1;
+    const Taken x(a, b);
+    if (!x.moves(a, b)) continue;
+    const int64_t slice = (int64_t)b * H + h;
+    char *const tail = tail_of<DT>(kv ? a.to.v_tail : a.to.k_tail, slice);
+    if (a.inside) copy_tail<DT>(tail, tail_of<DT>(a.new_tails[kv], slice), lane);
+    else make_tail<DT, CODE>(a, x, h, kv, tail, lane);
   }
 }
 
-// The lengths and tails of a cache as they are before its sequences take one another's.
-struct SnapArgs {
-  lkv_cache8 c;
-  uint4 *tails;        // K's, then V's
-  int32_t *lengths;
-  int64_t vectors;     // of one
-};
-__global__ void __launch_bounds__(256) k_cache8_snapshot(const __grid_constant__ SnapArgs a) {
+// Within one cache, before its sequences take one another's tokens: the lengths
+// as they are, and the tails as they will be. A warp a tail.
+template <int DT, int CODE>
+__global__ void __launch_bounds__(128) k_cache8_take_tails(const __grid_constant__ TakeArgs a, int32_t *lengths) {
   wait_prerequisites();
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < a.c.batch) a.lengths[i] = a.c.lengths[i];
-  if (i < a.vectors) {
-    a.tails[i] = ((const uint4 *)a.c.k_tail)[i];
-    a.tails[a.vectors + i] = ((const uint4 *)a.c.v_tail)[i];
-  }
+  const int64_t warp = (int64_t)blockIdx.x * 4 + threadIdx.x / 32, i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+  if (i < a.to.batch) lengths[i] = a.to.lengths[i];
+  const int H = a.to.n_kv_heads, kv = (int)warp & 1;
+  const int64_t slice = warp >> 1;
+  if (slice >= (int64_t)a.to.batch * H) return;
+  const int b = (int)(slice / H), h = (int)(slice % H);
+  const Taken x(a, b);
+  if (x.moves(a, b)) make_tail<DT, CODE>(a, x, h, kv, tail_of<DT>(a.new_tails[kv], slice), threadIdx.x & 31);
 }
 
 // ---------------------------------------------------------------- keep
@@ -289,7 +290,6 @@ struct KeepArgs {
   lkv_cache8 to, from;
   const int32_t *blocks, *counts;
   int32_t m;
-  int32_t inside;
   int32_t split;      // CTAs of a (sequence, KV head) and tensor
 };
 
@@ -514,7 +514,7 @@ static const char *check_pair(const lkv_cache8 *to, const lkv_cache8 **from, boo
   return nullptr;
 }
 
-static int64_t snapshot_bytes(const lkv_cache8 *c) {
+static int64_t tails_bytes(const lkv_cache8 *c) {
   const int64_t tail = (int64_t)c->batch * c->n_kv_heads * kBlock * kHeadDim * (c->dtype == LKV_DTYPE_BF16 ? 2 : 4);
   return 2 * tail + ((int64_t)c->batch * 4 + 15) / 16 * 16;
 }
@@ -532,7 +532,7 @@ extern "C" lkv_status lkv_cache8_take_workspace(const lkv_cache8 *c, const lkv_c
   bool inside = false;
   if (const char *m = check_pair(c, &source, &inside)) return refuse_in("lkv_cache8_take_workspace", m);
   if (!bytes) return refuse("lkv_cache8_take_workspace: null result");
-  *bytes = inside ? snapshot_bytes(c) : 0;
+  *bytes = inside ? tails_bytes(c) : 0;
   return LKV_OK;
 }
 
@@ -547,7 +547,7 @@ extern "C" lkv_status lkv_cache8_take(const lkv_cache8 *c, const lkv_cache8 *sou
   const int64_t ib = (int64_t)c->batch * 4;
   if (overlaps_cache8(c, sequences, ib) || overlaps_cache8(c, lengths, ib))
     return refuse("lkv_cache8_take: an input overlaps the cache's arrays");
-  const int64_t need = inside ? snapshot_bytes(c) : 0;
+  const int64_t need = inside ? tails_bytes(c) : 0;
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return refuse("lkv_cache8_take: the workspace is smaller than lkv_cache8_take_workspace says");
     if (overlaps_cache8(c, workspace, need) || overlap(workspace, need, sequences, ib) || overlap(workspace, need, lengths, ib))
@@ -564,23 +564,22 @@ extern "C" lkv_status lkv_cache8_take(const lkv_cache8 *c, const lkv_cache8 *sou
   a.lengths = lengths;
   a.inside = inside;
   a.items = inside ? c->batch : c->batch < kTakeItems ? c->batch : kTakeItems;
+  const bool bf = c->dtype == LKV_DTYPE_BF16, i8 = c->code == LKV_CODE_INT8;
   if (inside) {
-    SnapArgs s{};
-    s.c = *c;
-    s.vectors = (int64_t)c->batch * c->n_kv_heads * kBlock * kHeadDim * (c->dtype == LKV_DTYPE_BF16 ? 2 : 4) / 16;
-    s.tails = (uint4 *)workspace;
-    s.lengths = (int32_t *)(s.tails + 2 * s.vectors);
-    e = launch_next(k_cache8_snapshot, dim3((unsigned)((s.vectors + 255) / 256)), 256, 0, st, s);
+    const int64_t slices = (int64_t)c->batch * c->n_kv_heads, tails = slices * kBlock * kHeadDim * (bf ? 2 : 4);
+    a.new_tails[0] = workspace;
+    a.new_tails[1] = (char *)workspace + tails;
+    int32_t *const before = (int32_t *)((char *)workspace + 2 * tails);
+    auto *fn = bf ? (i8 ? k_cache8_take_tails<1, LKV_CODE_INT8> : k_cache8_take_tails<1, LKV_CODE_E4M3>)
+                  : (i8 ? k_cache8_take_tails<0, LKV_CODE_INT8> : k_cache8_take_tails<0, LKV_CODE_E4M3>);
+    e = launch_next(fn, dim3((unsigned)((2 * slices + 3) / 4)), 128, 0, st, a, before);
     if (e != cudaSuccess) return cuda_refuse("lkv_cache8_take", e);
-    a.from.k_tail = s.tails;
-    a.from.v_tail = s.tails + s.vectors;
-    a.from.lengths = s.lengths;
+    a.from.lengths = before;
   }
   const int groups = (c->batch + a.items - 1) / a.items;  // below 2^16: 2^20 sequences at most
   const int wide = kMovePerSm * sms;
   const dim3 grid((unsigned)((wide + groups - 1) / groups), (unsigned)groups);
   const size_t smem = (size_t)take_smem(a.items);
-  const bool bf = c->dtype == LKV_DTYPE_BF16, i8 = c->code == LKV_CODE_INT8;
   if (bf) e = i8 ? launch_sized(k_cache8_take<1, LKV_CODE_INT8>, grid, smem, st, a) : launch_sized(k_cache8_take<1, LKV_CODE_E4M3>, grid, smem, st, a);
   else e = i8 ? launch_sized(k_cache8_take<0, LKV_CODE_INT8>, grid, smem, st, a) : launch_sized(k_cache8_take<0, LKV_CODE_E4M3>, grid, smem, st, a);
   return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_take", e);
@@ -609,7 +608,6 @@ extern "C" lkv_status lkv_cache8_keep(const lkv_cache8 *c, const lkv_cache8 *sou
   a.blocks = blocks;
   a.counts = counts;
   a.m = m;
-  a.inside = inside;
   // CTAs for a GPU full of them: runs of 8 blocks of a list at least, or parts
   // of 128 bytes of its blocks, no more than the GPU holds at once (of 8 x 32768
   // tokens in place, 256 CTAs and 512: 128 and 157 us)

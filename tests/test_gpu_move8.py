@@ -83,6 +83,31 @@ def test_take_within_a_cache(fmt, dtype, b, h, n):
         c = download(d)
 
 
+@pytest.mark.parametrize("b,h,n", [(24, 2, 6000), (200, 2, 2500), (520, 1, 1100)])
+def test_take_within_a_cache_of_narrow_columns(b, h, n):
+    """Many sequences of many blocks: a block's bytes are several CTAs' work, which
+    its scale and the tails made of it must not depend on."""
+    r = random.Random(b)
+    have = [r.randrange(n - 400, n + 1) for _ in range(b)]
+    d = lkv.Cache8(batch=b, n_kv_heads=h, capacity=(n + 31) // 16 * 16, dtype=BF16, fmt="int8")
+    g = torch.Generator(device="cuda").manual_seed(b)
+    for x in (d.k_codes, d.v_codes):
+        x.copy_(torch.randint(-127, 128, x.shape, device="cuda", generator=g))
+    for x in (d.k_scale, d.v_scale, d.k_tail, d.v_tail):
+        x.copy_(torch.rand(x.shape, device="cuda", generator=g) + .01)
+    d.lengths.copy_(ints(have))
+    c = download(d)
+    for turn in range(4):
+        to = [(i + 1 + turn) % b for i in range(b)] if turn % 2 == 0 else [r.randrange(b) for _ in range(b)]
+        lengths = [c[1][x] if r.random() < .3 else r.randrange(c[1][x] // 2, c[1][x] + 1) for x in to]
+        want, bad = mv.take(c, c, to, lengths)
+        assert not bad
+        d.take(sequences=ints(to), lengths=ints(lengths))
+        mv.same(download(d), want)
+        checked(d, bad)
+        c = download(d)
+
+
 @pytest.mark.parametrize("inside", [False, True])
 def test_take_of_what_is_not_there(inside):
     """Such sequences are left as they are, the others are not."""
