@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
           const int b = j * kRwBlocks + 2 * pw + (t >> 2);
           const uint4 *p = (const uint4 *)(codes + ((int64_t)j * kRwTok + 4 * t) * kHeadDim);
           cr[t] = make_uint4(0, 0, 0, 0);
-          if (b < z.full) cr[t] = once ? __ldcs(p) : __ldg(p);
+          if (b < z.full) cr[t] = once ? __ldcs(p) : *p;
         }
       };
       if (s1 > s0) load(s0);
