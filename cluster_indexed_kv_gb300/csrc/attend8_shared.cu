@@ -7,8 +7,9 @@ namespace lkv {
 // Two launches. The first takes each prefix's blocks once for the rows of all
 // sequences behind it and leaves parts (attend8_shared.cuh): in tensor memory's
 // tiles of 128 rows (bf16), or in tiles of 16. The second takes each sequence's
-// own blocks and joins its rows with their parts; where sequences have many rows
-// the first has taken their own blocks too, and the second joins parts alone.
+// own blocks, beside the first one's last CTAs, and joins its rows with their
+// parts; where sequences have many rows the first has taken their own blocks too,
+// and the second joins parts alone.
 struct SharedPlan {
   int nt;            // row tiles of 8 nt rows, 16: the kernel for many rows
   bool own_parts;    // the own tokens too
@@ -23,14 +24,19 @@ static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t
   const int64_t R = (int64_t)n * group, rows = c->batch * R, S = (int64_t)c->batch * c->n_kv_heads;
   if (rows * c->n_kv_heads > 0x7fffffff - 256) return "too many rows";
   const bool fp32 = c->dtype == LKV_DTYPE_FP32;
+  const int64_t len = max_len > 0 && max_len < c->capacity ? max_len : c->capacity, blocks = (len + kBlock - 1) / kBlock;
   // On a GB300, int8, 8 KV heads, 4 query heads: up to 16 rows are faster in tiles
-  // of 16 (4 samples of a 2048-token prompt 21 us, in tiles of 128 26 us), more
-  // would read the prefix once for each 16. From 9 rows a sequence the own tokens
-  // go to the tiles of 128 too: 8 x 4 tokens over 2000 of their own 34.5 us, in
-  // tiles of 16 38.7; 27 x 3 tokens of 8 heads over 1000 48 and 63; with one token
-  // each of 32 sequences, 4 rows, 64 and 55.
+  // of 16 (4 samples of a 2048-token prompt 16 us, in tiles of 128 26 us), more
+  // would read the prefix once for each 16.
   s->nt = !fp32 && rows > 16 ? 16 : rows <= 8 ? 1 : 2;
-  s->own_parts = s->nt == 16 && R > 8;
+  // From 17 rows a sequence the own tokens go to the tiles of 128 too (27 x 3 tokens
+  // of 8 heads over 1000 47 us, in tiles of 16 56; 8 x 8 tokens over 2000 39 and 48),
+  // up to 8 they do not (32 x 1 over 600 64 and 55), and between them where that
+  // makes few steps a CTA: with 8.2 of 4 x 4 tokens over 4000 39 us, in tiles of 16
+  // 54; with 9.7 (8 x 4 over 2000) 35.5 and 37.3; with 13.5 (32 x 4 over 64) 98 and
+  // 90; with 16.8 (32 x 3 over 300) 50 and 44.
+  const int64_t steps = S * (kSharedStart + (len + kSharedStep - 1) / kSharedStep);
+  s->own_parts = s->nt == 16 && (R > 16 || (R > 8 && steps <= 11 * (int64_t)sms));
   const int part_rows = 8 * s->nt;
   s->ctas = s->nt == 16 ? sms : sms * (fp32 && s->nt == 2 ? 1 : 2);
   s->tiles = ((rows + part_rows - 1) / part_rows + (p->batch < c->batch ? p->batch : c->batch)) * c->n_kv_heads;
@@ -38,7 +44,6 @@ static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t
   s->own_nt = R <= 8 ? 1 : 2;
   s->row_tiles = (int)((R + 8 * s->own_nt - 1) / (8 * s->own_nt));
   s->own_tiles = S * s->row_tiles;
-  const int64_t len = max_len > 0 && max_len < c->capacity ? max_len : c->capacity, blocks = (len + kBlock - 1) / kBlock;
   const int64_t slots = (int64_t)sms * (fp32 && s->own_nt == 2 ? 1 : 2);
   int64_t cluster = slots / s->own_tiles, most = blocks / (2 * kAtWarps);  // a turn for every warp
   if (cluster > most) cluster = most;
@@ -159,7 +164,9 @@ extern "C" lkv_status lkv_cache8_attend_shared(const lkv_cache8 *c, const lkv_ca
   a.part_rows = 8 * s.nt;
   a.part_blocks = s.nt == 16 ? kSharedStep / kBlock : 1;
   a.start_units = s.nt == 16 ? kSharedStart : 0;
-  a.least_units = s.nt == 16 ? 2 : 16;  // 256 tokens a CTA at least: fewer make parts for nothing
+  // 256 tokens a CTA at least: fewer make parts for nothing (4 samples of 2048
+  // tokens with 8, 12 and 16 blocks 17.5, 21 and 16 us)
+  a.least_units = s.nt == 16 ? 2 : 16;
   a.own_parts = s.own_parts;
   a.seq = (int4 *)((char *)workspace + s.seq_at);
   a.tile = (int2 *)((char *)workspace + s.tile_at);

@@ -354,3 +354,46 @@ def test_many_samples_of_one_prompt(fmt, dtype):
     assert all(torch.equal(x, y) for x, y in zip(before, own.read(64)))
     own.check()
     prefix.check()
+
+
+@pytest.mark.parametrize("b,n", [(120, 3), (90, 3), (120, 2), (60, 4), (60, 5)])
+def test_own_tokens_of_some_rows(b, n):
+    """8 to 20 rows a sequence, of more sequences and fewer: either kernel takes their own tokens."""
+    own = [1 + 7 * i % 30 for i in range(b)]
+    g = gen(b + n)
+    p, c = cache(g, 2, [300, 70], "int8", BF16), cache(g, 2, own, "int8", BF16)
+    to = [i % 2 for i in range(b)]
+    q = torch.randn(b, 8, n, 128, generator=g).to(BF16)
+    check(c, p, to, own, [300, 70], q)
+    counts = [i % (n + 1) for i in range(b)]
+    check(c, p, to, own, [300, 70], q, counts=counts, max_len=max(own))
+    c[0].check()
+
+
+@pytest.mark.parametrize("fmt,dtype,b,n", [("int8", BF16, 4, 1), ("e4m3", F32, 3, 2), ("int8", BF16, 40, 1), ("e4m3", BF16, 12, 3)])
+def test_steps_in_a_row(fmt, dtype, b, n):
+    """Writes and attentions by turns with nothing between them: each sees what was written before it, and no later."""
+    g = gen(b)
+    pre = [700, 20]
+    p, c = cache(g, 2, pre, fmt, dtype), cache(g, 2, [33] * b, fmt, dtype, room=96)
+    to = i32(*[i % 2 for i in range(b)])
+    d = c[0]
+    steps = [torch.randn(3, b, 8, n, 128, generator=g).to(dtype).cuda() for _ in range(12)]
+    start = [t.clone() for t in (d.k_codes.view(torch.int8), d.v_codes.view(torch.int8), d.k_scale, d.v_scale, d.k_tail, d.v_tail, d.lengths)]
+    got = []
+    for apart in (False, True):
+        for t, x in zip((d.k_codes.view(torch.int8), d.v_codes.view(torch.int8), d.k_scale, d.v_scale, d.k_tail, d.v_tail, d.lengths), start):
+            t.copy_(x)
+        torch.cuda.synchronize()
+        outs = []
+        for x in steps:
+            d.write(x[1, :, :2].contiguous(), x[2, :, :2].contiguous())
+            if apart:
+                torch.cuda.synchronize()
+            outs.append(d.attend_shared(x[0], p[0], to))
+            if apart:
+                torch.cuda.synchronize()
+        got.append(outs)
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    d.check()
