@@ -61,7 +61,8 @@ static cudaError_t launch_part(const SharedArgs &a, unsigned grid, int cluster, 
   auto *fn = k_attend8<DT, CODE, NT, MODE>;
   const int used = (int)sizeof(AtSmem<NT>) > kRingBytes ? (int)sizeof(AtSmem<NT>) : kRingBytes;
   const int smem = 1024 + used + (MODE == kPrefix ? (int)Prefixes::bytes(a.c.batch, a.p.batch, false) : 0);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemAllowed allowed;
+  cudaError_t e = allowed.allow((const void *)fn, 1024 + used + (MODE == kPrefix ? (int)Prefixes::bytes(kSharedMost, kSharedMost, false) : 0));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
@@ -172,9 +173,9 @@ extern "C" lkv_status lkv_cache8_attend_shared(const lkv_cache8 *c, const lkv_ca
   a.tile = (int2 *)((char *)workspace + s.tile_at);
   a.parts = (float *)((char *)workspace + s.parts_at);
   const int64_t SP = (int64_t)prefix->batch * prefix->n_kv_heads;
-  CUtensorMap maps[4];
-  if (!codes_map(&maps[0], prefix->k_codes, prefix->capacity, SP, kBlock) || !codes_map(&maps[1], prefix->v_codes, prefix->capacity, SP, kBlock) ||
-      !codes_map(&maps[2], c->k_codes, c->capacity, S, kBlock) || !codes_map(&maps[3], c->v_codes, c->capacity, S, kBlock)) {
+  CUtensorMap maps[4];  // of the prefixes and of the own tokens, where tiles of 16 take them
+  if ((s.nt != 16 && (!codes_map(&maps[0], prefix->k_codes, prefix->capacity, SP, kBlock) || !codes_map(&maps[1], prefix->v_codes, prefix->capacity, SP, kBlock))) ||
+      (!s.own_parts && (!codes_map(&maps[2], c->k_codes, c->capacity, S, kBlock) || !codes_map(&maps[3], c->v_codes, c->capacity, S, kBlock)))) {
     set_unbound_error("lkv_cache8_attend_shared: the driver refused a tensor map of the codes");
     return LKV_ECUDA;
   }

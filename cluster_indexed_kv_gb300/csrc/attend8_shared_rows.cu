@@ -689,7 +689,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_shared_join(const __grid_co
 cudaError_t launch_shared_rows(const SharedArgs &a, int ctas, cudaStream_t st) {
   auto *fn = a.c.code == LKV_CODE_INT8 ? k_shared_rows<LKV_CODE_INT8> : k_shared_rows<LKV_CODE_E4M3>;
   const size_t smem = kShSmem + (size_t)Prefixes::bytes(a.c.batch, a.p.batch, a.own_parts);
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SmemAllowed allowed[2];
+  const cudaError_t e = allowed[a.c.code == LKV_CODE_INT8].allow((const void *)fn, (int)(kShSmem + Prefixes::bytes(kSharedMost, kSharedMost, true)));
   return e != cudaSuccess ? e : launch_next(fn, dim3((unsigned)ctas), kShThreads, smem, st, a);
 }
 

@@ -519,10 +519,12 @@ static int64_t tails_bytes(const lkv_cache8 *c) {
   return 2 * tail + ((int64_t)c->batch * 4 + 15) / 16 * 16;
 }
 
-template <class Args>
-static cudaError_t launch_sized(void (*fn)(Args), dim3 grid, size_t smem, cudaStream_t st, const Args &a) {
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  return e != cudaSuccess ? e : launch_next(fn, grid, 32, smem, st, a);
+// A warp a CTA, with `smem` bytes of the at most `most` that the kernel takes.
+template <auto FN, class Args>
+static cudaError_t launch_sized(dim3 grid, size_t smem, size_t most, cudaStream_t st, const Args &a) {
+  static SmemAllowed allowed;
+  const cudaError_t e = allowed.allow((const void *)FN, (int)most);
+  return e != cudaSuccess ? e : launch_next(FN, grid, 32, smem, st, a);
 }
 
 }  // namespace lkv
@@ -579,9 +581,9 @@ extern "C" lkv_status lkv_cache8_take(const lkv_cache8 *c, const lkv_cache8 *sou
   const int groups = (c->batch + a.items - 1) / a.items;  // below 2^16: 2^20 sequences at most
   const int wide = kMovePerSm * sms;
   const dim3 grid((unsigned)((wide + groups - 1) / groups), (unsigned)groups);
-  const size_t smem = (size_t)take_smem(a.items);
-  if (bf) e = i8 ? launch_sized(k_cache8_take<1, LKV_CODE_INT8>, grid, smem, st, a) : launch_sized(k_cache8_take<1, LKV_CODE_E4M3>, grid, smem, st, a);
-  else e = i8 ? launch_sized(k_cache8_take<0, LKV_CODE_INT8>, grid, smem, st, a) : launch_sized(k_cache8_take<0, LKV_CODE_E4M3>, grid, smem, st, a);
+  const size_t smem = (size_t)take_smem(a.items), most = (size_t)take_smem(kTakeInside);
+  if (bf) e = i8 ? launch_sized<k_cache8_take<1, LKV_CODE_INT8>>(grid, smem, most, st, a) : launch_sized<k_cache8_take<1, LKV_CODE_E4M3>>(grid, smem, most, st, a);
+  else e = i8 ? launch_sized<k_cache8_take<0, LKV_CODE_INT8>>(grid, smem, most, st, a) : launch_sized<k_cache8_take<0, LKV_CODE_E4M3>>(grid, smem, most, st, a);
   return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_take", e);
 }
 
@@ -629,7 +631,7 @@ extern "C" lkv_status lkv_cache8_keep(const lkv_cache8 *c, const lkv_cache8 *sou
     e = launch_next(fn, grid, kInsideThreads, 0, st, a);
     return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_keep", e);
   }
-  if (bf) e = i8 ? launch_sized(k_cache8_keep<1, LKV_CODE_INT8>, grid, smem, st, a) : launch_sized(k_cache8_keep<1, LKV_CODE_E4M3>, grid, smem, st, a);
-  else e = i8 ? launch_sized(k_cache8_keep<0, LKV_CODE_INT8>, grid, smem, st, a) : launch_sized(k_cache8_keep<0, LKV_CODE_E4M3>, grid, smem, st, a);
+  if (bf) e = i8 ? launch_sized<k_cache8_keep<1, LKV_CODE_INT8>>(grid, smem, smem, st, a) : launch_sized<k_cache8_keep<1, LKV_CODE_E4M3>>(grid, smem, smem, st, a);
+  else e = i8 ? launch_sized<k_cache8_keep<0, LKV_CODE_INT8>>(grid, smem, smem, st, a) : launch_sized<k_cache8_keep<0, LKV_CODE_E4M3>>(grid, smem, smem, st, a);
   return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_keep", e);
 }
