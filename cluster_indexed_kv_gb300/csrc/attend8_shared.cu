@@ -4,6 +4,10 @@
 
 namespace lkv {
 
+// Tiles of 16: blocks that a CTA takes at least, as fewer make parts for nothing (4
+// samples of 2048 tokens with 8, 12 and 16 blocks 17.5, 21 and 16 us).
+constexpr int kSharedFewLeast = 16;
+
 // Two launches. The first takes each prefix's blocks once for the rows of all
 // sequences behind it and leaves parts (attend8_shared.cuh): in tensor memory's
 // tiles of 128 rows (bf16), or in tiles of 16. The second takes each sequence's
@@ -48,6 +52,15 @@ static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t
   int64_t cluster = slots / s->own_tiles, most = blocks / (2 * kAtWarps);  // a turn for every warp
   if (cluster > most) cluster = most;
   s->cluster = (int)(cluster < 1 ? 1 : cluster > kAtMaxCluster ? kAtMaxCluster : cluster);
+  if (s->nt != 16) {
+    // Where the prefixes can fill every CTA, some are left out for the own tokens'
+    // to run beside them: 4 samples of 32K tokens 33 -> 29 us, of 131K 73 -> 68; in
+    // fp32, 16 of 152 CTAs, 44 -> 42 and 122 -> 119. More than an eighth cost more than
+    // that: 24 of 152, 6 fp32 samples of 131K 197 -> 220.
+    const int64_t own = s->own_tiles * s->cluster, per_sm = fp32 && s->own_nt == 2 ? 1 : 2;
+    const int64_t room = s->ctas > sms ? own : (own + per_sm - 1) / per_sm;
+    if (room <= s->ctas / 8 && s->tiles * (p->capacity / kBlock) / kSharedFewLeast > s->ctas - room) s->ctas -= (int)room;
+  }
   if (s->tiles > 0x7fffffff || s->own_tiles * s->cluster > 0x7fffffff) return "too many rows";
   s->seq_at = 0;
   s->tile_at = (int64_t)c->batch * 16;
@@ -60,9 +73,9 @@ template <int DT, int CODE, int NT, int MODE>
 static cudaError_t launch_part(const SharedArgs &a, unsigned grid, int cluster, const CUtensorMap &km, const CUtensorMap &vm, cudaStream_t st) {
   auto *fn = k_attend8<DT, CODE, NT, MODE>;
   const int used = (int)sizeof(AtSmem<NT>) > kRingBytes ? (int)sizeof(AtSmem<NT>) : kRingBytes;
-  const int smem = 1024 + used + (MODE == kPrefix ? (int)Prefixes::bytes(a.c.batch, a.p.batch, false) : 0);
+  const int smem = 1024 + used + (MODE == kPrefix ? (int)Prefixes<false>::bytes(a.c.batch, a.p.batch, false) : 0);
   static SmemAllowed allowed;
-  cudaError_t e = allowed.allow((const void *)fn, 1024 + used + (MODE == kPrefix ? (int)Prefixes::bytes(kSharedMost, kSharedMost, false) : 0));
+  cudaError_t e = allowed.allow((const void *)fn, 1024 + used + (MODE == kPrefix ? (int)Prefixes<false>::bytes(kSharedMost, kSharedMost, false) : 0));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
@@ -163,11 +176,7 @@ extern "C" lkv_status lkv_cache8_attend_shared(const lkv_cache8 *c, const lkv_ca
   a.scale_log2 = scale_log2;
   a.row_tiles = s.row_tiles;
   a.part_rows = 8 * s.nt;
-  a.part_blocks = s.nt == 16 ? kSharedStep / kBlock : 1;
-  a.start_units = s.nt == 16 ? kSharedStart : 0;
-  // 256 tokens a CTA at least: fewer make parts for nothing (4 samples of 2048
-  // tokens with 8, 12 and 16 blocks 17.5, 21 and 16 us)
-  a.least_units = s.nt == 16 ? 2 : 16;
+  a.least_units = s.nt == 16 ? 2 : kSharedFewLeast;
   a.own_parts = s.own_parts;
   a.seq = (int4 *)((char *)workspace + s.seq_at);
   a.tile = (int2 *)((char *)workspace + s.tile_at);

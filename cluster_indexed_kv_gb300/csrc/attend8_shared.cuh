@@ -20,8 +20,7 @@ constexpr int kSharedMost = 1024;  // sequences, and prefixes, that a call takes
 struct SharedArgs : AttendArgs {
   lkv_cache8 p;               // the prefixes
   const int32_t *prefix_of;   // null: all of prefix 0
-  int32_t part_rows, part_blocks;
-  int32_t start_units;        // that stand for what beginning a tile costs, before those of its blocks
+  int32_t part_rows;
   int32_t least_units;        // that a CTA takes, at least
   int32_t own_parts;          // whether the sequences' own tokens are parts too
   int4 *seq;                  // [batch]: the first tile of the sequence's prefix (-1: none), its place behind that prefix, its own first tile (-1: none)
@@ -45,8 +44,18 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
+// Row tiles of the kernel for many rows of bf16 caches, its units, and the steps'
+// time that beginning a tile costs it. With 4, 7, 10 and 14: 8 x 256 tokens behind
+// 16K 635, 573, 581 and 596 us; 32 x 5 behind 8K 62, 59, 64 and 73.
+constexpr int kSharedRows = 128, kSharedStep = 128, kSharedStart = 7;
+// The same for tiles of 16, in blocks, where a CTA may begin a second one. With 0, 16,
+// 24 and 30: 5 fp32 samples behind 5 prefixes of 100 to 16000 tokens 76, 51, 44
+// and 38 us; 6 behind one of 8191 35.5, 33.4, 32.1 and 31.6.
+constexpr int kSharedFewStart = 30;
+
 // The work, in shared memory: list e < G is prefix e's, and list G + b
-// sequence b's own.
+// sequence b's own. ROWS: for tiles of 128.
+template <bool ROWS>
 struct Prefixes {
   int64_t *at;       // [lists + 1]: units before each list's tiles
   int *tiles;        // [lists + 1]: tiles before
@@ -57,13 +66,16 @@ struct Prefixes {
   int *rows;         // [batch]: tokens of its rows that are no padding
   int16_t *order;    // [batch]: sequences, prefix by prefix
   int16_t *of;       // [batch]: the sequence's prefix, -1 for none (or an empty one)
-  int G, lists, run, start;
+  int *plan;         // start and ctas as below
+  int G, lists, run;
+  int start;         // units that stand for what beginning a tile costs, where a CTA may have several, before those of its blocks
+  int ctas;          // that take part
 
   static __host__ __device__ int64_t bytes(int batch, int G, bool own) {
-    return 12 * (int64_t)(G + (own ? batch : 0) + 2) + 12 * (int64_t)(G + 1) + 12 * (int64_t)batch;
+    return 12 * (int64_t)(G + (own ? batch : 0) + 2) + 12 * (int64_t)(G + 1) + 12 * (int64_t)batch + 8;
   }
   __device__ Prefixes(const SharedArgs &a, void *area) : G(a.p.batch), lists(a.p.batch + (a.own_parts ? a.c.batch : 0)),
-                                                          run(a.part_blocks * kBlock), start(a.start_units) {
+                                                          run(ROWS ? kSharedStep : kBlock), start(ROWS ? kSharedStart : kSharedFewStart), ctas(1) {
     const int B = a.c.batch;
     at = (int64_t *)area;
     tiles = (int *)(at + lists + 1);
@@ -74,6 +86,7 @@ struct Prefixes {
     rows = before + B;
     order = (int16_t *)(rows + B);
     of = order + B;
+    plan = (int *)(of + B);
   }
   // a list's tokens, and the units of one of its tiles
   __device__ __forceinline__ int len(int list) const { return list < G ? plen[list] : before[list - G] + rows[list - G]; }
@@ -114,7 +127,7 @@ struct Prefixes {
         }
         if (turn) break;
         int64_t sum = 0;
-        int nt = 0, seqs = 0;
+        int nt = 0, seqs = 0, most = 0;  // tiles, sequences, the largest list's tiles
 #pragma unroll 1
         for (int e0 = 0; e0 < lists; e0 += 32) {
           const int e = e0 + lane;
@@ -123,6 +136,7 @@ struct Prefixes {
           int64_t u = (int64_t)rt * a.c.n_kv_heads * units(tokens);
           int t = rt * a.c.n_kv_heads, s = e < G ? have : 0;
           const int mine = s;
+          most = max(most, t);
 #pragma unroll 1
           for (int d = 1; d < 32; d *= 2) {
             const int64_t u2 = __shfl_up_sync(0xffffffffu, u, d);
@@ -145,11 +159,36 @@ struct Prefixes {
           nt += __shfl_sync(0xffffffffu, t, 31);
           seqs += __shfl_sync(0xffffffffu, s, 31);
         }
+        if constexpr (!ROWS) {
+          // a CTA for each tile at least; one list whose tiles can each have CTAs of
+          // their own is shared so, and evenly
+          int P = (int)min((int64_t)gridDim.x, max((int64_t)nt, quotient(sum - (int64_t)nt * start, a.least_units))), stand = start;
+          if (__reduce_max_sync(0xffffffffu, most) == nt && nt > 0) {
+            if (P < (int)gridDim.x) P -= P % nt;
+            if (P % nt == 0) {
+              sum -= (int64_t)nt * start;
+              stand = 0;
+#pragma unroll 1
+              for (int e = lane; e < lists; e += 32)
+                if (at[e + 1]) at[e + 1] = sum;
+            }
+          }
+          if (lane == 0) {
+            plan[0] = stand;
+            plan[1] = P;
+          }
+        }
         if (lane == 0) at[0] = tiles[0] = first[0] = 0;
         __syncwarp();
       }
     }
     __syncthreads();
+    if constexpr (!ROWS) {
+      start = plan[0];
+      ctas = plan[1];
+    } else {
+      ctas = (int)min((int64_t)gridDim.x, max((int64_t)1, quotient(at[lists], a.least_units)));
+    }
     for (int g = threadIdx.x; g < G; g += blockDim.x) pnu[g] = units(plen[g]);
     if (blockIdx.x == 0) {
       auto own = [&](int b) { return lists > G && tiles[G + b + 1] > tiles[G + b] ? tiles[G + b] : -1; };
@@ -162,13 +201,9 @@ struct Prefixes {
     }
     __syncthreads();
   }
-  // CTAs that take part
-  __device__ __forceinline__ int64_t takers(const SharedArgs &a) const {
-    return max((int64_t)1, min((int64_t)gridDim.x, quotient(at[lists], a.least_units)));
-  }
   // this CTA's units
   __device__ __forceinline__ void share(const SharedArgs &a, int64_t &x0, int64_t &x1) const {
-    const int64_t total = at[lists], P = takers(a);
+    const int64_t total = at[lists], P = ctas;
     x0 = blockIdx.x < P ? quotient(total * blockIdx.x, P) : 0;
     x1 = blockIdx.x < P ? quotient(total * (blockIdx.x + 1), P) : 0;
   }
@@ -194,7 +229,7 @@ struct Prefixes {
   }
   // the tile that begins at unit x of the row, for whoever joins its parts (one thread of the CTA that has the unit)
   __device__ __forceinline__ void announce(const SharedArgs &a, const Piece &p, int64_t x) const {
-    const int64_t P = takers(a), last = x + nu(p.list) - 1;
+    const int64_t P = ctas, last = x + nu(p.list) - 1;
     // the last CTA that begins at or before unit `last`
     a.tile[p.tile] = make_int2((int)blockIdx.x, (int)quotient(P * (last + 1) - 1, at[lists]) - (int)blockIdx.x + 1);
   }
@@ -203,7 +238,8 @@ struct Prefixes {
 // Row r of a list: where its query is (in rows of q, of KV head h) and the last
 // of the list's `len` tokens that it sees; at < 0: no row, or padding.
 struct ListRow { int64_t at; int pos; };
-__device__ __forceinline__ ListRow list_row(const SharedArgs &a, const Prefixes &p, int list, int h, int len, int64_t r) {
+template <bool ROWS>
+__device__ __forceinline__ ListRow list_row(const SharedArgs &a, const Prefixes<ROWS> &p, int list, int h, int len, int64_t r) {
   ListRow x{-1, -1};
   const int per = a.n * a.group, G = a.p.batch;
   const int64_t m = quotient(r, per);
@@ -217,11 +253,7 @@ __device__ __forceinline__ ListRow list_row(const SharedArgs &a, const Prefixes 
 }
 
 // The kernel for many rows of bf16 caches and the join of what it leaves
-// (attend8_shared_rows.cu): row tiles of kSharedRows, units of kSharedStep tokens.
-constexpr int kSharedRows = 128, kSharedStep = 128;
-// Steps' time that beginning a tile costs. With 4, 7, 10 and 14: 8 x 256 tokens
-// behind 16K 635, 573, 581 and 596 us; 32 x 5 behind 8K 62, 59, 64 and 73.
-constexpr int kSharedStart = 7;
+// (attend8_shared_rows.cu).
 cudaError_t launch_shared_rows(const SharedArgs &a, int ctas, cudaStream_t st);
 cudaError_t launch_shared_join(const SharedArgs &a, cudaStream_t st);
 

@@ -77,7 +77,7 @@ __device__ __forceinline__ void group_sync(int id, int threads) { asm volatile("
 
 // What a CTA is at.
 struct SharedPiece {
-  Prefixes::Piece p;
+  Prefixes<true>::Piece p;
   int64_t x, end;             // of the row of units: where the CTA is, and its end
   const uint8_t *codes[2];    // the list's cache: K's and V's codes, scales and tails of the KV head
   const float *scale[2];
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
   unsigned char *const area = raw + (base - smem_at(raw));
   const uint32_t q_at = base, k_at = base + kRwTile, v_at = base + 3 * kRwTile;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // the warp: uniform for the compiler too
-  Prefixes pre(a, area + 5 * kRwTile);
+  Prefixes<true> pre(a, area + 5 * kRwTile);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       if (threadIdx.x == 32 * kShK) {
         seg.go = seg.x < seg.end && !abort_s;
         if (seg.go) {
-          const Prefixes::Piece p = pre.piece(a, seg.x, seg.end);
+          const Prefixes<true>::Piece p = pre.piece(a, seg.x, seg.end);
           if (p.u0 == 0) pre.announce(a, p, seg.x);
           seg.p = p;
           auto from = [&](const lkv_cache8 &c, int b) {
@@ -688,9 +688,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_shared_join(const __grid_co
 
 cudaError_t launch_shared_rows(const SharedArgs &a, int ctas, cudaStream_t st) {
   auto *fn = a.c.code == LKV_CODE_INT8 ? k_shared_rows<LKV_CODE_INT8> : k_shared_rows<LKV_CODE_E4M3>;
-  const size_t smem = kShSmem + (size_t)Prefixes::bytes(a.c.batch, a.p.batch, a.own_parts);
+  const size_t smem = kShSmem + (size_t)Prefixes<true>::bytes(a.c.batch, a.p.batch, a.own_parts);
   static SmemAllowed allowed[2];
-  const cudaError_t e = allowed[a.c.code == LKV_CODE_INT8].allow((const void *)fn, (int)(kShSmem + Prefixes::bytes(kSharedMost, kSharedMost, true)));
+  const cudaError_t e = allowed[a.c.code == LKV_CODE_INT8].allow((const void *)fn, (int)(kShSmem + Prefixes<true>::bytes(kSharedMost, kSharedMost, true)));
   return e != cudaSuccess ? e : launch_next(fn, dim3((unsigned)ctas), kShThreads, smem, st, a);
 }
 

@@ -397,3 +397,18 @@ def test_steps_in_a_row(fmt, dtype, b, n):
     for x, y in zip(*got):
         assert torch.equal(x, y)
     d.check()
+
+
+@pytest.mark.parametrize("fmt,dtype", [("int8", BF16), ("e4m3", F32)])
+@pytest.mark.parametrize("pre,b,h", [
+    ([2000, 16, 700, 1, 9000], 4, 2), ([17] * 40 + [3000], 41, 1), ([16 * 16 * 9], 4, 2), ([16 * 16 * 9 + 1], 4, 2), ([16 * 16 * 200], 2, 1), ([48], 3, 5)])
+def test_few_rows_of_uneven_prefixes(fmt, dtype, pre, b, h):
+    """Tiles of 16 rows: short prefixes beside long ones, and one whose blocks are shared evenly, or not quite."""
+    g = gen(len(pre) + b)
+    own = [1 + 5 * i % 40 for i in range(b)]
+    p, c = cache(g, h, pre, fmt, dtype), cache(g, h, own, fmt, dtype)
+    to = [(i * 3 + 4) % len(pre) for i in range(b)]
+    q = torch.randn(b, 2 * h, 1, 128, generator=g).to(dtype)
+    check(c, p, to, own, pre, q)
+    check(c, p, to, own, pre, q, max_len=40)
+    c[0].check()
