@@ -35,7 +35,7 @@ static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t
   s->nt = !fp32 && rows > 16 ? 16 : rows <= 8 ? 1 : 2;
   // From 17 rows a sequence the own tokens go to the tiles of 128 too (27 x 3 tokens
   // of 8 heads over 1000 47 us, in tiles of 16 56; 8 x 8 tokens over 2000 39 and 48),
-  // up to 8 they do not (32 x 1 over 600 64 and 55), and between them where that
+  // up to 8 they do not (32 x 1 over 600 64 and 43), and between them where that
   // makes few steps a CTA: with 8.2 of 4 x 4 tokens over 4000 39 us, in tiles of 16
   // 54; with 9.7 (8 x 4 over 2000) 35.5 and 37.3; with 13.5 (32 x 4 over 64) 98 and
   // 90; with 16.8 (32 x 3 over 300) 50 and 44.
