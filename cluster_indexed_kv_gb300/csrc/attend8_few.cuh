@@ -448,8 +448,10 @@ __device__ __forceinline__ void sum_prefix(const SharedArgs &a, int64_t slice, i
       float4 x[kSumAtOnce];
       auto load = [&](int k0) {
 #pragma unroll
-        for (int k = 0; k < kSumAtOnce; ++k)
+        for (int k = 0; k < kSumAtOnce; ++k) {
+          x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (k0 + k < some) x[k] = *(const float4 *)(at(j0 + k0 + k) + part_place(rr, 4 * lane));
+        }
       };
       load(0);
       float m = -INFINITY, t = -INFINITY, mine = 0.f;
@@ -553,9 +555,10 @@ __device__ __forceinline__ void add_prefix(const PrefixSum<RT> &z, int r, int d,
 // of 2048 tokens 9.6 us.
 //
 // Behind prefixes: 4 samples of a 2048-token prompt (8 KV heads, 16 rows of each)
-// 16 us, 6 samples of 8191 tokens in fp32 33 us (a tile of 16 rows a CTA: 4 turns,
+// 17 us, 6 samples of 8191 tokens in fp32 34 us (a tile of 16 rows a CTA: 4 turns,
 // the partial block as long as 4 more). The own tokens need nothing of the kernel
-// before this one, whose parts are read last: 21 and 44 us with its end awaited first.
+// before this one but its word for what came before both, and its parts are read
+// last: 21 and 44 us with its end awaited first (the word costs 0.7 us).
 template <int DT, int CODE, int NT, int MODE>
 __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
     k_attend8(const __grid_constant__ ArgsOf<MODE> a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -576,6 +579,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
   const int G = MODE == kPrefix ? c.batch : c.batch * a.row_tiles;
   // the prefixes' tables lie behind what the rings and merges use
   [[maybe_unused]] __shared__ __align__(16) std::conditional_t<MODE == kOwn, PrefixSum<RT>, int> prefix;
+  [[maybe_unused]] __shared__ uint64_t vouched_s[kAtWarps];  // what each warp's reads go by (see vouch)
   constexpr int kUsed = (int)sizeof(Sm) > kRingBytes ? (int)sizeof(Sm) : kRingBytes;
   static_assert(kUsed % 8 == 0, "the tables begin with 8-byte words");
   [[maybe_unused]] auto pre = [&] {
@@ -602,12 +606,16 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
       tma_prefetch(&vmap);
     }
   }
-  __syncwarp();
   // Own tokens behind prefixes: the kernel before this one has waited for all
-  // before it, in every CTA, by the time this one starts, and what it writes is
-  // read, and waited for, last.
-  if constexpr (MODE != kOwn) wait_prerequisites();
-  if (streamed) launch_dependents();
+  // before it and vouches for that; what it writes is read, and waited for, last.
+  if constexpr (MODE == kOwn) {
+    if (w.lane == 0) vouched_s[wid] = vouched(a);
+  } else {
+    wait_prerequisites();
+  }
+  __syncwarp();
+  if constexpr (MODE == kPrefix) launch_vouched(a);
+  else if (streamed) launch_dependents();
   uint32_t phase = 0;      // parities of the two barriers
   bool dead = false;       // a copy did not arrive in time: the warp takes no more
   const int64_t es = DT == 1 ? 2 : 4;
@@ -831,9 +839,18 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
     }
     if constexpr (MODE == kOwn) {  // a CTA of a cluster takes the rows that it will write
       wait_prerequisites();
+      const uint64_t now = vouched_now(a);
       for (int row = part + parts * wid; row < RT; row += parts * kAtWarps) sum_prefix(a, slice, r0 + row, prefix, row, w.lane);
+      if (__syncthreads_or(vouched_s[wid] != now)) {  // copies go over what was just written here
+        if (w.lane == 0) vouched_s[wid] = now;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+        x = x0;
+        continue;
+      }
+    } else {
+      __syncthreads();
     }
-    __syncthreads();
     if (threadIdx.x < RT) {
       const int row = threadIdx.x;
       float top = -INFINITY, topt = -INFINITY, l = 0.f;
@@ -917,6 +934,9 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 || DT == 1 ? 2 : 1)
       put_out<DT>(a, slice, tile.cnt, r0 + row, 2 * p, s, l, top - topt);
     }
     cluster_barrier();  // no CTA leaves while another reads its shared memory
+  }
+  if constexpr (MODE == kPrefix) {
+    if (a.late && blockIdx.x == 0 && threadIdx.x == 0) vouch(a);
   }
 }
 

@@ -21,8 +21,10 @@ struct SharedPlan {
   int64_t tiles;     // at most
   int own_nt, row_tiles, cluster;
   int64_t own_tiles;
-  int64_t seq_at, tile_at, parts_at, bytes;  // the workspace
+  int64_t seq_at, tile_at, parts_at, bytes;  // the workspace, at its beginning what the first launch vouches with
 };
+
+static thread_local int32_t vouch_late = 0;  // lkv_diag_shared_late
 
 static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t group, int32_t n, int32_t max_len, int sms, SharedPlan *s) {
   const int64_t R = (int64_t)n * group, rows = c->batch * R, S = (int64_t)c->batch * c->n_kv_heads;
@@ -62,8 +64,8 @@ static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t
     if (room <= s->ctas / 8 && s->tiles * (p->capacity / kBlock) / kSharedFewLeast > s->ctas - room) s->ctas -= (int)room;
   }
   if (s->tiles > 0x7fffffff || s->own_tiles * s->cluster > 0x7fffffff) return "too many rows";
-  s->seq_at = 0;
-  s->tile_at = (int64_t)c->batch * 16;
+  s->seq_at = 16;
+  s->tile_at = s->seq_at + (int64_t)c->batch * 16;
   s->parts_at = s->tile_at + (s->tiles * 8 + 15) / 16 * 16;
   s->bytes = s->parts_at + (s->ctas + s->tiles) * part_floats(part_rows) * 4;
   return nullptr;
@@ -120,6 +122,11 @@ static const char *check_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_
 }
 
 }  // namespace lkv
+
+extern "C" lkv_status lkv_diag_shared_late(int32_t on) {
+  lkv::vouch_late = on != 0;
+  return LKV_OK;
+}
 
 extern "C" lkv_status lkv_cache8_attend_shared_workspace(const lkv_cache8 *c, const lkv_cache8 *prefix, int32_t group, int32_t n,
                                                          int32_t max_len, int64_t *bytes) {
@@ -181,6 +188,8 @@ extern "C" lkv_status lkv_cache8_attend_shared(const lkv_cache8 *c, const lkv_ca
   a.seq = (int4 *)((char *)workspace + s.seq_at);
   a.tile = (int2 *)((char *)workspace + s.tile_at);
   a.parts = (float *)((char *)workspace + s.parts_at);
+  a.vouch = (uint64_t *)workspace;
+  a.late = vouch_late;
   const int64_t SP = (int64_t)prefix->batch * prefix->n_kv_heads;
   CUtensorMap maps[4];  // of the prefixes and of the own tokens, where tiles of 16 take them
   if ((s.nt != 16 && (!codes_map(&maps[0], prefix->k_codes, prefix->capacity, SP, kBlock) || !codes_map(&maps[1], prefix->v_codes, prefix->capacity, SP, kBlock))) ||

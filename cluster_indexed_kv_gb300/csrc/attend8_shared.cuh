@@ -26,7 +26,42 @@ struct SharedArgs : AttendArgs {
   int4 *seq;                  // [batch]: the first tile of the sequence's prefix (-1: none), its place behind that prefix, its own first tile (-1: none)
   int2 *tile;                 // [tiles]: a tile's first CTA, and how many it has
   float *parts;
+  uint64_t *vouch;            // what the first kernel vouches with, another value each time (see vouch)
+  int32_t late;               // it does so at its end (lkv_diag_shared_late)
 };
+
+// The second kernel begins while the first still runs, and takes the sequences' own
+// tokens meanwhile, which the launches before both have written. What the first
+// one's wait (griddepcontrol.wait) promises, it promises the first kernel; so one of
+// its threads passes it on, behind that wait: it releases the time at `vouch`, and
+// each warp of the second kernel acquires what stands there ahead of its reads. Behind
+// its own wait it looks again: if it is the same, it was this call's, and everything
+// before the release was there to be read. If it is not, the tokens are taken again.
+__device__ __forceinline__ void vouch(const SharedArgs &a) {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(a.vouch), "l"(t) : "memory");
+}
+// What stands there, by the lane that also issues the warp's copies.
+__device__ __forceinline__ uint64_t vouched(const SharedArgs &a) {
+  uint64_t t;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(t) : "l"(a.vouch) : "memory");
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+  return t;
+}
+// The same behind the kernel's own wait.
+__device__ __forceinline__ uint64_t vouched_now(const SharedArgs &a) {
+  uint64_t t;
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(t) : "l"(a.vouch));
+  return t;
+}
+// The first kernel's threads, behind their wait: the second may start.
+__device__ __forceinline__ void launch_vouched(const SharedArgs &a) {
+  if (threadIdx.x == 0) {
+    if (blockIdx.x == 0 && !a.late) vouch(a);
+    launch_dependents();
+  }
+}
 
 // A part: the rows of o, then the exponents of the units of o and l, and l of
 // each. Four values of d go together, those of row r at place (d / 4) ^ (r % 32):

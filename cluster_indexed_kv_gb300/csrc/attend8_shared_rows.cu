@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   wait_prerequisites();
-  launch_dependents();
+  launch_vouched(a);
   pre.fill(a);
   if (threadIdx.x == 32 * kShK) pre.share(a, seg.x, seg.end);
   tmem_before();
@@ -377,7 +377,10 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
         done += st.s1 - st.s0;
       }
     }
-    if (threadIdx.x == 0) bulk_wait_all();
+    if (threadIdx.x == 0) {
+      bulk_wait_all();
+      if (a.late && blockIdx.x == 0) vouch(a);
+    }
     tmem_before();
     __syncthreads();
   } else if (warp < kShIssuer) {

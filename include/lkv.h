@@ -706,6 +706,14 @@ lkv_status lkv_cache8_attend_shared(const lkv_cache8 *cache, const lkv_cache8 *p
 lkv_status lkv_cache8_attend_shared_workspace(const lkv_cache8 *cache, const lkv_cache8 *prefix,
                                               int32_t group, int32_t n, int32_t max_len, int64_t *bytes);
 
+/* Check of a rare path (no counterpart in the pages). The second kernel of a
+ * shared attention reads the own tokens while the first one runs, on the word of
+ * that one that what was launched before both has ended; had it not been given in
+ * time, the second would take them again behind the first one's end. With on not
+ * 0, the word is given at the first kernel's end in the shared attentions that this
+ * thread launches from now on, so that this happens; results are the same. */
+lkv_status lkv_diag_shared_late(int32_t on);
+
 /* Blocking: waits for stream, then reports and clears what calls on this
  * cache recorded: LKV_ETIMEOUT (an attention, take or keep whose copies did not
  * arrive: what it made is not complete), else LKV_ECAPACITY, else LKV_EINVAL

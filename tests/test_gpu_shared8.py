@@ -412,3 +412,34 @@ def test_few_rows_of_uneven_prefixes(fmt, dtype, pre, b, h):
     check(c, p, to, own, pre, q)
     check(c, p, to, own, pre, q, max_len=40)
     c[0].check()
+
+
+@pytest.mark.parametrize("fmt,dtype,b,own,n", [
+    ("int8", BF16, 4, 33, 1), ("int8", BF16, 3, 700, 1), ("e4m3", BF16, 2, 5000, 2), ("e4m3", F32, 3, 33, 2), ("int8", F32, 2, 2000, 4),
+    ("int8", BF16, 40, 33, 1), ("e4m3", BF16, 9, 300, 2), ("int8", BF16, 6, 40, 20)])
+def test_own_tokens_taken_again(fmt, dtype, b, own, n):
+    """The first kernel's word for what was written before the call comes late: the second takes the own tokens again, of
+    every step what was written before it, and the bits are those of a word in time."""
+    g = gen(b + own)
+    p, c = cache(g, 2, [700, 20], fmt, dtype), cache(g, 2, [max(own - 3 * i, 1) for i in range(b - 1)] + [0], fmt, dtype, room=96)
+    to = i32(*[i % 3 - 1 for i in range(b)])
+    d = c[0]
+    steps = [torch.randn(3, b, 8, n, 128, generator=g).to(dtype).cuda() for _ in range(3)]
+    start = [t.clone() for t in (d.k_codes.view(torch.int8), d.v_codes.view(torch.int8), d.k_scale, d.v_scale, d.k_tail, d.v_tail, d.lengths)]
+    got = []
+    for late in (False, True):
+        for t, x in zip((d.k_codes.view(torch.int8), d.v_codes.view(torch.int8), d.k_scale, d.v_scale, d.k_tail, d.v_tail, d.lengths), start):
+            t.copy_(x)
+        _lib.lkv_diag_shared_late(late)
+        try:
+            outs = []
+            for x in steps:
+                d.write(x[1, :, :2].contiguous(), x[2, :, :2].contiguous())
+                outs.append(d.attend_shared(x[0], p[0], to))
+        finally:
+            _lib.lkv_diag_shared_late(False)
+        torch.cuda.synchronize()
+        got.append(outs)
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    d.check()
