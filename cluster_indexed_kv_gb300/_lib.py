@@ -26,7 +26,8 @@ EXPORTED = ("lkv_create", "lkv_destroy", "lkv_build_index", "lkv_load_index",
             "lkv_rope_init", "lkv_rope_apply", "lkv_rope_apply_axes", "lkv_cache8_write", "lkv_cache8_read",
             "lkv_cache8_attend", "lkv_cache8_attend_workspace", "lkv_cache8_take",
             "lkv_cache8_take_workspace", "lkv_cache8_keep", "lkv_cache8_attend_shared",
-            "lkv_cache8_attend_shared_workspace", "lkv_cache8_status", "lkv_diag_shared_late")
+            "lkv_cache8_attend_shared_workspace", "lkv_cache8_status", "lkv_diag_shared_late",
+            "lkv_diag_shared_hold")
 LKV_FILTER_TENSOR, LKV_FILTER_SIMT = 0, 1
 LKV_TRIGGER_ADAPTIVE, LKV_TRIGGER_EVERY, LKV_TRIGGER_INTERVAL = 0, 1, 2
 LKV_FILL_PREFIX, LKV_FILL_SKIP = 0, 1
@@ -182,6 +183,8 @@ def load(path: str = LIB_PATH):
         L.lkv_cache8_status.restype = st
         L.lkv_diag_shared_late.argtypes = [i32]
         L.lkv_diag_shared_late.restype = st
+        L.lkv_diag_shared_hold.argtypes = [i32, i64]
+        L.lkv_diag_shared_hold.restype = st
         L.lkv_sync.argtypes = [vp]
         L.lkv_sync.restype = st
         L.lkv_last_error.argtypes = [vp]
@@ -340,6 +343,10 @@ def lkv_diag_wait_timeout(ctx, limit_ns: int) -> None:
 
 def lkv_diag_shared_late(on: bool) -> None:
     _check(load().lkv_diag_shared_late(int(on)), None)
+
+
+def lkv_diag_shared_hold(step: int, limit_ns: int = 0) -> None:
+    _check(load().lkv_diag_shared_hold(step, limit_ns), None)
 
 
 def lkv_sync(ctx) -> None:

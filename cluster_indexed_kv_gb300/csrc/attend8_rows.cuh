@@ -113,13 +113,13 @@ struct RowsSync {
 
 // Wait for the phase; false, and the abort flag raised, when it does not come
 // in time or another wait of the CTA has given up.
-__device__ __forceinline__ bool rows_wait(uint64_t *bar, uint32_t phase, volatile int *abort) {
+__device__ __forceinline__ bool rows_wait(uint64_t *bar, uint32_t phase, volatile int *abort, uint64_t limit = kCopyLimitNs) {
   if (bar_try(bar, phase)) return true;
   uint64_t t0, t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
   while (!bar_try(bar, phase)) {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    if (*abort || t - t0 > kCopyLimitNs) {
+    if (*abort || t - t0 > limit) {
       *abort = 1;
       return false;
     }
@@ -127,8 +127,8 @@ __device__ __forceinline__ bool rows_wait(uint64_t *bar, uint32_t phase, volatil
   return true;
 }
 // The same for a whole warp, uniformly.
-__device__ __forceinline__ bool rows_wait_warp(uint64_t *bar, uint32_t phase, volatile int *abort) {
-  return __all_sync(0xffffffffu, rows_wait(bar, phase, abort));
+__device__ __forceinline__ bool rows_wait_warp(uint64_t *bar, uint32_t phase, volatile int *abort, uint64_t limit = kCopyLimitNs) {
+  return __all_sync(0xffffffffu, rows_wait(bar, phase, abort, limit));
 }
 
 // The e of a largest magnitude (bits) < 2^e, within the fp32 scales' reach.

@@ -25,6 +25,8 @@ struct SharedPlan {
 };
 
 static thread_local int32_t vouch_late = 0;  // lkv_diag_shared_late
+static thread_local int32_t hold_step = INT32_MAX;  // lkv_diag_shared_hold
+static thread_local int64_t hold_limit = (int64_t)kCopyLimitNs;
 
 static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t group, int32_t n, int32_t max_len, int sms, SharedPlan *s) {
   const int64_t R = (int64_t)n * group, rows = c->batch * R, S = (int64_t)c->batch * c->n_kv_heads;
@@ -128,6 +130,14 @@ extern "C" lkv_status lkv_diag_shared_late(int32_t on) {
   return LKV_OK;
 }
 
+extern "C" lkv_status lkv_diag_shared_hold(int32_t step, int64_t limit_ns) {
+  using namespace lkv;
+  if (step >= 0 && (limit_ns < 1 || limit_ns > 1000000000)) return refuse("lkv_diag_shared_hold: limit_ns must be 1..1e9");
+  hold_step = step < 0 ? INT32_MAX : step;
+  hold_limit = step < 0 ? (int64_t)kCopyLimitNs : limit_ns;
+  return LKV_OK;
+}
+
 extern "C" lkv_status lkv_cache8_attend_shared_workspace(const lkv_cache8 *c, const lkv_cache8 *prefix, int32_t group, int32_t n,
                                                          int32_t max_len, int64_t *bytes) {
   using namespace lkv;
@@ -190,6 +200,8 @@ extern "C" lkv_status lkv_cache8_attend_shared(const lkv_cache8 *c, const lkv_ca
   a.parts = (float *)((char *)workspace + s.parts_at);
   a.vouch = (uint64_t *)workspace;
   a.late = vouch_late;
+  a.hold = hold_step;
+  a.limit_ns = (uint64_t)hold_limit;
   const int64_t SP = (int64_t)prefix->batch * prefix->n_kv_heads;
   CUtensorMap maps[4];  // of the prefixes and of the own tokens, where tiles of 16 take them
   if ((s.nt != 16 && (!codes_map(&maps[0], prefix->k_codes, prefix->capacity, SP, kBlock) || !codes_map(&maps[1], prefix->v_codes, prefix->capacity, SP, kBlock))) ||

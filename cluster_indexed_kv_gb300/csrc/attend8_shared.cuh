@@ -28,6 +28,8 @@ struct SharedArgs : AttendArgs {
   float *parts;
   uint64_t *vouch;            // what the first kernel vouches with, another value each time (see vouch)
   int32_t late;               // it does so at its end (lkv_diag_shared_late)
+  int32_t hold;               // the step of each CTA from which on there are no products (lkv_diag_shared_hold)
+  uint64_t limit_ns;          // of a wait between a CTA's warps
 };
 
 // The second kernel begins while the first still runs, and takes the sequences' own

@@ -84,6 +84,7 @@ struct SharedPiece {
   const uint16_t *tail[2];
   int len;
   int go;                     // whether there is a piece
+  int dead;                   // a wait in an earlier one has given up: this one has no steps, but tiles and parts are told of
   int once;                   // whether its tokens are read for this row tile alone
   int last;                   // the last token that a row sees
   uint32_t top, tail_top[2];  // largest V scale of the piece's blocks, largest magnitudes of the tails (bits)
@@ -103,7 +104,7 @@ struct Steps {
     tail_rows = p.len - full * kBlock;
     // steps behind the last token that a row sees are nobody's
     s0 = max(p.p.u0 - kSharedStart, 0);
-    s1 = max(min(p.p.u1 - kSharedStart, (p.last + kRwTok) / kRwTok), s0);
+    s1 = p.dead ? s0 : max(min(p.p.u1 - kSharedStart, (p.last + kRwTok) / kRwTok), s0);
     tail = s1 > s0 && full < nb && s1 * kRwBlocks >= nb;
   }
 };
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       int g = done + ((done ^ w) & 1);
       if (!any) {  // no row of this warp's is there
         for (; ok && g < end; g += 2) {
-          ok = rows_wait_warp(&sy.sfull[w], (g >> 1) & 1, &abort_s);
+          ok = rows_wait_warp(&sy.sfull[w], (g >> 1) & 1, &abort_s, a.limit_ns);
           if (ok && lane == 0) {
             bar_arrive(&sy.pfull[w][0]);
             bar_arrive(&sy.pfull[w][1]);
@@ -281,11 +282,11 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       }
 #pragma unroll 1
       for (; ok && g < end; g += 2) {
-        ok = rows_wait_warp(&sy.scfull[g & 3], (g >> 2) & 1, &abort_s);
+        ok = rows_wait_warp(&sy.scfull[g & 3], (g >> 2) & 1, &abort_s, a.limit_ns);
         if (!ok) break;
         const float4 *const sc = scales[g & 3];
         const bool open = __float_as_int(sc[kRwBlocks - 1].w) <= last_open;
-        ok = rows_wait_warp(&sy.sfull[w], (g >> 1) & 1, &abort_s);
+        ok = rows_wait_warp(&sy.sfull[w], (g >> 1) & 1, &abort_s, a.limit_ns);
         if (!ok) break;
         tmem_after();
         float sum = 0.f;
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
         l += sum;
       }
       // the last step's product, if there was one
-      if (ok && any && end - done > ((done ^ w) & 1)) ok = rows_wait_warp(&sy.odone[w][1], ((g - 2) >> 1) & 1, &abort_s);
+      if (ok && any && end - done > ((done ^ w) & 1)) ok = rows_wait_warp(&sy.odone[w][1], ((g - 2) >> 1) & 1, &abort_s, a.limit_ns);
       // (a row whose scores are all NaN has no reference, but l and O, which are NaN, count)
       seg.ref[w][row] = seen ? ref : -INFINITY;
       seg.l[w][row] = l;
@@ -390,7 +391,8 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
     while (true) {
       __syncthreads();
       if (threadIdx.x == 32 * kShK) {
-        seg.go = seg.x < seg.end && !abort_s;
+        seg.go = seg.x < seg.end;
+        seg.dead = abort_s;
         if (seg.go) {
           const Prefixes<true>::Piece p = pre.piece(a, seg.x, seg.end);
           if (p.u0 == 0) pre.announce(a, p, seg.x);
@@ -465,7 +467,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
       for (int g = done; g < done + s1 - s0; ++g) {
         const int j = g - done + s0, st = g & 1;
         const bool ends = z.tail && (j + 1) * kRwBlocks >= z.nb;  // the step's last block is the partial one
-        if (!rows_wait_warp(kv ? &sy.vempty[st] : &sy.kempty[st], ((g >> 1) & 1) ^ 1, &abort_s)) break;
+        if (!rows_wait_warp(kv ? &sy.vempty[st] : &sy.kempty[st], ((g >> 1) & 1) ^ 1, &abort_s, a.limit_ns)) break;
         unsigned char *const to_tile = area + (1 + 2 * kv + st) * kRwTile;
         const int half = (lane >> 2) & 1, run = lane & 3;
 #pragma unroll
@@ -518,14 +520,14 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
         // -------------------------------------------------------------- products
         // The whole warp goes along, one lane issues: descriptors and addresses stay
         // in uniform registers.
-        const int first = __shfl_sync(0xffffffffu, done, 0), stop = __shfl_sync(0xffffffffu, end, 0);
+        const int first = __shfl_sync(0xffffffffu, done, 0), stop = __shfl_sync(0xffffffffu, min(end, a.hold), 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint32_t q_lo = q_at >> 4, k_lo = k_at >> 4, v_lo = v_at >> 4;
         const bool one = elect_one();
         tmem_after();
         auto qk = [&](int g) {
           const int w = g & 1;
-          if (!rows_wait_warp(&sy.kfull[w], (g >> 1) & 1, &abort_s)) return false;
+          if (!rows_wait_warp(&sy.kfull[w], (g >> 1) & 1, &abort_s, a.limit_ns)) return false;
           tmem_after();
           if (one) {
 #pragma unroll
@@ -542,10 +544,10 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
         // O += P V of a step's first and then second 64 tokens, each as soon as its weights are there
         auto pv = [&](int g) {
           const int w = g & 1;
-          if (!rows_wait_warp(&sy.vfull[w], (g >> 1) & 1, &abort_s)) return false;
+          if (!rows_wait_warp(&sy.vfull[w], (g >> 1) & 1, &abort_s, a.limit_ns)) return false;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (!rows_wait_warp(&sy.pfull[w][h], (g >> 1) & 1, &abort_s)) return false;
+            if (!rows_wait_warp(&sy.pfull[w][h], (g >> 1) & 1, &abort_s, a.limit_ns)) return false;
             tmem_after();
             if (one) {
 #pragma unroll
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
           }
           return true;
         };
-        bool ok = first == stop || (qk(first) && (stop - first < 2 || qk(first + 1)));
+        bool ok = first >= stop || (qk(first) && (stop - first < 2 || qk(first + 1)));
         for (int g = first; ok && g < stop; ++g) ok = pv(g) && (g + 2 >= stop || qk(g + 2));
       } else if (warp == kShScales) {
         // -------------------------------------------------------------- scales
@@ -590,7 +592,7 @@ __global__ void __launch_bounds__(kShThreads, 1) k_shared_rows(const __grid_cons
           load(g + 4);
 #pragma unroll 1
           for (int i = g; ok && i < min(g + 4, end); ++i) {
-            ok = rows_wait_warp(&scempty[i & 3], ((i >> 2) & 1) ^ 1, &abort_s);
+            ok = rows_wait_warp(&scempty[i & 3], ((i >> 2) & 1) ^ 1, &abort_s, a.limit_ns);
             if (!ok) break;
             if (lane / kRwBlocks == i - g) scales[i & 3][lane % kRwBlocks] = s;
             __syncwarp();

@@ -714,6 +714,14 @@ lkv_status lkv_cache8_attend_shared_workspace(const lkv_cache8 *cache, const lkv
  * thread launches from now on, so that this happens; results are the same. */
 lkv_status lkv_diag_shared_late(int32_t on);
 
+/* Failure-path check (no counterpart in the pages): in the shared attentions of
+ * bf16 caches and more than 16 rows that this thread launches from now on, each
+ * CTA's steps (of 128 tokens) from the one numbered `step` (from 0) on get no
+ * products, so that the waits for those give up after limit_ns nanoseconds
+ * (1..1e9, else LKV_EINVAL): the output is not complete and lkv_cache8_status
+ * returns LKV_ETIMEOUT. A negative step ends that. */
+lkv_status lkv_diag_shared_hold(int32_t step, int64_t limit_ns);
+
 /* Blocking: waits for stream, then reports and clears what calls on this
  * cache recorded: LKV_ETIMEOUT (an attention, take or keep whose copies did not
  * arrive: what it made is not complete), else LKV_ECAPACITY, else LKV_EINVAL

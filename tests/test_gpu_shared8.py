@@ -443,3 +443,64 @@ def test_own_tokens_taken_again(fmt, dtype, b, own, n):
     for x, y in zip(*got):
         assert torch.equal(x, y)
     d.check()
+
+
+@pytest.mark.parametrize("fmt,pre,b,h,group,n,step", [
+    ("int8", [20 + i % 300 for i in range(200)], 200, 2, 2, 1, 0), ("e4m3", [20 + i % 300 for i in range(200)], 200, 2, 2, 1, 1),
+    ("int8", [300] * 100, 100, 2, 2, 20, 0), ("int8", [40000, 64], 40, 2, 4, 2, 3), ("int8", [700], 8, 2, 4, 64, 1)])
+def test_a_wait_that_gives_up(fmt, pre, b, h, group, n, step):
+    """Products that never come: the waits for them end, every tile and part of the call is told of all the same (the second
+    kernel finds its way by them), the call is reported, and the next one is right."""
+    g = gen(b + n + step)
+    own = [n + i % 40 for i in range(b)]
+    p, c = cache(g, h, pre, fmt, BF16)[0], cache(g, h, own, fmt, BF16)[0]
+    to = i32(*[i % len(pre) for i in range(b)])
+    q = torch.randn(b, h * group, n, 128, generator=g).to(BF16).cuda()
+    want = c.attend_shared(q, p, to)
+    c.check()
+    R = n * group
+    listed = [-(-sum(x % len(pre) == y for x in range(b)) * R // 128) * h for y in range(len(pre))] + ([-(-R // 128) * h] * b if R > 16 else [])
+    most = (-(-b * R // 128) + min(len(pre), b)) * h + (b * h * -(-R // 128) if R > 16 else 0)
+    bytes_ = _lib.lkv_cache8_attend_shared_workspace(c._at, p._at, group, n, 0)
+    ws = torch.zeros(bytes_, dtype=torch.uint8, device="cuda")  # a tile that is not told of: no parts
+    tiles_at = 16 + 16 * b
+    parts_at = tiles_at + (8 * most + 15) // 16 * 16
+    ws[parts_at:] = 255  # a part that is not told of: NaN
+    _lib.lkv_diag_shared_hold(step, 1_000_000)
+    try:
+        _lib._check(_lib.load().lkv_cache8_attend_shared(c._at, p._at, to.data_ptr(), q.data_ptr(), group, n, None, 128 ** -0.5, 0,
+                                                         torch.empty_like(q).data_ptr(), ws.data_ptr(), bytes_, torch.cuda.current_stream().cuda_stream), None)
+    finally:
+        _lib.lkv_diag_shared_hold(-1)
+    with pytest.raises(_lib.LKVError) as e:
+        c.check()
+    assert e.value.status == _lib.LKV_ETIMEOUT
+    tiles = ws[tiles_at:tiles_at + 8 * sum(listed)].view(torch.int32).view(-1, 2).cpu()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert (tiles[:, 0] >= 0).all() and (tiles[:, 1] >= 1).all() and (tiles.sum(1) <= sms).all()
+    parts = ws[parts_at:].view(torch.float32).view(-1, 128 * 131).cpu()
+    for t, (first, count) in enumerate(tiles.tolist()):
+        assert not parts[first + t:first + t + count, 128 * 128:128 * 130].isnan().any(), t
+    assert torch.equal(c.attend_shared(q, p, to), want)
+    c.check()
+
+
+def test_a_call_that_does_not_come_to_the_step():
+    """... has waited for nothing that did not come: it is right."""
+    g = gen(11)
+    p, c = cache(g, 2, [5000, 64], "int8", BF16)[0], cache(g, 2, [2 + i for i in range(40)], "int8", BF16)[0]
+    to, q = i32(*[i % 2 for i in range(40)]), torch.randn(40, 8, 2, 128, generator=g).to(BF16).cuda()
+    want = c.attend_shared(q, p, to)
+    _lib.lkv_diag_shared_hold(40, 1_000_000)
+    try:
+        assert torch.equal(c.attend_shared(q, p, to), want)
+    finally:
+        _lib.lkv_diag_shared_hold(-1)
+    c.check()
+
+
+def test_a_wait_that_gives_up_refuses_limits():
+    for limit in (0, -1, 1_000_000_001):
+        with pytest.raises(_lib.LKVError):
+            _lib.lkv_diag_shared_hold(0, limit)
+    _lib.lkv_diag_shared_hold(-1, 0)
