@@ -47,6 +47,7 @@ static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t
   s->own_parts = s->nt == 16 && (R > 16 || (R > 8 && steps <= 11 * (int64_t)sms));
   const int part_rows = 8 * s->nt;
   s->ctas = s->nt == 16 ? sms : sms * (fp32 && s->nt == 2 ? 1 : 2);
+  const int64_t most_ctas = s->ctas;
   s->tiles = ((rows + part_rows - 1) / part_rows + (p->batch < c->batch ? p->batch : c->batch)) * c->n_kv_heads;
   if (s->own_parts) s->tiles += S * ((R + part_rows - 1) / part_rows);
   s->own_nt = R <= 8 ? 1 : 2;
@@ -69,7 +70,8 @@ static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t
   s->seq_at = 16;
   s->tile_at = s->seq_at + (int64_t)c->batch * 16;
   s->parts_at = s->tile_at + (s->tiles * 8 + 15) / 16 * 16;
-  s->bytes = s->parts_at + (s->ctas + s->tiles) * part_floats(part_rows) * 4;
+  // parts for all CTAs: the workspace does not depend on the prefixes' capacity
+  s->bytes = s->parts_at + (most_ctas + s->tiles) * part_floats(part_rows) * 4;
   return nullptr;
 }
 

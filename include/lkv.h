@@ -702,7 +702,7 @@ lkv_status lkv_cache8_attend_shared(const lkv_cache8 *cache, const lkv_cache8 *p
                                     void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Bytes of workspace that lkv_cache8_attend_shared needs for these sizes, into
- * *bytes. Errors: LKV_EINVAL. */
+ * *bytes: the same for prefixes of any capacity. Errors: LKV_EINVAL, LKV_ECUDA. */
 lkv_status lkv_cache8_attend_shared_workspace(const lkv_cache8 *cache, const lkv_cache8 *prefix,
                                               int32_t group, int32_t n, int32_t max_len, int64_t *bytes);
 

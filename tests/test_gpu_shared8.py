@@ -504,3 +504,19 @@ def test_a_wait_that_gives_up_refuses_limits():
         with pytest.raises(_lib.LKVError):
             _lib.lkv_diag_shared_hold(0, limit)
     _lib.lkv_diag_shared_hold(-1, 0)
+
+
+@pytest.mark.parametrize("dtype,b,n", [(BF16, 4, 1), (F32, 2, 1), (F32, 3, 4), (BF16, 9, 1)])
+def test_one_cache_behind_prefixes_of_several_capacities(dtype, b, n):
+    """Prompts of different lengths in caches of their own, by turns behind one cache, in either order."""
+    g = gen(b)
+    h, group = 8, 4
+    lengths = [20 + i for i in range(b)]
+    prompts = [cache(g, h, [length], "int8", dtype, room=room) for length, room in ((500, 32768 - 512), (2040, 0), (512, 0))]
+    q = torch.randn(b, h * group, n, 128, generator=g).to(dtype)
+    for order in ((0, 1, 2), (2, 1, 0)):
+        c = cache(gen(b + 1), h, lengths, "int8", dtype, room=256 - 32)
+        for x in order:
+            check(c, prompts[x], None, lengths, [(500, 2040, 512)[x]], q)
+        sizes = {_lib.lkv_cache8_attend_shared_workspace(c[0]._at, prompts[x][0]._at, group, n, 0) for x in order}
+        assert len(sizes) == 1
