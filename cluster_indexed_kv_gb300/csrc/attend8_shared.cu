@@ -58,10 +58,15 @@ static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t
   if (cluster > most) cluster = most;
   s->cluster = (int)(cluster < 1 ? 1 : cluster > kAtMaxCluster ? kAtMaxCluster : cluster);
   if (s->nt != 16) {
-    // Where the prefixes can fill every CTA, some are left out for the own tokens'
-    // to run beside them: 4 samples of 32K tokens 33 -> 29 us, of 131K 73 -> 68; in
-    // fp32, 16 of 152 CTAs, 44 -> 42 and 122 -> 119. More than an eighth cost more than
-    // that: 24 of 152, 6 fp32 samples of 131K 197 -> 220.
+    // Where prefixes as long as their cache has room for would fill every CTA, some
+    // are left out for the own tokens' to run beside them: 4 samples of 32K tokens 33
+    // -> 29 us, of 131K 73 -> 68; in fp32, 16 of 152 CTAs, 44 -> 42 and 122 -> 119. More
+    // than an eighth cost more than that: 24 of 152, 6 fp32 samples of 131K 197 -> 220.
+    // Their lengths are known on the device alone. Short prefixes in a cache of 131K
+    // tokens, against a cache that they fill: 1 to 4 samples, bf16 and fp32, of 64
+    // tokens 1.3 to 1.8 us faster, of 512 0.1 to 1.5 faster, of 2048 from 1.4 faster to
+    // 0.8 slower (4 samples, 17.8 -> 18.6), of 4096 the same. All CTAs launched, and as
+    // many leaving again where the lengths say so: 4 samples of 131K 68 -> 77.
     const int64_t own = s->own_tiles * s->cluster, per_sm = fp32 && s->own_nt == 2 ? 1 : 2;
     const int64_t room = s->ctas > sms ? own : (own + per_sm - 1) / per_sm;
     if (room <= s->ctas / 8 && s->tiles * (p->capacity / kBlock) / kSharedFewLeast > s->ctas - room) s->ctas -= (int)room;

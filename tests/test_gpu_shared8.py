@@ -520,3 +520,15 @@ def test_one_cache_behind_prefixes_of_several_capacities(dtype, b, n):
             check(c, prompts[x], None, lengths, [(500, 2040, 512)[x]], q)
         sizes = {_lib.lkv_cache8_attend_shared_workspace(c[0]._at, prompts[x][0]._at, group, n, 0) for x in order}
         assert len(sizes) == 1
+
+
+@pytest.mark.parametrize("dtype,b,n", [(BF16, 4, 1), (BF16, 1, 1), (F32, 2, 1), (F32, 4, 4)])
+def test_a_short_prefix_in_a_large_cache(dtype, b, n):
+    """The split goes by the prefix cache's capacity: what it holds may be a small part of that, or nothing."""
+    g = gen(b)
+    lengths = [20 + i for i in range(b)]
+    q = torch.randn(b, 32, n, 128, generator=g).to(dtype)
+    c = cache(g, 8, lengths, "int8", dtype, room=64)
+    for pre in (0, 1, 100, 1000):
+        check(c, cache(g, 8, [pre], "int8", dtype, room=32768), None, lengths, [pre], q)
+    c[0].check()
