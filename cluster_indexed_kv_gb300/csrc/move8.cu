@@ -12,7 +12,9 @@ namespace lkv {
 // computed but the tail of a sequence that ends inside an older block.
 constexpr int kMoveStage = 16384;        // bytes of a stage's codes
 constexpr int kMoveStages = 4;
-constexpr int kMovePerSm = 3;            // CTAs that an SM's shared memory holds
+constexpr int kMovePerSm = 3;            // CTAs that an SM's shared memory holds, where their tables are small
+constexpr int kSmShared = 228 * 1024;    // an SM's shared memory, of which each CTA takes kSmReserved more than it asks for
+constexpr int kSmReserved = 1024;
 constexpr int kBlockBytes = kBlock * kHeadDim;
 constexpr int kTakeItems = 32;           // destinations of a CTA between two caches
 constexpr int kTakeInside = 1024;        // and within one, all of them: 16 bytes of each in a stage
@@ -121,7 +123,9 @@ __host__ __device__ inline int64_t take_smem(int items) {
 // Bound by bytes. On a GB300, 8 KV heads: one prompt of 8191 tokens into 16
 // sequences 48 us, 87% of the measured copy rate; 8 sequences of 32768 into
 // another cache 175 us (91%), and round within their own 185 us; 24 beams of 517
-// tokens put in order 10.3 us, two launches' latency.
+// tokens put in order 10.3 us, two launches' latency. Within a cache columns get
+// narrower with the distinct sources (all are in one stage), and slow: 520 sequences
+// of 1100 tokens from nine of them 380 us, each from another 16 ms.
 template <int DT, int CODE>
 __global__ void __launch_bounds__(32) k_cache8_take(const __grid_constant__ TakeArgs a) {
   extern __shared__ __align__(128) unsigned char area[];
@@ -579,9 +583,11 @@ extern "C" lkv_status lkv_cache8_take(const lkv_cache8 *c, const lkv_cache8 *sou
     a.from.lengths = before;
   }
   const int groups = (c->batch + a.items - 1) / a.items;  // below 2^16: 2^20 sequences at most
-  const int wide = kMovePerSm * sms;
-  const dim3 grid((unsigned)((wide + groups - 1) / groups), (unsigned)groups);
+  // As many CTAs as there is room for at once, as each has an even share: within a
+  // cache of some 300 sequences or more, with their tables, two an SM.
   const size_t smem = (size_t)take_smem(a.items), most = (size_t)take_smem(kTakeInside);
+  const int fit = kSmShared / ((int)smem + kSmReserved + 64), wide = (fit < kMovePerSm ? fit : kMovePerSm) * sms;
+  const dim3 grid((unsigned)((wide + groups - 1) / groups), (unsigned)groups);
   if (bf) e = i8 ? launch_sized<k_cache8_take<1, LKV_CODE_INT8>>(grid, smem, most, st, a) : launch_sized<k_cache8_take<1, LKV_CODE_E4M3>>(grid, smem, most, st, a);
   else e = i8 ? launch_sized<k_cache8_take<0, LKV_CODE_INT8>>(grid, smem, most, st, a) : launch_sized<k_cache8_take<0, LKV_CODE_E4M3>>(grid, smem, most, st, a);
   return e == cudaSuccess ? LKV_OK : cuda_refuse("lkv_cache8_take", e);

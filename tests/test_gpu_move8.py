@@ -305,3 +305,19 @@ def test_refusals():
     lkv.Cache8(batch=1025, n_kv_heads=1, capacity=16, dtype=BF16).take(large)
     mv.same(download(d), c)
     d.check()
+
+
+@pytest.mark.parametrize("b,h,n", [(300, 2, 150), (345, 2, 150), (1024, 2, 100)])
+def test_take_within_a_cache_where_fewer_ctas_fit(b, h, n):
+    """The tables of many sequences leave room for two CTAs an SM in place of three."""
+    r = random.Random(b)
+    have = [r.randrange(n - 60, n + 1) for _ in range(b)]
+    c = mv.filled(b, h, (n + 31) // 16 * 16, "int8", BF16, have, 5)
+    d = upload(c)
+    for to in ([(i * 7 + 3) % b for i in range(b)], [i - i % 64 for i in range(b)]):
+        lengths = [c[1][x] if i % 3 else c[1][x] - r.randrange(40) for i, x in enumerate(to)]
+        want, bad = mv.take(c, c, to, lengths)  # some are cut to less than nothing: those stay
+        d.take(sequences=ints(to), lengths=ints(lengths))
+        mv.same(download(d), want)
+        checked(d, bad)
+        c = download(d)
