@@ -77,7 +77,8 @@ __device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcont
 
 // Whether a kernel has been allowed its largest dynamic shared memory on a
 // device: once a process (two such calls for each attention behind prefixes took
-// 3 of its 17 us from Python).
+// 3 of its 17 us from Python). The runtime keeps that for the device, in every
+// context and past a reset of the primary one.
 struct SmemAllowed {
   std::atomic<bool> on[64]{};
   cudaError_t allow(const void *fn, int bytes) {

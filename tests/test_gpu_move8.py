@@ -1,5 +1,7 @@
 """Taking and keeping tokens of the 8-bit cache: every bit of what it holds after."""
 import random
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -7,6 +9,7 @@ import torch
 import cluster_indexed_kv_gb300 as lkv
 from cluster_indexed_kv_gb300 import _lib
 from tests import _move8_ref as mv
+from tests.conftest import ROOT
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -321,3 +324,93 @@ def test_take_within_a_cache_where_fewer_ctas_fit(b, h, n):
         mv.same(download(d), want)
         checked(d, bad)
         c = download(d)
+
+
+# An own cache, a prefix cache, queries and what the calls make of them, once in
+# torch's context and once in another one on the same device.
+OTHER_CONTEXT = '''
+import ctypes as C
+import torch
+import cluster_indexed_kv_gb300 as lkv
+from cluster_indexed_kv_gb300 import _lib
+from tests import _move8_ref as mv
+from tests.conftest import ROOT
+from tests.test_gpu_move8 import upload
+
+lkv.build()
+cu = C.CDLL("libcuda.so.1")
+
+
+def ok(e):
+    assert e == 0, e
+
+
+def arrays(c):
+    return [c.k_codes, c.v_codes, c.k_scale, c.v_scale, c.k_tail, c.v_tail, c.lengths, c._ticket]
+
+
+class There:
+    """A tensor's bytes in the context that is current."""
+    def __init__(self, t):
+        self.host = t.detach().cpu().contiguous().flatten().view(torch.uint8)
+        self.at = C.c_uint64()
+        ok(cu.cuMemAlloc_v2(C.byref(self.at), C.c_size_t(self.host.numel())))
+        ok(cu.cuMemcpyHtoD_v2(self.at, C.c_void_p(self.host.data_ptr()), C.c_size_t(self.host.numel())))
+
+    def back(self):
+        got = torch.empty_like(self.host)
+        ok(cu.cuMemcpyDtoH_v2(C.c_void_p(got.data_ptr()), self.at, C.c_size_t(got.numel())))
+        return got
+
+
+def view(c, at):
+    return _lib.lkv_cache8(c.batch, c.n_kv_heads, c.capacity, c._view.dtype, c._view.code, 0, *[x.at.value for x in at])
+
+
+def calls(L, own, prefix, q, out, ws, ws_bytes, group, n, order, blocks, counts, spare):
+    """Attention behind the prefixes, sequences put in order, blocks kept and copied."""
+    for status in (L.lkv_cache8_attend_shared(own, prefix, None, q, group, n, None, 0.1, 0, out, ws, ws_bytes, None),
+                   L.lkv_cache8_take(own, None, order, None, ws, ws_bytes, None),
+                   L.lkv_cache8_keep(spare, own, blocks, 1, counts, None), L.lkv_cache8_take(spare, own, order, None, None, 0, None)):
+        assert status == 0, _lib.lkv_last_error(None)
+
+
+for dtype, b, n in ((torch.bfloat16, 2, 1), (torch.bfloat16, 6, 1), (torch.bfloat16, 3, 20), (torch.float32, 3, 1)):
+    h, group = 2, 4
+    made = [mv.filled(k, h, 96, "int8", dtype, [70 - i for i in range(k)], seed) for k, seed in ((b, 1), (1, 2), (b, 3))]
+    caches = [upload(x) for x in made]
+    q = torch.randn(b, h * group, n, 128).to(dtype).cuda()
+    order = torch.tensor([(i + 1) % b for i in range(b)], dtype=torch.int32).cuda()
+    blocks, counts = torch.ones(b, h, 1, dtype=torch.int32).cuda(), torch.ones(b, dtype=torch.int32).cuda()
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    out = torch.zeros_like(q)
+    L = _lib.load()
+    torch.cuda.synchronize()
+    ctx, dev = C.c_void_p(), C.c_int()
+    ok(cu.cuDeviceGet(C.byref(dev), 0))
+    start, more = [[x.cpu() for x in arrays(c)] for c in caches], [x.cpu() for x in (q, out, order, blocks, counts)]
+    calls(L, caches[0]._at, caches[1]._at, q.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(), group, n, order.data_ptr(), blocks.data_ptr(),
+          counts.data_ptr(), caches[2]._at)
+    torch.cuda.synchronize()
+    want = [x.cpu().flatten().view(torch.uint8) for c in caches for x in arrays(c)] + [out.cpu().flatten().view(torch.uint8)]
+    ok(cu.cuCtxCreate_v2(C.byref(ctx), 0, dev))
+    there = [[There(x) for x in s] for s in start]
+    views = [view(c, at) for c, at in zip(caches, there)]
+    tq, to, tr, tb, tc = (There(x) for x in more)
+    tw = There(torch.zeros(64 << 20, dtype=torch.uint8))
+    at = [C.addressof(v) for v in views]
+    calls(L, at[0], at[1], tq.at.value, to.at.value, tw.at.value, 64 << 20, group, n, tr.at.value, tb.at.value, tc.at.value, at[2])
+    ok(cu.cuCtxSynchronize())
+    got = [x.back() for s in there for x in s] + [to.back()]
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    ok(cu.cuCtxDestroy_v2(ctx))
+    assert out.any()
+print("same in both")
+'''
+
+
+def test_another_context_on_the_device():
+    """What a kernel has been allowed in one context holds in another: the same bits in both."""
+    r = subprocess.run([sys.executable, "-c", OTHER_CONTEXT], capture_output=True, text=True, cwd=ROOT, timeout=300)
+    assert r.returncode == 0 and "same in both" in r.stdout, r.stdout + r.stderr
