@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
       // K: 4 whole rows a load, 16 codes a lane: a load takes a pass for each
       // 128-byte line (8 half rows a load: 296 against 284 us for 32 tokens over
       // 32K, 64 slices). V: tokens 8 tc.., d 16 dc.., which fills its tile
-      // without bank conflicts.
+      // without bank conflicts. Plain loads: the write before may end while this
+      // kernel runs already, which read-only ones must not meet.
       const int kr_row = lane >> 3, kr_half = (lane >> 2) & 1, kr_run = lane & 3;
       const int tc = (pw * 32 + lane) & 15, dc = (pw * 32 + lane) >> 4;
       const float kf = pow2f(-ke), vf = pow2f(-max(ve, unit - kUnitSpan));
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
           const int u = j * kRwBlocks + 2 * pw + (t >> 2), b = tile.block(u);
           const bool there = u < tile.nb && b < full;
           const uint8_t *p = kc + ((int64_t)b * kBlock + 4 * (t & 3) + kr_row) * kHeadDim + 16 * (lane & 7);
-          kr[t] = there ? __ldg((const uint4 *)p) : make_uint4(0, 0, 0, 0);
+          kr[t] = there ? *(const uint4 *)p : make_uint4(0, 0, 0, 0);
         }
       };
       auto load_v = [&](int j) {
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) k_attend8_rows(const __grid_con
         const bool there = u < tile.nb && b < full;
         const uint8_t *p = vc + ((int64_t)b * kBlock + 8 * (tc & 1)) * kHeadDim + 16 * dc;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) vr[i] = there ? __ldg((const uint4 *)(p + i * kHeadDim)) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 8; ++i) vr[i] = there ? *(const uint4 *)(p + i * kHeadDim) : make_uint4(0, 0, 0, 0);
       };
       if (steps > 0) {
         load_k(s0);
