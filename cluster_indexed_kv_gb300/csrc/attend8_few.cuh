@@ -428,7 +428,7 @@ struct PrefixSum {
 // Row `row` of the sequence's (slice: sequence and KV head): the sum of its
 // prefix's parts, by a warp, into r of z: a lane takes four values of d, and
 // a part's exponents and total. As many parts are on their way together as
-// registers hold: in fours, a step of 32 samples of 32K tokens took 44.5 us, so 42.7.
+// registers hold: in fours, a step of 32 samples of 32K tokens took 1.8 us longer.
 constexpr int kSumAtOnce = 16;
 template <int RT>
 __device__ __forceinline__ void sum_prefix(const SharedArgs &a, int64_t slice, int row, PrefixSum<RT> &z, int r, int lane) {

@@ -34,7 +34,7 @@ static const char *plan_shared(const lkv_cache8 *c, const lkv_cache8 *p, int32_t
   const bool fp32 = c->dtype == LKV_DTYPE_FP32;
   const int64_t len = max_len > 0 && max_len < c->capacity ? max_len : c->capacity, blocks = (len + kBlock - 1) / kBlock;
   // On a GB300, int8, 8 KV heads, 4 query heads: up to 16 rows are faster in tiles
-  // of 16 (4 samples of a 2048-token prompt 16 us, in tiles of 128 26 us), more
+  // of 16 (4 samples of a 2048-token prompt 17 us, in tiles of 128 26 us), more
   // would read the prefix once for each 16.
   s->nt = !fp32 && rows > 16 ? 16 : rows <= 8 ? 1 : 2;
   // From 17 rows a sequence the own tokens go to the tiles of 128 too (27 x 3 tokens

@@ -35,7 +35,8 @@ struct SharedArgs : AttendArgs {
 // The second kernel begins while the first still runs, and takes the sequences' own
 // tokens meanwhile, which the launches before both have written. What the first
 // one's wait (griddepcontrol.wait) promises, it promises the first kernel; so one of
-// its threads passes it on, behind that wait: it releases the time at `vouch`, and
+// its threads passes it on, behind that wait: it releases the time at `vouch` (in
+// ticks of 32 ns, never the same for two calls, which take microseconds), and
 // each warp of the second kernel acquires what stands there ahead of its reads. Behind
 // its own wait it looks again: if it is the same, it was this call's, and everything
 // before the release was there to be read. If it is not, the tokens are taken again.

@@ -26,11 +26,12 @@ namespace lkv {
 // same memory on their way in; bytes 1390 at the measured copy rate. It takes 2130
 // (8 x 256 tokens behind 16K) to 2400 (a step of 16 or 32 samples): the chain of a
 // half, weights 2850 and then P V and the next S 1000 to 1400, is two steps long,
-// and the producers work 1500 to 1800 of the time. Tensor pipe 39% active, issue
-// slots 49%, LSU data pipe 44%. Beside the steps a piece costs its beginning (5000
+// and the producers work 1500 to 1800 of the time. With 54 steps a CTA (32 samples
+// with 4 new tokens each behind 32K, profiled): tensor pipe 39% active, issue slots
+// 50%, LSU data pipe 47%. Beside the steps a piece costs its beginning (5000
 // clocks: tables, rows, queries, each a round trip or two) and its end (3000 to
 // 4000). On a GB300, 8 KV heads, 4 query heads: 32 samples of a 32K prompt, 14 steps a
-// CTA, 30 us; 8 x 256 tokens behind 16K 535 us, 1.03 PFLOP/s, 53% of the measured
+// CTA, 30 us; 8 x 256 tokens behind 16K 535 us, 1.03 PFLOP/s, 52% of the measured
 // bf16 rate. Measured before, the latter: K, V and scales by the same four warps
 // 2870 us; warps with one role each 751; V as it lies and a whole warp along with
 // the issuing lane 637 (a lane on its own took 1900 clocks a step to issue); 7

@@ -121,11 +121,12 @@ __host__ __device__ inline int64_t take_smem(int items) {
 // this one, from the cache as it was.
 //
 // Bound by bytes. On a GB300, 8 KV heads: one prompt of 8191 tokens into 16
-// sequences 48 us, 87% of the measured copy rate; 8 sequences of 32768 into
-// another cache 175 us (91%), and round within their own 185 us; 24 beams of 517
-// tokens put in order 10.3 us, two launches' latency. Within a cache columns get
-// narrower with the distinct sources (all are in one stage), and slow: 520 sequences
-// of 1100 tokens from nine of them 380 us, each from another 16 ms.
+// sequences 49 us, 86% of the measured copy rate; 8 sequences of 32768 into
+// another cache 176 us (90%), and round within their own 189 us (84%); 24 beams of
+// 517 tokens put in order 10.4 us, two launches' latency. Within a cache columns get
+// narrower with the distinct sources (all are in one stage), and slow: each of 24, 64
+// and 256 sequences from another at 67, 45 and 12% of the copy rate (88, 354 and 2540
+// us); 520 of 1100 tokens from nine of them 380 us, each from another 16 ms.
 template <int DT, int CODE>
 __global__ void __launch_bounds__(32) k_cache8_take(const __grid_constant__ TakeArgs a) {
   extern __shared__ __align__(128) unsigned char area[];
@@ -358,7 +359,7 @@ struct KeepLane {
 // Between two caches: a CTA (a warp) takes a run of a list.
 //
 // Bound by bytes. On a GB300, half the blocks of 8 x 32768 tokens (8 KV heads,
-// int8): 98 us, 80% of the measured copy rate, the check of the lists among it;
+// int8): 97 us, 82% of the measured copy rate, the check of the lists among it;
 // of one such sequence 16 us.
 template <int DT, int CODE>
 __global__ void __launch_bounds__(32) k_cache8_keep(const __grid_constant__ KeepArgs a) {
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(32) k_cache8_keep(const __grid_constant__ Keep
 // of different heads and parts of blocks do not depend on one another.
 //
 // Bound by bytes, or by what few CTAs keep on their way. On a GB300, half the
-// blocks of 8 x 32768 tokens 128 us, 62% of the measured copy rate; of one such
+// blocks of 8 x 32768 tokens 129 us, 61% of the measured copy rate; of one such
 // sequence 21 us (67 us with bulk copies of 256 bytes, which the copy engine
 // takes as long for as for 2 KB).
 constexpr int kInsideThreads = 256, kInsideLoads = 4;
